@@ -159,8 +159,11 @@ int gemm_scale_bias_act_cfg(int64_t M, int64_t N, int64_t K,
  *              overlapping A, B, C or the bias.  Its first bytes hold one
  *              32-bit arrival counter per tile and must be zero before the
  *              first call (allocate it zero-filled); every call leaves them
- *              zero again, so the same workspace serves any number of calls
- *              in stream order.  Calls that may run at the same time (other
+ *              zero again (the first 512 bytes in all, what calls of up to
+ *              128 tiles count in), so the same workspace serves any number
+ *              of calls in stream order, of any shapes as long as none is
+ *              forced to split over more than 128 tiles after another has
+ *              split over fewer.  Calls that may run at the same time (other
  *              streams, other threads) need workspaces of their own.
  *   workspace_bytes  its size; gsr_workspace_bytes gives what the library's
  *              choice needs (at most 4 MiB + 512 bytes for any shape)

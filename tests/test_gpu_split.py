@@ -262,3 +262,26 @@ def test_split_with_a_less_aligned_c(gsr, orc, c_off):
     PT.assert_bitwise(f"split C+{2 * c_off}B", bits(c.cpu()), ref)
     host = buf.cpu()
     assert bool((host[:c_off] == 3.0).all()) and bool((host[c_off + M * N:] == 3.0).all()), "guard values written"
+
+
+@pytest.mark.parametrize("entry", ["workspace", "noalloc"])
+def test_one_workspace_for_few_and_many_tiles(gsr, native, orc, entry):
+    """Calls of 64 and of 128 tiles in turn on one workspace (and on the
+    library's scratch array): the partial sums of the first lie where the
+    second counts arrivals, and every output is written all the same."""
+    ws = gsr.new_workspace(gsr.workspace_bytes(64, 4096, 4096))
+    for i, (M, N, K) in enumerate([(1, 4096, 4096), (64, 4096, 4096), (16, 4096, 4096), (48, 4096, 4096)]):
+        assert tiles_of(gsr, M, N, 22) == (64, 128, 64, 128)[i] and 0 < gsr.workspace_bytes(M, N, K) <= ws.numel()
+        a, b = W.integer_inputs(M, N, K, seed=101 + i)
+        ref, _ = orc.gemm_scale_relu(bits(a), bits(b), 0.5)
+        ad, bd = a.to(DEV), b.to(DEV)
+        c = torch.full((M, N), float("nan"), dtype=torch.float16, device=DEV)
+        say(f"[gpu] one {entry} for {M}x{N}x{K}")
+        if entry == "workspace":
+            gsr.gemm_scale_relu_ws(ad, bd, 0.5, ws, c=c)
+            assert counters_zero(ws, 128)
+        else:
+            assert native.gemm_scale_bias_act_noalloc(M, N, K, ad.data_ptr(), bd.data_ptr(), 0, c.data_ptr(), 0.5, 0,
+                                                      torch.cuda.current_stream().cuda_stream, -1, 0) == 0
+        torch.cuda.synchronize()
+        PT.assert_bitwise(f"{entry} {M}x{N}x{K}", bits(c.cpu()), ref)

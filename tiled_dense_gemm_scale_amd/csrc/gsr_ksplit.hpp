@@ -264,6 +264,15 @@ struct KsSum {
             });
         });
         if (tid == 0) __hip_atomic_store(p.ws_count + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // A call of at most 64 tiles keeps its partial sums from byte 256 on,
+        // where a call of 65..128 tiles has counters: the first 64 sums (part
+        // 0 of tile 0, units 0..7) go back to zero too, once the thread that
+        // read each of them is past its read.
+        if (tile == 0 && tiles <= 64 && u < 8) {
+            uint64_t* dst = words(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) __hip_atomic_store(dst + i, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
     }
 };
 
