@@ -219,6 +219,64 @@ int gemm_scale_bias_act_noalloc(int64_t M, int64_t N, int64_t K,
  * that call does not split, -1 for a negative dimension.  Host only. */
 int64_t gsr_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/* ---- rows sorted by group and back ------------------------------------------
+ * The rows around a product whose weights differ from row to row (routed
+ * experts): T tokens, each with k choices among `groups` groups, give n = T k
+ * slots; slot t k + j is token t's choice j.  A slot whose id is outside
+ * [0, groups) is dropped.  Rows of fp16 values are row-major and contiguous,
+ * `width` values each; any 2-byte alignment is accepted and the widest unit
+ * (16, 8, 4 or 2 bytes) that the addresses and the width allow is used.
+ * Counts are below 2^31 (GSR_ERROR_TOO_LARGE), matrices may be larger than
+ * 2^31 bytes.  Outputs must not overlap inputs or each other
+ * (GSR_ERROR_INVALID_VALUE).  No kernel here uses atomics on memory: equal
+ * inputs give equal bits.  Ownership, streams and errors as above. */
+
+/* Slots sorted by group, in slot order within a group:
+ *   ids        T x k ids, row-major, of id_bytes = 4 or 8 bytes each, signed
+ *   offsets    groups + 1 values: group e has the sorted rows offsets[e] ..
+ *              offsets[e + 1] - 1; offsets[groups] is the count of kept slots
+ *   rows       n values: the token of each sorted row, -1 from
+ *              offsets[groups] on
+ *   positions  T x k values: the sorted row of each slot, -1 for a dropped one
+ * groups is 1..1024.  workspace: gsr_group_workspace_bytes(T, k, groups) bytes
+ * (0 up to 8192 slots), 16-byte aligned, any content, and one per call that
+ * may run at the same time; GSR_ERROR_INVALID_VALUE if smaller.  T = 0 or
+ * k = 0 writes the offsets only (zeros). */
+int gsr_group_rows(int64_t tokens, int64_t k, int64_t groups, const void* ids, int32_t id_bytes,
+                   int32_t* offsets, int32_t* rows, int32_t* positions,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The bytes gsr_group_rows needs; -1 for arguments it rejects.  Host only. */
+int64_t gsr_group_workspace_bytes(int64_t tokens, int64_t k, int64_t groups);
+
+/* out[p] = x[rows[p]] for p < rows_out; zeros where rows[p] is outside
+ * [0, rows_in).  An index may occur any number of times. */
+int gsr_gather_rows(int64_t rows_out, int64_t rows_in, int64_t width,
+                    const void* x, const int32_t* rows, void* out, void* stream);
+
+/* out[t] = sum over j of weights[t, j] * y[positions[t, j]], j ascending, in
+ * binary32, one narrowing to binary16; choices whose position is outside
+ * [0, rows_in) have no term (whatever lies in y).  weights: T x k binary32,
+ * or NULL for ones, which makes this the gradient of gsr_gather_rows. */
+int gsr_combine_rows(int64_t tokens, int64_t k, int64_t rows_in, int64_t width,
+                     const void* y, const int32_t* positions, const float* weights,
+                     void* out, void* stream);
+
+/* The gradient of gsr_combine_rows for dout (T x width):
+ *   dy        (rows_in x width): weights[t, j] * dout[t] in row
+ *             positions[t, j]; zeros in the rows p with rows[p] outside
+ *             [0, tokens).  With the rows and positions of gsr_group_rows
+ *             every row is written; rows that neither names stay as they were.
+ *             Positions inside [0, rows_in) must be distinct.
+ *   dweights  (T x k binary32): the products <dout[t], y[positions[t, j]]>,
+ *             0 for a choice without a position.
+ * weights and dweights are both given or both NULL; without them dy = dout's
+ * rows and y is not read (it may be NULL). */
+int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_t width,
+                              const void* dout, const void* y, const int32_t* positions,
+                              const float* weights, const int32_t* rows,
+                              void* dy, float* dweights, void* stream);
+
 /* Tuning table: exact problem shapes mapped to a launch, consulted before the
  * built-in selector (by every entry point called with config id -1, and by
  * gsr_select_config).  The file is text, one entry per line,

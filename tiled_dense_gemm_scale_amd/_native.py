@@ -86,6 +86,16 @@ def lib() -> ctypes.CDLL:
             L.gemm_scale_bias_act_noalloc.restype = ctypes.c_int
             L.gsr_workspace_bytes.argtypes = [i64, i64, i64]
             L.gsr_workspace_bytes.restype = i64
+            L.gsr_group_rows.argtypes = [i64, i64, i64, vp, i32, vp, vp, vp, vp, i64, vp]
+            L.gsr_group_rows.restype = ctypes.c_int
+            L.gsr_group_workspace_bytes.argtypes = [i64, i64, i64]
+            L.gsr_group_workspace_bytes.restype = i64
+            L.gsr_gather_rows.argtypes = [i64, i64, i64, vp, vp, vp, vp]
+            L.gsr_gather_rows.restype = ctypes.c_int
+            L.gsr_combine_rows.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, vp]
+            L.gsr_combine_rows.restype = ctypes.c_int
+            L.gsr_combine_rows_backward.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.gsr_combine_rows_backward.restype = ctypes.c_int
             L.gsr_load_tuning.argtypes = [ctypes.c_char_p]
             L.gsr_load_tuning.restype = ctypes.c_int
             L.gsr_clear_tuning.argtypes = []
@@ -177,6 +187,38 @@ def workspace_bytes(M: int, N: int, K: int) -> int:
     if got < 0:
         raise GsrError(GSR_ERROR_INVALID_VALUE, status_string(GSR_ERROR_INVALID_VALUE))
     return got
+
+
+def group_rows(tokens: int, k: int, groups: int, ids: int, id_bytes: int, offsets: int, rows: int, positions: int,
+               workspace: int, workspace_bytes: int, stream: int) -> int:
+    """Raw entry point: slots sorted by group.  Returns the gsr_status."""
+    return lib().gsr_group_rows(tokens, k, groups, ids or None, int(id_bytes), offsets or None, rows or None,
+                                positions or None, workspace or None, int(workspace_bytes), stream or None)
+
+
+def group_workspace_bytes(slots: int, groups: int) -> int:
+    """Workspace bytes that group_rows needs for this many slots (0: none)."""
+    got = int(lib().gsr_group_workspace_bytes(int(slots), 1, int(groups)))
+    if got < 0:
+        raise GsrError(GSR_ERROR_INVALID_VALUE, status_string(GSR_ERROR_INVALID_VALUE))
+    return got
+
+
+def gather_rows(rows_out: int, rows_in: int, width: int, x: int, rows: int, out: int, stream: int) -> int:
+    return lib().gsr_gather_rows(rows_out, rows_in, width, x or None, rows or None, out or None, stream or None)
+
+
+def combine_rows(tokens: int, k: int, rows_in: int, width: int, y: int, positions: int, weights: int, out: int,
+                 stream: int) -> int:
+    return lib().gsr_combine_rows(tokens, k, rows_in, width, y or None, positions or None, weights or None,
+                                  out or None, stream or None)
+
+
+def combine_rows_backward(tokens: int, k: int, rows_in: int, width: int, dout: int, y: int, positions: int,
+                          weights: int, rows: int, dy: int, dweights: int, stream: int) -> int:
+    return lib().gsr_combine_rows_backward(tokens, k, rows_in, width, dout or None, y or None, positions or None,
+                                           weights or None, rows or None, dy or None, dweights or None,
+                                           stream or None)
 
 
 def load_tuning(path: str) -> None:

@@ -10,13 +10,15 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libgsr.so")
-SOURCES = [os.path.join(CSRC, "gsr_api.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("gsr_api.hip", "gsr_rows_api.hip")]
 # The digest of the sources a build used is written beside the library, so a
 # library older than its sources can be told apart from a current one.
 DIGEST_SUFFIX = ".sources"
@@ -58,20 +60,30 @@ def hipcc() -> str:
 
 
 def build(output: str = LIBRARY, verbose: bool = False, extra=()) -> str:
-    cmd = [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
-           # no packed-fp32 VALU instructions anywhere in the device code
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           "-I", INCLUDE, "-I", CSRC, *extra, *SOURCES, "-o", output + ".tmp"]
+    flags = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
+             # no packed-fp32 VALU instructions anywhere in the device code
+             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+             "-I", INCLUDE, "-I", CSRC, *extra]
     if verbose:
-        cmd.insert(1, "-Rpass-analysis=kernel-resource-usage")
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+        flags.insert(0, "-Rpass-analysis=kernel-resource-usage")
     noise = "'-packed-fp32-ops' is not a recognized feature for this target"
-    err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
-    if verbose and err:
-        print(err)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
+        return err
+
+    # one compiler per source, all at once, then the link
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(len(SOURCES)) as pool:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
+        errs = list(pool.map(lambda so: run([hipcc(), *flags, "-c", so[0], "-o", so[1]]), zip(SOURCES, objects)))
+        errs.append(run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", output + ".tmp"]))
+    if verbose:
+        print("\n".join(e for e in errs if e))
     digest = source_digest()
     os.replace(output + ".tmp", output)
     with open(output + DIGEST_SUFFIX, "w") as f:

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "gsr.h"
+#include "gsr_host.hpp"
 #include "gsr_kernels.hpp"
 #include "gsr_pipeline.hpp"
 #include "gsr_interleave.hpp"
@@ -34,25 +35,51 @@ static __device__ __align__(256) uint8_t scratch[kScratchBytes];
 
 namespace {
 
-using gsr::Problem;
-
-typedef hipError_t (*launch_fn)(const Problem&, int grid, hipStream_t);
-
-template <typename T>
-struct as_is {
-    using type = T;
+struct DeviceInfo {
+    bool ok;
+    bool gfx950;
 };
 
-// Enqueues `kernel` and returns the status of this launch alone.  The status
-// comes from hipLaunchKernel's return value, not from hipGetLastError: an
-// error that an earlier, unrelated HIP call left pending on the calling
-// thread is neither reported as this launch's nor cleared.
-template <typename... P>
-hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, typename as_is<P>::type... args)
+constexpr int kMaxDevices = 64;
+std::once_flag g_once[kMaxDevices];
+DeviceInfo g_info[kMaxDevices];
+
+}  // namespace
+
+int gsr::host::check_device()
 {
-    void* argv[] = {(void*)&args...};
-    return hipLaunchKernel((const void*)kernel, grid, block, argv, 0, s);
+    int count = 0;
+    if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
+        (void)hipGetLastError();
+        return GSR_ERROR_NO_DEVICE;
+    }
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
+        (void)hipGetLastError();
+        return GSR_ERROR_NO_DEVICE;
+    }
+    std::call_once(g_once[dev], [dev]() {
+        hipDeviceProp_t prop;
+        DeviceInfo info{false, false};
+        if (hipGetDeviceProperties(&prop, dev) == hipSuccess) {
+            info.ok = true;
+            info.gfx950 = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+        } else {
+            (void)hipGetLastError();
+        }
+        g_info[dev] = info;
+    });
+    if (!g_info[dev].ok) return GSR_ERROR_NO_DEVICE;
+    if (!g_info[dev].gfx950) return GSR_ERROR_UNSUPPORTED_DEVICE;
+    return GSR_SUCCESS;
 }
+
+namespace {
+
+using gsr::Problem;
+using namespace gsr::host;
+
+typedef hipError_t (*launch_fn)(const Problem&, int grid, hipStream_t);
 
 template <int BM, int BN, int BK, int WM, int WN, bool VEC>
 hipError_t launch_staged(const Problem& p, int grid, hipStream_t s)
@@ -172,8 +199,6 @@ const Entry* entry_of(int id)
         if (e.cfg.id == id) return &e;
     return nullptr;
 }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tile selection.  A candidate's cost is the time of one tile,
 //     2 * bm * bn * K / (per-CU rate) + per-tile overhead,
@@ -327,43 +352,6 @@ Launch resolve(int64_t M, int64_t N, int64_t K, int config_id)
     return Launch{id, entry_of(id)->cfg.group_m, entry_of(id)->cfg.xcd_remap};
 }
 
-struct DeviceInfo {
-    bool ok;
-    bool gfx950;
-};
-
-constexpr int kMaxDevices = 64;
-std::once_flag g_once[kMaxDevices];
-DeviceInfo g_info[kMaxDevices];
-
-int check_device()
-{
-    int count = 0;
-    if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
-        (void)hipGetLastError();
-        return GSR_ERROR_NO_DEVICE;
-    }
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
-        (void)hipGetLastError();
-        return GSR_ERROR_NO_DEVICE;
-    }
-    std::call_once(g_once[dev], [dev]() {
-        hipDeviceProp_t prop;
-        DeviceInfo info{false, false};
-        if (hipGetDeviceProperties(&prop, dev) == hipSuccess) {
-            info.ok = true;
-            info.gfx950 = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-        } else {
-            (void)hipGetLastError();
-        }
-        g_info[dev] = info;
-    });
-    if (!g_info[dev].ok) return GSR_ERROR_NO_DEVICE;
-    if (!g_info[dev].gfx950) return GSR_ERROR_UNSUPPORTED_DEVICE;
-    return GSR_SUCCESS;
-}
-
 // The scratch array's address on the current device, looked up once per
 // device (with that device current) on its first use.
 std::once_flag g_scratch_once[kMaxDevices];
@@ -390,23 +378,6 @@ int scratch_of_current_device(void** out)
     });
     *out = g_scratch_ptr[dev];
     return g_scratch_status[dev];
-}
-
-// The element-wise kernel's load unit for an operand whose rows are `len`
-// fp16 values long: the largest power of two up to 16 bytes dividing both the
-// address and the row length in bytes, so that every row start (and the end
-// of the matrix) falls on a multiple of it.
-int load_unit(const void* p, int64_t len)
-{
-    int u = 16;
-    while (u > 2 && ((((uintptr_t)p) % (uintptr_t)u) != 0 || ((uint64_t)len * 2u) % (uint64_t)u != 0)) u >>= 1;
-    return u;
-}
-
-bool overlaps(const void* a, uint64_t abytes, const void* b, uint64_t bbytes)
-{
-    const uint64_t x = (uint64_t)(uintptr_t)a, y = (uint64_t)(uintptr_t)b;
-    return abytes > 0 && bbytes > 0 && x < y + bbytes && y < x + abytes;
 }
 
 int validate(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const void* C)

@@ -1,0 +1,52 @@
+// gsr_host.hpp -- host-side pieces that the library's translation units
+// share: the launch, the device check and the argument helpers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gsr {
+namespace host {
+
+template <typename T>
+struct as_is {
+    using type = T;
+};
+
+// Enqueues `kernel` and returns the status of this launch alone.  The status
+// comes from hipLaunchKernel's return value, not from hipGetLastError: an
+// error that an earlier, unrelated HIP call left pending on the calling
+// thread is neither reported as this launch's nor cleared.
+template <typename... P>
+hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, typename as_is<P>::type... args)
+{
+    void* argv[] = {(void*)&args...};
+    return hipLaunchKernel((const void*)kernel, grid, block, argv, 0, s);
+}
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The widest unit (16, 8, 4 or 2 bytes) for an operand whose rows are `len`
+// fp16 values long: the largest power of two up to 16 bytes dividing both the
+// address and the row length in bytes, so that every row start (and the end
+// of the matrix) falls on a multiple of it.
+inline int load_unit(const void* p, int64_t len)
+{
+    int u = 16;
+    while (u > 2 && ((((uintptr_t)p) % (uintptr_t)u) != 0 || ((uint64_t)len * 2u) % (uint64_t)u != 0)) u >>= 1;
+    return u;
+}
+
+inline bool overlaps(const void* a, uint64_t abytes, const void* b, uint64_t bbytes)
+{
+    const uint64_t x = (uint64_t)(uintptr_t)a, y = (uint64_t)(uintptr_t)b;
+    return abytes > 0 && bbytes > 0 && x < y + bbytes && y < x + abytes;
+}
+
+inline bool misaligned(const void* p, uintptr_t unit) { return ((uintptr_t)p & (unit - 1)) != 0; }
+
+// GSR_SUCCESS when the current device is a gfx950 (gsr_api.hip).
+__attribute__((visibility("hidden"))) int check_device();
+
+}  // namespace host
+}  // namespace gsr

@@ -622,7 +622,7 @@ gemm_scale_relu_kernel(Problem p)
 
 // K == 0: every output is the empty sum, so C[m,n] = act(alpha * 0 + bias[n])
 // (+0 without a bias).
-__global__ void __launch_bounds__(256) fill_epilogue_kernel(uint16_t* C, uint32_t M, uint32_t N,
+static __global__ void __launch_bounds__(256) fill_epilogue_kernel(uint16_t* C, uint32_t M, uint32_t N,
                                                             const uint16_t* bias, float alpha, int act)
 {
     const uint32_t count = M * N;
