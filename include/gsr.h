@@ -277,6 +277,34 @@ int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_
                               const float* weights, const int32_t* rows,
                               void* dy, float* dweights, void* stream);
 
+/* Grouped products: every group of rows has a B (and bias) of its own, as the
+ * experts of a routed layer do.  For group e and its rows
+ * offsets[e] <= r < offsets[e + 1]:
+ *
+ *     C[r,n] = act( alpha * sum_{k<K} A[rows[r],k] * B[e,k,n] + bias[e,n] )
+ *
+ *   C        P x N; rows outside every group stay as they were
+ *   A        a_rows x K with rows, P x K (row r itself) without (rows NULL,
+ *            a_rows ignored)
+ *   rows     NULL, or P row indices; an index outside [0, a_rows) is a row of
+ *            zeros.  The copy of A's rows into group order is not made: the
+ *            kernels fetch them where they are.
+ *   B        groups x K x N; bias NULL or groups x N
+ *   offsets  groups + 1 values on the device, not decreasing, in [0, P] (the
+ *            offsets of gsr_group_rows); a group may be empty.  Other values
+ *            are clamped: they make wrong results, never an access outside.
+ * Epilogue, precision, alignment, ownership and errors as gemm_scale_bias_act
+ * (same kernels per tile, so a group's outputs are the bits of that call on
+ * its rows with the same configuration).  GSR_ERROR_TOO_LARGE for P >= 2^31,
+ * more than 1024 groups, K or N >= 2^22, one group's B of 2^31 bytes or more,
+ * or, with rows, an A of 2^31 bytes or more; P x N, P x K and the whole B may
+ * be larger.  config_id: -1, or one of 21, 22, 28, 31 and 32 (forced tile;
+ * others GSR_ERROR_INVALID_CONFIG). */
+int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
+                                const void* A, int64_t a_rows, const int32_t* rows,
+                                const void* B, const void* bias, void* C, const int32_t* offsets,
+                                float alpha, int32_t activation, void* stream, int32_t config_id);
+
 /* Tuning table: exact problem shapes mapped to a launch, consulted before the
  * built-in selector (by every entry point called with config id -1, and by
  * gsr_select_config).  The file is text, one entry per line,

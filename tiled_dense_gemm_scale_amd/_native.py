@@ -96,6 +96,8 @@ def lib() -> ctypes.CDLL:
             L.gsr_combine_rows.restype = ctypes.c_int
             L.gsr_combine_rows_backward.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
             L.gsr_combine_rows_backward.restype = ctypes.c_int
+            L.gemm_grouped_scale_bias_act.argtypes = [i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, f32, i32, vp, i32]
+            L.gemm_grouped_scale_bias_act.restype = ctypes.c_int
             L.gsr_load_tuning.argtypes = [ctypes.c_char_p]
             L.gsr_load_tuning.restype = ctypes.c_int
             L.gsr_clear_tuning.argtypes = []
@@ -219,6 +221,15 @@ def combine_rows_backward(tokens: int, k: int, rows_in: int, width: int, dout: i
     return lib().gsr_combine_rows_backward(tokens, k, rows_in, width, dout or None, y or None, positions or None,
                                            weights or None, rows or None, dy or None, dweights or None,
                                            stream or None)
+
+
+def gemm_grouped_scale_bias_act(P: int, N: int, K: int, groups: int, A: int, a_rows: int, rows: int, B: int, bias: int,
+                                C: int, offsets: int, alpha: float, activation: int, stream: int,
+                                config_id: int = -1) -> int:
+    """Raw entry point of the grouped products.  Returns the gsr_status."""
+    return lib().gemm_grouped_scale_bias_act(P, N, K, groups, A or None, a_rows, rows or None, B or None, bias or None,
+                                             C or None, offsets or None, float(alpha), int(activation),
+                                             stream or None, int(config_id))
 
 
 def load_tuning(path: str) -> None:

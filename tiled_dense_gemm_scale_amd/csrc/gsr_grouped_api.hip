@@ -1,0 +1,182 @@
+// gsr_grouped_api.hip -- host side of the grouped products of include/gsr.h:
+// argument checks, the tile and the launch on the caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "gsr.h"
+#include "gsr_host.hpp"
+#include "gsr_interleave16c.hpp"
+#include "gsr_interleave16d.hpp"
+#include "gsr_kspec.hpp"
+
+namespace gsr {
+
+// K == 0: every row of a group is act(alpha * 0 + bias[n]) (+0 without one).
+static __global__ void __launch_bounds__(256) fill_grouped_kernel(Problem p)
+{
+    for (int e = blockIdx.x; e < p.groups; e += gridDim.x) {
+        const int lo = min(max(p.offsets[e], 0), p.M), hi = min(p.offsets[e + 1], p.M);
+        for (int64_t i = (int64_t)lo * p.N + threadIdx.x; i < (int64_t)hi * p.N; i += 256) {
+            const int n = (int)(i % p.N);
+            const float b = p.bias ? (float)__builtin_bit_cast(_Float16, p.bias[(int64_t)e * p.N + n]) : 0.0f;
+            p.C[i] = (p.bias != nullptr || p.act != kActRelu)
+                         ? __builtin_bit_cast(uint16_t, (_Float16)activate(0.0f * p.alpha + b, p.act))
+                         : (uint16_t)0;
+        }
+    }
+}
+
+}  // namespace gsr
+
+namespace {
+
+using gsr::Problem;
+using namespace gsr::host;
+
+constexpr int64_t kLimit = (int64_t)1 << 31;
+constexpr int64_t kMaxGroups = 1024;
+
+typedef hipError_t (*launch_fn)(const Problem&, int grid, hipStream_t);
+
+template <class T>
+hipError_t launch_ilv16d(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel(gsr::gemm_scale_relu_ilv16d_kernel<T, true>, dim3(grid), dim3(T::NT), s, p);
+}
+
+template <class T>
+hipError_t launch_ilv16c(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel(gsr::gemm_scale_relu_ilv16c_kernel<T, true>, dim3(grid), dim3(T::NT), s, p);
+}
+
+template <int BM, int BN, int S, int D>
+hipError_t launch_kspec(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel((gsr::gemm_scale_relu_kspec_kernel<BM, BN, S, D, false, true>), dim3(grid), dim3(512), s, p);
+}
+
+template <int BM, int BN>
+hipError_t launch_staged(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, true>), dim3(grid), dim3(256), s, p);
+}
+
+// The grouped forms of the selector's tiles, under the ids of their dense
+// forms, with the element-wise kernel that stands in for them.
+struct Entry {
+    int id;
+    int bm, bn;
+    launch_fn vec;
+    int elem_bm, elem_bn;
+    launch_fn elem;
+    int group_m;
+};
+const Entry kTable[] = {
+    {21, 64, 64, launch_kspec<64, 64, 4, 2>, 64, 64, launch_staged<64, 64>, 4},
+    {22, 32, 64, launch_kspec<32, 64, 4, 2>, 64, 64, launch_staged<64, 64>, 4},
+    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, 128, 128, launch_staged<128, 128>, 4},
+    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, 128, 128, launch_staged<128, 128>, 4},
+    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, 128, 128, launch_staged<128, 128>, 4},
+};
+
+const Entry* entry_of(int id)
+{
+    for (const Entry& e : kTable)
+        if (e.id == id) return &e;
+    return nullptr;
+}
+
+// The tile: the dense selector's estimate on the tile rows that `groups`
+// groups of uneven, unknown sizes are expected to give, one for a group that
+// fits a tile and half a tile more than its rows fill otherwise.
+const Entry& select(int64_t P, int64_t groups, int64_t N, int64_t K)
+{
+    const double used = (double)std::min(groups, P), mean = (double)P / used;
+    const Entry* best = nullptr;
+    double best_t = 1e300;
+    for (const Entry& e : kTable) {
+        const double tiles = used * std::max(1.0, mean / e.bm + 0.5) * (double)cdiv(N, e.bn);
+        const double t = launch_cost(e.id, std::ceil(tiles), K);
+        if (t < best_t) best_t = t, best = &e;
+    }
+    return *best;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups, const void* A, int64_t a_rows,
+                                const int32_t* rows, const void* B, const void* bias, void* C,
+                                const int32_t* offsets, float alpha, int32_t activation, void* stream,
+                                int32_t config_id)
+{
+    if (P < 0 || N < 0 || K < 0 || groups < 0 || a_rows < 0) return GSR_ERROR_INVALID_VALUE;
+    if (rows == nullptr) a_rows = P;
+    // 32-bit byte offsets within a tile of C, within one group's B and, with
+    // rows, within A
+    if (P >= kLimit || N >= kLimit || K >= kLimit || a_rows >= kLimit || groups > kMaxGroups) return GSR_ERROR_TOO_LARGE;
+    if (N * 512 >= kLimit || K * 512 >= kLimit || N * K * 2 >= kLimit) return GSR_ERROR_TOO_LARGE;
+    if (rows != nullptr && a_rows * K * 2 >= kLimit) return GSR_ERROR_TOO_LARGE;
+    if (!std::isfinite(alpha)) return GSR_ERROR_INVALID_VALUE;
+    if (activation != GSR_ACT_RELU && activation != GSR_ACT_GELU && activation != GSR_ACT_NONE)
+        return GSR_ERROR_INVALID_VALUE;
+    if (config_id < -1 || (config_id >= 0 && entry_of(config_id) == nullptr)) return GSR_ERROR_INVALID_CONFIG;
+    if (P == 0 || N == 0 || groups == 0) return GSR_SUCCESS;
+    if (C == nullptr || offsets == nullptr || misaligned(C, 2) || misaligned(offsets, 4) || misaligned(rows, 4) ||
+        misaligned(A, 2) || misaligned(B, 2) || misaligned(bias, 2))
+        return GSR_ERROR_INVALID_VALUE;
+    if (K > 0 && (B == nullptr || (A == nullptr && a_rows > 0))) return GSR_ERROR_INVALID_VALUE;
+    const uint64_t cb = (uint64_t)P * (uint64_t)N * 2u;
+    if (overlaps(C, cb, A, (uint64_t)a_rows * (uint64_t)K * 2u) ||
+        overlaps(C, cb, B, (uint64_t)groups * (uint64_t)K * (uint64_t)N * 2u) ||
+        overlaps(C, cb, offsets, (uint64_t)(groups + 1) * 4u) ||
+        (rows != nullptr && overlaps(C, cb, rows, (uint64_t)P * 4u)) ||
+        (bias != nullptr && overlaps(C, cb, bias, (uint64_t)groups * (uint64_t)N * 2u)))
+        return GSR_ERROR_INVALID_VALUE;
+    const int st = check_device();
+    if (st != GSR_SUCCESS) return st;
+
+    Problem p{};
+    p.A = (const uint16_t*)A;
+    p.B = (const uint16_t*)B;
+    p.C = (uint16_t*)C;
+    p.bias = (const uint16_t*)bias;
+    p.M = (int)P;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.alpha = alpha;
+    p.act = (int)activation;
+    p.offsets = offsets;
+    p.rows = rows;
+    p.groups = (int)groups;
+    p.a_rows = (int)a_rows;
+    p.ksplit = 1;
+    p.kchunk = (int)K;
+    p.xcd_remap = 1;
+    p.unit_a = load_unit(A, K);
+    p.unit_b = load_unit(B, N);
+    p.unit_c = load_unit(C, N);
+    hipStream_t s = (hipStream_t)stream;
+    if (K == 0) {
+        const hipError_t err = launch_kernel(gsr::fill_grouped_kernel, dim3((unsigned)groups), dim3(256), s, p);
+        return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+    }
+    const Entry& e = config_id >= 0 ? *entry_of(config_id) : select(P, groups, N, K);
+    const bool vec = p.unit_a == 16 && p.unit_b == 16 && (((uintptr_t)bias & 7u) == 0);
+    const int bm = vec ? e.bm : e.elem_bm, bn = vec ? e.bn : e.elem_bn;
+    p.tiles_n = (int)cdiv(N, bn);
+    p.group_m = e.group_m;
+    // tile rows: at most one part-filled tile for each group that has rows
+    const int64_t used = std::min(groups, P);
+    const int64_t grid = (P + used * (bm - 1)) / bm * p.tiles_n;
+    if (grid >= kLimit) return GSR_ERROR_TOO_LARGE;
+    const hipError_t err = (vec ? e.vec : e.elem)(p, (int)grid, s);
+    return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+}
+
+}  // extern "C"

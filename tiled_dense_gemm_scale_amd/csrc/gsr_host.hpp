@@ -48,5 +48,9 @@ inline bool misaligned(const void* p, uintptr_t unit) { return ((uintptr_t)p & (
 // GSR_SUCCESS when the current device is a gfx950 (gsr_api.hip).
 __attribute__((visibility("hidden"))) int check_device();
 
+// The selector's estimate of a launch (gsr_api.hip): `wgs` workgroups of tile
+// configuration `id` over K, in us.
+__attribute__((visibility("hidden"))) double launch_cost(int id, double wgs, int64_t K);
+
 }  // namespace host
 }  // namespace gsr

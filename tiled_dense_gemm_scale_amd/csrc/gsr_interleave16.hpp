@@ -147,7 +147,7 @@ __device__ __forceinline__ void ilv16_epilogue_t(const Problem& p, const f32x4 (
     });
 }
 
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+static __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_scale_relu_ilv16_kernel(Problem p)
 {
     using T = Ilv16Cfg;

@@ -108,7 +108,7 @@ __device__ __forceinline__ void for_each_ic(F& f, std::integer_sequence<int, I..
     (f(std::integral_constant<int, I>{}), ...);
 }
 
-template <class T>
+template <class T, bool GROUPED = false>
 __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
 {
     constexpr int BK = T::BK, CH = T::CH, FM = T::FM, FN = T::FN;
@@ -130,9 +130,14 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    int tm, tn;
-    tile_of(blockIdx.x, gridDim.x, p, tm, tn);
-    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    int m0 = 0, n0;
+    if constexpr (GROUPED) {
+        if (!group_tile<T::BM, T::BN>(p, n0)) return;
+    } else {
+        int tm, tn;
+        tile_of(blockIdx.x, gridDim.x, p, tm, tn);
+        m0 = tm * T::BM, n0 = tn * T::BN;
+    }
     const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N;
     const uint32_t lds0 = lds_address(smem);
     // K-steps: the two-plus-three layout runs them in pairs (an odd count
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
         // ======================= copy waves =================================
         const uint32_t cw = (uint32_t)(wave - T::NW);
         const uint64_t a_base = (uint64_t)(uintptr_t)p.A + ((uint64_t)m0 * K) * 2u;
-        const uint32_t a_recs = ((uint32_t)p.M * K - (uint32_t)m0 * K) * 2u;
+        const uint32_t a_recs = ((uint32_t)a_extent<GROUPED>(p) * K - (uint32_t)m0 * K) * 2u;
         const uint64_t b_base = (uint64_t)(uintptr_t)p.B + (uint64_t)n0 * 2u;
         const uint32_t b_recs = (K * N - (uint32_t)n0) * 2u;
         auto rsrc_of = [](uint64_t base, uint32_t recs) {
@@ -166,6 +171,14 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
         const uint32_t av0 = arow + 16u * c0, av1 = arow + 32u * K * 2u + 16u * (c0 ^ 4u);
         const uint32_t kc0 = 8u * c0, kc1 = 8u * (c0 ^ 4u);
         const uint32_t a_istride = 64u * K * 2u;
+        uint32_t av[T::A_PER];  // GROUPED: each copy's row is looked up
+        if constexpr (GROUPED) {
+#pragma unroll
+            for (int i = 0; i < T::A_PER; ++i) {
+                const int r = a_row<GROUPED>(p, (int)(8u * cw + ((uint32_t)lane >> 3)) + 32 * i);
+                av[i] = r < 0 ? kOutOfRange : (uint32_t)r * K * 2u + 16u * ((i & 1) ? (c0 ^ 4u) : c0);
+            }
+        }
         // B: copy i fills chunk positions 64 (cw + 4i) + lane of the stage:
         // row k = RPK (cw + 4i) + lane / CPR, logical chunk
         // (lane % CPR) ^ fb16(k) (fb16 touches chunk bits 1-3 only)
@@ -182,7 +195,9 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
 #pragma unroll
             for (int i = 0; i < T::A_PER; ++i) {
                 const uint32_t kc = (i & 1) ? kc1 : kc0;
-                const uint32_t off = (kc < kleft) ? ((i & 1) ? av1 : av0) + (uint32_t)(i >> 1) * a_istride : kOutOfRange;
+                uint32_t off;
+                if constexpr (GROUPED) off = (kc < kleft) ? av[i] : kOutOfRange;
+                else off = (kc < kleft) ? ((i & 1) ? av1 : av0) + (uint32_t)(i >> 1) * a_istride : kOutOfRange;
                 copy16_to_lds(ra, off, lds0 + stage * (uint32_t)T::A_BYTES + (cw + (uint32_t)i * T::NCW) * 1024u);
             }
         };

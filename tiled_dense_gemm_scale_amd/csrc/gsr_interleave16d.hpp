@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t fb16(uint32_t k)
     return ((k & 3u) + (((c ^ (c >> 1)) & 1u) << 2)) << 1;
 }
 
-template <class T>
+template <class T, bool GROUPED = false>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_scale_relu_ilv16d_kernel(Problem p)
 {
@@ -134,15 +134,20 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / T::WN, wn = wave % T::WN;
 
-    int tm, tn;
-    tile_of(blockIdx.x, gridDim.x, p, tm, tn);
-    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    int m0 = 0, n0;
+    if constexpr (GROUPED) {
+        if (!group_tile<T::BM, T::BN>(p, n0)) return;
+    } else {
+        int tm, tn;
+        tile_of(blockIdx.x, gridDim.x, p, tm, tn);
+        m0 = tm * T::BM, n0 = tn * T::BN;
+    }
     const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N;
     const uint32_t lds0 = lds_address(smem);
 
     // ---- descriptors that advance along K (as in the register-transpose kernel)
     uint64_t a_base = (uint64_t)(uintptr_t)p.A + ((uint64_t)m0 * K) * 2u;
-    uint32_t a_recs = ((uint32_t)p.M * K - (uint32_t)m0 * K) * 2u;
+    uint32_t a_recs = ((uint32_t)a_extent<GROUPED>(p) * K - (uint32_t)m0 * K) * 2u;
     uint64_t b_base = (uint64_t)(uintptr_t)p.B + (uint64_t)n0 * 2u;
     uint32_t b_recs = (K * N - (uint32_t)n0) * 2u;
     auto rsrc_of = [](uint64_t base, uint32_t recs) {
@@ -167,6 +172,14 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     uint32_t av0 = arow + 16u * c0, av1 = arow + 32u * K * 2u + 16u * (c0 ^ 4u);
     uint32_t kc0 = 8u * c0, kc1 = 8u * (c0 ^ 4u);
     const uint32_t a_istride = 64u * K * 2u;
+    uint32_t av[T::A_PER];  // GROUPED: each copy's row is looked up
+    if constexpr (GROUPED) {
+#pragma unroll
+        for (int i = 0; i < T::A_PER; ++i) {
+            const int r = a_row<GROUPED>(p, 8 * wave + (lane >> 3) + 32 * i);
+            av[i] = r < 0 ? kOutOfRange : (uint32_t)r * K * 2u + 16u * ((i & 1) ? (c0 ^ 4u) : c0);
+        }
+    }
 
     // ---- B copy plan --------------------------------------------------------
     // Copy i of this wave fills B chunk positions P = 64 (wave + 4i) + lane:
@@ -229,7 +242,9 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
 
     auto copy_a = [&](int S, int i, uint32_t kleft, const i32x4& ra) {
         const uint32_t kc = (i & 1) ? kc1 : kc0;
-        const uint32_t off = (kc < kleft) ? ((i & 1) ? av1 : av0) + (uint32_t)(i >> 1) * a_istride : kOutOfRange;
+        uint32_t off;
+        if constexpr (GROUPED) off = (kc < kleft) ? av[i] : kOutOfRange;
+        else off = (kc < kleft) ? ((i & 1) ? av1 : av0) + (uint32_t)(i >> 1) * a_istride : kOutOfRange;
         copy16_to_lds(ra, off, lds0 + (uint32_t)(S * T::A_BYTES) + (uint32_t)(wave + i * T::NW) * 1024u);
     };
     auto copy_b = [&](int S, int i, const i32x4& rb) {

@@ -160,6 +160,13 @@ struct Problem {
     int ksplit, kchunk;
     float* ws_part;
     uint32_t* ws_count;
+    // grouped products (the GROUPED kernels): group e multiplies the rows
+    // offsets[e] .. offsets[e + 1] - 1 of C with its own B (K x N) and bias
+    // (N), all below `M` there; row r of C takes row rows[r] of A's a_rows, or
+    // row r when rows is null.
+    const int32_t* offsets;
+    const int32_t* rows;
+    int groups, a_rows;
 };
 
 // Eight outputs (16 bytes) at byte offset `off` of C, a multiple of 16 from
@@ -324,6 +331,85 @@ __device__ __forceinline__ void tile_of(int pid, int nwg, const Problem& p, int&
     tn = within / gs;
 }
 
+// The tile of a grouped product that this workgroup computes: every group's
+// rows are cut into tiles of BM by themselves, the tiles of all groups are
+// numbered one behind the other as tile rows, and tile_of orders them as it
+// does a dense grid's.  The group sizes are on the device, so every workgroup
+// adds them up for itself: a lane per group, one scan over the lanes per 64
+// groups.  The grid is an upper bound; false for the workgroups past the last
+// tile.  On true, `p` is that tile alone: its group's B and bias, its first
+// row's C (and A or rows), M its row count; bases are 64-bit, so only a tile
+// has to lie within 32-bit offsets.  Sizes are clamped to p.M rows in all,
+// so no offsets make it reach outside.
+template <int BM, int BN>
+__device__ __forceinline__ bool group_tile(Problem& p, int& n0)
+{
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = 0, inc = 0;  // the lane's group: first row, rows, tiles up to and with it
+    auto scan = [&](int e0) {
+        const int e = e0 + lane;
+        lo = n = 0;
+        if (e < p.groups) {
+            lo = min(max(p.offsets[e], 0), p.M);
+            n = max(min(p.offsets[e + 1], p.M) - lo, 0);
+        }
+        inc = (n + BM - 1) / BM;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        return __builtin_amdgcn_readlane(inc, 63);
+    };
+    int total = scan(0);
+    for (int e0 = 64; e0 < p.groups; e0 += 64) total += scan(e0);
+    const int nwg = total * p.tiles_n;
+    if ((int)blockIdx.x >= nwg) return false;
+    Problem q = p;
+    q.tiles_m = total;
+    int tm, tn;
+    tile_of(blockIdx.x, nwg, q, tm, tn);
+    int e0 = 0, before = 0;
+    if (p.groups > 64) {
+        int sum = scan(0);
+        while (tm >= before + sum) {
+            before += sum;
+            e0 += 64;
+            sum = scan(e0);
+        }
+    }
+    const int at = __ffsll((unsigned long long)__ballot(before + inc > tm)) - 1;  // the lane whose group holds tile row tm
+    const int e = e0 + at;
+    const int rows = __builtin_amdgcn_readlane(n, at);
+    const int skip = (tm - (before + __builtin_amdgcn_readlane(inc, at) - (rows + BM - 1) / BM)) * BM;
+    const int row0 = __builtin_amdgcn_readlane(lo, at) + skip;
+    p.M = min(BM, rows - skip);
+    p.B += (int64_t)e * p.K * p.N;
+    p.C += (int64_t)row0 * p.N;
+    if (p.bias != nullptr) p.bias += (int64_t)e * p.N;
+    if (p.rows != nullptr) p.rows += row0;
+    else p.A += (int64_t)row0 * p.K;
+    n0 = tn * BN;
+    return true;
+}
+
+// Rows of A that a kernel's buffer of A covers.
+template <bool GROUPED>
+__device__ __forceinline__ int a_extent(const Problem& p)
+{
+    return (GROUPED && p.rows != nullptr) ? p.a_rows : p.M;
+}
+
+// The row of A behind row m of the problem, or -1 for none.
+template <bool GROUPED>
+__device__ __forceinline__ int a_row(const Problem& p, int m)
+{
+    if (m >= p.M) return -1;
+    if (!GROUPED || p.rows == nullptr) return m;
+    const int r = p.rows[m];
+    return (uint32_t)r < (uint32_t)p.a_rows ? r : -1;
+}
+
 template <int BM, int BN, int BK, int WM, int WN, bool VEC>
 struct TileKernel {
     static constexpr int NT = kWave * WM * WN;  // threads per workgroup
@@ -347,7 +433,7 @@ struct TileKernel {
     static_assert(LDS_BYTES <= 163840, "LDS budget of one workgroup on gfx950");
 };
 
-template <int BM, int BN, int BK, int WM, int WN, bool VEC>
+template <int BM, int BN, int BK, int WM, int WN, bool VEC, bool GROUPED = false>
 __global__ void __launch_bounds__(kWave * WM * WN)
 gemm_scale_relu_kernel(Problem p)
 {
@@ -361,11 +447,16 @@ gemm_scale_relu_kernel(Problem p)
     const int wave = tid >> 6;
     const int wm = wave / WN, wn = wave % WN;
 
-    int tm, tn;
-    tile_of(blockIdx.x, gridDim.x, p, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+    int m0 = 0, n0;
+    if constexpr (GROUPED) {
+        if (!group_tile<BM, BN>(p, n0)) return;
+    } else {
+        int tm, tn;
+        tile_of(blockIdx.x, gridDim.x, p, tm, tn);
+        m0 = tm * BM, n0 = tn * BN;
+    }
 
-    const uint32_t a_bytes = (uint32_t)p.M * (uint32_t)p.K * 2u;
+    const uint32_t a_bytes = (uint32_t)a_extent<GROUPED>(p) * (uint32_t)p.K * 2u;
     const uint32_t b_bytes = (uint32_t)p.K * (uint32_t)p.N * 2u;
     const uint32_t c_bytes = (uint32_t)p.M * (uint32_t)p.N * 2u;
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.A, a_bytes);
@@ -383,6 +474,11 @@ gemm_scale_relu_kernel(Problem p)
 
     u32x4 areg[T::A_PER];
     u32x4 breg[T::B_PER][8];
+    int arow[T::A_PER];  // GROUPED: the thread's rows of A
+    if constexpr (GROUPED) {
+#pragma unroll
+        for (int i = 0; i < T::A_PER; ++i) arow[i] = a_row<GROUPED>(p, a_r0 + i * A_ROW_STEP);
+    }
 
     // On the element-wise path each operand is read in the widest unit its
     // alignment allows (p.unit_a, p.unit_b); the unit is picked once per
@@ -395,9 +491,10 @@ gemm_scale_relu_kernel(Problem p)
         const int kval = min(max(p.K - kk, 0), 8);
 #pragma unroll
         for (int i = 0; i < T::A_PER; ++i) {
-            const int r = a_r0 + i * A_ROW_STEP;
-            const int m = m0 + r;
-            const int nv = (m < p.M) ? kval : 0;
+            int m = m0 + a_r0 + i * A_ROW_STEP;
+            bool in = m < p.M;
+            if constexpr (GROUPED) m = arow[i], in = m >= 0;
+            const int nv = in ? kval : 0;
             areg[i] = load8_unit<U>(ra, (uint32_t)m * (uint32_t)p.K + (uint32_t)kk, nv);
         }
     };

@@ -40,7 +40,7 @@
 
 namespace gsr {
 
-template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT>
+template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED = false>
 __global__ void __launch_bounds__(512)
 gemm_scale_relu_kspec_kernel(Problem p)
 {
@@ -66,9 +66,14 @@ gemm_scale_relu_kspec_kernel(Problem p)
         kbeg = part * p.kchunk;
         kend = min(p.K, kbeg + p.kchunk);
     }
-    int tm, tn;
-    tile_of(tile, SPLIT ? p.tiles_m * p.tiles_n : (int)gridDim.x, p, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+    int m0 = 0, n0;
+    if constexpr (GROUPED) {
+        if (!group_tile<BM, BN>(p, n0)) return;
+    } else {
+        int tm, tn;
+        tile_of(tile, SPLIT ? p.tiles_m * p.tiles_n : (int)gridDim.x, p, tm, tn);
+        m0 = tm * BM, n0 = tn * BN;
+    }
     const int ksteps = (kend - kbeg + BK - 1) / BK;
 
     using Sum = KsSum<BM, BN, NW, 512>;  // the cross-wave sum runs on all eight waves
@@ -77,7 +82,7 @@ gemm_scale_relu_kspec_kernel(Problem p)
 
     if (copier) {
         // ---- copy waves ----------------------------------------------------------
-        const i32x4 ra = raw_rsrc(p.A, (uint32_t)p.M * (uint32_t)p.K * 2u);
+        const i32x4 ra = raw_rsrc(p.A, (uint32_t)a_extent<GROUPED>(p) * (uint32_t)p.K * 2u);
         const i32x4 rb = raw_rsrc(p.B, (uint32_t)p.K * (uint32_t)p.N * 2u);
         const uint32_t lds0 = lds_address(smem);
         uint32_t a_off[T::A_PER];
@@ -88,8 +93,9 @@ gemm_scale_relu_kspec_kernel(Problem p)
             const int P = 64 * (wave + i * NW) + lane;
             const int r = P / CHA;
             const int c = (P % CHA) ^ (int)swz_a16((uint32_t)r);
-            const int m = m0 + r;
+            int m = m0 + r;
             a_ok[i] = m < p.M;
+            if constexpr (GROUPED) m = a_row<GROUPED>(p, r), a_ok[i] = m >= 0;
             a_k[i] = 8 * c;
             a_off[i] = ((uint32_t)m * (uint32_t)p.K + (uint32_t)(kbeg + 8 * c)) * 2u;
         }

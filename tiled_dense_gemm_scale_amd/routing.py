@@ -1,6 +1,7 @@
-"""Routed experts around the fused product: the rows of a batch sorted by
-group (group_rows), copied into that order (gather_rows) and summed back with
-their weights (combine_rows and its gradient).
+"""Routed experts on the fused product: the rows of a batch sorted by group
+(group_rows), every group's product with its own weights (gemm_grouped), the
+rows copied into group order (gather_rows) and summed back with their weights
+(combine_rows and its gradient), and the whole layer (expert_mlp).
 
 Every function enqueues on `stream` (default: the current stream of the
 inputs' device); what it allocates itself is allocated for that stream.
@@ -15,7 +16,8 @@ import torch
 from . import _native
 from ._native import group_workspace_bytes
 
-__all__ = ["group_rows", "group_workspace_bytes", "gather_rows", "combine_rows", "combine_rows_backward"]
+__all__ = ["group_rows", "group_workspace_bytes", "gather_rows", "combine_rows", "combine_rows_backward",
+           "gemm_grouped", "expert_mlp"]
 
 
 @contextlib.contextmanager
@@ -175,3 +177,54 @@ def combine_rows_backward(dout: torch.Tensor, y: Optional[torch.Tensor], positio
             dweights.data_ptr() if weights is not None else 0, s)
     _native.check(st)
     return dy, dweights
+
+
+ACTIVATIONS = {"relu": _native.GSR_ACT_RELU, "gelu": _native.GSR_ACT_GELU, "none": _native.GSR_ACT_NONE}
+
+
+def gemm_grouped(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, alpha: float = 1.0, activation: str = "relu",
+                 c: Optional[torch.Tensor] = None, stream=None, config_id: int = -1) -> torch.Tensor:
+    """c[r] = act(alpha * a[rows[r]] @ b[e] + bias[e]) for the rows
+    offsets[e] <= r < offsets[e + 1] of every group e: a (T, K) fp16 with rows
+    (P,) int32 (an index outside [0, T) is a row of zeros), or a (P, K) without;
+    b (E, K, N) fp16, bias (E, N) fp16 or None, offsets (E + 1,) int32 on the
+    device (group_rows's), act "relu", "gelu" (tanh form) or "none".  Rows of
+    c outside every group stay as they were; a c allocated here holds
+    anything there.  Returns c (P, N)."""
+    check("a", a, torch.float16, (None, None), None)
+    dev, T, K = a.device, int(a.shape[0]), int(a.shape[1])
+    check("b", b, torch.float16, (None, K, None), dev)
+    E, N = int(b.shape[0]), int(b.shape[2])
+    check("offsets", offsets, torch.int32, (E + 1,), dev)
+    if rows is not None:
+        check("rows", rows, torch.int32, (None,), dev)
+    P = T if rows is None else int(rows.shape[0])
+    if bias is not None:
+        check("bias", bias, torch.float16, (E, N), dev)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    with on_stream(dev, stream) as s:
+        c = torch.empty((P, N), dtype=torch.float16, device=dev) if c is None else c
+        check("c", c, torch.float16, (P, N), dev)
+        st = _native.gemm_grouped_scale_bias_act(
+            P, N, K, E, a.data_ptr(), T, rows.data_ptr() if rows is not None else 0, b.data_ptr(),
+            bias.data_ptr() if bias is not None else 0, c.data_ptr(), offsets.data_ptr(), alpha,
+            ACTIVATIONS[activation], s, config_id)
+    _native.check(st)
+    return c
+
+
+def expert_mlp(x: torch.Tensor, ids: torch.Tensor, weights: Optional[torch.Tensor], up: torch.Tensor,
+               down: torch.Tensor, bias_up: Optional[torch.Tensor] = None, bias_down: Optional[torch.Tensor] = None,
+               activation: str = "gelu", stream=None) -> torch.Tensor:
+    """A layer of routed experts: out[t] = sum_j weights[t, j] *
+    (act(x[t] @ up[e] + bias_up[e]) @ down[e] + bias_down[e]) with
+    e = ids[t, j]; choices whose id names no expert are left out.  x (T, H),
+    ids (T, k) int32 or int64, weights (T, k) float32 or None (ones), up
+    (E, H, F), down (E, F, H).  The rows are sorted once; the products fetch
+    x's rows where they are.  Returns out (T, H) fp16."""
+    offsets, rows, positions = group_rows(ids, int(up.shape[0]), stream=stream)
+    hidden = gemm_grouped(x, up, offsets, rows=rows, bias=bias_up, activation=activation, stream=stream)
+    y = gemm_grouped(hidden, down, offsets, bias=bias_down, activation="none", stream=stream)
+    return combine_rows(y, positions, weights, stream=stream)
