@@ -305,6 +305,45 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
                                 const void* B, const void* bias, void* C, const int32_t* offsets,
                                 float alpha, int32_t activation, void* stream, int32_t config_id);
 
+/* Low-rank adapters of many requests beside one product: row m uses the
+ * weights B + scales[l] * La_l^T Lb_l^T of its own adapter l = ids[m],
+ *
+ *     C[m,n] = act( alpha * ( sum_k A[m,k] * B[k,n]
+ *                   + scales[l] * sum_r ( sum_k A[m,k] * La[l,r,k] ) * Lb[l,n,r] ) + bias[n] )
+ *
+ *   La  adapters x rank x K, Lb  adapters x N x rank, IEEE binary16 (the
+ *       layouts of a checkpoint's two factors; 16-byte aligned with K and
+ *       rank multiples of 8 they are read in 16-byte units, else value by
+ *       value); adapters of a smaller rank are padded with zeros
+ *   ids  M adapter indices in any order; an index outside [0, adapters) is a
+ *        row without an adapter
+ *   scales  adapters binary32 values, or NULL (ones)
+ * The inner sum is binary32 and enters the second product with 22 bits of its
+ * row's largest value; both sums, the scale, the bias and the activation are
+ * binary32, with one narrowing to binary16.  An adapter's values reach its
+ * own rows only, whatever they are.  rank is at most 256
+ * (GSR_ERROR_TOO_LARGE); one adapter's La and Lb are below 2^31 bytes each
+ * and the whole arrays may be larger.  adapters = 0 or rank = 0 is the product
+ * alone.  Two kernels are enqueued.
+ *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its
+ *              first 512 bytes zero before the first call and again after
+ *              each), of gsr_adapter_workspace_bytes(M, N, K, rank) bytes;
+ *              with less GSR_ERROR_INVALID_VALUE, or no K split if only that
+ *              does not fit
+ *   config_id  -1, or one of 21, 22, 28, 31, 32; splits as
+ *              gemm_scale_bias_act_ws's (at most 128 tiles split)
+ * Otherwise as gemm_scale_bias_act_ws. */
+int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K,
+                                 const void* A, const void* B, const void* bias, void* C,
+                                 int64_t adapters, int64_t rank, const void* la, const void* lb,
+                                 const int32_t* ids, const float* scales, float alpha, int32_t activation,
+                                 void* workspace, int64_t workspace_bytes,
+                                 void* stream, int32_t config_id, int32_t splits);
+
+/* The bytes gemm_adapters_scale_bias_act needs (0: none); -1 for sizes it
+ * rejects.  Host only. */
+int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank);
+
 /* Tuning table: exact problem shapes mapped to a launch, consulted before the
  * built-in selector (by every entry point called with config id -1, and by
  * gsr_select_config).  The file is text, one entry per line,

@@ -26,13 +26,14 @@ import torch
 from . import _native
 from ._native import (GsrError, clear_tuning, config_ids, get_config, load_tuning, num_configs, select_config,
                       status_string, tuning_entries, version, workspace_bytes)
+from .adapters import adapter_workspace_bytes, gemm_adapters
 from .routing import (combine_rows, combine_rows_backward, expert_mlp, gather_rows, gemm_grouped, group_rows,
                       group_workspace_bytes)
 
 __all__ = ["gemm_scale_relu", "gemm_scale_relu_ex", "gemm_scale_bias_act", "gemm_launch", "GsrError",
            "gemm_scale_relu_ws", "gemm_scale_bias_act_ws", "workspace_bytes", "new_workspace",
            "group_rows", "group_workspace_bytes", "gather_rows", "combine_rows", "combine_rows_backward",
-           "gemm_grouped", "expert_mlp",
+           "gemm_grouped", "expert_mlp", "gemm_adapters", "adapter_workspace_bytes",
            "select_config", "get_config", "num_configs", "config_ids", "status_string", "version", "configs",
            "ACTIVATIONS",
            "load_tuning", "clear_tuning", "tuning_entries"]

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libgsr.so")
-SOURCES = [os.path.join(CSRC, n) for n in ("gsr_api.hip", "gsr_rows_api.hip", "gsr_grouped_api.hip")]
+SOURCES = [os.path.join(CSRC, n) for n in ("gsr_api.hip", "gsr_rows_api.hip", "gsr_grouped_api.hip",
+                                            "gsr_adapters_api.hip")]
 # The digest of the sources a build used is written beside the library, so a
 # library older than its sources can be told apart from a current one.
 DIGEST_SUFFIX = ".sources"

@@ -1,0 +1,272 @@
+// gsr_adapters_api.hip -- host side of the product with low-rank adapters:
+// argument checks, the workspace's layout, the two launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "gsr.h"
+#include "gsr_adapters.hpp"
+#include "gsr_host.hpp"
+#include "gsr_interleave16c.hpp"
+#include "gsr_interleave16d.hpp"
+#include "gsr_kspec.hpp"
+
+namespace {
+
+using gsr::Problem;
+using gsr::ShrinkArgs;
+using namespace gsr::host;
+
+constexpr int64_t kLimit = (int64_t)1 << 31;
+constexpr int64_t kMaxRank = gsr::kShrinkMaxRank;
+constexpr int64_t kCounterBytes = kSplitCounters * 4;
+
+typedef hipError_t (*launch_fn)(const Problem&, int grid, hipStream_t);
+
+template <class T>
+hipError_t launch_ilv16d(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel(gsr::gemm_scale_relu_ilv16d_kernel<T, false, true>, dim3(grid), dim3(T::NT), s, p);
+}
+
+template <class T>
+hipError_t launch_ilv16c(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel(gsr::gemm_scale_relu_ilv16c_kernel<T, false, true>, dim3(grid), dim3(T::NT), s, p);
+}
+
+template <int BM, int BN, int S, int D, bool SPLIT>
+hipError_t launch_kspec(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel((gsr::gemm_scale_relu_kspec_kernel<BM, BN, S, D, SPLIT, false, true>), dim3(grid), dim3(512), s, p);
+}
+
+template <int BM, int BN>
+hipError_t launch_staged(const Problem& p, int grid, hipStream_t s)
+{
+    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, false, true>), dim3(grid), dim3(256), s, p);
+}
+
+// The tiles with an adapter form, under the ids of their dense forms.
+struct Entry {
+    int id;
+    int bm, bn;
+    launch_fn vec, split;
+    int elem_bm, elem_bn;
+    launch_fn elem;
+};
+const Entry kTable[] = {
+    {21, 64, 64, launch_kspec<64, 64, 4, 2, false>, launch_kspec<64, 64, 4, 2, true>, 64, 64, launch_staged<64, 64>},
+    {22, 32, 64, launch_kspec<32, 64, 4, 2, false>, launch_kspec<32, 64, 4, 2, true>, 64, 64, launch_staged<64, 64>},
+    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, nullptr, 128, 128, launch_staged<128, 128>},
+    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, nullptr, 128, 128, launch_staged<128, 128>},
+    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, nullptr, 128, 128, launch_staged<128, 128>},
+};
+
+const Entry* entry_of(int id)
+{
+    for (const Entry& e : kTable)
+        if (e.id == id) return &e;
+    return nullptr;
+}
+
+// A dense configuration's stand-in here: the four-wave K-split tiles run as
+// their copy-wave twins, 25 and 29 as 28 and 31.
+const Entry& stand_in(int id)
+{
+    switch (id) {
+    case 16: id = 21; break;
+    case 17: case 18: id = 22; break;
+    case 25: id = 28; break;
+    case 29: id = 31; break;
+    default: break;
+    }
+    return *entry_of(id);
+}
+
+int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// The shrink launch: 16 rows per workgroup, K in as many parts as bring the
+// grid to about kShrinkGrid workgroups, of 128 values at least.  Parts count
+// their arrivals in the counters at the workspace's start, one per 16 rows.
+struct ShrinkPlan {
+    int blocks, parts, kchunk, rank_pad;
+};
+
+ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t rank)
+{
+    constexpr int64_t kShrinkGrid = 512;
+    ShrinkPlan s;
+    s.rank_pad = (int)cdiv(rank, 32) * 32;
+    s.blocks = (int)cdiv(M, gsr::kShrinkRows);
+    int64_t parts = 1;
+    if (s.blocks <= kSplitCounters) parts = std::max<int64_t>(1, std::min<int64_t>({32, K / 128, kShrinkGrid / s.blocks}));
+    s.kchunk = (int)(cdiv(cdiv(K, parts), 32) * 32);
+    s.parts = (int)cdiv(K, s.kchunk);
+    return s;
+}
+
+// The workspace: counters, hi and lo halves of t, the rows' scales, then the
+// partial sums of the shrink launch, whose place the product's split takes
+// over when it has ended.
+struct Layout {
+    int64_t hi, lo, row_scale, partial;
+};
+
+Layout layout_of(int64_t M, const ShrinkPlan& s)
+{
+    Layout w;
+    w.hi = kCounterBytes;
+    w.lo = w.hi + round256(M * s.rank_pad * 2);
+    w.row_scale = w.lo + round256(M * s.rank_pad * 2);
+    w.partial = w.row_scale + round256(M * 4);
+    return w;
+}
+
+int64_t shrink_partial_bytes(const ShrinkPlan& s)
+{
+    return s.parts > 1 ? (int64_t)s.parts * s.blocks * gsr::kShrinkRows * s.rank_pad * 4 : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank)
+{
+    if (M < 0 || N < 0 || K < 0 || rank < 0 || M >= kLimit || N >= kLimit || K >= kLimit || rank > kMaxRank) return -1;
+    if (M == 0 || N == 0 || K == 0 || rank == 0) return 0;
+    const ShrinkPlan s = shrink_plan(M, K, rank);
+    const Entry& e = stand_in(dense_launch(M, N, K).id);
+    const int64_t split = e.split ? dense_split(M, N, K, cdiv(M, e.bm) * cdiv(N, e.bn), e.bm, e.bn, 0).partial_bytes : 0;
+    return layout_of(M, s).partial + std::max(shrink_partial_bytes(s), split);
+}
+
+int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const void* bias,
+                                 void* C, int64_t adapters, int64_t rank, const void* la, const void* lb,
+                                 const int32_t* ids, const float* scales, float alpha, int32_t activation,
+                                 void* workspace, int64_t workspace_bytes, void* stream, int32_t config_id,
+                                 int32_t splits)
+{
+    if (config_id < -1 || (config_id >= 0 && entry_of(config_id) == nullptr)) return GSR_ERROR_INVALID_CONFIG;
+    if (M < 0 || N < 0 || K < 0 || adapters < 0 || rank < 0 || splits < 0 || splits > kSplitMaxParts || workspace_bytes < 0)
+        return GSR_ERROR_INVALID_VALUE;
+    if (adapters == 0 || rank == 0 || M == 0 || N == 0 || K == 0)  // the product alone
+        return gemm_scale_bias_act_ex(M, N, K, A, B, bias, C, alpha, activation, stream, config_id);
+    if (M >= kLimit || N >= kLimit || K >= kLimit || adapters >= kLimit || rank > kMaxRank) return GSR_ERROR_TOO_LARGE;
+    // 32-bit byte offsets within a matrix and within one adapter
+    if (M * K * 2 >= kLimit || K * N * 2 >= kLimit || M * N * 2 >= kLimit || N * rank * 2 >= kLimit || K * rank * 2 >= kLimit)
+        return GSR_ERROR_TOO_LARGE;
+    if (!std::isfinite(alpha)) return GSR_ERROR_INVALID_VALUE;
+    if (activation != GSR_ACT_RELU && activation != GSR_ACT_GELU && activation != GSR_ACT_NONE)
+        return GSR_ERROR_INVALID_VALUE;
+    if (A == nullptr || B == nullptr || C == nullptr || la == nullptr || lb == nullptr || ids == nullptr ||
+        workspace == nullptr)
+        return GSR_ERROR_INVALID_VALUE;
+    if (misaligned(A, 2) || misaligned(B, 2) || misaligned(C, 2) || misaligned(bias, 2) || misaligned(la, 2) ||
+        misaligned(lb, 2) || misaligned(ids, 4) || misaligned(scales, 4) || misaligned(workspace, 16))
+        return GSR_ERROR_INVALID_VALUE;
+    const struct {
+        const void* p;
+        uint64_t bytes;
+    } in[] = {{A, (uint64_t)(M * K * 2)},
+              {B, (uint64_t)(K * N * 2)},
+              {bias, bias ? (uint64_t)(N * 2) : 0},
+              {la, (uint64_t)adapters * (uint64_t)(rank * K * 2)},
+              {lb, (uint64_t)adapters * (uint64_t)(rank * N * 2)},
+              {ids, (uint64_t)(M * 4)},
+              {scales, scales ? (uint64_t)(adapters * 4) : 0}};
+    const uint64_t cb = (uint64_t)(M * N * 2), wb = (uint64_t)workspace_bytes;
+    for (const auto& i : in)
+        if (overlaps(C, cb, i.p, i.bytes) || overlaps(workspace, wb, i.p, i.bytes)) return GSR_ERROR_INVALID_VALUE;
+    if (overlaps(C, cb, workspace, wb)) return GSR_ERROR_INVALID_VALUE;
+
+    Launch l = dense_launch(M, N, K);
+    const Entry& e = config_id >= 0 ? *entry_of(config_id) : stand_in(l.id);
+    if (e.id != l.id) l = Launch{e.id, 4, e.id == 28 ? 2 : 1};
+    Problem p{};
+    p.A = (const uint16_t*)A;
+    p.B = (const uint16_t*)B;
+    p.C = (uint16_t*)C;
+    p.bias = (const uint16_t*)bias;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.alpha = alpha;
+    p.act = (int)activation;
+    p.group_m = l.group_m;
+    p.xcd_remap = l.xcd_remap;
+    p.ksplit = 1;
+    p.kchunk = (int)K;
+    p.unit_a = load_unit(A, K);
+    p.unit_b = load_unit(B, N);
+    p.unit_c = load_unit(C, N);
+    const bool vec = p.unit_a == 16 && p.unit_b == 16 && (((uintptr_t)bias & 7u) == 0);
+    p.tiles_m = (int)cdiv(M, vec ? e.bm : e.elem_bm);
+    p.tiles_n = (int)cdiv(N, vec ? e.bn : e.elem_bn);
+    const int tiles = p.tiles_m * p.tiles_n;
+
+    const ShrinkPlan sp = shrink_plan(M, K, rank);
+    const Layout w = layout_of(M, sp);
+    if (workspace_bytes < w.partial + shrink_partial_bytes(sp)) return GSR_ERROR_INVALID_VALUE;
+    Split split{1, K, 0};
+    if (splits > 1 && e.split == nullptr) return GSR_ERROR_INVALID_CONFIG;
+    if (vec && e.split != nullptr) {
+        split = dense_split(M, N, K, tiles, e.bm, e.bn, splits);
+        if (split.parts > 1 && (tiles > kSplitCounters || workspace_bytes < w.partial + split.partial_bytes)) {
+            if (splits > 1) return GSR_ERROR_INVALID_VALUE;
+            split = Split{1, K, 0};
+        }
+    }
+    const int st = check_device();
+    if (st != GSR_SUCCESS) return st;
+
+    uint8_t* const ws = (uint8_t*)workspace;
+    ShrinkArgs a{};
+    a.A = p.A;
+    a.la = (const uint16_t*)la;
+    a.ids = ids;
+    a.scales = scales;
+    a.hi = (uint16_t*)(ws + w.hi);
+    a.lo = (uint16_t*)(ws + w.lo);
+    a.row_scale = (float*)(ws + w.row_scale);
+    a.partial = (float*)(ws + w.partial);
+    a.count = (uint32_t*)ws;
+    a.M = p.M;
+    a.K = p.K;
+    a.adapters = (int)adapters;
+    a.rank = (int)rank;
+    a.rank_pad = sp.rank_pad;
+    a.parts = sp.parts;
+    a.kchunk = sp.kchunk;
+    const bool shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
+    hipStream_t s = (hipStream_t)stream;
+    hipError_t err = launch_kernel(shrink_vec ? gsr::adapter_shrink_kernel<true> : gsr::adapter_shrink_kernel<false>,
+                                   dim3((unsigned)(sp.blocks * sp.parts)),
+                                   dim3(64 * gsr::kShrinkWaves), s, a);
+    if (err != hipSuccess) return GSR_ERROR_LAUNCH;
+
+    p.ids = ids;
+    p.row_scale = a.row_scale;
+    p.t_hi = a.hi;
+    p.t_lo = a.lo;
+    p.lb = (const uint16_t*)lb;
+    p.adapters = (int)adapters;
+    p.rank = (int)rank;
+    p.rank_pad = sp.rank_pad;
+    p.lb_vec = load_unit(lb, rank) == 16;
+    if (split.parts > 1) {
+        p.ksplit = split.parts;
+        p.kchunk = (int)split.kchunk;
+        p.ws_count = (uint32_t*)ws;
+        p.ws_part = (float*)(ws + w.partial);
+        err = e.split(p, tiles * split.parts, s);
+    } else {
+        err = (vec ? e.vec : e.elem)(p, tiles, s);
+    }
+    return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+}
+
+}  // extern "C"

@@ -283,7 +283,6 @@ int select(int64_t M, int64_t N, int64_t K)
 // Workspace layout: one 32-bit arrival counter per tile (a region rounded up
 // to 256 bytes), then parts x tiles partial tiles of bm x bn fp32, row-major.
 constexpr int kSplitStep = 128;    // K-step of the K-split kernels
-constexpr int kSplitMaxParts = 16;
 
 struct SplitPlan {
     int parts;       // 1: no split
@@ -336,9 +335,6 @@ int split_parts_for(int64_t M, int64_t N, int64_t K, int64_t tiles)
 // ---- tuning table: exact shapes -> launch choice ---------------------------
 // Written by an offline sweep (tiled_dense_gemm_scale_amd/tune.py) and loaded
 // with gsr_load_tuning; a shape found here overrides select().
-struct Launch {
-    int id, group_m, xcd_remap;
-};
 struct Tuned {
     int64_t M, N, K;
     Launch l;
@@ -366,6 +362,18 @@ Launch resolve(int64_t M, int64_t N, int64_t K, int config_id)
     const int id = select(M, N, K);
     return Launch{id, entry_of(id)->cfg.group_m, entry_of(id)->cfg.xcd_remap};
 }
+
+}  // namespace
+
+gsr::host::Launch gsr::host::dense_launch(int64_t M, int64_t N, int64_t K) { return resolve(M, N, K, -1); }
+
+gsr::host::Split gsr::host::dense_split(int64_t M, int64_t N, int64_t K, int64_t tiles, int bm, int bn, int want)
+{
+    const SplitPlan plan = split_plan(tiles, bm, bn, K, want > 0 ? want : split_parts_for(M, N, K, tiles));
+    return Split{plan.parts, plan.kchunk, plan.parts > 1 ? plan.bytes - split_count_bytes(tiles) : 0};
+}
+
+namespace {
 
 // The scratch array's address on the current device, looked up once per
 // device (with that device current) on its first use.

@@ -52,5 +52,21 @@ __attribute__((visibility("hidden"))) int check_device();
 // configuration `id` over K, in us.
 __attribute__((visibility("hidden"))) double launch_cost(int id, double wgs, int64_t K);
 
+// The dense product's launch for a shape (the tuning table, else the
+// selector), and the library's K split of it on bm x bn tiles: `parts` parts
+// of kchunk values of K (parts 1: none) whose fp32 partial tiles take
+// `partial_bytes`.  want 0: the library's choice; else at most that many.
+struct Launch {
+    int id, group_m, xcd_remap;
+};
+struct Split {
+    int parts;
+    int64_t kchunk, partial_bytes;
+};
+__attribute__((visibility("hidden"))) Launch dense_launch(int64_t M, int64_t N, int64_t K);
+__attribute__((visibility("hidden"))) Split dense_split(int64_t M, int64_t N, int64_t K, int64_t tiles, int bm, int bn, int want);
+constexpr int kSplitMaxParts = 16;
+constexpr int64_t kSplitCounters = 128;  // arrival counters at a workspace's start that every call leaves at zero
+
 }  // namespace host
 }  // namespace gsr

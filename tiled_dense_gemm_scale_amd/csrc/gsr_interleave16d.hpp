@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t fb16(uint32_t k)
     return ((k & 3u) + (((c ^ (c >> 1)) & 1u) << 2)) << 1;
 }
 
-template <class T, bool GROUPED = false>
+template <class T, bool GROUPED = false, bool ADAPT = false>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_scale_relu_ilv16d_kernel(Problem p)
 {
@@ -375,6 +375,7 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     // last of them the wait states a matrix result needs before other
     // instructions read it (64, well above the 16x16x32 requirement).
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+    if constexpr (ADAPT) adapter_add16<8>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
     ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
 }
 

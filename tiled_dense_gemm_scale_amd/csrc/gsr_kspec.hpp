@@ -40,7 +40,7 @@
 
 namespace gsr {
 
-template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED = false>
+template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED = false, bool ADAPT = false>
 __global__ void __launch_bounds__(512)
 gemm_scale_relu_kspec_kernel(Problem p)
 {
@@ -176,6 +176,8 @@ gemm_scale_relu_kspec_kernel(Problem p)
             for (int b = 0; b < TM; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+        if constexpr (ADAPT)
+            if (part == 0) adapter_start32(p, acc, m0, n0, wave, NW);
 
         half8 xs0[2][TN], ys0[2][TM], xs1[2][TN], ys1[2][TM];
 #pragma unroll
