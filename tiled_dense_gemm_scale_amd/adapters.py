@@ -8,7 +8,7 @@ import torch
 
 from . import _native
 from ._native import adapter_workspace_bytes
-from .routing import ACTIVATIONS, check, check_workspace, on_stream
+from .routing import ACTIVATIONS, enqueue, matrix, need, output, workspace_of
 
 __all__ = ["gemm_adapters", "adapter_workspace_bytes"]
 
@@ -24,27 +24,27 @@ def gemm_adapters(a: torch.Tensor, b: torch.Tensor, lora_a: torch.Tensor, lora_b
     (ones); R is at most 256.  workspace: new_workspace(
     adapter_workspace_bytes(M, N, K, R)), one per call that may run at the same
     time.  Returns c (M, N)."""
-    check("a", a, torch.float16, (None, None), None)
-    dev, M, K = a.device, int(a.shape[0]), int(a.shape[1])
-    check("b", b, torch.float16, (K, None), dev)
-    N = int(b.shape[1])
-    check("lora_a", lora_a, torch.float16, (None, None, K), dev)
-    L, R = int(lora_a.shape[0]), int(lora_a.shape[1])
-    check("lora_b", lora_b, torch.float16, (L, N, R), dev)
-    check("ids", ids, torch.int32, (M,), dev)
-    if scales is not None:
-        check("scales", scales, torch.float32, (L,), dev)
-    if bias is not None:
-        check("bias", bias, torch.float16, (N,), dev)
+    matrix("a", a, torch.float16, 2)
+    (M, K), dev = a.shape, a.get_device()
+    matrix("b", b, torch.float16, 2, dev)
+    matrix("lora_a", lora_a, torch.float16, 3, dev)
+    if b.shape[0] != K or lora_a.shape[2] != K:
+        raise ValueError(f"b and lora_a must have shapes ({K}, *) and (*, *, {K}), got {tuple(b.shape)} and {tuple(lora_a.shape)}")
+    N = b.shape[1]
+    L, R = lora_a.shape[0], lora_a.shape[1]
+    lb = need("lora_b", lora_b, torch.float16, (L, N, R), dev)
+    iptr = need("ids", ids, torch.int32, (M,), dev)
+    sptr = need("scales", scales, torch.float32, (L,), dev) if scales is not None else 0
+    bias_ptr = need("bias", bias, torch.float16, (N,), dev) if bias is not None else 0
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    wptr, wbytes = check_workspace(workspace, dev)
-    with on_stream(dev, stream) as s:
-        c = torch.empty((M, N), dtype=torch.float16, device=dev) if c is None else c
-        check("c", c, torch.float16, (M, N), dev)
-        st = _native.gemm_adapters_scale_bias_act(
-            M, N, K, a.data_ptr(), b.data_ptr(), bias.data_ptr() if bias is not None else 0, c.data_ptr(), L, R,
-            lora_a.data_ptr(), lora_b.data_ptr(), ids.data_ptr(), scales.data_ptr() if scales is not None else 0, alpha,
-            ACTIVATIONS[activation], wptr, wbytes, s, config_id, splits)
-    _native.check(st)
-    return c
+    wptr, wbytes = workspace_of(workspace, dev)
+
+    def go(s):
+        o = output("c", c, torch.float16, (M, N), a)
+        _native.check(_native.gemm_adapters_scale_bias_act(
+            M, N, K, a.data_ptr(), b.data_ptr(), bias_ptr, o.data_ptr(), L, R, lora_a.data_ptr(), lb, iptr, sptr, alpha,
+            ACTIVATIONS[activation], wptr, wbytes, s, config_id, splits))
+        return o
+
+    return enqueue(dev, stream, go)

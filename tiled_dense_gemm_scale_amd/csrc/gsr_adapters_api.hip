@@ -20,7 +20,7 @@ using gsr::ShrinkArgs;
 using namespace gsr::host;
 
 constexpr int64_t kLimit = (int64_t)1 << 31;
-constexpr int64_t kMaxRank = gsr::kShrinkMaxRank;
+constexpr int64_t kMaxRank = 256;
 constexpr int64_t kCounterBytes = kSplitCounters * 4;
 
 typedef hipError_t (*launch_fn)(const Problem&, int grid, hipStream_t);
@@ -88,46 +88,26 @@ const Entry& stand_in(int id)
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// The shrink launch: 16 rows per workgroup, K in as many parts as bring the
-// grid to about kShrinkGrid workgroups, of 128 values at least.  Parts count
-// their arrivals in the counters at the workspace's start, one per 16 rows.
-struct ShrinkPlan {
-    int blocks, parts, kchunk, rank_pad;
-};
+// The shrink launch.  Few rows: a workgroup per 16 rows, adapter and chunk of
+// ranks, so that one decode step's adapters spread over the chip.  Many rows:
+// one per 16 rows and four chunks, which takes all adapters of its rows.
+constexpr int64_t kShrinkFewRows = 128;
 
-ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t rank)
-{
-    constexpr int64_t kShrinkGrid = 512;
-    ShrinkPlan s;
-    s.rank_pad = (int)cdiv(rank, 32) * 32;
-    s.blocks = (int)cdiv(M, gsr::kShrinkRows);
-    int64_t parts = 1;
-    if (s.blocks <= kSplitCounters) parts = std::max<int64_t>(1, std::min<int64_t>({32, K / 128, kShrinkGrid / s.blocks}));
-    s.kchunk = (int)(cdiv(cdiv(K, parts), 32) * 32);
-    s.parts = (int)cdiv(K, s.kchunk);
-    return s;
-}
-
-// The workspace: counters, hi and lo halves of t, the rows' scales, then the
-// partial sums of the shrink launch, whose place the product's split takes
-// over when it has ended.
+// The workspace: counters, the records of t, their scales, then the partial
+// sums of the product's K split.
 struct Layout {
-    int64_t hi, lo, row_scale, partial;
+    int chunks;
+    int64_t t, t_scale, partial;
 };
 
-Layout layout_of(int64_t M, const ShrinkPlan& s)
+Layout layout_of(int64_t M, int64_t rank)
 {
     Layout w;
-    w.hi = kCounterBytes;
-    w.lo = w.hi + round256(M * s.rank_pad * 2);
-    w.row_scale = w.lo + round256(M * s.rank_pad * 2);
-    w.partial = w.row_scale + round256(M * 4);
+    w.chunks = (int)cdiv(rank, gsr::kAdapterChunk);
+    w.t = kCounterBytes;
+    w.t_scale = w.t + round256(M * w.chunks * 64);
+    w.partial = w.t_scale + round256(M * w.chunks * 4);
     return w;
-}
-
-int64_t shrink_partial_bytes(const ShrinkPlan& s)
-{
-    return s.parts > 1 ? (int64_t)s.parts * s.blocks * gsr::kShrinkRows * s.rank_pad * 4 : 0;
 }
 
 }  // namespace
@@ -138,10 +118,9 @@ int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ran
 {
     if (M < 0 || N < 0 || K < 0 || rank < 0 || M >= kLimit || N >= kLimit || K >= kLimit || rank > kMaxRank) return -1;
     if (M == 0 || N == 0 || K == 0 || rank == 0) return 0;
-    const ShrinkPlan s = shrink_plan(M, K, rank);
     const Entry& e = stand_in(dense_launch(M, N, K).id);
     const int64_t split = e.split ? dense_split(M, N, K, cdiv(M, e.bm) * cdiv(N, e.bn), e.bm, e.bn, 0).partial_bytes : 0;
-    return layout_of(M, s).partial + std::max(shrink_partial_bytes(s), split);
+    return layout_of(M, rank).partial + split;
 }
 
 int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const void* bias,
@@ -208,9 +187,8 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     p.tiles_n = (int)cdiv(N, vec ? e.bn : e.elem_bn);
     const int tiles = p.tiles_m * p.tiles_n;
 
-    const ShrinkPlan sp = shrink_plan(M, K, rank);
-    const Layout w = layout_of(M, sp);
-    if (workspace_bytes < w.partial + shrink_partial_bytes(sp)) return GSR_ERROR_INVALID_VALUE;
+    const Layout w = layout_of(M, rank);
+    if (workspace_bytes < w.partial) return GSR_ERROR_INVALID_VALUE;
     Split split{1, K, 0};
     if (splits > 1 && e.split == nullptr) return GSR_ERROR_INVALID_CONFIG;
     if (vec && e.split != nullptr) {
@@ -229,33 +207,30 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     a.la = (const uint16_t*)la;
     a.ids = ids;
     a.scales = scales;
-    a.hi = (uint16_t*)(ws + w.hi);
-    a.lo = (uint16_t*)(ws + w.lo);
-    a.row_scale = (float*)(ws + w.row_scale);
-    a.partial = (float*)(ws + w.partial);
-    a.count = (uint32_t*)ws;
+    a.t = (uint16_t*)(ws + w.t);
+    a.t_scale = (float*)(ws + w.t_scale);
     a.M = p.M;
     a.K = p.K;
     a.adapters = (int)adapters;
     a.rank = (int)rank;
-    a.rank_pad = sp.rank_pad;
-    a.parts = sp.parts;
-    a.kchunk = sp.kchunk;
-    const bool shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
+    a.chunks = w.chunks;
+    const bool few = M <= kShrinkFewRows, shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
+    const int nb = few || w.chunks == 1 ? 1 : 4;
+    a.slots = few ? (int)std::min<int64_t>({M, adapters, gsr::kShrinkRows}) : 1;
     hipStream_t s = (hipStream_t)stream;
-    hipError_t err = launch_kernel(shrink_vec ? gsr::adapter_shrink_kernel<true> : gsr::adapter_shrink_kernel<false>,
-                                   dim3((unsigned)(sp.blocks * sp.parts)),
+    hipError_t err = launch_kernel(nb == 1 ? (shrink_vec ? gsr::adapter_shrink_kernel<true, 1> : gsr::adapter_shrink_kernel<false, 1>)
+                                           : (shrink_vec ? gsr::adapter_shrink_kernel<true, 4> : gsr::adapter_shrink_kernel<false, 4>),
+                                   dim3((unsigned)cdiv(M, gsr::kShrinkRows), (unsigned)cdiv(w.chunks, nb), (unsigned)a.slots),
                                    dim3(64 * gsr::kShrinkWaves), s, a);
     if (err != hipSuccess) return GSR_ERROR_LAUNCH;
 
     p.ids = ids;
-    p.row_scale = a.row_scale;
-    p.t_hi = a.hi;
-    p.t_lo = a.lo;
+    p.t = a.t;
+    p.t_scale = a.t_scale;
     p.lb = (const uint16_t*)lb;
     p.adapters = (int)adapters;
     p.rank = (int)rank;
-    p.rank_pad = sp.rank_pad;
+    p.chunks = w.chunks;
     p.lb_vec = load_unit(lb, rank) == 16;
     if (split.parts > 1) {
         p.ksplit = split.parts;

@@ -375,7 +375,7 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     // last of them the wait states a matrix result needs before other
     // instructions read it (64, well above the 16x16x32 requirement).
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-    if constexpr (ADAPT) adapter_add16<8>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
+    if constexpr (ADAPT) adapter_add16<8, 2>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
     ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
 }
 

@@ -167,24 +167,22 @@ struct Problem {
     const int32_t* offsets;
     const int32_t* rows;
     int groups, a_rows;
-    // low-rank adapters (the ADAPT kernels): row m adds row_scale[m] *
-    // (t_hi[m] + t_lo[m]) @ Lb_l^T to its sum, l = ids[m] in [0, adapters),
-    // with t M x rank_pad and Lb adapters x N x rank; lb_vec: Lb is 16-byte
-    // aligned and rank a multiple of 8
+    // low-rank adapters (the ADAPT kernels, gsr_adapters.hpp): row m's inner
+    // sums as `chunks` records and scales, Lb adapters x N x rank, l = ids[m];
+    // lb_vec: Lb is 16-byte aligned and rank a multiple of 8
     const int32_t* ids;
-    const float* row_scale;
-    const uint16_t* t_hi;
-    const uint16_t* t_lo;
+    const uint16_t* t;
+    const float* t_scale;
     const uint16_t* lb;
-    int adapters, rank, rank_pad;
+    int adapters, rank, chunks;
     bool lb_vec;
 };
 
 // gsr_adapters.hpp
-template <int GN, int FN, int FM>
+template <int GN, int CB, int FN, int FM>
 __device__ void adapter_add16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0);
-template <int TN, int TM>
-__device__ void adapter_start32(const Problem& p, f32x16 (&acc)[TN][TM], int m0, int n0, int first, int stride);
+template <int TN, int TM, int BATCH>
+struct AdapterItems;
 
 // Eight outputs (16 bytes) at byte offset `off` of C, a multiple of 16 from
 // C's start, written in stores of the launch's unit for C (U = 16, 8, 4 or 2
@@ -602,7 +600,11 @@ gemm_scale_relu_kernel(Problem p)
         for (int b = 0; b < TM; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-    if constexpr (ADAPT) adapter_start32(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
+    if constexpr (ADAPT) {
+        AdapterItems<TN, TM, 2> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
+        items.load(p);
+        items.finish(p, acc);
+    }
 
     const int ksteps = (p.K + BK - 1) / BK;
 

@@ -36,6 +36,9 @@
 // meet the other parts' in the workspace (KsSum::split_sum_store).
 #pragma once
 
+#include <type_traits>
+
+#include "gsr_adapters.hpp"
 #include "gsr_ksplit.hpp"
 
 namespace gsr {
@@ -176,8 +179,14 @@ gemm_scale_relu_kspec_kernel(Problem p)
             for (int b = 0; b < TM; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+        // the adapters' first batch is in flight behind the product
+        using Items = AdapterItems<TN, TM, TM == 1 ? 4 : 2>;
+        [[maybe_unused]] std::conditional_t<ADAPT, Items, int> items = [&] {
+            if constexpr (ADAPT) return Items(p, m0, n0, wave, NW);
+            else return 0;
+        }();
         if constexpr (ADAPT)
-            if (part == 0) adapter_start32(p, acc, m0, n0, wave, NW);
+            if (part == 0) items.load(p);
 
         half8 xs0[2][TN], ys0[2][TM], xs1[2][TN], ys1[2][TM];
 #pragma unroll
@@ -229,6 +238,7 @@ gemm_scale_relu_kspec_kernel(Problem p)
         } else if (ksteps > 0) {
             mma_step(xs1, ys1);
         }
+        if constexpr (ADAPT) items.finish(p, acc);
 
         Sum::load_bias(p, tid, n0, bvs);
         wait_vmcnt<0>();

@@ -21,10 +21,10 @@ __all__ = ["group_rows", "group_workspace_bytes", "gather_rows", "combine_rows",
 
 
 @contextlib.contextmanager
-def on_stream(device: torch.device, stream):
-    """The launch environment: `device` current, and `stream` (None: the
-    current one, a torch stream, or a hipStream_t as an integer) as the stream
-    that allocations belong to.  Yields the stream's handle."""
+def _environment(device: torch.device, stream):
+    """`device` current, and `stream` (None: the current one, a torch stream,
+    or a hipStream_t as an integer) as the stream that allocations belong to.
+    Yields the stream's handle."""
     with torch.cuda.device(device):
         if stream is None:
             yield int(torch.cuda.current_stream(device).cuda_stream)
@@ -37,9 +37,26 @@ def on_stream(device: torch.device, stream):
                 yield int(s.cuda_stream)
 
 
-def check(name: str, t: torch.Tensor, dtypes, shape, device: Optional[torch.device]) -> torch.Tensor:
-    """`t` as a contiguous tensor of one of `dtypes`, of `shape` (None: any
-    length in that place) and on `device`; raises TypeError or ValueError."""
+# A launch takes 3 us of host time, less than the context managers and stream
+# objects around it would; so the usual call, on its device's current stream,
+# reads the stream's handle as torch's own generated code does.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def enqueue(index: int, stream, go):
+    """go(stream handle) with device `index` current and allocations made for
+    that stream; what it returns."""
+    if stream is None and _current_stream is not None and _current_device() == index:
+        return go(_current_stream(index))
+    with _environment(torch.device("cuda", index), stream) as s:
+        return go(s)
+
+
+def check(name: str, t: torch.Tensor, dtypes, shape, index: Optional[int]) -> None:
+    """Refuses (TypeError, ValueError) a `t` that is not a contiguous tensor
+    of one of `dtypes`, of `shape` (None: any length in that place), on device
+    `index` (None: any)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
@@ -50,16 +67,47 @@ def check(name: str, t: torch.Tensor, dtypes, shape, device: Optional[torch.devi
         raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def need(name: str, t: torch.Tensor, dtype, shape, index: int) -> int:
+    """`t`'s address once it is what check() lets pass; the usual case first."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    check(name, t, dtype, tuple(shape), index)
+    return t.data_ptr()
+
+
+def matrix(name: str, t, dtype, rank: int, index: Optional[int] = None) -> int:
+    """need() for a tensor of `rank` dimensions of any length (index None: on
+    any device)."""
+    try:
+        at = t.get_device()
+        if t.dtype is dtype and t.dim() == rank and at >= 0 and (index is None or at == index) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    check(name, t, dtype, (None,) * rank, index)
+    return t.data_ptr()
+
+
+def output(name: str, t: Optional[torch.Tensor], dtype, shape, like: torch.Tensor) -> torch.Tensor:
+    """`t` after need(), or a new tensor on `like`'s device."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    need(name, t, dtype, shape, like.get_device())
     return t
 
 
-def check_workspace(workspace: torch.Tensor, device: torch.device) -> Tuple[int, int]:
-    check("workspace", workspace, torch.uint8, (None,), device)
-    return workspace.data_ptr(), workspace.numel()
+def workspace_of(workspace: torch.Tensor, index: int) -> Tuple[int, int]:
+    """The workspace's address and bytes."""
+    return matrix("workspace", workspace, torch.uint8, 1, index), workspace.numel()
 
 
 def group_rows(ids: torch.Tensor, groups: int, offsets: Optional[torch.Tensor] = None,
@@ -75,49 +123,48 @@ def group_rows(ids: torch.Tensor, groups: int, offsets: Optional[torch.Tensor] =
     any content, allocated here when not given."""
     if not isinstance(ids, torch.Tensor) or ids.dim() not in (1, 2):
         raise ValueError("ids must be a tensor of shape (tokens, k) or (tokens,)")
-    check("ids", ids, (torch.int32, torch.int64), tuple(ids.shape), None)
-    groups = int(groups)
-    T, k = int(ids.shape[0]), int(ids.shape[1]) if ids.dim() == 2 else 1
-    dev, n = ids.device, T * k
-    with on_stream(dev, stream) as s:
-        need = group_workspace_bytes(n, groups)
-        if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        wptr, wbytes = check_workspace(workspace, dev)
-        new = dict(dtype=torch.int32, device=dev)
-        offsets = torch.empty(groups + 1, **new) if offsets is None else offsets
-        rows = torch.empty(n, **new) if rows is None else rows
-        positions = torch.empty(ids.shape, **new) if positions is None else positions
-        check("offsets", offsets, torch.int32, (groups + 1,), dev)
-        check("rows", rows, torch.int32, (n,), dev)
-        check("positions", positions, torch.int32, tuple(ids.shape), dev)
-        st = _native.group_rows(T, k, groups, ids.data_ptr(), ids.element_size(), offsets.data_ptr(), rows.data_ptr(),
-                                positions.data_ptr(), wptr, wbytes, s)
-    _native.check(st)
-    return offsets, rows, positions
+    if ids.dtype not in (torch.int32, torch.int64) or ids.get_device() < 0 or not ids.is_contiguous():
+        check("ids", ids, (torch.int32, torch.int64), ids.shape, None)
+    shape, dev, groups = ids.shape, ids.get_device(), int(groups)
+    T, k = shape[0], shape[1] if len(shape) == 2 else 1
+    n = T * k
+
+    def go(s):
+        ws, wbytes, out = workspace, 0, [offsets, rows, positions]
+        if ws is None:
+            wbytes = group_workspace_bytes(n, groups)
+            ws = ids.new_empty(wbytes, dtype=torch.uint8) if wbytes else None
+        wptr, wbytes = workspace_of(ws, dev) if ws is not None else (0, 0)
+        for i, (name, want) in enumerate((("offsets", (max(groups, 0) + 1,)), ("rows", (n,)), ("positions", shape))):
+            out[i] = output(name, out[i], torch.int32, want, ids)
+        _native.check(_native.group_rows(T, k, groups, ids.data_ptr(), ids.element_size(), out[0].data_ptr(),
+                                         out[1].data_ptr(), out[2].data_ptr(), wptr, wbytes, s))
+        return tuple(out)
+
+    return enqueue(dev, stream, go)
 
 
 def gather_rows(x: torch.Tensor, rows: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[p] = x[rows[p]] for x (T, H) fp16 and rows (P,) int32; zeros where
     rows[p] is outside [0, T).  Its gradient is combine_rows(dout, positions)
     without weights.  Returns out (P, H)."""
-    check("x", x, torch.float16, (None, None), None)
-    T, H = int(x.shape[0]), int(x.shape[1])
-    check("rows", rows, torch.int32, (None,), x.device)
-    P = int(rows.shape[0])
-    with on_stream(x.device, stream) as s:
-        out = torch.empty((P, H), dtype=torch.float16, device=x.device) if out is None else out
-        check("out", out, torch.float16, (P, H), x.device)
-        st = _native.gather_rows(P, T, H, x.data_ptr(), rows.data_ptr(), out.data_ptr(), s)
-    _native.check(st)
-    return out
+    matrix("x", x, torch.float16, 2)
+    matrix("rows", rows, torch.int32, 1, x.get_device())
+    (T, H), P = x.shape, rows.shape[0]
+
+    def go(s):
+        y = output("out", out, torch.float16, (P, H), x)
+        _native.check(_native.gather_rows(P, T, H, x.data_ptr(), rows.data_ptr(), y.data_ptr(), s))
+        return y
+
+    return enqueue(x.get_device(), stream, go)
 
 
-def _positions(positions: torch.Tensor, device: torch.device) -> Tuple[int, int]:
+def _positions(positions: torch.Tensor, index: int) -> Tuple[int, int]:
     if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
         raise ValueError("positions must be a tensor of shape (tokens, k) or (tokens,)")
-    check("positions", positions, torch.int32, tuple(positions.shape), device)
-    return int(positions.shape[0]), int(positions.shape[1]) if positions.dim() == 2 else 1
+    need("positions", positions, torch.int32, positions.shape, index)
+    return positions.shape[0], positions.shape[1] if positions.dim() == 2 else 1
 
 
 def combine_rows(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -126,18 +173,17 @@ def combine_rows(y: torch.Tensor, positions: torch.Tensor, weights: Optional[tor
     positions (T, k) or (T,) int32 and weights like positions, float32 (None:
     ones); fp32 sums in order of j, rounded once to fp16.  Positions outside
     [0, P) have no term.  Returns out (T, H)."""
-    check("y", y, torch.float16, (None, None), None)
-    P, H = int(y.shape[0]), int(y.shape[1])
-    T, k = _positions(positions, y.device)
-    if weights is not None:
-        check("weights", weights, torch.float32, tuple(positions.shape), y.device)
-    with on_stream(y.device, stream) as s:
-        out = torch.empty((T, H), dtype=torch.float16, device=y.device) if out is None else out
-        check("out", out, torch.float16, (T, H), y.device)
-        st = _native.combine_rows(T, k, P, H, y.data_ptr(), positions.data_ptr(),
-                                  weights.data_ptr() if weights is not None else 0, out.data_ptr(), s)
-    _native.check(st)
-    return out
+    matrix("y", y, torch.float16, 2)
+    (P, H), dev = y.shape, y.get_device()
+    T, k = _positions(positions, dev)
+    wptr = need("weights", weights, torch.float32, positions.shape, dev) if weights is not None else 0
+
+    def go(s):
+        o = output("out", out, torch.float16, (T, H), y)
+        _native.check(_native.combine_rows(T, k, P, H, y.data_ptr(), positions.data_ptr(), wptr, o.data_ptr(), s))
+        return o
+
+    return enqueue(dev, stream, go)
 
 
 def combine_rows_backward(dout: torch.Tensor, y: Optional[torch.Tensor], positions: torch.Tensor,
@@ -150,33 +196,31 @@ def combine_rows_backward(dout: torch.Tensor, y: Optional[torch.Tensor], positio
     float32) with <dout[t], y[positions[t, j]]>, 0 for a dropped choice.
     rows (P,) and positions are group_rows's; positions inside [0, P) must be
     distinct.  Without weights, y may be None and dweights is None."""
-    check("dout", dout, torch.float16, (None, None), None)
-    T, H, dev = int(dout.shape[0]), int(dout.shape[1]), dout.device
+    matrix("dout", dout, torch.float16, 2)
+    (T, H), dev = dout.shape, dout.get_device()
     tokens, k = _positions(positions, dev)
     if tokens != T:
         raise ValueError(f"positions must have {T} tokens as dout does, got {tokens}")
-    check("rows", rows, torch.int32, (None,), dev)
-    P = int(rows.shape[0])
+    matrix("rows", rows, torch.int32, 1, dev)
+    P, wptr, yptr = rows.shape[0], 0, 0
     if weights is not None:
-        check("weights", weights, torch.float32, tuple(positions.shape), dev)
+        wptr = need("weights", weights, torch.float32, positions.shape, dev)
         if y is None:
             raise ValueError("y is needed for the weights' gradient")
     elif dweights is not None:
         raise ValueError("dweights without weights")
     if y is not None:
-        check("y", y, torch.float16, (P, H), dev)
-    with on_stream(dev, stream) as s:
-        dy = torch.empty((P, H), dtype=torch.float16, device=dev) if dy is None else dy
-        check("dy", dy, torch.float16, (P, H), dev)
-        if weights is not None:
-            dweights = torch.empty(positions.shape, dtype=torch.float32, device=dev) if dweights is None else dweights
-            check("dweights", dweights, torch.float32, tuple(positions.shape), dev)
-        st = _native.combine_rows_backward(
-            T, k, P, H, dout.data_ptr(), y.data_ptr() if y is not None else 0, positions.data_ptr(),
-            weights.data_ptr() if weights is not None else 0, rows.data_ptr(), dy.data_ptr(),
-            dweights.data_ptr() if weights is not None else 0, s)
-    _native.check(st)
-    return dy, dweights
+        yptr = need("y", y, torch.float16, (P, H), dev)
+
+    def go(s):
+        gy = output("dy", dy, torch.float16, (P, H), dout)
+        gw = output("dweights", dweights, torch.float32, positions.shape, dout) if weights is not None else None
+        _native.check(_native.combine_rows_backward(T, k, P, H, dout.data_ptr(), yptr, positions.data_ptr(), wptr,
+                                                    rows.data_ptr(), gy.data_ptr(),
+                                                    gw.data_ptr() if gw is not None else 0, s))
+        return gy, gw
+
+    return enqueue(dev, stream, go)
 
 
 ACTIVATIONS = {"relu": _native.GSR_ACT_RELU, "gelu": _native.GSR_ACT_GELU, "none": _native.GSR_ACT_NONE}
@@ -192,27 +236,29 @@ def gemm_grouped(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, rows: 
     device (group_rows's), act "relu", "gelu" (tanh form) or "none".  Rows of
     c outside every group stay as they were; a c allocated here holds
     anything there.  Returns c (P, N)."""
-    check("a", a, torch.float16, (None, None), None)
-    dev, T, K = a.device, int(a.shape[0]), int(a.shape[1])
-    check("b", b, torch.float16, (None, K, None), dev)
-    E, N = int(b.shape[0]), int(b.shape[2])
-    check("offsets", offsets, torch.int32, (E + 1,), dev)
+    matrix("a", a, torch.float16, 2)
+    (T, K), dev = a.shape, a.get_device()
+    matrix("b", b, torch.float16, 3, dev)
+    if b.shape[1] != K:
+        raise ValueError(f"b must have shape (*, {K}, *), got {tuple(b.shape)}")
+    E, N = b.shape[0], b.shape[2]
+    optr = need("offsets", offsets, torch.int32, (E + 1,), dev)
+    P, rptr = T, 0
     if rows is not None:
-        check("rows", rows, torch.int32, (None,), dev)
-    P = T if rows is None else int(rows.shape[0])
-    if bias is not None:
-        check("bias", bias, torch.float16, (E, N), dev)
+        matrix("rows", rows, torch.int32, 1, dev)
+        P, rptr = rows.shape[0], rows.data_ptr()
+    bias_ptr = need("bias", bias, torch.float16, (E, N), dev) if bias is not None else 0
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    with on_stream(dev, stream) as s:
-        c = torch.empty((P, N), dtype=torch.float16, device=dev) if c is None else c
-        check("c", c, torch.float16, (P, N), dev)
-        st = _native.gemm_grouped_scale_bias_act(
-            P, N, K, E, a.data_ptr(), T, rows.data_ptr() if rows is not None else 0, b.data_ptr(),
-            bias.data_ptr() if bias is not None else 0, c.data_ptr(), offsets.data_ptr(), alpha,
-            ACTIVATIONS[activation], s, config_id)
-    _native.check(st)
-    return c
+
+    def go(s):
+        o = output("c", c, torch.float16, (P, N), a)
+        _native.check(_native.gemm_grouped_scale_bias_act(P, N, K, E, a.data_ptr(), T, rptr, b.data_ptr(), bias_ptr,
+                                                          o.data_ptr(), optr, alpha, ACTIVATIONS[activation], s,
+                                                          config_id))
+        return o
+
+    return enqueue(dev, stream, go)
 
 
 def expert_mlp(x: torch.Tensor, ids: torch.Tensor, weights: Optional[torch.Tensor], up: torch.Tensor,
