@@ -236,35 +236,20 @@ const Candidate kCandidates[] = {
 };
 constexpr double kPartMin = 0.80, kPartA = 0.35;  // a part-filled last wave: max(kPartMin, kPartA + (1 - kPartA) * fill)
 
-}  // namespace
-
-// The estimated time, in us, of `wgs` workgroups of configuration `id` over
-// K; 0 for a configuration that is no candidate.
-double gsr::host::launch_cost(int id, double wgs, int64_t K)
-{
-    const double cus = 256.0;
-    for (const Candidate& c : kCandidates) {
-        if (c.id != id) continue;
-        const gsr_config& g = entry_of(c.id)->cfg;
-        const double full = std::floor(wgs / cus), fill = (wgs - full * cus) / cus;
-        const double waves = full + (fill > 0.0 ? std::max(kPartMin, kPartA + (1.0 - kPartA) * fill) : 0.0);
-        const double tile = 2.0 * g.block_m * g.block_n * (double)(K > 0 ? K : 1) / (c.tflops_per_cu * 1e6) + c.tile_us;
-        return waves * tile;
-    }
-    return 0.0;
-}
-
-namespace {
-
 int select(int64_t M, int64_t N, int64_t K)
 {
+    const double cus = 256.0;
     int best = 28;
     double best_t = 1e300;
     for (const Candidate& c : kCandidates) {
         const bool copy_wave = c.id == 21 || c.id == 22, four_wave = c.id == 16 || c.id == 18;
         if ((copy_wave && K <= 256) || (four_wave && K > 256)) continue;
         const gsr_config& g = entry_of(c.id)->cfg;
-        const double t = launch_cost(c.id, (double)cdiv(M, g.block_m) * (double)cdiv(N, g.block_n), K);
+        const double wgs = (double)cdiv(M, g.block_m) * (double)cdiv(N, g.block_n);
+        const double full = std::floor(wgs / cus), fill = (wgs - full * cus) / cus;
+        const double waves = full + (fill > 0.0 ? std::max(kPartMin, kPartA + (1.0 - kPartA) * fill) : 0.0);
+        const double tile = 2.0 * g.block_m * g.block_n * (double)(K > 0 ? K : 1) / (c.tflops_per_cu * 1e6) + c.tile_us;
+        const double t = waves * tile;
         if (t < best_t) {
             best_t = t;
             best = c.id;
@@ -272,6 +257,20 @@ int select(int64_t M, int64_t N, int64_t K)
     }
     return best;
 }
+
+}  // namespace
+
+double gsr::host::tile_time(int id, int64_t K)
+{
+    for (const Candidate& c : kCandidates)
+        if (c.id == id) {
+            const gsr_config& g = entry_of(id)->cfg;
+            return 2.0 * g.block_m * g.block_n * (double)K / (c.tflops_per_cu * 1e6) + c.tile_us;
+        }
+    return 0.0;
+}
+
+namespace {
 
 // ---- K split across workgroups ---------------------------------------------
 // The copy-wave K-split tiles (configurations 21 and 22) cover few outputs, so

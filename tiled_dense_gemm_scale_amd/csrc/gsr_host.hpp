@@ -48,9 +48,9 @@ inline bool misaligned(const void* p, uintptr_t unit) { return ((uintptr_t)p & (
 // GSR_SUCCESS when the current device is a gfx950 (gsr_api.hip).
 __attribute__((visibility("hidden"))) int check_device();
 
-// The selector's estimate of a launch (gsr_api.hip): `wgs` workgroups of tile
-// configuration `id` over K, in us.
-__attribute__((visibility("hidden"))) double launch_cost(int id, double wgs, int64_t K);
+// The selector's time of one tile of configuration `id` over K, in us
+// (gsr_api.hip; 0 for an id that is no candidate of it).
+__attribute__((visibility("hidden"))) double tile_time(int id, int64_t K);
 
 // The dense product's launch for a shape (the tuning table, else the
 // selector), and the library's K split of it on bm x bn tiles: `parts` parts
