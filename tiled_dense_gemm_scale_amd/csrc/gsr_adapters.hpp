@@ -11,14 +11,14 @@
 // (rank x K and N x rank: the reduced index is contiguous, so a lane's operand
 // is one 16-byte load and needs no LDS).
 //
-// t is an fp16 operand in step 2 without losing its fp32 value.  Its ranks go
-// in chunks of 16; a row's chunk is scaled by the power of two that brings its
-// largest |t| into [1, 2), and each value is split into its fp16 rounding and
-// the fp16 rounding of the rest, which leaves at most 2^-23 of that largest
-// value (hi has 11 bits, lo the 11 bits below, down to fp16's smallest step of
-// 2^-24).  The product runs over both halves and the power of two multiplies
-// its fp32 result, so no magnitude of t overflows or underflows.  A chunk's
-// record is its 16 hi values and then its 16 lo values: 64 bytes, the K = 32
+// t is an fp16 operand in step 2 without losing its fp32 value.  A row is
+// scaled by the power of two that brings its largest |t| into [1, 2), and each
+// value is split into its fp16 rounding and the fp16 rounding of the rest,
+// which leaves at most 2^-23 of that largest value (hi has 11 bits, lo the 11
+// bits below, down to fp16's smallest step of 2^-24).  The product runs over
+// both halves and the power of two multiplies its fp32 result, so no
+// magnitude of t overflows or underflows.  Ranks go in chunks of 16: a chunk's
+// record is its 16 hi values and then its 16 lo values, 64 bytes, the K = 32
 // operand of one 16x16x32 MFMA against the chunk of Lb taken twice.
 //
 // Rows of one tile may belong to different adapters.  The loops run once per
@@ -65,13 +65,17 @@ struct ShrinkArgs {
     const int32_t* ids;     // M
     const float* scales;    // adapters, or null (ones)
     uint16_t* t;            // M x chunks records
-    float* t_scale;         // M x chunks
+    float* t_scale;         // M
+    float* partial;         // parts > 1: parts x (16 blocks) x (16 chunks)
+    uint32_t* count;        // parts > 1: blocks
     int M, K, adapters, rank, chunks;
-    int slots;              // workgroups that share a row block's adapters
+    int blocks;             // of 16 rows
+    int parts, kchunk;      // K in parts of kchunk values (a multiple of 32)
+    int slots;              // workgroups that share a block's adapters
 };
 
-constexpr int kShrinkWaves = 16;
 constexpr int kShrinkRows = 16;  // rows per workgroup
+constexpr int kShrinkMaxRank = 256;
 
 // f(l) for each distinct adapter among 16 rows, as the lanes hold their ids,
 // in order of the lowest row.
@@ -86,51 +90,37 @@ __device__ __forceinline__ void for_each_adapter(int id, F&& f)
     }
 }
 
-// A workgroup takes 16 rows, NB chunks of ranks and every slots-th distinct
-// adapter of the rows; its 16 waves cut K into runs of 32-value steps, walked
-// STEPS at a time so that their loads are in flight together, and the waves'
-// sums meet in LDS and are added in wave order.  A row's chunk is finished by
-// one workgroup, so nothing is shared between workgroups and no order depends
-// on timing.  Bound by the bytes of A and La (a decode step reads each
-// adapter once; prompts read A once and La from the caches), which is why few
-// rows get a workgroup per adapter and chunk, and many rows one per row block
-// that reads A once for four chunks.
-template <bool VEC, int NB>
-__global__ void __launch_bounds__(64 * kShrinkWaves) adapter_shrink_kernel(ShrinkArgs s)
+// The sums of 16 rows over this workgroup's part of K for NB chunks of ranks
+// from chunk c0: the W waves cut the part into runs of 32-value steps, walk
+// every adapter's run STEPS steps at a time, so that their loads are in flight
+// together, and leave what they have in sums[wave][row][rank].
+template <bool VEC, int NB, int W, int STEPS>
+__device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, float (&sums)[W][kShrinkRows][kAdapterChunk * NB + 4],
+                                            int id, int m0, int c0, int kbeg, int kend, int slot)
 {
-    constexpr int STEPS = NB == 1 ? 8 : 4;
-    __shared__ float sums[kShrinkWaves][kShrinkRows][kAdapterChunk * NB + 4];
-    __shared__ int done[kShrinkRows];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int lrow = lane & 15, lq = lane >> 4;
-    const int m0 = blockIdx.x * kShrinkRows, c0 = blockIdx.y * NB, r0 = c0 * kAdapterChunk;
-
-    const int id = adapter_of(s.ids, m0 + lrow, s.M, s.adapters);
-    const int steps = (s.K + 31) / 32;
-    const int ks0 = steps * wave / kShrinkWaves, ks1 = steps * (wave + 1) / kShrinkWaves;
+    const int lane = threadIdx.x & 63, lrow = lane & 15, lq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int steps = (kend - kbeg + 31) / 32;
+    const int ks0 = steps * wave / W, ks1 = steps * (wave + 1) / W;
     const __amdgpu_buffer_rsrc_t ra = make_rsrc(s.A, (uint32_t)s.M * (uint32_t)s.K * 2u);
     const uint32_t arow = (uint32_t)(m0 + lrow) * (uint32_t)s.K;
     const bool ain = m0 + lrow < s.M;
-
     f32x4 out[NB] = {};
-    bool mine = false;
     int at = 0;
     for_each_adapter(id, [&](int l) {
-        if (at++ % s.slots != (int)blockIdx.z) return;
-        mine |= id == l;
+        if (at++ % s.slots != slot) return;
         const __amdgpu_buffer_rsrc_t rl = make_rsrc(s.la + (int64_t)l * s.rank * s.K, (uint32_t)s.rank * (uint32_t)s.K * 2u);
         f32x4 d[NB] = {};
         for (int ks = ks0; ks < ks1; ks += STEPS) {
             half8 x[STEPS], w[STEPS][NB];
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-                const int k = 32 * (ks + i) + 8 * lq;
-                const int len = ks + i < ks1 ? s.K : 0;
+                const int k = kbeg + 32 * (ks + i) + 8 * lq;
+                const int len = ks + i < ks1 ? kend : 0;
                 x[i] = piece8<VEC>(ra, arow, k, len, ain);
 #pragma unroll
                 for (int q = 0; q < NB; ++q) {
-                    const int r = r0 + 16 * q + lrow;
+                    const int r = kAdapterChunk * (c0 + q) + lrow;
                     w[i][q] = piece8<VEC>(rl, (uint32_t)r * (uint32_t)s.K, k, len, r < s.rank);
                 }
             }
@@ -144,38 +134,155 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) adapter_shrink_kernel(Shrin
 #pragma unroll
             for (int i = 0; i < 4; ++i) out[q][i] = id == l ? out[q][i] + d[q][i] : out[q][i];
     });
-    if (__ballot(mine) == 0) return;  // the same in every wave
 #pragma unroll
     for (int q = 0; q < NB; ++q) *(f32x4*)&sums[wave][lrow][16 * q + 4 * lq] = out[q];
-    if (wave == 0 && lq == 0) done[lrow] = mine ? id : -1;
-    __syncthreads();
+}
 
-    // thread t: row t / 16 % 16 and rank t % 16 of chunk t / 256
-    const int row = (tid >> 4) & 15, c = tid & 15, q = tid >> 8;
-    if (q >= NB || c0 + q >= s.chunks) return;  // whole waves
-    const int l = done[row];
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kShrinkWaves; ++w) t += sums[w][row][16 * q + c];
-    t *= (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
-    bool odd = !(fabsf(t) <= 3.0e38f);
-    float big = fabsf(t);
-#pragma unroll
-    for (int x = 8; x > 0; x >>= 1) {
-        big = fmaxf(big, __shfl_xor(big, x));
-        odd |= (bool)__shfl_xor((int)odd, x);
-    }
+// Writes row m's records: this thread holds ranks c + 16 j of the row for j in
+// v[], the 16 lanes around it the rest.
+template <int N>
+__device__ __forceinline__ void shrink_store(const ShrinkArgs& s, int m, int l, int c, int j0, int stride, float (&v)[N], float big, bool odd)
+{
     if (l < 0) return;
     // 2^e <= big < 2^(e + 1); zeros, and rows with an infinity or a NaN, keep 2^0
     int e = 0;
-    if (!odd && big > 0.0f) e = max(__builtin_amdgcn_frexp_expf(big) - 1, -100);
-    const int64_t rec = (int64_t)(m0 + row) * s.chunks + c0 + q;
-    const float v = t * ldexpf(1.0f, -e);
-    const _Float16 hi = (_Float16)v;
-    const _Float16 lo = odd ? (_Float16)0.0f : (_Float16)(v - (float)hi);
-    s.t[rec * 32 + c] = __builtin_bit_cast(uint16_t, hi);
-    s.t[rec * 32 + 16 + c] = __builtin_bit_cast(uint16_t, lo);
-    if (c == 0) s.t_scale[rec] = ldexpf(1.0f, e);
+    if (!odd && big > 0.0f) e = min(max(__builtin_amdgcn_frexp_expf(big) - 1, -40), 100);
+    const float down = ldexpf(1.0f, -e);
+    if (c == 0 && j0 == 0) s.t_scale[m] = ldexpf(1.0f, e);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int j = j0 + i * stride;
+        if (j >= s.chunks) break;
+        const float x = v[i] * down;
+        const _Float16 hi = (_Float16)x;
+        const _Float16 lo = odd ? (_Float16)0.0f : (_Float16)(x - (float)hi);
+        uint16_t* rec = s.t + ((int64_t)m * s.chunks + j) * 32;
+        rec[c] = __builtin_bit_cast(uint16_t, hi);
+        rec[16 + c] = __builtin_bit_cast(uint16_t, lo);
+    }
+}
+
+// Many rows: a workgroup takes 16 rows, every slots-th of their adapters and
+// all ranks, NB chunks at a time, with 16 waves on K.  A is read once (from the
+// caches for further chunks) and an adapter's La once per 16 rows from the
+// caches.
+template <bool VEC, int NB>
+__global__ void __launch_bounds__(1024) adapter_shrink_rows_kernel(ShrinkArgs s)
+{
+    constexpr int W = 16, ROUNDS = kShrinkMaxRank / kAdapterChunk / 4;
+    __shared__ float sums[W][kShrinkRows][kAdapterChunk * NB + 4];
+    __shared__ float bigs[kShrinkRows][4];
+    const int tid = threadIdx.x, m0 = blockIdx.x * kShrinkRows;
+    const int id = adapter_of(s.ids, m0 + (tid & 15), s.M, s.adapters);
+
+    // thread t: row t / 16 % 16 and rank t % 16 of chunks t / 256, + NB, ...
+    const int row = (tid >> 4) & 15, c = tid & 15, q = tid >> 8;
+    int l = adapter_of(s.ids, m0 + row, s.M, s.adapters), at = 0;
+    bool mine = false;
+    for_each_adapter(id, [&](int a) { mine |= at++ % s.slots == (int)blockIdx.z && l == a; });
+    if (at <= (int)blockIdx.z) return;  // no adapter for this workgroup
+    l = mine ? l : -1;
+    const float scale = (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
+    float v[NB == 1 ? 1 : ROUNDS], big = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < (NB == 1 ? 1 : ROUNDS); ++i) {
+        v[i] = 0.0f;
+        if (i * NB >= s.chunks) continue;
+        if (i > 0) __syncthreads();  // the sums of the chunks before have been read
+        shrink_sums<VEC, NB, W, NB == 1 ? 8 : 4>(s, sums, id, m0, i * NB, 0, s.K, blockIdx.z);
+        __syncthreads();
+        if (q < NB && i * NB + q < s.chunks) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) v[i] += sums[w][row][16 * q + c];
+            v[i] *= scale;
+            odd |= !(fabsf(v[i]) <= 3.0e38f);
+            big = fmaxf(big, fabsf(v[i]));
+        }
+    }
+    big = odd ? __builtin_inff() : big;
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor(big, x));
+    if (NB > 1) {
+        if (c == 0) bigs[row][q] = big;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) big = fmaxf(big, bigs[row][x]);
+    }
+    if (q < NB) shrink_store(s, m0 + row, l, c, q, NB, v, big, !(big <= 3.0e38f));
+}
+
+// Few rows (a decode step): the adapters' La is most of the bytes, so a block
+// of 16 rows spreads over workgroups of four waves, one per part of K, chunk
+// and every slots-th adapter, which meet in the workspace: the workgroup of a
+// block that arrives last adds the parts in part order and writes the records
+// (device-scope accesses and the arrival counter as in KsSum::split_sum_store,
+// so no order depends on timing and no workgroup waits).
+template <bool VEC>
+__global__ void __launch_bounds__(256) adapter_shrink_parts_kernel(ShrinkArgs s)
+{
+    constexpr int W = 4, ROUNDS = kShrinkMaxRank / kAdapterChunk;
+    __shared__ float sums[W][kShrinkRows][kAdapterChunk + 4];
+    __shared__ int last;
+    const int tid = threadIdx.x;
+    const int block = blockIdx.x / s.parts, part = blockIdx.x - block * s.parts;
+    const int m0 = block * kShrinkRows;
+    const int id = adapter_of(s.ids, m0 + (tid & 15), s.M, s.adapters);
+    if (__ballot(id >= 0) == 0) return;  // in every workgroup of the block
+    const int row = tid >> 4, c = tid & 15;  // thread t: row t / 16, rank t % 16 of a chunk
+    const int l = adapter_of(s.ids, m0 + row, s.M, s.adapters);
+    // the adapter's place among the block's decides whose it is
+    bool mine = false;
+    int at = 0;
+    for_each_adapter(id, [&](int a) {
+        const bool ours = at++ % s.slots == (int)blockIdx.z;
+        mine |= ours && l == a;
+    });
+    const float scale = (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
+
+    const int kbeg = part * s.kchunk, kend = min(s.K, kbeg + s.kchunk);
+    shrink_sums<VEC, 1, W, 8>(s, sums, id, m0, blockIdx.y, kbeg, kend, blockIdx.z);
+    __syncthreads();
+    const int64_t stride = (int64_t)s.blocks * kShrinkRows * s.chunks * kAdapterChunk;  // one part
+    float* const at0 = s.partial + (int64_t)(m0 + row) * s.chunks * kAdapterChunk + c;
+    if (mine) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) v += sums[w][row][c];
+        __hip_atomic_store(at0 + part * stride + blockIdx.y * kAdapterChunk, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums have reached device scope
+    __syncthreads();
+    if (tid == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(s.count + block, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        last = before == (uint32_t)(s.parts * gridDim.y * gridDim.z) - 1u;
+    }
+    __syncthreads();
+    if (!last) return;
+    if (tid == 0) __hip_atomic_store(s.count + block, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+
+    float v[ROUNDS], big = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) {
+        v[j] = 0.0f;
+        if (j >= s.chunks) continue;
+        for (int g = 0; g < s.parts; g += 8) {
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // parts past the last read its sums again and add nothing
+                u[i] = __hip_atomic_load(at0 + min(g + i, s.parts - 1) * stride + j * kAdapterChunk, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j] += g + i < s.parts ? u[i] : 0.0f;
+        }
+        v[j] *= scale;
+        odd |= !(fabsf(v[j]) <= 3.0e38f);
+        big = fmaxf(big, fabsf(v[j]));
+    }
+    big = odd ? __builtin_inff() : big;
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor(big, x));
+    shrink_store(s, m0 + row, l, c, 0, 1, v, big, !(big <= 3.0e38f));
 }
 
 // ---- step 2 ---------------------------------------------------------------------
@@ -191,89 +298,162 @@ __device__ __forceinline__ half8 lb_piece(const Problem& p, __amdgpu_buffer_rsrc
     return p.lb_vec ? piece8<true>(rl, row, r, p.rank, n < p.N) : piece8<false>(rl, row, r, p.rank, n < p.N);
 }
 
-// acc += t @ Lb^T on the 16x16x32 MFMA for FN x FM blocks (n, m) of 16x16 at
-// column n0, row m0 of the problem: lane l holds row 16 b + l % 16 and columns
-// 16 a + 4 (l / 16) + 0..3.  One MFMA per block and chunk: lanes 0-31 hold hi,
-// lanes 32-63 lo.  Nothing hides behind these loads, so they go out early and
-// together: the ids of all row blocks first, a row block's records while the
-// block before it is worked on, and Lb's fragments of CB chunks at a time,
-// which stay in registers from row block to row block while the adapter does
-// not change (as in a batch of prompts) and its rank needs no more of them.
-// The adapters of a row block are looped over with the column blocks'
-// contribution in registers of its own, and every accumulator is then changed
-// once, in straight-line code: changing accumulators inside a loop made the
-// register allocator spill them (756 registers on the 128x256 tile).  GN of
-// the FN column blocks are worked on at a time; GN and CB are what the wave's
-// registers hold.
-template <int GN, int CB, int FN, int FM>
-__device__ __forceinline__ void adapter_add16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0)
+// acc += x^T-block * y-block with the accumulator in AGPRs before and after.
+// Not mfma16_inplace: its operands come from vector instructions and the
+// accumulators around it may be moved, so the compiler has to see a matrix
+// instruction to keep the wait states these need.
+__device__ __forceinline__ void mfma16_pinned(f32x4& acc, const half8& x, const half8& y)
 {
-    static_assert(FN % GN == 0, "whole groups of column blocks");
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, acc, 0, 0, 0);
+    asm volatile("" : "+a"(acc));
+}
+
+// Bits 15 and 31 set where a half of `d` is an infinity or a NaN.
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t d) { return ((d & 0x7c007c00u) + 0x04000400u) & 0x80008000u; }
+
+// acc, all zeros, becomes t @ Lb^T on the 16x16x32 MFMA for FN x FM blocks
+// (n, m) of 16x16 at column n0, row m0 of the problem: lane l holds row
+// 16 b + l % 16 and columns 16 a + 4 (l / 16) + 0..3.  One MFMA per block and
+// chunk: lanes 0-31 hold hi, lanes 32-63 lo.
+//
+// It runs before the product's loop, behind the first operand copies, because
+// the registers of the loop's operands are free then: the records of all row
+// blocks and an adapter's fragments for all column blocks (CB chunks of each)
+// are requested together, so a tile whose rows share an adapter waits once per
+// CB chunks.  Accumulators are changed by matrix instructions alone inside the
+// loop over adapters (changing them with vector instructions there made the
+// register allocator spill them), so the rows of other adapters take part with
+// t = 0, and the rows' scales multiply all accumulators once at the end.
+// 0 * infinity and 0 * NaN would then reach those rows: fragments with such
+// values have them replaced by zeros, and the caller, told so by the returned
+// true, runs adapter_nonfinite16 after its epilogue.
+template <int CB, bool VEC, int FN, int FM>
+__device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0)
+{
     const int lane = threadIdx.x & 63, lrow = lane & 15, lq = lane >> 4;
-    int id[FM];
+    // buffers that start at this wave's first row: 32-bit offsets, and zeros past the last row
+    const uint32_t rows = (uint32_t)max(min(p.M - m0, 16 * FM), 0), rec_bytes = (uint32_t)p.chunks * 64u;
+    const __amdgpu_buffer_rsrc_t rid = make_rsrc(p.ids + m0, rows * 4u);
+    const __amdgpu_buffer_rsrc_t rsc = make_rsrc(p.t_scale + m0, rows * 4u);
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(p.t + (int64_t)m0 * p.chunks * 32, rows * rec_bytes);
+    int id[FM], all = 0;
+    float sc[FM];
 #pragma unroll
-    for (int b = 0; b < FM; ++b) id[b] = adapter_of(p.ids, m0 + 16 * b + lrow, p.M, p.adapters);
-    auto records = [&](int b, int c0, half8 (&t)[CB], float (&sc)[CB]) {
+    for (int b = 0; b < FM; ++b) id[b] = (int)__builtin_amdgcn_raw_buffer_load_b32(rid, (uint32_t)(16 * b + lrow) * 4u, 0, 0);
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
-            const int64_t rec = (int64_t)min(m0 + 16 * b + lrow, p.M - 1) * p.chunks + min(c0 + j, p.chunks - 1);
-            t[j] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 8 * lq));
-            sc[j] = p.t_scale[rec];
-        }
-    };
+    for (int b = 0; b < FM; ++b) sc[b] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsc, (uint32_t)(16 * b + lrow) * 4u, 0, 0));
 #pragma unroll
-    for (int g = 0; g < FN; g += GN) {
-        half8 x[CB][GN], t0[CB];
-        float s0[CB];
-        records(0, 0, t0, s0);
+    for (int b = 0; b < FM; ++b) {
+        if ((uint32_t)(16 * b + lrow) >= rows || (uint32_t)id[b] >= (uint32_t)p.adapters) id[b] = -1, sc[b] = 1.0f;
+        all |= (id[b] >= 0 ? 1 : 0) << b;
+    }
+    if (__ballot(all != 0) == 0) return false;
+    bool odd = false;
+    for (int c = 0; c < p.chunks; c += CB) {
+        half8 t[CB][FM];
 #pragma unroll
         for (int j = 0; j < CB; ++j)
 #pragma unroll
-            for (int a = 0; a < GN; ++a) x[j][a] = (half8)(_Float16)0.0f;
-        int held = -1;  // the adapter whose first CB chunks x holds
+            for (int b = 0; b < FM; ++b)
+                t[j][b] = __builtin_bit_cast(half8, __builtin_amdgcn_raw_buffer_load_b128(
+                    rt, (uint32_t)(16 * b + lrow) * rec_bytes + (uint32_t)min(c + j, p.chunks - 1) * 64u + 16u * (uint32_t)lq, 0, 0));
+        int todo = all;
+        while (const uint64_t any = __ballot(todo != 0)) {
+            const int src = __ffsll((unsigned long long)any) - 1;
+            const int tb = __ffs(__builtin_amdgcn_readlane(todo, src)) - 1;
+            int v = id[0];
 #pragma unroll
-        for (int b = 0; b < FM; ++b) {
-            half8 t1[CB];
-            float s1[CB];
-            if (b + 1 < FM) records(b + 1, 0, t1, s1);
-            f32x4 delta[GN] = {};
-            uint64_t todo = __ballot(id[b] >= 0);
-            while (todo) {
-                const int l = __builtin_amdgcn_readlane(id[b], __ffsll((unsigned long long)todo) - 1);
-                todo &= ~__ballot(id[b] == l);
-                for (int c0 = 0; c0 < p.chunks; c0 += CB) {
-                    if (held != l || p.chunks > CB) {
-                        held = l;
-                        const __amdgpu_buffer_rsrc_t rl = lb_rsrc(p, l);
+            for (int b = 1; b < FM; ++b) v = tb == b ? id[b] : v;
+            const int l = __builtin_amdgcn_readlane(v, src);
+            const __amdgpu_buffer_rsrc_t rl = lb_rsrc(p, l);
+            half8 x[CB][FN];  // chunks past the last are zeros
 #pragma unroll
-                        for (int j = 0; j < CB; ++j)
+            for (int j = 0; j < CB; ++j)
 #pragma unroll
-                            for (int a = 0; a < GN; ++a)
-                                x[j][a] = lb_piece(p, rl, n0 + 16 * (g + a) + lrow, kAdapterChunk * (c0 + j) + 8 * (lq & 1));
-                        if (c0 > 0 || p.chunks > CB) records(b, c0, t0, s0);
-                    }
+                for (int a = 0; a < FN; ++a) {
+                    const int n = n0 + 16 * a + lrow;
+                    x[j][a] = piece8<VEC>(rl, (uint32_t)n * (uint32_t)p.rank, kAdapterChunk * (c + j) + 8 * (lq & 1),
+                                          p.rank, n < p.N);
+                    // value by value: one fragment at a time, for the registers' sake
+                    if constexpr (!VEC) asm volatile("" : "+v"(x[j][a]));
+                }
+            uint32_t bad = 0;
 #pragma unroll
-                    for (int j = 0; j < CB; ++j) {
-                        if (c0 + j >= p.chunks) break;
+            for (int j = 0; j < CB; ++j)
 #pragma unroll
-                        for (int a = 0; a < GN; ++a) {
-                            const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[j][a], t0[j], f32x4{}, 0, 0, 0);
+                for (int a = 0; a < FN; ++a)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) delta[a][i] += id[b] == l ? s0[j] * d[i] : 0.0f;
+                    for (int i = 0; i < 4; ++i) bad |= nonfinite2(__builtin_bit_cast(u32x4, x[j][a])[i]);
+            if (__ballot(bad != 0) != 0) {
+                odd = true;
+#pragma unroll
+                for (int j = 0; j < CB; ++j)
+#pragma unroll
+                    for (int a = 0; a < FN; ++a) {
+                        u32x4 w = __builtin_bit_cast(u32x4, x[j][a]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t f = nonfinite2(w[i]);
+                            w[i] &= ~((f >> 15) * 0xffffu);
                         }
+                        x[j][a] = __builtin_bit_cast(half8, w);
                     }
+            }
+#pragma unroll
+            for (int b = 0; b < FM; ++b) {
+                if (__ballot(id[b] == l) == 0) continue;
+                if (id[b] == l) todo &= ~(1 << b);
+#pragma unroll
+                for (int j = 0; j < CB; ++j) {
+                    const half8 y = id[b] == l ? t[j][b] : (half8)(_Float16)0.0f;
+#pragma unroll
+                    for (int a = 0; a < FN; ++a) mfma16_pinned(acc[a][b], x[j][a], y);
                 }
             }
+        }
+    }
+    // a matrix result may be read by other instructions after 18 wait states
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int a = 0; a < GN; ++a) {
+    for (int b = 0; b < FM; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[g + a][b][i] += delta[a][i];
-                asm volatile("" : "+a"(acc[g + a][b]));  // back where the products left it
+        for (int a = 0; a < FN; ++a) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[a][b][i] *= sc[b];
+            asm volatile("" : "+a"(acc[a][b]));  // where the product's loop wants them
+        }
+    return odd;
+}
+
+// What adapter_start16 left out: outputs of the wave's WTM x WTN sub-tile whose
+// adapter has an infinity or a NaN in their column's Lb row become what that
+// makes of the sum (a NaN that is there already stays).  The wave has stored
+// the sub-tile itself.
+template <int WTM, int WTN>
+__device__ __forceinline__ void adapter_nonfinite16(const Problem& p, int m0, int n0)
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int lane = threadIdx.x & 63;
+    for (int m = m0; m < min(m0 + WTM, p.M); ++m) {
+        const int l = p.ids[m];
+        if ((uint32_t)l >= (uint32_t)p.adapters) continue;
+        for (int n = n0 + lane; n < min(n0 + WTN, p.N); n += 64) {
+            const uint16_t* row = p.lb + ((int64_t)l * p.N + n) * p.rank;
+            const uint16_t* rec = p.t + (int64_t)m * p.chunks * 32;
+            float sum = 0.0f;
+            bool odd = false;
+            for (int r = 0; r < p.rank; ++r) {
+                if ((row[r] & 0x7c00u) != 0x7c00u) continue;
+                const uint16_t* h = rec + (r / kAdapterChunk) * 32 + r % kAdapterChunk;
+                const float t = (float)__builtin_bit_cast(_Float16, h[0]) + (float)__builtin_bit_cast(_Float16, h[16]);
+                sum += t * (float)__builtin_bit_cast(_Float16, row[r]);
+                odd = true;
             }
-            if (b + 1 < FM) {
-#pragma unroll
-                for (int j = 0; j < CB; ++j) t0[j] = t1[j], s0[j] = s1[j];
-            }
+            uint16_t* c = p.C + (int64_t)m * p.N + n;
+            if (!odd || (c[0] & 0x7fffu) > 0x7c00u) continue;
+            const float b = p.bias ? (float)__builtin_bit_cast(_Float16, p.bias[n]) : 0.0f;
+            c[0] = __builtin_bit_cast(uint16_t, (_Float16)activate(p.alpha * sum + b, p.act));
         }
     }
 }
@@ -288,17 +468,19 @@ template <int TN, int TM, int BATCH>
 struct AdapterItems {
     int m0, n0, first, stride;
     int id[TM], todo = 0;
+    float sc[TM];             // the rows' scales
     int item = 0, l = -1, c;  // the next item: adapter l's chunk c
     int ls[BATCH], n = 0;     // the batch: its adapters and its size
     half8 x[BATCH][TN], hi[BATCH][TM], lo[BATCH][TM];
-    float sc[BATCH][TM];
 
     __device__ __forceinline__ AdapterItems(const Problem& p, int m0_, int n0_, int first_, int stride_)
         : m0(m0_), n0(n0_), first(first_), stride(stride_), c(p.chunks)
     {
 #pragma unroll
         for (int b = 0; b < TM; ++b) {
-            id[b] = adapter_of(p.ids, m0 + 32 * b + (int)(threadIdx.x & 31), p.M, p.adapters);
+            const int m = m0 + 32 * b + (int)(threadIdx.x & 31);
+            id[b] = adapter_of(p.ids, m, p.M, p.adapters);
+            sc[b] = id[b] >= 0 ? p.t_scale[m] : 0.0f;
             todo |= (id[b] >= 0 ? 1 : 0) << b;
         }
     }
@@ -346,7 +528,6 @@ struct AdapterItems {
                 const int64_t rec = (int64_t)min(m0 + 32 * b + frow, p.M - 1) * p.chunks + ch;
                 hi[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 8 * fhi));
                 lo[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 16 + 8 * fhi));
-                sc[j][b] = p.t_scale[rec];
             }
         }
     }
@@ -366,7 +547,7 @@ struct AdapterItems {
                     d = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[j][a], hi[j][b], d, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[a][b][i] = id[b] == ls[j] ? acc[a][b][i] + sc[j][b] * d[i] : acc[a][b][i];
+                        acc[a][b][i] = id[b] == ls[j] ? acc[a][b][i] + sc[b] * d[i] : acc[a][b][i];
                 }
             }
         }

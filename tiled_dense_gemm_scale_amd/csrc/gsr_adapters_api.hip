@@ -20,7 +20,7 @@ using gsr::ShrinkArgs;
 using namespace gsr::host;
 
 constexpr int64_t kLimit = (int64_t)1 << 31;
-constexpr int64_t kMaxRank = 256;
+constexpr int64_t kMaxRank = gsr::kShrinkMaxRank;
 constexpr int64_t kCounterBytes = kSplitCounters * 4;
 
 typedef hipError_t (*launch_fn)(const Problem&, int grid, hipStream_t);
@@ -28,25 +28,29 @@ typedef hipError_t (*launch_fn)(const Problem&, int grid, hipStream_t);
 template <class T>
 hipError_t launch_ilv16d(const Problem& p, int grid, hipStream_t s)
 {
-    return launch_kernel(gsr::gemm_scale_relu_ilv16d_kernel<T, false, true>, dim3(grid), dim3(T::NT), s, p);
+    return launch_kernel(p.lb_vec ? gsr::gemm_scale_relu_ilv16d_kernel<T, false, gsr::kAdaptVec>
+                                  : gsr::gemm_scale_relu_ilv16d_kernel<T, false, gsr::kAdaptElem>,
+                         dim3(grid), dim3(T::NT), s, p);
 }
 
 template <class T>
 hipError_t launch_ilv16c(const Problem& p, int grid, hipStream_t s)
 {
-    return launch_kernel(gsr::gemm_scale_relu_ilv16c_kernel<T, false, true>, dim3(grid), dim3(T::NT), s, p);
+    return launch_kernel(p.lb_vec ? gsr::gemm_scale_relu_ilv16c_kernel<T, false, gsr::kAdaptVec>
+                                  : gsr::gemm_scale_relu_ilv16c_kernel<T, false, gsr::kAdaptElem>,
+                         dim3(grid), dim3(T::NT), s, p);
 }
 
 template <int BM, int BN, int S, int D, bool SPLIT>
 hipError_t launch_kspec(const Problem& p, int grid, hipStream_t s)
 {
-    return launch_kernel((gsr::gemm_scale_relu_kspec_kernel<BM, BN, S, D, SPLIT, false, true>), dim3(grid), dim3(512), s, p);
+    return launch_kernel((gsr::gemm_scale_relu_kspec_kernel<BM, BN, S, D, SPLIT, false, gsr::kAdaptVec>), dim3(grid), dim3(512), s, p);
 }
 
 template <int BM, int BN>
 hipError_t launch_staged(const Problem& p, int grid, hipStream_t s)
 {
-    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, false, true>), dim3(grid), dim3(256), s, p);
+    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, false, gsr::kAdaptVec>), dim3(grid), dim3(256), s, p);
 }
 
 // The tiles with an adapter form, under the ids of their dense forms.
@@ -88,13 +92,35 @@ const Entry& stand_in(int id)
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// The shrink launch.  Few rows: a workgroup per 16 rows, adapter and chunk of
-// ranks, so that one decode step's adapters spread over the chip.  Many rows:
-// one per 16 rows and four chunks, which takes all adapters of its rows.
-constexpr int64_t kShrinkFewRows = 128;
+// The shrink launch.  Up to kShrinkFewRows rows, a block of 16 spreads over
+// parts of at least kShrinkPart values of K, chunks of ranks and adapters;
+// blocks count arrivals in the counters at the workspace's start.  More rows
+// take one workgroup per block and share of its adapters, as many shares as
+// the chip has room for.
+constexpr int64_t kShrinkFewRows = 64, kShrinkPart = 1024, kShrinkMaxParts = 16;
 
-// The workspace: counters, the records of t, their scales, then the partial
-// sums of the product's K split.
+struct ShrinkPlan {
+    int blocks, parts, kchunk;  // parts 0: all of K in one workgroup
+    int slots;
+};
+
+ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t adapters)
+{
+    ShrinkPlan s{(int)cdiv(M, gsr::kShrinkRows), 0, (int)K, 1};
+    const int64_t most = std::min<int64_t>({M, adapters, gsr::kShrinkRows});
+    if (M > kShrinkFewRows) {
+        s.slots = (int)std::max<int64_t>(1, std::min<int64_t>(most, 256 / s.blocks));
+        return s;
+    }
+    s.slots = (int)most;
+    s.kchunk = (int)std::max<int64_t>(kShrinkPart, cdiv(cdiv(K, kShrinkMaxParts), 32) * 32);
+    s.parts = (int)cdiv(K, s.kchunk);
+    return s;
+}
+
+// The workspace: counters, the records of t, the rows' scales, then the
+// partial sums of the shrink launch, whose place those of the product's K
+// split take when it has ended.
 struct Layout {
     int chunks;
     int64_t t, t_scale, partial;
@@ -106,8 +132,13 @@ Layout layout_of(int64_t M, int64_t rank)
     w.chunks = (int)cdiv(rank, gsr::kAdapterChunk);
     w.t = kCounterBytes;
     w.t_scale = w.t + round256(M * w.chunks * 64);
-    w.partial = w.t_scale + round256(M * w.chunks * 4);
+    w.partial = w.t_scale + round256(M * 4);
     return w;
+}
+
+int64_t shrink_partial_bytes(const ShrinkPlan& s, int chunks)
+{
+    return (int64_t)s.parts * s.blocks * gsr::kShrinkRows * chunks * gsr::kAdapterChunk * 4;
 }
 
 }  // namespace
@@ -120,7 +151,8 @@ int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ran
     if (M == 0 || N == 0 || K == 0 || rank == 0) return 0;
     const Entry& e = stand_in(dense_launch(M, N, K).id);
     const int64_t split = e.split ? dense_split(M, N, K, cdiv(M, e.bm) * cdiv(N, e.bn), e.bm, e.bn, 0).partial_bytes : 0;
-    return layout_of(M, rank).partial + split;
+    const Layout w = layout_of(M, rank);
+    return w.partial + std::max(split, shrink_partial_bytes(shrink_plan(M, K, 1), w.chunks));
 }
 
 int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const void* bias,
@@ -188,7 +220,8 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     const int tiles = p.tiles_m * p.tiles_n;
 
     const Layout w = layout_of(M, rank);
-    if (workspace_bytes < w.partial) return GSR_ERROR_INVALID_VALUE;
+    const ShrinkPlan sp = shrink_plan(M, K, adapters);
+    if (workspace_bytes < w.partial + shrink_partial_bytes(sp, w.chunks)) return GSR_ERROR_INVALID_VALUE;
     Split split{1, K, 0};
     if (splits > 1 && e.split == nullptr) return GSR_ERROR_INVALID_CONFIG;
     if (vec && e.split != nullptr) {
@@ -214,14 +247,24 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     a.adapters = (int)adapters;
     a.rank = (int)rank;
     a.chunks = w.chunks;
-    const bool few = M <= kShrinkFewRows, shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
-    const int nb = few || w.chunks == 1 ? 1 : 4;
-    a.slots = few ? (int)std::min<int64_t>({M, adapters, gsr::kShrinkRows}) : 1;
+    a.partial = (float*)(ws + w.partial);
+    a.count = (uint32_t*)ws;
+    a.blocks = sp.blocks;
+    a.parts = sp.parts;
+    a.kchunk = sp.kchunk;
+    a.slots = sp.slots;
+    const bool shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
     hipStream_t s = (hipStream_t)stream;
-    hipError_t err = launch_kernel(nb == 1 ? (shrink_vec ? gsr::adapter_shrink_kernel<true, 1> : gsr::adapter_shrink_kernel<false, 1>)
-                                           : (shrink_vec ? gsr::adapter_shrink_kernel<true, 4> : gsr::adapter_shrink_kernel<false, 4>),
-                                   dim3((unsigned)cdiv(M, gsr::kShrinkRows), (unsigned)cdiv(w.chunks, nb), (unsigned)a.slots),
-                                   dim3(64 * gsr::kShrinkWaves), s, a);
+    hipError_t err;
+    if (sp.parts > 0)
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_parts_kernel<true> : gsr::adapter_shrink_parts_kernel<false>,
+                            dim3((unsigned)(sp.blocks * sp.parts), (unsigned)w.chunks, (unsigned)a.slots), dim3(256), s, a);
+    else if (w.chunks == 1)
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, 1> : gsr::adapter_shrink_rows_kernel<false, 1>,
+                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(1024), s, a);
+    else
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, 4> : gsr::adapter_shrink_rows_kernel<false, 4>,
+                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(1024), s, a);
     if (err != hipSuccess) return GSR_ERROR_LAUNCH;
 
     p.ids = ids;

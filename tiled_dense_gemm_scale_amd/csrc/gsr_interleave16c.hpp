@@ -72,6 +72,7 @@ struct Ilv16CCfg {
     // configuration 29's read plan: X[7] at X7_0 / X7_1, Y[b] at Y0 + YS b
     static constexpr int X7_0 = Ilv16HDCfg::X7_0, X7_1 = Ilv16HDCfg::X7_1;
     static constexpr int Y0_0 = Ilv16HDCfg::Y0_0, Y0_1 = Ilv16HDCfg::Y0_1, YS = 4, BAR = Ilv16HDCfg::BAR;
+    static constexpr int ADAPTER_CHUNKS = 1;             // chunks at a time in adapter_start16
 };
 
 // The 128x128 tile (configuration 32): four MFMA waves of 64x64, 4 (n) x 4
@@ -99,6 +100,7 @@ struct Ilv16QCCfg {
     static constexpr int SLOTS = FM * FN;                // 16 MFMAs per substep
     static constexpr int X7_0 = 1, X7_1 = 2;
     static constexpr int Y0_0 = 0, Y0_1 = 1, YS = 2, BAR = 1;
+    static constexpr int ADAPTER_CHUNKS = 2;
 };
 
 // f(integral_constant<int, I>) for each I of the sequence, in order
@@ -108,7 +110,7 @@ __device__ __forceinline__ void for_each_ic(F& f, std::integer_sequence<int, I..
     (f(std::integral_constant<int, I>{}), ...);
 }
 
-template <class T, bool GROUPED = false, bool ADAPT = false>
+template <class T, bool GROUPED = false, int ADAPT = kAdaptNone>
 __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
 {
     constexpr int BK = T::BK, CH = T::CH, FM = T::FM, FN = T::FN;
@@ -248,6 +250,15 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
 
     // ========================== MFMA waves ==================================
     const int wm = wave / T::WN, wn = wave % T::WN;
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int a = 0; a < FN; ++a)
+#pragma unroll
+        for (int b = 0; b < FM; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // before anything else of the loop is in registers
+    [[maybe_unused]] bool odd = false;
+    if constexpr (ADAPT != kAdaptNone) odd = adapter_start16<T::ADAPTER_CHUNKS, ADAPT == kAdaptVec>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
     const uint32_t lrow = (uint32_t)lane & 15u, lq = (uint32_t)lane >> 4;
     const uint32_t lch = ((lq & 1u) << 1) | (lq >> 1);
     // A^T fragment b, substep 0 (substep 1: byte offset ^ 64)
@@ -278,12 +289,6 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
             }
         }
     }
-
-    f32x4 acc[FN][FM];
-#pragma unroll
-    for (int a = 0; a < FN; ++a)
-#pragma unroll
-        for (int b = 0; b < FM; ++b) acc[a][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     half8 X[FN - 1];  // B^T fragments 0..6, refilled one by one
     half8 X7[2];      // B^T fragment 7, one per substep parity
@@ -387,8 +392,9 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
     // last of them the wait states a matrix result needs before other
     // instructions read it (64, well above the 16x16x32 requirement).
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-    if constexpr (ADAPT) adapter_add16<4, 1>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
     ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
+    if constexpr (ADAPT != kAdaptNone)
+        if (odd) adapter_nonfinite16<T::WTM, T::WTN>(p, m0 + wm * T::WTM, n0 + wn * T::WTN);
 }
 
 }  // namespace gsr

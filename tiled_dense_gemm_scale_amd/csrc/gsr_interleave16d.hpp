@@ -73,6 +73,9 @@ struct Ilv16DCfg : Ilv16Cfg {
     static constexpr int BAR = 6;                       // wait + barrier slot of substep 1
     static constexpr int BC0 = 4, BCD = 8;              // B copies in substep 0: first slot, stride
     static constexpr int AC0 = 8, ACD = 7;              // A copies in substep 1: first slot, stride
+    // chunks of ranks at a time in adapter_start16 (two spill, and were 12 %
+    // slower over the whole call at rank 16, 17 % at 64)
+    static constexpr int ADAPTER_CHUNKS = 1;
 };
 
 // The 128x256 tile (configuration 29; gsr_interleave16c.hpp runs the same
@@ -107,7 +110,7 @@ __device__ __forceinline__ uint32_t fb16(uint32_t k)
     return ((k & 3u) + (((c ^ (c >> 1)) & 1u) << 2)) << 1;
 }
 
-template <class T, bool GROUPED = false, bool ADAPT = false>
+template <class T, bool GROUPED = false, int ADAPT = kAdaptNone>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 gemm_scale_relu_ilv16d_kernel(Problem p)
 {
@@ -166,21 +169,13 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
         return (k < K) ? rsrc_of(b_base + (uint64_t)k * N * 2u, b_recs - k * N * 2u) : rsrc_of(b_base, 0u);
     };
 
+    // The copy and read plans are functions of the lane: a kernel with adapters
+    // makes them a second time after its adapters' section, where nothing of
+    // them should stay in registers.
     // ---- A copy plan (as in the register-transpose kernel) ------------------
-    const uint32_t c0 = ((uint32_t)lane & 7u) ^ ((uint32_t)lane >> 3) ^ (uint32_t)wave;
-    const uint32_t arow = (8u * (uint32_t)wave + ((uint32_t)lane >> 3)) * K * 2u;
-    uint32_t av0 = arow + 16u * c0, av1 = arow + 32u * K * 2u + 16u * (c0 ^ 4u);
-    uint32_t kc0 = 8u * c0, kc1 = 8u * (c0 ^ 4u);
+    uint32_t av0, av1, kc0, kc1;
     const uint32_t a_istride = 64u * K * 2u;
     uint32_t av[T::A_PER];  // GROUPED: each copy's row is looked up
-    if constexpr (GROUPED) {
-#pragma unroll
-        for (int i = 0; i < T::A_PER; ++i) {
-            const int r = a_row<GROUPED>(p, 8 * wave + (lane >> 3) + 32 * i);
-            av[i] = r < 0 ? kOutOfRange : (uint32_t)r * K * 2u + 16u * ((i & 1) ? (c0 ^ 4u) : c0);
-        }
-    }
-
     // ---- B copy plan --------------------------------------------------------
     // Copy i of this wave fills B chunk positions P = 64 (wave + 4i) + lane:
     // row k = P / 32 = 2 wave + 8 i + lane / 32, physical chunk lane % 32,
@@ -188,28 +183,33 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     // Columns past N read as zero (N is a multiple of 8 on this path, so a
     // chunk is wholly in or out); rows past K fall past the descriptor.
     uint32_t b_voff[T::B_PER];
+    auto copy_plan = [&](uint32_t l) {
+        const uint32_t c0 = (l & 7u) ^ (l >> 3) ^ (uint32_t)wave;
+        const uint32_t arow = (8u * (uint32_t)wave + (l >> 3)) * K * 2u;
+        av0 = arow + 16u * c0, av1 = arow + 32u * K * 2u + 16u * (c0 ^ 4u);
+        kc0 = 8u * c0, kc1 = 8u * (c0 ^ 4u);
+        if constexpr (GROUPED) {
 #pragma unroll
-    for (int i = 0; i < T::B_PER; ++i) {
-        const uint32_t k = 2u * (uint32_t)wave + 8u * (uint32_t)i + ((uint32_t)lane >> 5);
-        const uint32_t c = ((uint32_t)lane & 31u) ^ fb16(k);
-        b_voff[i] = ((uint32_t)n0 + 8u * c < N) ? (k * N + 8u * c) * 2u : kOutOfRange;
-    }
+            for (int i = 0; i < T::A_PER; ++i) {
+                const int r = a_row<GROUPED>(p, 8 * wave + (int)(l >> 3) + 32 * i);
+                av[i] = r < 0 ? kOutOfRange : (uint32_t)r * K * 2u + 16u * ((i & 1) ? (c0 ^ 4u) : c0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < T::B_PER; ++i) {
+            const uint32_t k = 2u * (uint32_t)wave + 8u * (uint32_t)i + (l >> 5);
+            const uint32_t c = (l & 31u) ^ fb16(k);
+            b_voff[i] = ((uint32_t)n0 + 8u * c < N) ? (k * N + 8u * c) * 2u : kOutOfRange;
+        }
+    };
 
     // ---- fragment addresses -------------------------------------------------
     // Lane group g = l / 16 takes k-group chunk lch(g) = (g & 1) * 2 + g / 2
     // of its substep for both operands (the A^T layout needs that order to be
     // free of bank conflicts).
-    const uint32_t lrow = (uint32_t)lane & 15u, lq = (uint32_t)lane >> 4;
-    const uint32_t lch = ((lq & 1u) << 1) | (lq >> 1);
     // A^T fragment b (0..3; b + 4 is 64 rows = 8 KiB further, same swizzle),
     // substep 0; substep 1 flips chunk bit 2 (byte offset ^ 64).
     uint32_t yb[2][4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t ry = (uint32_t)wm * T::WTM + (uint32_t)b * 16u + lrow;
-        yb[0][b] = ry * (BK * 2) + ((lch ^ swz_a<CH>(ry)) << 4);
-        yb[1][b] = yb[0][b] ^ 64u;
-    }
     // B^T fragment a (0..7) by transpose reads: in 16-lane group g, lane
     // i = 4e + q supplies the address of row 8 lch(g) + e (+ 4 for the second
     // read, + 32 for substep 1) and columns 16a + 4q .. +3 of this wave's 128;
@@ -217,7 +217,15 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     // xa: B stages 0 and 1 (the stage offset rides in the immediate), xa2:
     // B stage 2.
     uint32_t xa[FN], xa2[FN];
-    {
+    auto read_plan = [&](uint32_t l) {
+        const uint32_t lrow = l & 15u, lq = l >> 4;
+        const uint32_t lch = ((lq & 1u) << 1) | (lq >> 1);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t ry = (uint32_t)wm * T::WTM + (uint32_t)b * 16u + lrow;
+            yb[0][b] = ry * (BK * 2) + ((lch ^ swz_a<CH>(ry)) << 4);
+            yb[1][b] = yb[0][b] ^ 64u;
+        }
         const uint32_t e = lrow >> 2, q = lrow & 3u;
         const uint32_t krow0 = 8u * lch + e;
         const uint32_t h = fb16(krow0) >> 1;
@@ -227,7 +235,9 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
             xa[a] = base + ((((uint32_t)a) ^ h) << 5);
             xa2[a] = xa[a] + 2u * (uint32_t)T::B_BYTES;
         }
-    }
+    };
+    copy_plan((uint32_t)lane);
+    if constexpr (ADAPT == kAdaptNone) read_plan((uint32_t)lane);
 
     f32x4 acc[FN][FM];
 #pragma unroll
@@ -323,6 +333,7 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
 
+    [[maybe_unused]] bool odd = false;
     // ---- prologue: A(0), B(0) in stage 0, A(1), B(1) in stage 1 -------------
     const int ksteps = (((int)K + BK - 1) / BK + 1) & ~1;  // even
     {
@@ -337,6 +348,13 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
         for (int i = 0; i < T::A_PER; ++i) copy_a(1, i, kleft1, ra1);
 #pragma unroll
         for (int i = 0; i < T::B_PER; ++i) copy_b(1, i, rb1);
+        if constexpr (ADAPT != kAdaptNone) {
+            odd = adapter_start16<T::ADAPTER_CHUNKS, ADAPT == kAdaptVec>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
+            uint32_t l = (uint32_t)lane;
+            asm volatile("" : "+v"(l));  // a lane the compiler cannot know again
+            copy_plan(l);
+            read_plan(l);
+        }
         wait_vmcnt<T::A_PER + T::B_PER>();  // stage 0's copies are in
         lds_barrier();
         // substep-0 operands of step 0
@@ -375,8 +393,9 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     // last of them the wait states a matrix result needs before other
     // instructions read it (64, well above the 16x16x32 requirement).
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-    if constexpr (ADAPT) adapter_add16<8, 2>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
     ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
+    if constexpr (ADAPT != kAdaptNone)
+        if (odd) adapter_nonfinite16<T::WTM, T::WTN>(p, m0 + wm * T::WTM, n0 + wn * T::WTN);
 }
 
 }  // namespace gsr

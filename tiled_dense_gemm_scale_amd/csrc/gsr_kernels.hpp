@@ -168,7 +168,7 @@ struct Problem {
     const int32_t* rows;
     int groups, a_rows;
     // low-rank adapters (the ADAPT kernels, gsr_adapters.hpp): row m's inner
-    // sums as `chunks` records and scales, Lb adapters x N x rank, l = ids[m];
+    // sums as `chunks` records and a scale, Lb adapters x N x rank, l = ids[m];
     // lb_vec: Lb is 16-byte aligned and rank a multiple of 8
     const int32_t* ids;
     const uint16_t* t;
@@ -178,9 +178,16 @@ struct Problem {
     bool lb_vec;
 };
 
+// ADAPT of the kernels: without adapters, with Lb read in 16-byte units
+// (lb_vec), with Lb read value by value.  The tiles whose accumulators fill
+// the registers have a form of their own for each; the others look at lb_vec.
+enum : int { kAdaptNone = 0, kAdaptVec = 1, kAdaptElem = 2 };
+
 // gsr_adapters.hpp
-template <int GN, int CB, int FN, int FM>
-__device__ void adapter_add16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0);
+template <int CB, bool VEC, int FN, int FM>
+__device__ bool adapter_start16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0);
+template <int WTM, int WTN>
+__device__ void adapter_nonfinite16(const Problem& p, int m0, int n0);
 template <int TN, int TM, int BATCH>
 struct AdapterItems;
 
@@ -448,7 +455,7 @@ struct TileKernel {
     static_assert(LDS_BYTES <= 163840, "LDS budget of one workgroup on gfx950");
 };
 
-template <int BM, int BN, int BK, int WM, int WN, bool VEC, bool GROUPED = false, bool ADAPT = false>
+template <int BM, int BN, int BK, int WM, int WN, bool VEC, bool GROUPED = false, int ADAPT = kAdaptNone>
 __global__ void __launch_bounds__(kWave * WM * WN)
 gemm_scale_relu_kernel(Problem p)
 {
@@ -600,7 +607,7 @@ gemm_scale_relu_kernel(Problem p)
         for (int b = 0; b < TM; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-    if constexpr (ADAPT) {
+    if constexpr (ADAPT != kAdaptNone) {
         AdapterItems<TN, TM, 2> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
         items.load(p);
         items.finish(p, acc);

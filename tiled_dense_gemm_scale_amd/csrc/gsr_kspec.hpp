@@ -43,7 +43,7 @@
 
 namespace gsr {
 
-template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED = false, bool ADAPT = false>
+template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED = false, int ADAPT = kAdaptNone>
 __global__ void __launch_bounds__(512)
 gemm_scale_relu_kspec_kernel(Problem p)
 {
@@ -181,11 +181,11 @@ gemm_scale_relu_kspec_kernel(Problem p)
                 for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
         // the adapters' first batch is in flight behind the product
         using Items = AdapterItems<TN, TM, TM == 1 ? 4 : 2>;
-        [[maybe_unused]] std::conditional_t<ADAPT, Items, int> items = [&] {
-            if constexpr (ADAPT) return Items(p, m0, n0, wave, NW);
+        [[maybe_unused]] std::conditional_t<ADAPT != kAdaptNone, Items, int> items = [&] {
+            if constexpr (ADAPT != kAdaptNone) return Items(p, m0, n0, wave, NW);
             else return 0;
         }();
-        if constexpr (ADAPT)
+        if constexpr (ADAPT != kAdaptNone)
             if (part == 0) items.load(p);
 
         half8 xs0[2][TN], ys0[2][TM], xs1[2][TN], ys1[2][TM];
@@ -238,7 +238,7 @@ gemm_scale_relu_kspec_kernel(Problem p)
         } else if (ksteps > 0) {
             mma_step(xs1, ys1);
         }
-        if constexpr (ADAPT) items.finish(p, acc);
+        if constexpr (ADAPT != kAdaptNone) items.finish(p, acc);
 
         Sum::load_bias(p, tid, n0, bvs);
         wait_vmcnt<0>();
