@@ -27,7 +27,7 @@
 // another adapter's weights hold (NaN, infinities) cannot reach it.
 #pragma once
 
-#include "gsr_kernels.hpp"
+#include "gsr_pipeline.hpp"
 
 namespace gsr {
 
@@ -91,51 +91,164 @@ __device__ __forceinline__ void for_each_adapter(int id, F&& f)
 }
 
 // The sums of 16 rows over this workgroup's part of K for NB chunks of ranks
-// from chunk c0: the W waves cut the part into runs of 32-value steps, walk
-// every adapter's run STEPS steps at a time, so that their loads are in flight
-// together, and leave what they have in sums[wave][row][rank].
-template <bool VEC, int NB, int W, int STEPS>
-__device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, float (&sums)[W][kShrinkRows][kAdapterChunk * NB + 4],
-                                            int id, int m0, int c0, int kbeg, int kend, int slot)
+// from chunk c0.  The W waves cut the part into runs of 32-value steps; a wave
+// walks the run of every slots-th adapter of the rows and leaves what it has in
+// sums[wave][row][rank].
+//
+// An MFMA operand has a row per lane, and a load in that layout touches 16
+// rows with every 16 lanes: it ran at 10-12 bytes per clock and CU.  The
+// 128-bit path so copies into LDS with neighbouring lanes on neighbouring
+// bytes of a row (G 16-byte pieces of each of 16 rows per operand and batch),
+// piece c of row r at place c ^ shrink_swz(r), from where the operand reads
+// are free of bank conflicts.  A wave's LDS is its own: it waits for its
+// copies, no barrier, with DEPTH batches in flight across the ends of
+// adapters.
+template <int NB_, int W_, int G_, int DEPTH_>
+struct ShrinkCfg {
+    static constexpr int NB = NB_, W = W_, G = G_, DEPTH = DEPTH_;
+    static constexpr int OPER = 16 * G * 16;           // bytes of one operand's batch
+    static constexpr int BATCH = (1 + NB) * OPER;
+    static constexpr int COPIES = (1 + NB) * OPER / 1024;
+    static constexpr int RANKS = kAdapterChunk * NB + 4;  // row of the sums, padded
+    static constexpr int SUM_BYTES = W * kShrinkRows * RANKS * 4;
+    static constexpr int LDS_BYTES = W * DEPTH * BATCH > SUM_BYTES ? W * DEPTH * BATCH : SUM_BYTES;
+    static_assert(G == 8 || G == 16, "pieces per row");
+    static_assert(SUM_BYTES + kShrinkRows * 8 <= LDS_BYTES, "the rows' maxima fit behind the sums");
+    static_assert(LDS_BYTES <= 160 * 1024 && COPIES * DEPTH < 64, "LDS of a workgroup; the vmcnt field");
+};
+
+// Distinct places for one piece of 16 rows in the 256 bytes the LDS serves at
+// once: rows of 256 bytes (G = 16) or pairs of rows of 128 (G = 8).
+template <int G>
+__device__ __forceinline__ int shrink_swz(int r) { return G == 16 ? (r & 15) : ((r >> 1) & 7); }
+
+template <bool VEC, class T>
+__device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, uint8_t* smem, int id, int m0, int c0, int kbeg, int kend, int slot)
 {
+    constexpr int NB = T::NB, W = T::W, G = T::G, STEPS = G / 4;
     const int lane = threadIdx.x & 63, lrow = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int steps = (kend - kbeg + 31) / 32;
     const int ks0 = steps * wave / W, ks1 = steps * (wave + 1) / W;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(s.A, (uint32_t)s.M * (uint32_t)s.K * 2u);
-    const uint32_t arow = (uint32_t)(m0 + lrow) * (uint32_t)s.K;
-    const bool ain = m0 + lrow < s.M;
     f32x4 out[NB] = {};
-    int at = 0;
-    for_each_adapter(id, [&](int l) {
-        if (at++ % s.slots != slot) return;
-        const __amdgpu_buffer_rsrc_t rl = make_rsrc(s.la + (int64_t)l * s.rank * s.K, (uint32_t)s.rank * (uint32_t)s.K * 2u);
+    if constexpr (VEC) {
+        const i32x4 ra = raw_rsrc(s.A, (uint32_t)s.M * (uint32_t)s.K * 2u);
+        const uint32_t lds0 = lds_address(smem) + (uint32_t)(wave * T::DEPTH * T::BATCH);
+        const uint8_t* const base = smem + wave * T::DEPTH * T::BATCH;
+        const int batches = (ks1 - ks0 + STEPS - 1) / STEPS, klim = min(kend, kbeg + 32 * ks1);
+        // a walk over (adapter, batch): the copies' walk runs DEPTH - 1 ahead of the products'
+        struct Walk {
+            uint64_t todo;
+            int at, l, b;
+        };
+        auto advance = [&](Walk& w) {  // to the next unit of this workgroup's; l = -1 at the end
+            if (++w.b < batches && w.l >= 0) return;
+            w.b = 0;
+            w.l = -1;
+            while (w.todo != 0) {
+                const int l = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)w.todo) - 1);
+                w.todo &= ~__ballot(id == l);
+                if (w.at++ % s.slots == slot) {
+                    w.l = l;
+                    return;
+                }
+            }
+        };
+        auto copy = [&](const Walk& w, int buf) {
+            const i32x4 rl = raw_rsrc(s.la + (int64_t)w.l * s.rank * s.K, (uint32_t)s.rank * (uint32_t)s.K * 2u);
+            const int k0 = kbeg + 32 * (ks0 + w.b * STEPS);
+#pragma unroll
+            for (int o = 0; o < 1 + NB; ++o)
+#pragma unroll
+                for (int j = 0; j < T::OPER / 1024; ++j) {
+                    const int r = (64 / G) * j + lane / G;  // of the operand's 16 rows
+                    const int k = k0 + 8 * ((lane % G) ^ shrink_swz<G>(r));
+                    const int row = o == 0 ? m0 + r : kAdapterChunk * (c0 + o - 1) + r;
+                    const bool in = k < klim && row < (o == 0 ? s.M : s.rank);
+                    copy16_to_lds(o == 0 ? ra : rl, in ? ((uint32_t)row * (uint32_t)s.K + (uint32_t)k) * 2u : kOutOfRange,
+                                  lds0 + (uint32_t)(buf * T::BATCH + o * T::OPER + j * 1024));
+                }
+        };
+        Walk ahead{__ballot(id >= 0), 0, -1, 0}, here;
+        if (batches <= 0) ahead.todo = 0;
+        advance(ahead);
+        here = ahead;
+        int flying = 0, put = 0, get = 0;
         f32x4 d[NB] = {};
-        for (int ks = ks0; ks < ks1; ks += STEPS) {
-            half8 x[STEPS], w[STEPS][NB];
+        while (here.l >= 0) {
+            while (flying < T::DEPTH && ahead.l >= 0) {
+                copy(ahead, put);
+                put = put + 1 == T::DEPTH ? 0 : put + 1;
+                ++flying;
+                advance(ahead);
+            }
+            if (flying == T::DEPTH) wait_vmcnt<T::COPIES * (T::DEPTH - 1)>();
+            else wait_vmcnt<0>();
+            const uint8_t* buf = base + get * T::BATCH;
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-                const int k = kbeg + 32 * (ks + i) + 8 * lq;
-                const int len = ks + i < ks1 ? kend : 0;
-                x[i] = piece8<VEC>(ra, arow, k, len, ain);
+                const int place = lrow * (G * 16) + ((4 * i + lq) ^ shrink_swz<G>(lrow)) * 16;
+                const half8 x = __builtin_bit_cast(half8, *(const u32x4*)(buf + place));
+#pragma unroll
+                for (int q = 0; q < NB; ++q)
+                    d[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        __builtin_bit_cast(half8, *(const u32x4*)(buf + (1 + q) * T::OPER + place)), x, d[q], 0, 0, 0);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next copies land here
+            get = get + 1 == T::DEPTH ? 0 : get + 1;
+            --flying;
+            const int l = here.l;
+            advance(here);
+            if (here.b == 0) {  // the adapter's run is complete
+#pragma unroll
+                for (int q = 0; q < NB; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        out[q][i] = id == l ? out[q][i] + d[q][i] : out[q][i];
+                        d[q][i] = 0.0f;
+                    }
+            }
+        }
+    } else {
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(s.A, (uint32_t)s.M * (uint32_t)s.K * 2u);
+        const uint32_t arow = (uint32_t)(m0 + lrow) * (uint32_t)s.K;
+        const bool ain = m0 + lrow < s.M;
+        int at = 0;
+        for_each_adapter(id, [&](int l) {
+            if (at++ % s.slots != slot) return;
+            const __amdgpu_buffer_rsrc_t rl = make_rsrc(s.la + (int64_t)l * s.rank * s.K, (uint32_t)s.rank * (uint32_t)s.K * 2u);
+            f32x4 d[NB] = {};
+            for (int ks = ks0; ks < ks1; ++ks) {
+                const int k = kbeg + 32 * ks + 8 * lq;
+                const half8 x = piece8<false>(ra, arow, k, kend, ain);
 #pragma unroll
                 for (int q = 0; q < NB; ++q) {
                     const int r = kAdapterChunk * (c0 + q) + lrow;
-                    w[i][q] = piece8<VEC>(rl, (uint32_t)r * (uint32_t)s.K, k, len, r < s.rank);
+                    const half8 w = piece8<false>(rl, (uint32_t)r * (uint32_t)s.K, k, kend, r < s.rank);
+                    d[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, d[q], 0, 0, 0);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i)
+            for (int q = 0; q < NB; ++q)
 #pragma unroll
-                for (int q = 0; q < NB; ++q) d[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i][q], x[i], d[q], 0, 0, 0);
-        }
+                for (int i = 0; i < 4; ++i) out[q][i] = id == l ? out[q][i] + d[q][i] : out[q][i];
+        });
+    }
+    __syncthreads();  // the sums take the place of every wave's batches
+    float* const sums = (float*)smem;
 #pragma unroll
-        for (int q = 0; q < NB; ++q)
+    for (int q = 0; q < NB; ++q) *(f32x4*)(sums + (wave * kShrinkRows + lrow) * T::RANKS + 16 * q + 4 * lq) = out[q];
+    __syncthreads();
+}
+
+// Row `row`, rank c of chunk q, summed over the waves.
+template <class T>
+__device__ __forceinline__ float shrink_sum(const uint8_t* smem, int row, int q, int c)
+{
+    float v = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[q][i] = id == l ? out[q][i] + d[q][i] : out[q][i];
-    });
-#pragma unroll
-    for (int q = 0; q < NB; ++q) *(f32x4*)&sums[wave][lrow][16 * q + 4 * lq] = out[q];
+    for (int w = 0; w < T::W; ++w) v += ((const float*)smem)[(w * kShrinkRows + row) * T::RANKS + 16 * q + c];
+    return v;
 }
 
 // Writes row m's records: this thread holds ranks c + 16 j of the row for j in
@@ -163,19 +276,23 @@ __device__ __forceinline__ void shrink_store(const ShrinkArgs& s, int m, int l, 
 }
 
 // Many rows: a workgroup takes 16 rows, every slots-th of their adapters and
-// all ranks, NB chunks at a time, with 16 waves on K.  A is read once (from the
-// caches for further chunks) and an adapter's La once per 16 rows from the
-// caches.
-template <bool VEC, int NB>
-__global__ void __launch_bounds__(1024) adapter_shrink_rows_kernel(ShrinkArgs s)
+// all ranks, T::NB chunks at a time, with eight waves on K.  A is read once
+// (from the caches for further chunks) and an adapter's La once per 16 rows
+// from the caches.
+typedef ShrinkCfg<1, 8, 16, 2> ShrinkRows1;
+typedef ShrinkCfg<4, 8, 8, 2> ShrinkRows4;
+
+template <bool VEC, class T>
+__global__ void __launch_bounds__(512) adapter_shrink_rows_kernel(ShrinkArgs s)
 {
-    constexpr int W = 16, ROUNDS = kShrinkMaxRank / kAdapterChunk / 4;
-    __shared__ float sums[W][kShrinkRows][kAdapterChunk * NB + 4];
-    __shared__ float bigs[kShrinkRows][4];
+    constexpr int NB = T::NB, QT = 2, PER = (NB + QT - 1) / QT;        // chunks at a time per thread
+    constexpr int ROUNDS = NB == 1 ? 1 : kShrinkMaxRank / kAdapterChunk / NB;
+    static_assert(T::W == 8, "512 threads");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
     const int tid = threadIdx.x, m0 = blockIdx.x * kShrinkRows;
     const int id = adapter_of(s.ids, m0 + (tid & 15), s.M, s.adapters);
 
-    // thread t: row t / 16 % 16 and rank t % 16 of chunks t / 256, + NB, ...
+    // thread t: row t / 16 % 16 and rank t % 16 of chunks t / 256, + 2, ...
     const int row = (tid >> 4) & 15, c = tid & 15, q = tid >> 8;
     int l = adapter_of(s.ids, m0 + row, s.M, s.adapters), at = 0;
     bool mine = false;
@@ -183,33 +300,35 @@ __global__ void __launch_bounds__(1024) adapter_shrink_rows_kernel(ShrinkArgs s)
     if (at <= (int)blockIdx.z) return;  // no adapter for this workgroup
     l = mine ? l : -1;
     const float scale = (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
-    float v[NB == 1 ? 1 : ROUNDS], big = 0.0f;
+    float v[ROUNDS * PER], big = 0.0f;
     bool odd = false;
 #pragma unroll
-    for (int i = 0; i < (NB == 1 ? 1 : ROUNDS); ++i) {
-        v[i] = 0.0f;
+    for (int i = 0; i < ROUNDS; ++i) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[i * PER + j] = 0.0f;
         if (i * NB >= s.chunks) continue;
         if (i > 0) __syncthreads();  // the sums of the chunks before have been read
-        shrink_sums<VEC, NB, W, NB == 1 ? 8 : 4>(s, sums, id, m0, i * NB, 0, s.K, blockIdx.z);
-        __syncthreads();
-        if (q < NB && i * NB + q < s.chunks) {
+        shrink_sums<VEC, T>(s, smem, id, m0, i * NB, 0, s.K, blockIdx.z);
 #pragma unroll
-            for (int w = 0; w < W; ++w) v[i] += sums[w][row][16 * q + c];
-            v[i] *= scale;
-            odd |= !(fabsf(v[i]) <= 3.0e38f);
-            big = fmaxf(big, fabsf(v[i]));
+        for (int j = 0; j < PER; ++j) {
+            const int cq = q + QT * j;
+            if (cq >= NB || i * NB + cq >= s.chunks) continue;
+            const float u = shrink_sum<T>(smem, row, cq, c) * scale;
+            v[i * PER + j] = u;
+            odd |= !(fabsf(u) <= 3.0e38f);
+            big = fmaxf(big, fabsf(u));
         }
     }
     big = odd ? __builtin_inff() : big;
 #pragma unroll
     for (int x = 8; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor(big, x));
     if (NB > 1) {
-        if (c == 0) bigs[row][q] = big;
+        float* const bigs = (float*)(smem + T::SUM_BYTES) + row * QT;  // behind the sums others still read
+        if (c == 0) bigs[q] = big;
         __syncthreads();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) big = fmaxf(big, bigs[row][x]);
+        big = fmaxf(bigs[0], bigs[1]);
     }
-    if (q < NB) shrink_store(s, m0 + row, l, c, q, NB, v, big, !(big <= 3.0e38f));
+    if (q < NB) shrink_store(s, m0 + row, l, c, q, QT, v, big, !(big <= 3.0e38f));
 }
 
 // Few rows (a decode step): the adapters' La is most of the bytes, so a block
@@ -218,11 +337,15 @@ __global__ void __launch_bounds__(1024) adapter_shrink_rows_kernel(ShrinkArgs s)
 // block that arrives last adds the parts in part order and writes the records
 // (device-scope accesses and the arrival counter as in KsSum::split_sum_store,
 // so no order depends on timing and no workgroup waits).
+typedef ShrinkCfg<1, 4, 16, 2> ShrinkParts;
+
 template <bool VEC>
 __global__ void __launch_bounds__(256) adapter_shrink_parts_kernel(ShrinkArgs s)
 {
-    constexpr int W = 4, ROUNDS = kShrinkMaxRank / kAdapterChunk;
-    __shared__ float sums[W][kShrinkRows][kAdapterChunk + 4];
+    using T = ShrinkParts;
+    constexpr int ROUNDS = kShrinkMaxRank / kAdapterChunk;
+    static_assert(T::W == 4 && T::NB == 1, "256 threads, one chunk");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
     __shared__ int last;
     const int tid = threadIdx.x;
     const int block = blockIdx.x / s.parts, part = blockIdx.x - block * s.parts;
@@ -234,25 +357,20 @@ __global__ void __launch_bounds__(256) adapter_shrink_parts_kernel(ShrinkArgs s)
     // the adapter's place among the block's decides whose it is
     bool mine = false;
     int at = 0;
-    for_each_adapter(id, [&](int a) {
-        const bool ours = at++ % s.slots == (int)blockIdx.z;
-        mine |= ours && l == a;
-    });
+    for_each_adapter(id, [&](int a) { mine |= at++ % s.slots == (int)blockIdx.z && l == a; });
     const float scale = (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
 
-    const int kbeg = part * s.kchunk, kend = min(s.K, kbeg + s.kchunk);
-    shrink_sums<VEC, 1, W, 8>(s, sums, id, m0, blockIdx.y, kbeg, kend, blockIdx.z);
-    __syncthreads();
     const int64_t stride = (int64_t)s.blocks * kShrinkRows * s.chunks * kAdapterChunk;  // one part
     float* const at0 = s.partial + (int64_t)(m0 + row) * s.chunks * kAdapterChunk + c;
-    if (mine) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) v += sums[w][row][c];
-        __hip_atomic_store(at0 + part * stride + blockIdx.y * kAdapterChunk, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (at > (int)blockIdx.z) {  // there is an adapter for this workgroup
+        const int kbeg = part * s.kchunk, kend = min(s.K, kbeg + s.kchunk);
+        shrink_sums<VEC, T>(s, smem, id, m0, blockIdx.y, kbeg, kend, blockIdx.z);
+        if (mine)
+            __hip_atomic_store(at0 + part * stride + blockIdx.y * kAdapterChunk, shrink_sum<T>(smem, row, 0, c),
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums have reached device scope
+        __syncthreads();
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums have reached device scope
-    __syncthreads();
     if (tid == 0) {
         const uint32_t before = __hip_atomic_fetch_add(s.count + block, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         last = before == (uint32_t)(s.parts * gridDim.y * gridDim.z) - 1u;

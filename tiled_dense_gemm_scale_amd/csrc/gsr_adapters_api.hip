@@ -260,11 +260,13 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
         err = launch_kernel(shrink_vec ? gsr::adapter_shrink_parts_kernel<true> : gsr::adapter_shrink_parts_kernel<false>,
                             dim3((unsigned)(sp.blocks * sp.parts), (unsigned)w.chunks, (unsigned)a.slots), dim3(256), s, a);
     else if (w.chunks == 1)
-        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, 1> : gsr::adapter_shrink_rows_kernel<false, 1>,
-                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(1024), s, a);
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, gsr::ShrinkRows1>
+                                       : gsr::adapter_shrink_rows_kernel<false, gsr::ShrinkRows1>,
+                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
     else
-        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, 4> : gsr::adapter_shrink_rows_kernel<false, 4>,
-                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(1024), s, a);
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, gsr::ShrinkRows4>
+                                       : gsr::adapter_shrink_rows_kernel<false, gsr::ShrinkRows4>,
+                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
     if (err != hipSuccess) return GSR_ERROR_LAUNCH;
 
     p.ids = ids;
