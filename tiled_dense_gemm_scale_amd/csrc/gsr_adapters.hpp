@@ -580,16 +580,20 @@ __device__ __forceinline__ void adapter_nonfinite16(const Problem& p, int m0, in
 // 32 b + l % 32 and columns 32 a + 8 g + 4 (l / 32) + i in register 4 g + i.
 // The work items (adapter, chunk) are numbered; a wave takes items first,
 // first + stride, ... (waves that each hold a share of the sum share them
-// out), BATCH at a time: load() requests a batch, apply() adds it, so a batch
-// can be in flight behind the product.
-template <int TN, int TM, int BATCH>
+// out) in batches whose loads are in flight together: load() requests one,
+// apply() adds it, so one can be in flight behind the product.
+template <int TN, int TM>
 struct AdapterItems {
     int m0, n0, first, stride;
     int id[TM], todo = 0;
     float sc[TM];             // the rows' scales
     int item = 0, l = -1, c;  // the next item: adapter l's chunk c
-    int ls[BATCH], n = 0;     // the batch: its adapters and its size
-    half8 x[BATCH][TN], hi[BATCH][TM], lo[BATCH][TM];
+
+    template <int B>
+    struct Batch {
+        int n = 0, ls[B];  // its size and its adapters
+        half8 x[B][TN], hi[B][TM], lo[B][TM];
+    };
 
     __device__ __forceinline__ AdapterItems(const Problem& p, int m0_, int n0_, int first_, int stride_)
         : m0(m0_), n0(n0_), first(first_), stride(stride_), c(p.chunks)
@@ -628,57 +632,60 @@ struct AdapterItems {
         }
     }
 
-    __device__ __forceinline__ void load(const Problem& p)
+    template <int B>
+    __device__ __forceinline__ void load(const Problem& p, Batch<B>& w)
     {
         const int lane = threadIdx.x & 63, frow = lane & 31, fhi = lane >> 5;
-        n = 0;
+        w.n = 0;
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
+        for (int j = 0; j < B; ++j) {
             int ch = 0;
-            ls[j] = -1;
-            if (n == j && next(p, ls[j], ch)) ++n;
-            if (n <= j) continue;
-            const __amdgpu_buffer_rsrc_t rl = lb_rsrc(p, ls[j]);
+            w.ls[j] = -1;
+            if (w.n == j && next(p, w.ls[j], ch)) ++w.n;
+            if (w.n <= j) continue;
+            const __amdgpu_buffer_rsrc_t rl = lb_rsrc(p, w.ls[j]);
 #pragma unroll
-            for (int a = 0; a < TN; ++a) x[j][a] = lb_piece(p, rl, n0 + 32 * a + frow, kAdapterChunk * ch + 8 * fhi);
+            for (int a = 0; a < TN; ++a) w.x[j][a] = lb_piece(p, rl, n0 + 32 * a + frow, kAdapterChunk * ch + 8 * fhi);
 #pragma unroll
             for (int b = 0; b < TM; ++b) {
                 const int64_t rec = (int64_t)min(m0 + 32 * b + frow, p.M - 1) * p.chunks + ch;
-                hi[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 8 * fhi));
-                lo[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 16 + 8 * fhi));
+                w.hi[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 8 * fhi));
+                w.lo[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 16 + 8 * fhi));
             }
         }
     }
 
-    __device__ __forceinline__ void apply(f32x16 (&acc)[TN][TM])
+    template <int B>
+    __device__ __forceinline__ void apply(const Batch<B>& w, f32x16 (&acc)[TN][TM])
     {
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            if (j >= n) break;
+        for (int j = 0; j < B; ++j) {
+            if (j >= w.n) break;
 #pragma unroll
             for (int b = 0; b < TM; ++b) {
-                if (__ballot(id[b] == ls[j]) == 0) continue;
+                if (__ballot(id[b] == w.ls[j]) == 0) continue;
 #pragma unroll
                 for (int a = 0; a < TN; ++a) {
                     f32x16 d = {};
-                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[j][a], lo[j][b], d, 0, 0, 0);
-                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[j][a], hi[j][b], d, 0, 0, 0);
+                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.x[j][a], w.lo[j][b], d, 0, 0, 0);
+                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.x[j][a], w.hi[j][b], d, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[a][b][i] = id[b] == ls[j] ? acc[a][b][i] + sc[b] * d[i] : acc[a][b][i];
+                        acc[a][b][i] = id[b] == w.ls[j] ? acc[a][b][i] + sc[b] * d[i] : acc[a][b][i];
                 }
             }
         }
     }
 
-    // the batch in flight and all that follow it
-    __device__ __forceinline__ void finish(const Problem& p, f32x16 (&acc)[TN][TM])
+    // every item that is left, B at a time
+    template <int B>
+    __device__ __forceinline__ void rest(const Problem& p, f32x16 (&acc)[TN][TM])
     {
-        while (n > 0) {
-            apply(acc);
-            if (n < BATCH) break;
-            load(p);
-        }
+        Batch<B> w;
+        do {
+            load(p, w);
+            apply(w, acc);
+        } while (w.n == B);
     }
 };
 

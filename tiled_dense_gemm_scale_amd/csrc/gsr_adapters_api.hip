@@ -93,18 +93,18 @@ const Entry& stand_in(int id)
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // The shrink launch.  Up to kShrinkFewRows rows, a block of 16 spreads over
-// parts of at least kShrinkPart values of K, chunks of ranks and adapters;
-// blocks count arrivals in the counters at the workspace's start.  More rows
+// chunks of ranks, adapters and, while that makes fewer than kShrinkGrid
+// workgroups, parts of about kShrinkPart values of K; blocks count arrivals in the counters at the workspace's start.  More rows
 // take one workgroup per block and share of its adapters, as many shares as
 // the chip has room for.
-constexpr int64_t kShrinkFewRows = 64, kShrinkPart = 1024, kShrinkMaxParts = 16;
+constexpr int64_t kShrinkFewRows = 64, kShrinkPart = 1024, kShrinkMaxParts = 16, kShrinkGrid = 512;
 
 struct ShrinkPlan {
     int blocks, parts, kchunk;  // parts 0: all of K in one workgroup
     int slots;
 };
 
-ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t adapters)
+ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t adapters, int64_t rank)
 {
     ShrinkPlan s{(int)cdiv(M, gsr::kShrinkRows), 0, (int)K, 1};
     const int64_t most = std::min<int64_t>({M, adapters, gsr::kShrinkRows});
@@ -113,7 +113,9 @@ ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t adapters)
         return s;
     }
     s.slots = (int)most;
-    s.kchunk = (int)std::max<int64_t>(kShrinkPart, cdiv(cdiv(K, kShrinkMaxParts), 32) * 32);
+    const int64_t wgs = (int64_t)s.blocks * s.slots * cdiv(rank, gsr::kAdapterChunk);
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({kShrinkMaxParts, cdiv(K, kShrinkPart), kShrinkGrid / wgs}));
+    s.kchunk = (int)(cdiv(cdiv(K, parts), 32) * 32);
     s.parts = (int)cdiv(K, s.kchunk);
     return s;
 }
@@ -145,6 +147,7 @@ int64_t shrink_partial_bytes(const ShrinkPlan& s, int chunks)
 
 extern "C" {
 
+// (one adapter: the most parts)
 int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank)
 {
     if (M < 0 || N < 0 || K < 0 || rank < 0 || M >= kLimit || N >= kLimit || K >= kLimit || rank > kMaxRank) return -1;
@@ -152,7 +155,7 @@ int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ran
     const Entry& e = stand_in(dense_launch(M, N, K).id);
     const int64_t split = e.split ? dense_split(M, N, K, cdiv(M, e.bm) * cdiv(N, e.bn), e.bm, e.bn, 0).partial_bytes : 0;
     const Layout w = layout_of(M, rank);
-    return w.partial + std::max(split, shrink_partial_bytes(shrink_plan(M, K, 1), w.chunks));
+    return w.partial + std::max(split, shrink_partial_bytes(shrink_plan(M, K, 1, rank), w.chunks));
 }
 
 int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const void* bias,
@@ -220,7 +223,7 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     const int tiles = p.tiles_m * p.tiles_n;
 
     const Layout w = layout_of(M, rank);
-    const ShrinkPlan sp = shrink_plan(M, K, adapters);
+    const ShrinkPlan sp = shrink_plan(M, K, adapters, rank);
     if (workspace_bytes < w.partial + shrink_partial_bytes(sp, w.chunks)) return GSR_ERROR_INVALID_VALUE;
     Split split{1, K, 0};
     if (splits > 1 && e.split == nullptr) return GSR_ERROR_INVALID_CONFIG;

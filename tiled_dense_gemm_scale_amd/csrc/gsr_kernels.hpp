@@ -188,7 +188,7 @@ template <int CB, bool VEC, int FN, int FM>
 __device__ bool adapter_start16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0);
 template <int WTM, int WTN>
 __device__ void adapter_nonfinite16(const Problem& p, int m0, int n0);
-template <int TN, int TM, int BATCH>
+template <int TN, int TM>
 struct AdapterItems;
 
 // Eight outputs (16 bytes) at byte offset `off` of C, a multiple of 16 from
@@ -608,9 +608,8 @@ gemm_scale_relu_kernel(Problem p)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
     if constexpr (ADAPT != kAdaptNone) {
-        AdapterItems<TN, TM, 2> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
-        items.load(p);
-        items.finish(p, acc);
+        AdapterItems<TN, TM> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
+        items.template rest<TM == 1 ? 4 : 2>(p, acc);
     }
 
     const int ksteps = (p.K + BK - 1) / BK;

@@ -179,14 +179,17 @@ gemm_scale_relu_kspec_kernel(Problem p)
             for (int b = 0; b < TM; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-        // the adapters' first batch is in flight behind the product
-        using Items = AdapterItems<TN, TM, TM == 1 ? 4 : 2>;
+        // the adapters' first batch is in flight behind the product; the rest
+        // come in larger ones after it, when the operands' registers are free
+        constexpr int kFirst = TM == 1 ? 4 : 2, kRest = TM == 1 ? 8 : 5;
+        using Items = AdapterItems<TN, TM>;
         [[maybe_unused]] std::conditional_t<ADAPT != kAdaptNone, Items, int> items = [&] {
             if constexpr (ADAPT != kAdaptNone) return Items(p, m0, n0, wave, NW);
             else return 0;
         }();
+        [[maybe_unused]] typename Items::template Batch<kFirst> batch;
         if constexpr (ADAPT != kAdaptNone)
-            if (part == 0) items.load(p);
+            if (part == 0) items.load(p, batch);
 
         half8 xs0[2][TN], ys0[2][TM], xs1[2][TN], ys1[2][TM];
 #pragma unroll
@@ -238,7 +241,10 @@ gemm_scale_relu_kspec_kernel(Problem p)
         } else if (ksteps > 0) {
             mma_step(xs1, ys1);
         }
-        if constexpr (ADAPT != kAdaptNone) items.finish(p, acc);
+        if constexpr (ADAPT != kAdaptNone) {
+            items.apply(batch, acc);
+            if (batch.n == kFirst) items.template rest<kRest>(p, acc);
+        }
 
         Sum::load_bias(p, tid, n0, bvs);
         wait_vmcnt<0>();
