@@ -324,7 +324,8 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
  * own rows only, whatever they are.  rank is at most 256
  * (GSR_ERROR_TOO_LARGE); one adapter's La and Lb are below 2^31 bytes each
  * and the whole arrays may be larger.  adapters = 0 or rank = 0 is the product
- * alone.  Two kernels are enqueued.
+ * alone.  Two kernels are enqueued, or, for at most 64 rows, one whose first
+ * workgroups make the inner sums.
  *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its
  *              first 512 bytes zero before the first call and again after
  *              each), of gsr_adapter_workspace_bytes(M, N, K, rank) bytes;
@@ -332,13 +333,16 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
  *              does not fit
  *   config_id  -1, or one of 21, 22, 28, 31, 32; splits as
  *              gemm_scale_bias_act_ws's (at most 128 tiles split)
+ *   looks  how often a workgroup of the one-kernel form looks for inner sums
+ *          that are not there yet before it makes them itself, which gives
+ *          the same bits; -1: the library's number (for tests)
  * Otherwise as gemm_scale_bias_act_ws. */
 int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K,
                                  const void* A, const void* B, const void* bias, void* C,
                                  int64_t adapters, int64_t rank, const void* la, const void* lb,
                                  const int32_t* ids, const float* scales, float alpha, int32_t activation,
                                  void* workspace, int64_t workspace_bytes,
-                                 void* stream, int32_t config_id, int32_t splits);
+                                 void* stream, int32_t config_id, int32_t splits, int32_t looks);
 
 /* The bytes gemm_adapters_scale_bias_act needs (0: none); -1 for sizes it
  * rejects.  Host only. */

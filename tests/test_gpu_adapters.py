@@ -192,6 +192,40 @@ def test_forced_splits(gsr, config, splits):
         assert counters_zero(ws)
 
 
+@pytest.mark.parametrize("shape", [(1, 4096, 4096, 4, 64), (5, 200, 1032, 3, 16), (16, 1000, 2056, 16, 16),
+                                   (17, 136, 5000, 2, 40), (33, 512, 4096, 5, 16), (64, 264, 520, 8, 8),
+                                   (64, 72, 136, 2, 256)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("config", [21, 22])
+def test_inner_sums_that_are_not_there_yet(gsr, native, config, shape):
+    """The one-kernel form: a tile's workgroup that does not find the inner sums
+    (looks = 0: it never does; 1: hardly) makes them itself, with the same
+    bits, and the counters end at zero either way, call after call."""
+    M, N, K, L, R = shape
+    g = torch.Generator().manual_seed(M + K)
+    n = lambda std, *s: (torch.randn(*s, generator=g) * std).half().to(DEV)
+    a, b, la, lb = n(1.0, M, K), n(K ** -0.5, K, N), n(K ** -0.5, L, R, K), n(R ** -0.5, L, N, R)
+    bias, scales = n(1.0, N), torch.rand(L, generator=g).to(DEV) + 0.5
+    ids_host = ids_of("mixed", M, L, seed=K)
+    ids_host[0] = L - 1
+    ws = workspace(gsr, M, N, K, R, extra=4 << 20)
+    stream = torch.cuda.current_stream().cuda_stream
+    for splits in (0, 1, 3):
+        bits = {}
+        for ids_host in (ids_host, np.full(M, -1, np.int32)):
+            ids = torch.from_numpy(ids_host).to(DEV)
+            for looks in (-1, 0, 1, 0, -1):
+                c = torch.full((M, N), float("nan"), dtype=torch.float16, device=DEV)
+                say(f"adapters config={config} {shape} splits={splits} looks={looks}")
+                assert native.gemm_adapters_scale_bias_act(
+                    M, N, K, a.data_ptr(), b.data_ptr(), bias.data_ptr(), c.data_ptr(), L, R, la.data_ptr(), lb.data_ptr(),
+                    ids.data_ptr(), scales.data_ptr(), -0.75, 1, ws.data_ptr(), ws.numel(), stream, config, splits, looks) == 0
+                assert counters_zero(ws)
+                key = int(ids_host.max())
+                assert torch.equal(bits.setdefault(key, c).view(torch.int16), c.view(torch.int16))
+            ref, slack = reference(a.cpu(), b.cpu(), la.cpu(), lb.cpu(), ids_host, scales.cpu(), bias.cpu(), -0.75, "gelu")
+            within(f"splits {splits}", bits[key].cpu().double().numpy(), ref, slack)
+
+
 def test_one_workspace_for_all_entry_points(gsr):
     """Products with and without adapters in turn on one workspace."""
     shapes = [(1, 4096, 4096), (64, 4096, 4096), (16, 1000, 2056), (300, 264, 520)]

@@ -99,7 +99,7 @@ def lib() -> ctypes.CDLL:
             L.gemm_grouped_scale_bias_act.argtypes = [i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, f32, i32, vp, i32]
             L.gemm_grouped_scale_bias_act.restype = ctypes.c_int
             L.gemm_adapters_scale_bias_act.argtypes = [i64, i64, i64, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, f32, i32,
-                                                       vp, i64, vp, i32, i32]
+                                                       vp, i64, vp, i32, i32, i32]
             L.gemm_adapters_scale_bias_act.restype = ctypes.c_int
             L.gsr_adapter_workspace_bytes.argtypes = [i64, i64, i64, i64]
             L.gsr_adapter_workspace_bytes.restype = i64
@@ -239,13 +239,14 @@ def gemm_grouped_scale_bias_act(P: int, N: int, K: int, groups: int, A: int, a_r
 
 def gemm_adapters_scale_bias_act(M: int, N: int, K: int, A: int, B: int, bias: int, C: int, adapters: int, rank: int,
                                  la: int, lb: int, ids: int, scales: int, alpha: float, activation: int, workspace: int,
-                                 workspace_bytes: int, stream: int, config_id: int = -1, splits: int = 0) -> int:
+                                 workspace_bytes: int, stream: int, config_id: int = -1, splits: int = 0,
+                                 looks: int = -1) -> int:
     """Raw entry point of the product with low-rank adapters.  Returns the
     gsr_status."""
     return lib().gemm_adapters_scale_bias_act(M, N, K, A or None, B or None, bias or None, C or None, adapters, rank,
                                               la or None, lb or None, ids or None, scales or None, float(alpha),
                                               int(activation), workspace or None, int(workspace_bytes), stream or None,
-                                              int(config_id), int(splits))
+                                              int(config_id), int(splits), int(looks))
 
 
 def adapter_workspace_bytes(M: int, N: int, K: int, rank: int) -> int:

@@ -72,6 +72,11 @@ struct ShrinkArgs {
     int blocks;             // of 16 rows
     int parts, kchunk;      // K in parts of kchunk values (a multiple of 32)
     int slots;              // workgroups that share a block's adapters
+    // one launch for both steps (gsr_kspec.hpp): the blocks' records are there
+    // (flags), who is past looking (done), how often to look
+    uint32_t* flags;
+    uint32_t* done;
+    int looks;
 };
 
 constexpr int kShrinkRows = 16;  // rows per workgroup
@@ -92,8 +97,8 @@ __device__ __forceinline__ void for_each_adapter(int id, F&& f)
 
 // The sums of 16 rows over this workgroup's part of K for NB chunks of ranks
 // from chunk c0.  The W waves cut the part into runs of 32-value steps; a wave
-// walks the run of every slots-th adapter of the rows and leaves what it has in
-// sums[wave][row][rank].
+// walks its run of every slots-th adapter of the rows (from `slot` on) and
+// leaves what it has in sums[wave][row][rank].
 //
 // An MFMA operand has a row per lane, and a load in that layout touches 16
 // rows with every 16 lanes: it ran at 10-12 bytes per clock and CU.  The
@@ -123,7 +128,8 @@ template <int G>
 __device__ __forceinline__ int shrink_swz(int r) { return G == 16 ? (r & 15) : ((r >> 1) & 7); }
 
 template <bool VEC, class T>
-__device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, uint8_t* smem, int id, int m0, int c0, int kbeg, int kend, int slot)
+__device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, uint8_t* smem, int id, int m0, int c0, int kbeg, int kend, int slot,
+                                            int slots)
 {
     constexpr int NB = T::NB, W = T::W, G = T::G, STEPS = G / 4;
     const int lane = threadIdx.x & 63, lrow = lane & 15, lq = lane >> 4;
@@ -148,7 +154,7 @@ __device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, uint8_t* smem, 
             while (w.todo != 0) {
                 const int l = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)w.todo) - 1);
                 w.todo &= ~__ballot(id == l);
-                if (w.at++ % s.slots == slot) {
+                if (w.at++ % slots == slot) {
                     w.l = l;
                     return;
                 }
@@ -215,7 +221,7 @@ __device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, uint8_t* smem, 
         const bool ain = m0 + lrow < s.M;
         int at = 0;
         for_each_adapter(id, [&](int l) {
-            if (at++ % s.slots != slot) return;
+            if (at++ % slots != slot) return;
             const __amdgpu_buffer_rsrc_t rl = make_rsrc(s.la + (int64_t)l * s.rank * s.K, (uint32_t)s.rank * (uint32_t)s.K * 2u);
             f32x4 d[NB] = {};
             for (int ks = ks0; ks < ks1; ++ks) {
@@ -251,17 +257,20 @@ __device__ __forceinline__ float shrink_sum(const uint8_t* smem, int row, int q,
     return v;
 }
 
-// Writes row m's records: this thread holds ranks c + 16 j of the row for j in
-// v[], the 16 lanes around it the rest.
+// Writes the records of row `row` of t and t_scale: this thread holds ranks
+// c + 16 j of the row for j in v[], the 16 lanes around it the rest.  With
+// device-scope stores, for readers in the same launch.
 template <int N>
-__device__ __forceinline__ void shrink_store(const ShrinkArgs& s, int m, int l, int c, int j0, int stride, float (&v)[N], float big, bool odd)
+__device__ __forceinline__ void shrink_store(const ShrinkArgs& s, uint16_t* t, float* t_scale, int64_t row, int l, int c,
+                                             int j0, int stride, const float (&v)[N], float big)
 {
     if (l < 0) return;
+    const bool odd = !(big <= 3.0e38f);
     // 2^e <= big < 2^(e + 1); zeros, and rows with an infinity or a NaN, keep 2^0
     int e = 0;
     if (!odd && big > 0.0f) e = min(max(__builtin_amdgcn_frexp_expf(big) - 1, -40), 100);
     const float down = ldexpf(1.0f, -e);
-    if (c == 0 && j0 == 0) s.t_scale[m] = ldexpf(1.0f, e);
+    if (c == 0 && j0 == 0) __hip_atomic_store(t_scale + row, ldexpf(1.0f, e), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int j = j0 + i * stride;
@@ -269,9 +278,9 @@ __device__ __forceinline__ void shrink_store(const ShrinkArgs& s, int m, int l, 
         const float x = v[i] * down;
         const _Float16 hi = (_Float16)x;
         const _Float16 lo = odd ? (_Float16)0.0f : (_Float16)(x - (float)hi);
-        uint16_t* rec = s.t + ((int64_t)m * s.chunks + j) * 32;
-        rec[c] = __builtin_bit_cast(uint16_t, hi);
-        rec[16 + c] = __builtin_bit_cast(uint16_t, lo);
+        uint16_t* rec = t + (row * s.chunks + j) * 32;
+        __hip_atomic_store(rec + c, __builtin_bit_cast(uint16_t, hi), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(rec + 16 + c, __builtin_bit_cast(uint16_t, lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(512) adapter_shrink_rows_kernel(ShrinkArgs s)
         for (int j = 0; j < PER; ++j) v[i * PER + j] = 0.0f;
         if (i * NB >= s.chunks) continue;
         if (i > 0) __syncthreads();  // the sums of the chunks before have been read
-        shrink_sums<VEC, T>(s, smem, id, m0, i * NB, 0, s.K, blockIdx.z);
+        shrink_sums<VEC, T>(s, smem, id, m0, i * NB, 0, s.K, blockIdx.z, s.slots);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const int cq = q + QT * j;
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(512) adapter_shrink_rows_kernel(ShrinkArgs s)
         __syncthreads();
         big = fmaxf(bigs[0], bigs[1]);
     }
-    if (q < NB) shrink_store(s, m0 + row, l, c, q, QT, v, big, !(big <= 3.0e38f));
+    if (q < NB) shrink_store(s, s.t, s.t_scale, m0 + row, l, c, q, QT, v, big);
 }
 
 // Few rows (a decode step): the adapters' La is most of the bytes, so a block
@@ -337,70 +346,195 @@ __global__ void __launch_bounds__(512) adapter_shrink_rows_kernel(ShrinkArgs s)
 // block that arrives last adds the parts in part order and writes the records
 // (device-scope accesses and the arrival counter as in KsSum::split_sum_store,
 // so no order depends on timing and no workgroup waits).
-typedef ShrinkCfg<1, 4, 16, 2> ShrinkParts;
+typedef ShrinkCfg<1, 8, 8, 2> ShrinkParts;
 
-template <bool VEC>
-__global__ void __launch_bounds__(256) adapter_shrink_parts_kernel(ShrinkArgs s)
+// The finished row of a block: `at` gives the thread's rank c of chunk j summed
+// over the parts; scaled, with the row's largest value.
+template <int N, class F>
+__device__ __forceinline__ float shrink_row(const ShrinkArgs& s, int l, float (&v)[N], F&& at)
 {
-    using T = ShrinkParts;
-    constexpr int ROUNDS = kShrinkMaxRank / kAdapterChunk;
-    static_assert(T::W == 4 && T::NB == 1, "256 threads, one chunk");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
-    __shared__ int last;
-    const int tid = threadIdx.x;
-    const int block = blockIdx.x / s.parts, part = blockIdx.x - block * s.parts;
-    const int m0 = block * kShrinkRows;
-    const int id = adapter_of(s.ids, m0 + (tid & 15), s.M, s.adapters);
-    if (__ballot(id >= 0) == 0) return;  // in every workgroup of the block
-    const int row = tid >> 4, c = tid & 15;  // thread t: row t / 16, rank t % 16 of a chunk
-    const int l = adapter_of(s.ids, m0 + row, s.M, s.adapters);
-    // the adapter's place among the block's decides whose it is
-    bool mine = false;
-    int at = 0;
-    for_each_adapter(id, [&](int a) { mine |= at++ % s.slots == (int)blockIdx.z && l == a; });
     const float scale = (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
-
-    const int64_t stride = (int64_t)s.blocks * kShrinkRows * s.chunks * kAdapterChunk;  // one part
-    float* const at0 = s.partial + (int64_t)(m0 + row) * s.chunks * kAdapterChunk + c;
-    if (at > (int)blockIdx.z) {  // there is an adapter for this workgroup
-        const int kbeg = part * s.kchunk, kend = min(s.K, kbeg + s.kchunk);
-        shrink_sums<VEC, T>(s, smem, id, m0, blockIdx.y, kbeg, kend, blockIdx.z);
-        if (mine)
-            __hip_atomic_store(at0 + part * stride + blockIdx.y * kAdapterChunk, shrink_sum<T>(smem, row, 0, c),
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums have reached device scope
-        __syncthreads();
-    }
-    if (tid == 0) {
-        const uint32_t before = __hip_atomic_fetch_add(s.count + block, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        last = before == (uint32_t)(s.parts * gridDim.y * gridDim.z) - 1u;
-    }
-    __syncthreads();
-    if (!last) return;
-    if (tid == 0) __hip_atomic_store(s.count + block, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-
-    float v[ROUNDS], big = 0.0f;
+    float big = 0.0f;
     bool odd = false;
 #pragma unroll
-    for (int j = 0; j < ROUNDS; ++j) {
-        v[j] = 0.0f;
-        if (j >= s.chunks) continue;
-        for (int g = 0; g < s.parts; g += 8) {
-            float u[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)  // parts past the last read its sums again and add nothing
-                u[i] = __hip_atomic_load(at0 + min(g + i, s.parts - 1) * stride + j * kAdapterChunk, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j] += g + i < s.parts ? u[i] : 0.0f;
-        }
-        v[j] *= scale;
+    for (int j = 0; j < N; ++j) {
+        v[j] = j < s.chunks ? at(j) * scale : 0.0f;
         odd |= !(fabsf(v[j]) <= 3.0e38f);
         big = fmaxf(big, fabsf(v[j]));
     }
     big = odd ? __builtin_inff() : big;
 #pragma unroll
     for (int x = 8; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor(big, x));
-    shrink_store(s, m0 + row, l, c, 0, 1, v, big, !(big <= 3.0e38f));
+    return big;
+}
+
+constexpr int kShrinkRounds = kShrinkMaxRank / kAdapterChunk;
+
+// Workgroup `wg` of blocks x parts x chunks x slots, all 512 threads; true in
+// every thread of the one that wrote its block's records.
+template <bool VEC>
+__device__ __forceinline__ bool shrink_part(const ShrinkArgs& s, uint8_t* smem, int* last, int wg)
+{
+    using T = ShrinkParts;
+    static_assert(T::W == 8 && T::NB == 1, "512 threads, one chunk");
+    const int tid = threadIdx.x;
+    const int block = wg % s.blocks, part = wg / s.blocks % s.parts, chunk = wg / (s.blocks * s.parts) % s.chunks;
+    const int slot = wg / (s.blocks * s.parts * s.chunks);
+    const int m0 = block * kShrinkRows;
+    const int id = adapter_of(s.ids, m0 + (tid & 15), s.M, s.adapters);
+    if (__ballot(id >= 0) == 0) return false;  // in every workgroup of the block
+    const int row = (tid >> 4) & 15, c = tid & 15;  // threads 0..255: row t / 16, rank t % 16 of a chunk
+    const int l = tid < 256 ? adapter_of(s.ids, m0 + row, s.M, s.adapters) : -1;
+    // the adapter's place among the block's decides whose it is
+    bool mine = false;
+    int at = 0;
+    for_each_adapter(id, [&](int a) { mine |= at++ % s.slots == slot && l == a; });
+
+    const int64_t stride = (int64_t)s.blocks * kShrinkRows * s.chunks * kAdapterChunk;  // one part
+    float* const mine0 = s.partial + (int64_t)(m0 + row) * s.chunks * kAdapterChunk + c;
+    if (at > slot) {  // there is an adapter for this workgroup
+        const int kbeg = part * s.kchunk, kend = min(s.K, kbeg + s.kchunk);
+        shrink_sums<VEC, T>(s, smem, id, m0, chunk, kbeg, kend, slot, s.slots);
+        if (mine)
+            __hip_atomic_store(mine0 + part * stride + chunk * kAdapterChunk, shrink_sum<T>(smem, row, 0, c),
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums have reached device scope
+        __syncthreads();
+    }
+    if (tid == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(s.count + block, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *last = before == (uint32_t)(s.parts * s.chunks * s.slots) - 1u;
+    }
+    __syncthreads();
+    if (!__builtin_amdgcn_readfirstlane(*last)) return false;
+    if (tid == 0) __hip_atomic_store(s.count + block, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (tid < 256) {
+        float v[kShrinkRounds];
+        const float big = shrink_row(s, l, v, [&](int j) {
+            float sum = 0.0f;
+            for (int g = 0; g < s.parts; g += 8) {
+                float u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)  // parts past the last read its sums again and add nothing
+                    u[i] = __hip_atomic_load(mine0 + min(g + i, s.parts - 1) * stride + j * kAdapterChunk, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += g + i < s.parts ? u[i] : 0.0f;
+            }
+            return sum;
+        });
+        shrink_store(s, s.t, s.t_scale, m0 + row, l, c, 0, 1, v, big);
+    }
+    return true;
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(512) adapter_shrink_parts_kernel(ShrinkArgs s)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[ShrinkParts::LDS_BYTES];
+    __shared__ int last;
+    shrink_part<VEC>(s, smem, &last, blockIdx.x);
+}
+
+// ---- both steps in one launch (few rows) -------------------------------------------
+// The workgroups of step 1 come first in the grid; a tile's workgroup needs
+// their records only after its loop over K, when they have usually been there
+// for long.  It looks for them a limited number of times and, not having found
+// them, makes them itself in LDS, with the same sums in the same order: no
+// workgroup depends on another one's running, and the bits are the same either
+// way.  A block's records are announced by its flag.  Who writes a flag, and
+// every workgroup that is past looking, counts in `done`; the last of them all
+// puts flags and count back to zero.
+//
+// Bit b: block b (of at most four, M <= 64) has rows with an adapter.
+__device__ __forceinline__ uint32_t active_blocks(const ShrinkArgs& s)
+{
+    const uint64_t rows = __ballot(adapter_of(s.ids, threadIdx.x & 63, s.M, s.adapters) >= 0);
+    uint32_t m = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) m |= ((rows >> (16 * b)) & 0xffffull) ? 1u << b : 0u;
+    return m;
+}
+
+// One arrival at `done`; the last of tiles + active blocks clears.  One lane.
+__device__ __forceinline__ void shrink_done(const ShrinkArgs& s, int tiles, uint32_t active)
+{
+    const uint32_t before = __hip_atomic_fetch_add(s.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (before != (uint32_t)(tiles + __popc(active)) - 1u) return;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) __hip_atomic_store(s.flags + b, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(s.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// A workgroup of step 1 in the common grid.
+template <bool VEC>
+__device__ __forceinline__ void shrink_announce(const ShrinkArgs& s, uint8_t* smem, int* last, int wg, int tiles)
+{
+    if (!shrink_part<VEC>(s, smem, last, wg)) return;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's records have reached device scope
+    __syncthreads();
+    const uint32_t active = active_blocks(s);
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(s.flags + wg % s.blocks, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        shrink_done(s, tiles, active);
+    }
+}
+
+// One wave of a tile's workgroup, whose rows lie in the blocks of `want`: looks
+// until their records are there, at most s.looks times.  True: they are.
+__device__ __forceinline__ bool shrink_look(const ShrinkArgs& s, uint32_t want, uint32_t active, int tiles)
+{
+    const int lane = threadIdx.x & 63;
+    const bool ask = lane < 4 && (want & active) >> lane & 1u;
+    bool there = __ballot(ask) == 0;
+    for (int i = 0; i < s.looks && !there; ++i) {
+        const uint32_t f = ask ? __hip_atomic_load(s.flags + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1u;
+        there = __ballot(f == 0u) == 0;
+    }
+    if (lane == 0) shrink_done(s, tiles, active);
+    return there;
+}
+
+// The records of rows m0 .. m0 + rows - 1 (a multiple of 16 of them) made by
+// the tile's own workgroup of 512 threads, into t and t_scale in LDS behind the
+// ShrinkParts::LDS_BYTES that the sums take.
+template <bool VEC>
+__device__ __forceinline__ void shrink_here(const ShrinkArgs& s, uint8_t* smem, uint16_t* t, float* t_scale, int m0, int rows)
+{
+    using T = ShrinkParts;
+    const int tid = threadIdx.x, row = (tid >> 4) & 15, c = tid & 15;
+    for (int b0 = 0; b0 < rows; b0 += kShrinkRows) {
+        const int id = adapter_of(s.ids, m0 + b0 + (tid & 15), s.M, s.adapters);
+        if (__ballot(id >= 0) == 0) continue;
+        const int l = tid < 256 ? adapter_of(s.ids, m0 + b0 + row, s.M, s.adapters) : -1;
+        const float scale = (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
+        // the row's fp32 values wait in the place of its records
+        uint8_t* const wait = (uint8_t*)(t + (int64_t)(b0 + row) * s.chunks * 32) + 4 * c;
+        float big = 0.0f;
+        bool odd = false;
+        for (int j = 0; j < s.chunks; ++j) {
+            float v[1] = {0.0f};
+            for (int g = 0; g < s.parts; ++g) {
+                __syncthreads();  // the sums before have been read
+                shrink_sums<VEC, T>(s, smem, id, m0 + b0, j, g * s.kchunk, min(s.K, (g + 1) * s.kchunk), 0, 1);
+                v[0] += shrink_sum<T>(smem, row, 0, c);
+            }
+            v[0] *= scale;
+            odd |= !(fabsf(v[0]) <= 3.0e38f);
+            big = fmaxf(big, fabsf(v[0]));
+            if (tid < 256) *(volatile float*)(wait + 64 * j) = v[0];
+        }
+        big = odd ? __builtin_inff() : big;
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor(big, x));
+        if (tid < 256)
+            for (int j = 0; j < s.chunks; ++j) {
+                const float v[1] = {*(volatile float*)(wait + 64 * j)};  // the row's 16 lanes read before one writes
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                shrink_store(s, t, t_scale, b0 + row, l, c, j, 1, v, big);
+            }
+    }
+    __syncthreads();
 }
 
 // ---- step 2 ---------------------------------------------------------------------
@@ -582,29 +716,53 @@ __device__ __forceinline__ void adapter_nonfinite16(const Problem& p, int m0, in
 // first + stride, ... (waves that each hold a share of the sum share them
 // out) in batches whose loads are in flight together: load() requests one,
 // apply() adds it, so one can be in flight behind the product.
-template <int TN, int TM>
+//
+// SHARED: the records come from workgroups of the same launch (device-scope
+// loads) or from LDS, and are there only once records() has been told where;
+// until then a batch holds Lb's side alone.
+template <int TN, int TM, bool SHARED>
 struct AdapterItems {
     int m0, n0, first, stride;
+    const uint16_t* t;        // records, of the problem's rows from row t_row on
+    const float* t_scale;
+    int t_row;
     int id[TM], todo = 0;
     float sc[TM];             // the rows' scales
     int item = 0, l = -1, c;  // the next item: adapter l's chunk c
 
     template <int B>
     struct Batch {
-        int n = 0, ls[B];  // its size and its adapters
+        int n = 0, ls[B], ch[B];  // its size, its adapters and their chunks
         half8 x[B][TN], hi[B][TM], lo[B][TM];
     };
 
     __device__ __forceinline__ AdapterItems(const Problem& p, int m0_, int n0_, int first_, int stride_)
-        : m0(m0_), n0(n0_), first(first_), stride(stride_), c(p.chunks)
+        : m0(m0_), n0(n0_), first(first_), stride(stride_), t(p.t), t_scale(p.t_scale), t_row(0), c(p.chunks)
     {
 #pragma unroll
         for (int b = 0; b < TM; ++b) {
-            const int m = m0 + 32 * b + (int)(threadIdx.x & 31);
-            id[b] = adapter_of(p.ids, m, p.M, p.adapters);
-            sc[b] = id[b] >= 0 ? p.t_scale[m] : 0.0f;
+            id[b] = adapter_of(p.ids, row_of(b), p.M, p.adapters);
             todo |= (id[b] >= 0 ? 1 : 0) << b;
         }
+        if constexpr (!SHARED) scales();
+    }
+
+    __device__ __forceinline__ int row_of(int b) const { return m0 + 32 * b + (int)(threadIdx.x & 31); }
+
+    __device__ __forceinline__ void scales()
+    {
+#pragma unroll
+        for (int b = 0; b < TM; ++b) {
+            const float* at = t_scale + (id[b] >= 0 ? row_of(b) - t_row : 0);
+            sc[b] = SHARED ? __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : *at;
+        }
+    }
+
+    // SHARED: the records, and where the first of them belongs
+    __device__ __forceinline__ void records(const uint16_t* t_, const float* t_scale_, int t_row_)
+    {
+        t = t_, t_scale = t_scale_, t_row = t_row_;
+        scales();
     }
 
     // the wave's next item, or false
@@ -632,31 +790,55 @@ struct AdapterItems {
         }
     }
 
+    // the next batch's adapters and Lb
     template <int B>
-    __device__ __forceinline__ void load(const Problem& p, Batch<B>& w)
+    __device__ __forceinline__ void load_lb(const Problem& p, Batch<B>& w)
     {
         const int lane = threadIdx.x & 63, frow = lane & 31, fhi = lane >> 5;
         w.n = 0;
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-            int ch = 0;
-            w.ls[j] = -1;
-            if (w.n == j && next(p, w.ls[j], ch)) ++w.n;
+            w.ls[j] = -1, w.ch[j] = 0;
+            if (w.n == j && next(p, w.ls[j], w.ch[j])) ++w.n;
             if (w.n <= j) continue;
             const __amdgpu_buffer_rsrc_t rl = lb_rsrc(p, w.ls[j]);
 #pragma unroll
-            for (int a = 0; a < TN; ++a) w.x[j][a] = lb_piece(p, rl, n0 + 32 * a + frow, kAdapterChunk * ch + 8 * fhi);
+            for (int a = 0; a < TN; ++a) w.x[j][a] = lb_piece(p, rl, n0 + 32 * a + frow, kAdapterChunk * w.ch[j] + 8 * fhi);
+        }
+    }
+
+    __device__ __forceinline__ half8 piece(const uint16_t* at) const
+    {
+        if constexpr (SHARED) {
+            const uint64_t* q = (const uint64_t*)at;
+            const uint64_t u = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const uint64_t v = __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            return __builtin_bit_cast(half8, u32x4{(uint32_t)u, (uint32_t)(u >> 32), (uint32_t)v, (uint32_t)(v >> 32)});
+        } else {
+            return __builtin_bit_cast(half8, *(const u32x4*)at);
+        }
+    }
+
+    // its records (rows without an adapter read some other row's, or what lies there)
+    template <int B>
+    __device__ __forceinline__ void load_t(const Problem& p, Batch<B>& w) const
+    {
+        const int fhi = (threadIdx.x >> 5) & 1;
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            if (w.n <= j) break;
 #pragma unroll
             for (int b = 0; b < TM; ++b) {
-                const int64_t rec = (int64_t)min(m0 + 32 * b + frow, p.M - 1) * p.chunks + ch;
-                w.hi[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 8 * fhi));
-                w.lo[j][b] = __builtin_bit_cast(half8, *(const u32x4*)(p.t + rec * 32 + 16 + 8 * fhi));
+                const int r = id[b] >= 0 ? row_of(b) - t_row : 0;
+                const uint16_t* rec = t + ((int64_t)r * p.chunks + w.ch[j]) * 32 + 8 * fhi;
+                w.hi[j][b] = piece(rec);
+                w.lo[j][b] = piece(rec + 16);
             }
         }
     }
 
     template <int B>
-    __device__ __forceinline__ void apply(const Batch<B>& w, f32x16 (&acc)[TN][TM])
+    __device__ __forceinline__ void apply(const Batch<B>& w, f32x16 (&acc)[TN][TM]) const
     {
 #pragma unroll
         for (int j = 0; j < B; ++j) {
@@ -683,7 +865,8 @@ struct AdapterItems {
     {
         Batch<B> w;
         do {
-            load(p, w);
+            load_lb(p, w);
+            load_t(p, w);
             apply(w, acc);
         } while (w.n == B);
     }

@@ -47,6 +47,12 @@ hipError_t launch_kspec(const Problem& p, int grid, hipStream_t s)
     return launch_kernel((gsr::gemm_scale_relu_kspec_kernel<BM, BN, S, D, SPLIT, false, gsr::kAdaptVec>), dim3(grid), dim3(512), s, p);
 }
 
+template <int BM, int BN, int S, int D>
+hipError_t launch_shared(const Problem& p, const ShrinkArgs& a, int makers, int grid, hipStream_t s)
+{
+    return launch_kernel((gsr::gemm_adapters_kspec_kernel<BM, BN, S, D>), dim3(grid), dim3(512), s, p, a, makers);
+}
+
 template <int BM, int BN>
 hipError_t launch_staged(const Problem& p, int grid, hipStream_t s)
 {
@@ -58,15 +64,16 @@ struct Entry {
     int id;
     int bm, bn;
     launch_fn vec, split;
+    hipError_t (*shared)(const Problem&, const ShrinkArgs&, int makers, int grid, hipStream_t);  // both steps, or null
     int elem_bm, elem_bn;
     launch_fn elem;
 };
 const Entry kTable[] = {
-    {21, 64, 64, launch_kspec<64, 64, 4, 2, false>, launch_kspec<64, 64, 4, 2, true>, 64, 64, launch_staged<64, 64>},
-    {22, 32, 64, launch_kspec<32, 64, 4, 2, false>, launch_kspec<32, 64, 4, 2, true>, 64, 64, launch_staged<64, 64>},
-    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, nullptr, 128, 128, launch_staged<128, 128>},
-    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, nullptr, 128, 128, launch_staged<128, 128>},
-    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, nullptr, 128, 128, launch_staged<128, 128>},
+    {21, 64, 64, launch_kspec<64, 64, 4, 2, false>, launch_kspec<64, 64, 4, 2, true>, launch_shared<64, 64, 4, 2>, 64, 64, launch_staged<64, 64>},
+    {22, 32, 64, launch_kspec<32, 64, 4, 2, false>, launch_kspec<32, 64, 4, 2, true>, launch_shared<32, 64, 4, 2>, 64, 64, launch_staged<64, 64>},
+    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, nullptr, nullptr, 128, 128, launch_staged<128, 128>},
+    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, nullptr, nullptr, 128, 128, launch_staged<128, 128>},
+    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, nullptr, nullptr, 128, 128, launch_staged<128, 128>},
 };
 
 const Entry* entry_of(int id)
@@ -120,49 +127,51 @@ ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t adapters, int64_t rank)
     return s;
 }
 
-// The workspace: counters, the records of t, the rows' scales, then the
-// partial sums of the shrink launch, whose place those of the product's K
-// split take when it has ended.
+// Few rows on a copy-wave K-split tile: both steps in one launch, if the
+// workgroups that make the inner sums are few enough to run beside the tiles'
+// (the launch holds one workgroup per CU).
+constexpr int kSharedMakers = 128, kSharedLooks = 64;
+// its counters, behind those of a K split of at most 64 tiles: arrivals per
+// block, flags per block, done
+constexpr int kSharedCounters = 64, kSharedFlags = 68, kSharedDone = 72;
+
+// The workspace: counters, the records of t, the rows' scales, the partial
+// sums of step 1, those of the product's K split.
 struct Layout {
     int chunks;
-    int64_t t, t_scale, partial;
+    int64_t t, t_scale, partial, split;
 };
 
-Layout layout_of(int64_t M, int64_t rank)
+Layout layout_of(int64_t M, int64_t K, int64_t rank)
 {
     Layout w;
     w.chunks = (int)cdiv(rank, gsr::kAdapterChunk);
     w.t = kCounterBytes;
     w.t_scale = w.t + round256(M * w.chunks * 64);
     w.partial = w.t_scale + round256(M * 4);
+    const ShrinkPlan s = shrink_plan(M, K, 1, rank);  // one adapter: the most parts
+    w.split = w.partial + round256((int64_t)s.parts * s.blocks * gsr::kShrinkRows * w.chunks * gsr::kAdapterChunk * 4);
     return w;
-}
-
-int64_t shrink_partial_bytes(const ShrinkPlan& s, int chunks)
-{
-    return (int64_t)s.parts * s.blocks * gsr::kShrinkRows * chunks * gsr::kAdapterChunk * 4;
 }
 
 }  // namespace
 
 extern "C" {
 
-// (one adapter: the most parts)
 int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank)
 {
     if (M < 0 || N < 0 || K < 0 || rank < 0 || M >= kLimit || N >= kLimit || K >= kLimit || rank > kMaxRank) return -1;
     if (M == 0 || N == 0 || K == 0 || rank == 0) return 0;
     const Entry& e = stand_in(dense_launch(M, N, K).id);
     const int64_t split = e.split ? dense_split(M, N, K, cdiv(M, e.bm) * cdiv(N, e.bn), e.bm, e.bn, 0).partial_bytes : 0;
-    const Layout w = layout_of(M, rank);
-    return w.partial + std::max(split, shrink_partial_bytes(shrink_plan(M, K, 1, rank), w.chunks));
+    return layout_of(M, K, rank).split + split;
 }
 
 int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const void* bias,
                                  void* C, int64_t adapters, int64_t rank, const void* la, const void* lb,
                                  const int32_t* ids, const float* scales, float alpha, int32_t activation,
                                  void* workspace, int64_t workspace_bytes, void* stream, int32_t config_id,
-                                 int32_t splits)
+                                 int32_t splits, int32_t looks)
 {
     if (config_id < -1 || (config_id >= 0 && entry_of(config_id) == nullptr)) return GSR_ERROR_INVALID_CONFIG;
     if (M < 0 || N < 0 || K < 0 || adapters < 0 || rank < 0 || splits < 0 || splits > kSplitMaxParts || workspace_bytes < 0)
@@ -222,18 +231,25 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     p.tiles_n = (int)cdiv(N, vec ? e.bn : e.elem_bn);
     const int tiles = p.tiles_m * p.tiles_n;
 
-    const Layout w = layout_of(M, rank);
-    const ShrinkPlan sp = shrink_plan(M, K, adapters, rank);
-    if (workspace_bytes < w.partial + shrink_partial_bytes(sp, w.chunks)) return GSR_ERROR_INVALID_VALUE;
+    const Layout w = layout_of(M, K, rank);
+    if (workspace_bytes < w.split) return GSR_ERROR_INVALID_VALUE;
     Split split{1, K, 0};
     if (splits > 1 && e.split == nullptr) return GSR_ERROR_INVALID_CONFIG;
     if (vec && e.split != nullptr) {
         split = dense_split(M, N, K, tiles, e.bm, e.bn, splits);
-        if (split.parts > 1 && (tiles > kSplitCounters || workspace_bytes < w.partial + split.partial_bytes)) {
+        if (split.parts > 1 && (tiles > kSplitCounters || workspace_bytes < w.split + split.partial_bytes)) {
             if (splits > 1) return GSR_ERROR_INVALID_VALUE;
             split = Split{1, K, 0};
         }
     }
+    const ShrinkPlan sp = shrink_plan(M, K, adapters, rank);
+    const int makers = sp.blocks * std::max(sp.parts, 1) * w.chunks * sp.slots;
+    const bool shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
+    const bool shared = sp.parts > 0 && vec && e.shared != nullptr && shrink_vec && makers <= kSharedMakers &&
+                        (split.parts == 1 || tiles <= kSharedCounters);
+    // a split leaves the makers their CUs
+    while (shared && splits == 0 && split.parts > 1 && tiles * split.parts + makers > 256)
+        split = dense_split(M, N, K, tiles, e.bm, e.bn, split.parts - 1);
     const int st = check_device();
     if (st != GSR_SUCCESS) return st;
 
@@ -251,27 +267,14 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     a.rank = (int)rank;
     a.chunks = w.chunks;
     a.partial = (float*)(ws + w.partial);
-    a.count = (uint32_t*)ws;
+    a.count = (uint32_t*)ws + (shared ? kSharedCounters : 0);
     a.blocks = sp.blocks;
     a.parts = sp.parts;
     a.kchunk = sp.kchunk;
     a.slots = sp.slots;
-    const bool shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
-    hipStream_t s = (hipStream_t)stream;
-    hipError_t err;
-    if (sp.parts > 0)
-        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_parts_kernel<true> : gsr::adapter_shrink_parts_kernel<false>,
-                            dim3((unsigned)(sp.blocks * sp.parts), (unsigned)w.chunks, (unsigned)a.slots), dim3(256), s, a);
-    else if (w.chunks == 1)
-        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, gsr::ShrinkRows1>
-                                       : gsr::adapter_shrink_rows_kernel<false, gsr::ShrinkRows1>,
-                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
-    else
-        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, gsr::ShrinkRows4>
-                                       : gsr::adapter_shrink_rows_kernel<false, gsr::ShrinkRows4>,
-                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
-    if (err != hipSuccess) return GSR_ERROR_LAUNCH;
-
+    a.flags = (uint32_t*)ws + kSharedFlags;
+    a.done = (uint32_t*)ws + kSharedDone;
+    a.looks = looks < 0 ? kSharedLooks : looks;
     p.ids = ids;
     p.t = a.t;
     p.t_scale = a.t_scale;
@@ -284,11 +287,26 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
         p.ksplit = split.parts;
         p.kchunk = (int)split.kchunk;
         p.ws_count = (uint32_t*)ws;
-        p.ws_part = (float*)(ws + w.partial);
-        err = e.split(p, tiles * split.parts, s);
-    } else {
-        err = (vec ? e.vec : e.elem)(p, tiles, s);
+        p.ws_part = (float*)(ws + w.split);
     }
+    hipStream_t s = (hipStream_t)stream;
+    if (shared)
+        return e.shared(p, a, makers, makers + tiles * split.parts, s) == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+    hipError_t err;
+    if (sp.parts > 0)
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_parts_kernel<true> : gsr::adapter_shrink_parts_kernel<false>,
+                            dim3((unsigned)makers), dim3(512), s, a);
+    else if (w.chunks == 1)
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, gsr::ShrinkRows1>
+                                       : gsr::adapter_shrink_rows_kernel<false, gsr::ShrinkRows1>,
+                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
+    else
+        err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, gsr::ShrinkRows4>
+                                       : gsr::adapter_shrink_rows_kernel<false, gsr::ShrinkRows4>,
+                            dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
+    if (err != hipSuccess) return GSR_ERROR_LAUNCH;
+    if (split.parts > 1) err = e.split(p, tiles * split.parts, s);
+    else err = (vec ? e.vec : e.elem)(p, tiles, s);
     return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
 }
 

@@ -181,14 +181,16 @@ struct Problem {
 // ADAPT of the kernels: without adapters, with Lb read in 16-byte units
 // (lb_vec), with Lb read value by value.  The tiles whose accumulators fill
 // the registers have a form of their own for each; the others look at lb_vec.
-enum : int { kAdaptNone = 0, kAdaptVec = 1, kAdaptElem = 2 };
+// kAdaptShared: the launch also holds the workgroups that make the inner sums
+// (the copy-wave K-split tiles).
+enum : int { kAdaptNone = 0, kAdaptVec = 1, kAdaptElem = 2, kAdaptShared = 3 };
 
 // gsr_adapters.hpp
 template <int CB, bool VEC, int FN, int FM>
 __device__ bool adapter_start16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0);
 template <int WTM, int WTN>
 __device__ void adapter_nonfinite16(const Problem& p, int m0, int n0);
-template <int TN, int TM>
+template <int TN, int TM, bool SHARED>
 struct AdapterItems;
 
 // Eight outputs (16 bytes) at byte offset `off` of C, a multiple of 16 from
@@ -608,7 +610,7 @@ gemm_scale_relu_kernel(Problem p)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
     if constexpr (ADAPT != kAdaptNone) {
-        AdapterItems<TN, TM> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
+        AdapterItems<TN, TM, false> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
         items.template rest<TM == 1 ? 4 : 2>(p, acc);
     }
 

@@ -43,15 +43,26 @@
 
 namespace gsr {
 
-template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED = false, int ADAPT = kAdaptNone>
-__global__ void __launch_bounds__(512)
-gemm_scale_relu_kspec_kernel(Problem p)
+
+// LDS of a launch that also makes the inner sums: the operand ring, whose place
+// records of up to kShrinkMaxRank ranks take that a tile makes itself.
+template <int BM, int BN, int STAGES>
+constexpr int kspec_shared_lds()
+{
+    constexpr int ring = KsCfg<BM, BN, STAGES>::LDS_BYTES, own = ShrinkParts::LDS_BYTES + BM * 4 + BM * kShrinkRounds * 64;
+    return ring > own ? ring : own;
+}
+
+// One tile: workgroup `wg` of `nwg`.  kAdaptShared: `shrink` makes the inner
+// sums, `found` is an LDS word for what the looking wave found.
+struct NoShrink {};
+template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED, int ADAPT, class S>
+__device__ __forceinline__ void kspec_tile(Problem p, uint8_t* smem, int* last, int wg, int nwg,
+                                           [[maybe_unused]] S shrink, [[maybe_unused]] int* found)
 {
     using T = KsCfg<BM, BN, STAGES>;
     constexpr int BK = T::BK, NW = T::NW, CHA = T::CHA, CHN = T::CHN, TM = T::TM, TN = T::TN;
     static_assert(DEPTH >= 1 && DEPTH <= STAGES - 1, "steps in flight");
-
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS_BYTES];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -61,11 +72,11 @@ gemm_scale_relu_kspec_kernel(Problem p)
 
     // SPLIT: workgroup id = part * tiles + tile; part j covers K values
     // [j * kchunk, min(K, (j + 1) * kchunk))
-    int tile = blockIdx.x, part = 0, kbeg = 0, kend = p.K;
+    int tile = wg, part = 0, kbeg = 0, kend = p.K;
     if constexpr (SPLIT) {
         const int tiles = p.tiles_m * p.tiles_n;
-        part = blockIdx.x / tiles;
-        tile = blockIdx.x - part * tiles;
+        part = wg / tiles;
+        tile = wg - part * tiles;
         kbeg = part * p.kchunk;
         kend = min(p.K, kbeg + p.kchunk);
     }
@@ -74,7 +85,7 @@ gemm_scale_relu_kspec_kernel(Problem p)
         if (!group_tile<BM, BN>(p, n0)) return;
     } else {
         int tm, tn;
-        tile_of(tile, SPLIT ? p.tiles_m * p.tiles_n : (int)gridDim.x, p, tm, tn);
+        tile_of(tile, SPLIT ? p.tiles_m * p.tiles_n : nwg, p, tm, tn);
         m0 = tm * BM, n0 = tn * BN;
     }
     const int ksteps = (kend - kbeg + BK - 1) / BK;
@@ -82,6 +93,15 @@ gemm_scale_relu_kspec_kernel(Problem p)
     using Sum = KsSum<BM, BN, NW, 512>;  // the cross-wave sum runs on all eight waves
     static_assert(Sum::BYTES <= T::LDS_BYTES, "partial tiles fit in LDS");
     f32x4 bvs[Sum::NU][2];
+    // the records that were not there in time, by all eight waves
+    constexpr int kRecords = ShrinkParts::LDS_BYTES;  // their place in LDS, the rows' scales in front
+    [[maybe_unused]] auto make_records = [&]() __attribute__((always_inline)) {
+        if constexpr (ADAPT == kAdaptShared) {
+            static_assert(kRecords + BM * 4 + BM * kShrinkRounds * 64 <= kspec_shared_lds<BM, BN, STAGES>(), "records of every rank fit");
+            if (!__builtin_amdgcn_readfirstlane(*found))
+                shrink_here<true>(shrink, smem, (uint16_t*)(smem + kRecords + BM * 4), (float*)(smem + kRecords), m0, BM);
+        }
+    };
 
     if (copier) {
         // ---- copy waves ----------------------------------------------------------
@@ -145,6 +165,18 @@ gemm_scale_relu_kspec_kernel(Problem p)
         }
         Sum::load_bias(p, tid, n0, bvs);
         wait_vmcnt<0>();
+        if constexpr (ADAPT == kAdaptShared) {
+            if (part == 0) {
+                if (wave == NW - 1) {
+                    const uint32_t want = ((1u << (BM / 16)) - 1u) << (m0 / 16), active = active_blocks(shrink);
+                    // without any adapter nobody looks and nobody counts
+                    const bool there = active == 0 || shrink_look(shrink, want, active, p.tiles_m * p.tiles_n);
+                    if (lane == 0) *found = there;
+                }
+                lds_barrier();  // every wave is done with the operand buffers
+                make_records();
+            }
+        }
         lds_barrier();  // the MFMA waves' partial tiles may now overwrite the buffers
     } else {
         // ---- MFMA waves ---------------------------------------------------------------
@@ -182,14 +214,18 @@ gemm_scale_relu_kspec_kernel(Problem p)
         // the adapters' first batch is in flight behind the product; the rest
         // come in larger ones after it, when the operands' registers are free
         constexpr int kFirst = TM == 1 ? 4 : 2, kRest = TM == 1 ? 8 : 5;
-        using Items = AdapterItems<TN, TM>;
+        using Items = AdapterItems<TN, TM, ADAPT == kAdaptShared>;
         [[maybe_unused]] std::conditional_t<ADAPT != kAdaptNone, Items, int> items = [&] {
             if constexpr (ADAPT != kAdaptNone) return Items(p, m0, n0, wave, NW);
             else return 0;
         }();
         [[maybe_unused]] typename Items::template Batch<kFirst> batch;
-        if constexpr (ADAPT != kAdaptNone)
-            if (part == 0) items.load(p, batch);
+        if constexpr (ADAPT != kAdaptNone) {
+            if (part == 0) {
+                items.load_lb(p, batch);
+                if constexpr (ADAPT != kAdaptShared) items.load_t(p, batch);
+            }
+        }
 
         half8 xs0[2][TN], ys0[2][TM], xs1[2][TN], ys1[2][TM];
 #pragma unroll
@@ -241,6 +277,15 @@ gemm_scale_relu_kspec_kernel(Problem p)
         } else if (ksteps > 0) {
             mma_step(xs1, ys1);
         }
+        if constexpr (ADAPT == kAdaptShared) {
+            if (part == 0) {
+                lds_barrier();  // every wave is done with the operand buffers
+                make_records();
+                if (__builtin_amdgcn_readfirstlane(*found)) items.records(p.t, p.t_scale, 0);
+                else items.records((const uint16_t*)(smem + kRecords + BM * 4), (const float*)(smem + kRecords), m0);
+                items.load_t(p, batch);
+            }
+        }
         if constexpr (ADAPT != kAdaptNone) {
             items.apply(batch, acc);
             if (batch.n == kFirst) items.template rest<kRest>(p, acc);
@@ -255,13 +300,41 @@ gemm_scale_relu_kspec_kernel(Problem p)
 
     // ---- every wave: sum, epilogue, one 16-byte store per unit --------------------
     if constexpr (SPLIT) {
-        __shared__ int last;
         if (p.ksplit > 1) {
-            Sum::split_sum_store(p, smem, &last, tid, m0, n0, bvs, tile, part);
+            Sum::split_sum_store(p, smem, last, tid, m0, n0, bvs, tile, part);
             return;
         }
     }
     Sum::sum_store(p, smem, tid, m0, n0, bvs);
+}
+
+template <int BM, int BN, int STAGES, int DEPTH, bool SPLIT, bool GROUPED = false, int ADAPT = kAdaptNone>
+__global__ void __launch_bounds__(512) gemm_scale_relu_kspec_kernel(Problem p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[KsCfg<BM, BN, STAGES>::LDS_BYTES];
+    if constexpr (SPLIT) {
+        __shared__ int last;
+        kspec_tile<BM, BN, STAGES, DEPTH, SPLIT, GROUPED, ADAPT>(p, smem, &last, blockIdx.x, gridDim.x, NoShrink{}, nullptr);
+    } else {
+        kspec_tile<BM, BN, STAGES, DEPTH, SPLIT, GROUPED, ADAPT>(p, smem, nullptr, blockIdx.x, gridDim.x, NoShrink{}, nullptr);
+    }
+}
+
+// With adapters of at most 64 rows in one launch: `makers` workgroups that make
+// the inner sums, then the tiles' (K split over p.ksplit parts, or one).
+template <int BM, int BN, int STAGES, int DEPTH>
+__global__ void __launch_bounds__(512) gemm_adapters_kspec_kernel(Problem p, ShrinkArgs s, int makers)
+{
+    constexpr int kLds = kspec_shared_lds<BM, BN, STAGES>();
+    static_assert(kLds <= 163840, "LDS budget of one workgroup on gfx950");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds];
+    __shared__ int last, found;
+    const int tiles = p.tiles_m * p.tiles_n;
+    if ((int)blockIdx.x < makers) {
+        shrink_announce<true>(s, smem, &last, blockIdx.x, tiles);
+        return;
+    }
+    kspec_tile<BM, BN, STAGES, DEPTH, true, false, kAdaptShared>(p, smem, &last, (int)blockIdx.x - makers, tiles, s, &found);
 }
 
 }  // namespace gsr
