@@ -480,18 +480,18 @@ __device__ __forceinline__ void shrink_announce(const ShrinkArgs& s, uint8_t* sm
     }
 }
 
-// One wave of a tile's workgroup, whose rows lie in the blocks of `want`: looks
-// until their records are there, at most s.looks times.  True: they are.
-__device__ __forceinline__ bool shrink_look(const ShrinkArgs& s, uint32_t want, uint32_t active, int tiles)
+// One wave of a tile's workgroup, whose rows have adapters in the blocks of
+// `want`: looks until their records are there, at most s.looks times.  True:
+// they are.
+__device__ __forceinline__ bool shrink_look(const ShrinkArgs& s, uint32_t want)
 {
     const int lane = threadIdx.x & 63;
-    const bool ask = lane < 4 && (want & active) >> lane & 1u;
+    const bool ask = lane < 4 && ((want >> lane) & 1u);
     bool there = __ballot(ask) == 0;
     for (int i = 0; i < s.looks && !there; ++i) {
         const uint32_t f = ask ? __hip_atomic_load(s.flags + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1u;
         there = __ballot(f == 0u) == 0;
     }
-    if (lane == 0) shrink_done(s, tiles, active);
     return there;
 }
 
@@ -740,10 +740,14 @@ struct AdapterItems {
         : m0(m0_), n0(n0_), first(first_), stride(stride_), t(p.t), t_scale(p.t_scale), t_row(0), c(p.chunks)
     {
 #pragma unroll
-        for (int b = 0; b < TM; ++b) {
-            id[b] = adapter_of(p.ids, row_of(b), p.M, p.adapters);
-            todo |= (id[b] >= 0 ? 1 : 0) << b;
-        }
+        for (int b = 0; b < TM; ++b) id[b] = adapter_of(p.ids, row_of(b), p.M, p.adapters);
+    }
+
+    // once the ids have come
+    __device__ __forceinline__ void start()
+    {
+#pragma unroll
+        for (int b = 0; b < TM; ++b) todo |= (id[b] >= 0 ? 1 : 0) << b;
         if constexpr (!SHARED) scales();
     }
 

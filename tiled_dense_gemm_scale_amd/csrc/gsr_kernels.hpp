@@ -611,6 +611,7 @@ gemm_scale_relu_kernel(Problem p)
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
     if constexpr (ADAPT != kAdaptNone) {
         AdapterItems<TN, TM, false> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
+        items.start();
         items.template rest<TM == 1 ? 4 : 2>(p, acc);
     }
 

@@ -105,6 +105,8 @@ __device__ __forceinline__ void kspec_tile(Problem p, uint8_t* smem, int* last, 
 
     if (copier) {
         // ---- copy waves ----------------------------------------------------------
+        [[maybe_unused]] uint32_t active = 0;
+        if constexpr (ADAPT == kAdaptShared) active = active_blocks(shrink);
         const i32x4 ra = raw_rsrc(p.A, (uint32_t)a_extent<GROUPED>(p) * (uint32_t)p.K * 2u);
         const i32x4 rb = raw_rsrc(p.B, (uint32_t)p.K * (uint32_t)p.N * 2u);
         const uint32_t lds0 = lds_address(smem);
@@ -168,12 +170,13 @@ __device__ __forceinline__ void kspec_tile(Problem p, uint8_t* smem, int* last, 
         if constexpr (ADAPT == kAdaptShared) {
             if (part == 0) {
                 if (wave == NW - 1) {
-                    const uint32_t want = ((1u << (BM / 16)) - 1u) << (m0 / 16), active = active_blocks(shrink);
-                    // without any adapter nobody looks and nobody counts
-                    const bool there = active == 0 || shrink_look(shrink, want, active, p.tiles_m * p.tiles_n);
+                    const bool there = shrink_look(shrink, active & ((1u << (BM / 16)) - 1u) << (m0 / 16));
                     if (lane == 0) *found = there;
                 }
                 lds_barrier();  // every wave is done with the operand buffers
+                // the count returns while the MFMA waves take their records;
+                // without any adapter nobody counts
+                if (wave == NW - 1 && lane == 0 && active != 0) shrink_done(shrink, p.tiles_m * p.tiles_n, active);
                 make_records();
             }
         }
@@ -222,6 +225,7 @@ __device__ __forceinline__ void kspec_tile(Problem p, uint8_t* smem, int* last, 
         [[maybe_unused]] typename Items::template Batch<kFirst> batch;
         if constexpr (ADAPT != kAdaptNone) {
             if (part == 0) {
+                items.start();
                 items.load_lb(p, batch);
                 if constexpr (ADAPT != kAdaptShared) items.load_t(p, batch);
             }
