@@ -53,11 +53,15 @@ hipError_t launch_shared(const Problem& p, const ShrinkArgs& a, int makers, int 
     return launch_kernel((gsr::gemm_adapters_kspec_kernel<BM, BN, S, D>), dim3(grid), dim3(512), s, p, a, makers);
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int KG>
 hipError_t launch_staged(const Problem& p, int grid, hipStream_t s)
 {
-    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, false, gsr::kAdaptVec>), dim3(grid), dim3(256), s, p);
+    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, false, gsr::kAdaptVec, KG>), dim3(grid),
+                         dim3(256 * KG), s, p);
 }
+
+// The element-wise kernels, in the order of kElemTiles.
+const launch_fn kElem[] = {launch_staged<64, 64, 4>, launch_staged<64, 64, 1>, launch_staged<128, 128, 1>};
 
 // The tiles with an adapter form, under the ids of their dense forms.
 struct Entry {
@@ -65,15 +69,13 @@ struct Entry {
     int bm, bn;
     launch_fn vec, split;
     hipError_t (*shared)(const Problem&, const ShrinkArgs&, int makers, int grid, hipStream_t);  // both steps, or null
-    int elem_bm, elem_bn;
-    launch_fn elem;
 };
 const Entry kTable[] = {
-    {21, 64, 64, launch_kspec<64, 64, 4, 2, false>, launch_kspec<64, 64, 4, 2, true>, launch_shared<64, 64, 4, 2>, 64, 64, launch_staged<64, 64>},
-    {22, 32, 64, launch_kspec<32, 64, 4, 2, false>, launch_kspec<32, 64, 4, 2, true>, launch_shared<32, 64, 4, 2>, 64, 64, launch_staged<64, 64>},
-    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, nullptr, nullptr, 128, 128, launch_staged<128, 128>},
-    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, nullptr, nullptr, 128, 128, launch_staged<128, 128>},
-    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, nullptr, nullptr, 128, 128, launch_staged<128, 128>},
+    {21, 64, 64, launch_kspec<64, 64, 4, 2, false>, launch_kspec<64, 64, 4, 2, true>, launch_shared<64, 64, 4, 2>},
+    {22, 32, 64, launch_kspec<32, 64, 4, 2, false>, launch_kspec<32, 64, 4, 2, true>, launch_shared<32, 64, 4, 2>},
+    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, nullptr, nullptr},
+    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, nullptr, nullptr},
+    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, nullptr, nullptr},
 };
 
 const Entry* entry_of(int id)
@@ -227,8 +229,9 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     p.unit_b = load_unit(B, N);
     p.unit_c = load_unit(C, N);
     const bool vec = p.unit_a == 16 && p.unit_b == 16 && (((uintptr_t)bias & 7u) == 0);
-    p.tiles_m = (int)cdiv(M, vec ? e.bm : e.elem_bm);
-    p.tiles_n = (int)cdiv(N, vec ? e.bn : e.elem_bn);
+    const int elem = elem_choice(config_id, (double)cdiv(M, 64) * (double)cdiv(N, 64), (double)cdiv(M, 128) * (double)cdiv(N, 128));
+    p.tiles_m = (int)cdiv(M, vec ? e.bm : kElemTiles[elem].bm);
+    p.tiles_n = (int)cdiv(N, vec ? e.bn : kElemTiles[elem].bn);
     const int tiles = p.tiles_m * p.tiles_n;
 
     const Layout w = layout_of(M, K, rank);
@@ -306,7 +309,7 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
                             dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
     if (err != hipSuccess) return GSR_ERROR_LAUNCH;
     if (split.parts > 1) err = e.split(p, tiles * split.parts, s);
-    else err = (vec ? e.vec : e.elem)(p, tiles, s);
+    else err = (vec ? e.vec : kElem[elem])(p, tiles, s);
     return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
 }
 

@@ -59,28 +59,29 @@ hipError_t launch_kspec(const Problem& p, int grid, hipStream_t s)
     return launch_kernel((gsr::gemm_scale_relu_kspec_kernel<BM, BN, S, D, false, true>), dim3(grid), dim3(512), s, p);
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int KG>
 hipError_t launch_staged(const Problem& p, int grid, hipStream_t s)
 {
-    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, true>), dim3(grid), dim3(256), s, p);
+    return launch_kernel((gsr::gemm_scale_relu_kernel<BM, BN, 64, 2, 2, false, true, gsr::kAdaptNone, KG>), dim3(grid),
+                         dim3(256 * KG), s, p);
 }
 
+// The element-wise kernels, in the order of kElemTiles.
+const launch_fn kElem[] = {launch_staged<64, 64, 4>, launch_staged<64, 64, 1>, launch_staged<128, 128, 1>};
+
 // The grouped forms of the selector's tiles, under the ids of their dense
-// forms, with the element-wise kernel that stands in for them.
+// forms.
 struct Entry {
     int id;
     int bm, bn;
     launch_fn vec;
-    int elem_bm, elem_bn;
-    launch_fn elem;
-    int group_m;
 };
 const Entry kTable[] = {
-    {21, 64, 64, launch_kspec<64, 64, 4, 2>, 64, 64, launch_staged<64, 64>, 4},
-    {22, 32, 64, launch_kspec<32, 64, 4, 2>, 64, 64, launch_staged<64, 64>, 4},
-    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, 128, 128, launch_staged<128, 128>, 4},
-    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, 128, 128, launch_staged<128, 128>, 4},
-    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, 128, 128, launch_staged<128, 128>, 4},
+    {21, 64, 64, launch_kspec<64, 64, 4, 2>},
+    {22, 32, 64, launch_kspec<32, 64, 4, 2>},
+    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>},
+    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>},
+    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>},
 };
 
 const Entry* entry_of(int id)
@@ -90,10 +91,16 @@ const Entry* entry_of(int id)
     return nullptr;
 }
 
-// The tile.  The group sizes are on the device, so they are taken as spread
-// about their mean like an exponential distribution's, for which a group cut
-// into tiles of bm rows has 1 / (1 - exp(-bm / mean)) of them on average.  The
-// estimate is the larger of two times plus a twentieth of the smaller: the
+// Tiles of bm rows to expect of P rows in `used` groups.  The group sizes are on
+// the device, so they are taken as spread about their mean like an exponential
+// distribution's, for which a group has 1 / (1 - exp(-bm / mean)) of them on
+// average.
+double tile_rows(int64_t P, int64_t used, int bm)
+{
+    return (double)used / (1.0 - std::exp(-(double)bm * (double)used / (double)P));
+}
+
+// The tile.  The estimate is the larger of two times plus a twentieth of the smaller: the
 // tiles' (the dense selector's time of one, in rounds of 256 workgroups, a
 // part-filled last round costing 0.6 + 0.4 fill) and that of reading B once
 // per tile row at 5.5 TB/s.  Its constants come from a grid search over the
@@ -105,16 +112,16 @@ const Entry* entry_of(int id)
 // The 128 x 128 tile runs 5 % faster here than the dense fit has it.
 const Entry& select(int64_t P, int64_t groups, int64_t N, int64_t K)
 {
-    const double used = (double)std::min(groups, P), mean = (double)P / used;
+    const int64_t used = std::min(groups, P);
     const Entry* best = nullptr;
     double best_t = 1e300;
     for (const Entry& e : kTable) {
-        const double tile_rows = used / (1.0 - std::exp(-(double)e.bm / mean));
-        const double rounds = std::ceil(tile_rows * (double)cdiv(N, e.bn)) / 256.0;
+        const double rows = tile_rows(P, used, e.bm);
+        const double rounds = std::ceil(rows * (double)cdiv(N, e.bn)) / 256.0;
         const double full = std::floor(rounds), fill = rounds - full;
         const double work = std::max(1.0, full + (fill > 0.0 ? 0.6 + 0.4 * fill : 0.0)) * tile_time(e.id, K) *
                             (e.id == 32 ? 0.95 : 1.0);
-        const double read = tile_rows * (double)K * (double)N * 2.0 / 5.5e6;
+        const double read = rows * (double)K * (double)N * 2.0 / 5.5e6;
         const double t = std::max(work, read) + 0.05 * std::min(work, read);
         if (t < best_t) best_t = t, best = &e;
     }
@@ -181,16 +188,23 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
         const hipError_t err = launch_kernel(gsr::fill_grouped_kernel, dim3((unsigned)groups), dim3(256), s, p);
         return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
     }
-    const Entry& e = config_id >= 0 ? *entry_of(config_id) : select(P, groups, N, K);
     const bool vec = p.unit_a == 16 && p.unit_b == 16 && (((uintptr_t)bias & 7u) == 0);
-    const int bm = vec ? e.bm : e.elem_bm, bn = vec ? e.bn : e.elem_bn;
-    p.tiles_n = (int)cdiv(N, bn);
-    p.group_m = e.group_m;
-    // tile rows: at most one part-filled tile for each group that has rows
     const int64_t used = std::min(groups, P);
+    int bm, bn;
+    launch_fn fn;
+    p.group_m = 4;
+    if (vec) {
+        const Entry& e = config_id >= 0 ? *entry_of(config_id) : select(P, groups, N, K);
+        bm = e.bm, bn = e.bn, fn = e.vec;
+    } else {
+        const int i = elem_choice(config_id, tile_rows(P, used, 64) * (double)cdiv(N, 64), tile_rows(P, used, 128) * (double)cdiv(N, 128));
+        bm = kElemTiles[i].bm, bn = kElemTiles[i].bn, fn = kElem[i];
+    }
+    p.tiles_n = (int)cdiv(N, bn);
+    // tile rows: at most one part-filled tile for each group that has rows
     const int64_t grid = (P + used * (bm - 1)) / bm * p.tiles_n;
     if (grid >= kLimit) return GSR_ERROR_TOO_LARGE;
-    const hipError_t err = (vec ? e.vec : e.elem)(p, (int)grid, s);
+    const hipError_t err = fn(p, (int)grid, s);
     return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
 }
 

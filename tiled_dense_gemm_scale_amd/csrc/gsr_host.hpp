@@ -68,5 +68,20 @@ __attribute__((visibility("hidden"))) Split dense_split(int64_t M, int64_t N, in
 constexpr int kSplitMaxParts = 16;
 constexpr int64_t kSplitCounters = 128;  // arrival counters at a workspace's start that every call leaves at zero
 
+// The element-wise kernels of the grouped products and of those with adapters:
+// 0: 64x64 with four groups of waves on K, 1: 64x64, 2: 128x128.  For a forced
+// configuration id its tile's (the copy-wave K-split ones: 22 and 21); else by
+// the number of tiles the launch has of 64x64 and of 128x128.
+struct ElemTile {
+    int bm, bn;
+};
+constexpr ElemTile kElemTiles[3] = {{64, 64}, {64, 64}, {128, 128}};
+constexpr int64_t kElemFull128 = 256, kElemFull64 = 512;
+inline int elem_choice(int config_id, double tiles64, double tiles128)
+{
+    if (config_id >= 0) return config_id == 22 ? 0 : config_id == 21 ? 1 : 2;
+    return tiles128 >= (double)kElemFull128 ? 2 : tiles64 > (double)kElemFull64 ? 1 : 0;
+}
+
 }  // namespace host
 }  // namespace gsr

@@ -55,57 +55,41 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, uint3
 // 16-byte chunk c of LDS row r lives at chunk c ^ swz(r) (8 chunks per row).
 __device__ __forceinline__ uint32_t swz(uint32_t r) { return (r ^ (r >> 3)) & 7u; }
 
-// Eight consecutive fp16 values starting at element offset `elem`; the first
-// `nvalid` of them exist (0..8).  The vector form needs nvalid in {0, 8} and
-// a 16-byte aligned address; the element form loads the values one by one,
-// each at its own (2-byte aligned) address.
-template <bool VEC>
-__device__ __forceinline__ u32x4 load8(__amdgpu_buffer_rsrc_t rs, uint32_t elem, int nvalid)
-{
-    if constexpr (VEC) {
-        const uint32_t off = (nvalid > 0) ? elem * 2u : kOutOfRange;
-        return __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
-    } else {
-        uint32_t h[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t off = (e < nvalid) ? (elem + e) * 2u : kOutOfRange;
-            h[e] = __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0);
-        }
-        u32x4 v;
-        v[0] = h[0] | (h[1] << 16);
-        v[1] = h[2] | (h[3] << 16);
-        v[2] = h[4] | (h[5] << 16);
-        v[3] = h[6] | (h[7] << 16);
-        return v;
-    }
-}
-
-// load8 for the element-wise path with the operand's load unit U (16, 8, 4
-// or 2 bytes).  Every row of the operand starts on a multiple of the unit and
-// so does the end of the matrix, and a chunk starts on a multiple of 16 bytes
-// from its row, so each load is naturally aligned and lies wholly inside or
-// wholly outside the records.  Loads that hold no valid value are not issued;
-// values past `nvalid` inside a load (the next row's) are cleared.
+// Eight consecutive fp16 values, of which the first `nvalid` exist (0..8), with
+// the operand's load unit U (16, 8, 4 or 2 bytes): every row of the operand starts on a multiple of the unit, and
+// `off` is the chunk's byte offset in a buffer of `end` bytes that starts on a
+// dword.  A 16-byte buffer load needs dword alignment only, so from unit 4 on a
+// chunk is one load; with unit 2 it is one load at the dword below and one of
+// the dword behind, shifted together.  A load that would pass the buffer's end
+// (the last chunk of the matrix) is taken value by value.  Loads that hold no
+// valid value are not issued; values past `nvalid` are cleared.
 template <int U>
-__device__ __forceinline__ u32x4 load8_unit(__amdgpu_buffer_rsrc_t rs, uint32_t elem, int nvalid)
+__device__ __forceinline__ u32x4 load8_unit(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t end, int nvalid)
 {
     if constexpr (U == 16) {
-        return load8<true>(rs, elem, nvalid);  // nvalid is 0 or 8 with this unit
-    } else if constexpr (U == 2) {
-        return load8<false>(rs, elem, nvalid);
+        return __builtin_amdgcn_raw_buffer_load_b128(rs, nvalid > 0 ? off : kOutOfRange, 0, 0);  // nvalid is 0 or 8
     } else {
-        const uint32_t off = elem * 2u;
+        constexpr uint32_t NEED = U == 2 ? 20u : 16u;
+        const uint32_t at = off & ~3u;
         u32x4 v;
-        if constexpr (U == 8) {
-            const u32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(rs, nvalid > 0 ? off : kOutOfRange, 0, 0);
-            const u32x2 hi = __builtin_amdgcn_raw_buffer_load_b64(rs, nvalid > 4 ? off + 8u : kOutOfRange, 0, 0);
-            v = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        if (nvalid <= 0 || at + NEED <= end) {
+            const uint32_t o = nvalid > 0 ? at : kOutOfRange;
+            v = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+            if constexpr (U == 2) {
+                const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(rs, o + 16u, 0, 0), sh = (off & 2u) << 3;
+                const uint32_t x = v[1], y = v[2], z = v[3];
+                v[0] = __builtin_amdgcn_alignbit(x, v[0], sh);
+                v[1] = __builtin_amdgcn_alignbit(y, x, sh);
+                v[2] = __builtin_amdgcn_alignbit(z, y, sh);
+                v[3] = __builtin_amdgcn_alignbit(w, z, sh);
+            }
         } else {
-            static_assert(U == 4, "load units of 16, 8, 4 or 2 bytes");
+            uint32_t h[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, nvalid > 2 * i ? off + 4u * (uint32_t)i : kOutOfRange, 0, 0);
+            for (int e = 0; e < 8; ++e)
+                h[e] = __builtin_amdgcn_raw_buffer_load_b16(rs, e < nvalid ? off + 2u * (uint32_t)e : kOutOfRange, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = h[2 * i] | (h[2 * i + 1] << 16);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -457,16 +441,24 @@ struct TileKernel {
     static_assert(LDS_BYTES <= 163840, "LDS budget of one workgroup on gfx950");
 };
 
-template <int BM, int BN, int BK, int WM, int WN, bool VEC, bool GROUPED = false, int ADAPT = kAdaptNone>
-__global__ void __launch_bounds__(kWave * WM * WN)
+// KG > 1: KG groups of WM x WN waves share a tile, each with LDS buffers of its
+// own: group g takes the K-steps g, g + KG, ..., and the groups' fp32 sums are
+// added in group order through LDS.  A step is bound by the latency of its
+// loads, so with few tiles (fewer than the chip holds workgroups) this gives
+// each CU as many waves' loads in flight as many tiles would.
+template <int BM, int BN, int BK, int WM, int WN, bool VEC, bool GROUPED = false, int ADAPT = kAdaptNone, int KG = 1>
+__global__ void __launch_bounds__(kWave * WM * WN * KG)
 gemm_scale_relu_kernel(Problem p)
 {
     using T = TileKernel<BM, BN, BK, WM, WN, VEC>;
     constexpr int NT = T::NT, CH = T::CH, TM = T::TM, TN = T::TN;
 
-    __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS_BYTES];
+    static_assert(KG * T::LDS_BYTES <= 163840 && (KG - 1) * BM * BN * 4 <= KG * T::LDS_BYTES, "LDS");
+    __shared__ __attribute__((aligned(16))) uint8_t smem_all[KG * T::LDS_BYTES];
 
-    const int tid = threadIdx.x;
+    const int group = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    uint8_t* const smem = smem_all + group * T::LDS_BYTES;
+    const int tid = KG == 1 ? (int)threadIdx.x : (int)threadIdx.x % NT;
     const int lane = tid & 63;
     const int wave = tid >> 6;
     const int wm = wave / WN, wn = wave % WN;
@@ -483,8 +475,11 @@ gemm_scale_relu_kernel(Problem p)
     const uint32_t a_bytes = (uint32_t)a_extent<GROUPED>(p) * (uint32_t)p.K * 2u;
     const uint32_t b_bytes = (uint32_t)p.K * (uint32_t)p.N * 2u;
     const uint32_t c_bytes = (uint32_t)p.M * (uint32_t)p.N * 2u;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.A, a_bytes);
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.B, b_bytes);
+    // buffers of A and B from the dword their first value is in
+    const uint32_t a_mis = VEC ? 0u : (uint32_t)(uintptr_t)p.A & 2u, b_mis = VEC ? 0u : (uint32_t)(uintptr_t)p.B & 2u;
+    const uint32_t a_end = a_bytes + a_mis, b_end = b_bytes + b_mis;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc((const uint8_t*)p.A - a_mis, a_end);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc((const uint8_t*)p.B - b_mis, b_end);
     const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.C, c_bytes);
 
     // ---- this thread's share of each global -> LDS copy -------------------
@@ -519,7 +514,7 @@ gemm_scale_relu_kernel(Problem p)
             bool in = m < p.M;
             if constexpr (GROUPED) m = arow[i], in = m >= 0;
             const int nv = in ? kval : 0;
-            areg[i] = load8_unit<U>(ra, (uint32_t)m * (uint32_t)p.K + (uint32_t)kk, nv);
+            areg[i] = load8_unit<U>(ra, ((uint32_t)m * (uint32_t)p.K + (uint32_t)kk) * 2u + a_mis, a_end, nv);
         }
     };
     auto load_b = [&](auto unit_tag, int k0) {
@@ -535,13 +530,12 @@ gemm_scale_relu_kernel(Problem p)
                 for (int j = 0; j < 8; ++j) {
                     const int k = k0 + kb * 8 + j;
                     const int nv = (k < p.K) ? nval : 0;
-                    breg[i][j] = load8_unit<U>(rb, (uint32_t)k * (uint32_t)p.N + (uint32_t)n, nv);
+                    breg[i][j] = load8_unit<U>(rb, ((uint32_t)k * (uint32_t)p.N + (uint32_t)n) * 2u + b_mis, b_end, nv);
                 }
             }
         }
     };
     using U16 = std::integral_constant<int, 16>;
-    using U8 = std::integral_constant<int, 8>;
     using U4 = std::integral_constant<int, 4>;
     using U2 = std::integral_constant<int, 2>;
     auto with_unit = [&](int unit, auto&& f) {
@@ -549,8 +543,7 @@ gemm_scale_relu_kernel(Problem p)
             f(U16{});
         } else {
             if (unit == 16) f(U16{});
-            else if (unit == 8) f(U8{});
-            else if (unit == 4) f(U4{});
+            else if (unit >= 4) f(U4{});
             else f(U2{});
         }
     };
@@ -609,22 +602,25 @@ gemm_scale_relu_kernel(Problem p)
         for (int b = 0; b < TM; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-    if constexpr (ADAPT != kAdaptNone) {
-        AdapterItems<TN, TM, false> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
-        items.start();
-        items.template rest<TM == 1 ? 4 : 2>(p, acc);
-    }
+    if constexpr (ADAPT != kAdaptNone)
+        if (group == 0) {
+            AdapterItems<TN, TM, false> items(p, m0 + wm * T::WTM, n0 + wn * T::WTN, 0, 1);
+            items.start();
+            items.template rest<TM == 1 ? 4 : 2>(p, acc);
+        }
 
     const int ksteps = (p.K + BK - 1) / BK;
 
-    load_tile(0);
+    // a group's step t is step t KG + group of the tile; past the last they are zeros
+    const int rounds = (ksteps + KG - 1) / KG;
+    load_tile(group * BK);
     store_tile(0);
     __syncthreads();
 
-    for (int t = 0; t < ksteps; ++t) {
+    for (int t = 0; t < rounds; ++t) {
         const int cur = t & 1;
-        const bool more = (t + 1) < ksteps;
-        if (more) load_tile((t + 1) * BK);
+        const bool more = (t + 1) < rounds;
+        if (more) load_tile(((t + 1) * KG + group) * BK);
 
         const uint8_t* base = smem + cur * T::STAGE_BYTES;
 #pragma unroll
@@ -646,6 +642,29 @@ gemm_scale_relu_kernel(Problem p)
 
         if (more) store_tile(cur ^ 1);
         __syncthreads();
+    }
+
+    if constexpr (KG > 1) {
+        // accumulator block i of the group's thread, as four 16-byte pieces
+        auto place = [&](int g, int i, int q) { return (f32x4*)smem_all + (((g - 1) * TN * TM + i) * 4 + q) * NT + tid; };
+#pragma unroll
+        for (int i = 0; i < TN * TM; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x16 v = acc[i / TM][i % TM];
+                if (group > 0) *place(group, i, q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int i = 0; i < TN * TM; ++i)
+            for (int g = 1; g < KG; ++g)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4 v = *place(g, i, q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i / TM][i % TM][4 * q + e] += v[e];
+                }
     }
 
     // ---- epilogue: scale, clamp at zero, narrow, store ---------------------
