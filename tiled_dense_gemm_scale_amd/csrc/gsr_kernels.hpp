@@ -55,6 +55,24 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, uint3
 // 16-byte chunk c of LDS row r lives at chunk c ^ swz(r) (8 chunks per row).
 __device__ __forceinline__ uint32_t swz(uint32_t r) { return (r ^ (r >> 3)) & 7u; }
 
+// The eight values at `off` where a load cannot pass the buffer's end, all of
+// them whatever they are; zeros unless `in`.
+template <int U>
+__device__ __forceinline__ u32x4 load8_whole(__amdgpu_buffer_rsrc_t rs, uint32_t off, bool in)
+{
+    const uint32_t o = in ? off & ~3u : kOutOfRange;
+    u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+    if constexpr (U == 2) {
+        const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(rs, o + 16u, 0, 0), sh = (off & 2u) << 3;
+        const uint32_t x = v[1], y = v[2], z = v[3];
+        v[0] = __builtin_amdgcn_alignbit(x, v[0], sh);
+        v[1] = __builtin_amdgcn_alignbit(y, x, sh);
+        v[2] = __builtin_amdgcn_alignbit(z, y, sh);
+        v[3] = __builtin_amdgcn_alignbit(w, z, sh);
+    }
+    return v;
+}
+
 // Eight consecutive fp16 values, of which the first `nvalid` exist (0..8), with
 // the operand's load unit U (16, 8, 4 or 2 bytes): every row of the operand starts on a multiple of the unit, and
 // `off` is the chunk's byte offset in a buffer of `end` bytes that starts on a
@@ -70,19 +88,9 @@ __device__ __forceinline__ u32x4 load8_unit(__amdgpu_buffer_rsrc_t rs, uint32_t 
         return __builtin_amdgcn_raw_buffer_load_b128(rs, nvalid > 0 ? off : kOutOfRange, 0, 0);  // nvalid is 0 or 8
     } else {
         constexpr uint32_t NEED = U == 2 ? 20u : 16u;
-        const uint32_t at = off & ~3u;
         u32x4 v;
-        if (nvalid <= 0 || at + NEED <= end) {
-            const uint32_t o = nvalid > 0 ? at : kOutOfRange;
-            v = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
-            if constexpr (U == 2) {
-                const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(rs, o + 16u, 0, 0), sh = (off & 2u) << 3;
-                const uint32_t x = v[1], y = v[2], z = v[3];
-                v[0] = __builtin_amdgcn_alignbit(x, v[0], sh);
-                v[1] = __builtin_amdgcn_alignbit(y, x, sh);
-                v[2] = __builtin_amdgcn_alignbit(z, y, sh);
-                v[3] = __builtin_amdgcn_alignbit(w, z, sh);
-            }
+        if (nvalid <= 0 || (off & ~3u) + NEED <= end) {
+            v = load8_whole<U>(rs, off, nvalid > 0);
         } else {
             uint32_t h[8];
 #pragma unroll
@@ -503,9 +511,16 @@ gemm_scale_relu_kernel(Problem p)
     // alignment allows (p.unit_a, p.unit_b); the unit is picked once per
     // K-step (a uniform branch on a kernel argument) for a copy of the load
     // loop compiled for it, so the loads of a step still issue back to back.
-    // The vector path reads 16-byte units throughout.
-    auto load_a = [&](auto unit_tag, int k0) {
+    // So does the choice between whole and careful loads: in a step that ends
+    // far enough before K (whole_step) no chunk's load can pass the end of its
+    // buffer and none has k past K, and what a chunk holds past column N or
+    // row M reaches outputs only that are not stored; the last steps look at
+    // every chunk.  (With the look inside the loop each load was waited for
+    // before the next: 361 x 604 x 10048 with adapters took 235 us, not 104.)  The vector path reads
+    // 16-byte units throughout.
+    auto load_a = [&](auto unit_tag, auto whole_tag, int k0) {
         constexpr int U = decltype(unit_tag)::value;
+        constexpr bool WHOLE = decltype(whole_tag)::value;
         const int kk = k0 + a_kc * 8;
         const int kval = min(max(p.K - kk, 0), 8);
 #pragma unroll
@@ -513,12 +528,14 @@ gemm_scale_relu_kernel(Problem p)
             int m = m0 + a_r0 + i * A_ROW_STEP;
             bool in = m < p.M;
             if constexpr (GROUPED) m = arow[i], in = m >= 0;
-            const int nv = in ? kval : 0;
-            areg[i] = load8_unit<U>(ra, ((uint32_t)m * (uint32_t)p.K + (uint32_t)kk) * 2u + a_mis, a_end, nv);
+            const uint32_t off = ((uint32_t)m * (uint32_t)p.K + (uint32_t)kk) * 2u + a_mis;
+            if constexpr (WHOLE) areg[i] = load8_whole<U>(ra, off, in);
+            else areg[i] = load8_unit<U>(ra, off, a_end, in ? kval : 0);
         }
     };
-    auto load_b = [&](auto unit_tag, int k0) {
+    auto load_b = [&](auto unit_tag, auto whole_tag, int k0) {
         constexpr int U = decltype(unit_tag)::value;
+        constexpr bool WHOLE = decltype(whole_tag)::value;
 #pragma unroll
         for (int i = 0; i < T::B_PER; ++i) {
             const int blk = tid + i * NT;
@@ -529,8 +546,9 @@ gemm_scale_relu_kernel(Problem p)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int k = k0 + kb * 8 + j;
-                    const int nv = (k < p.K) ? nval : 0;
-                    breg[i][j] = load8_unit<U>(rb, ((uint32_t)k * (uint32_t)p.N + (uint32_t)n) * 2u + b_mis, b_end, nv);
+                    const uint32_t off = ((uint32_t)k * (uint32_t)p.N + (uint32_t)n) * 2u + b_mis;
+                    if constexpr (WHOLE) breg[i][j] = load8_whole<U>(rb, off, nval > 0);
+                    else breg[i][j] = load8_unit<U>(rb, off, b_end, (k < p.K) ? nval : 0);
                 }
             }
         }
@@ -548,8 +566,16 @@ gemm_scale_relu_kernel(Problem p)
         }
     };
     auto load_tile = [&](int k0) {
-        with_unit(p.unit_a, [&](auto u) { load_a(u, k0); });
-        with_unit(p.unit_b, [&](auto u) { load_b(u, k0); });
+        // a load takes at most 20 bytes from the dword at or below its chunk
+        const int left = p.K - (k0 + BK);
+        const bool whole_step = left >= 2 && (int64_t)left * p.N >= 10;
+        if (VEC || !whole_step) {
+            with_unit(p.unit_a, [&](auto u) { load_a(u, std::false_type{}, k0); });
+            with_unit(p.unit_b, [&](auto u) { load_b(u, std::false_type{}, k0); });
+        } else {
+            with_unit(p.unit_a, [&](auto u) { load_a(u, std::true_type{}, k0); });
+            with_unit(p.unit_b, [&](auto u) { load_b(u, std::true_type{}, k0); });
+        }
     };
 
     auto store_tile = [&](int stage) {
