@@ -216,24 +216,51 @@ __device__ __forceinline__ void shrink_sums(const ShrinkArgs& s, uint8_t* smem, 
             }
         }
     } else {
-        const __amdgpu_buffer_rsrc_t ra = make_rsrc(s.A, (uint32_t)s.M * (uint32_t)s.K * 2u);
-        const uint32_t arow = (uint32_t)(m0 + lrow) * (uint32_t)s.K;
+        // Unaligned rows: 16 bytes from the dword at or below a piece and the
+        // dword after it, shifted together, BATCH steps at a time; the steps
+        // that those could read past the end of K from, value by value.
+        // (All value by value, 4662 rows, K 557, rank 128: 118 us.)
+        constexpr int BATCH = 2;
+        const uint32_t amis = (uint32_t)(uintptr_t)s.A & 2u;
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc((const uint8_t*)s.A - amis, (uint32_t)s.M * (uint32_t)s.K * 2u + amis);
+        const uint32_t arow = (uint32_t)(m0 + lrow) * (uint32_t)s.K + amis / 2u;
         const bool ain = m0 + lrow < s.M;
+        const int whole = min(max((min(kend, s.K - 2) - kbeg) / 32, ks0), ks1);  // steps before this one end before that
         int at = 0;
         for_each_adapter(id, [&](int l) {
             if (at++ % slots != slot) return;
-            const __amdgpu_buffer_rsrc_t rl = make_rsrc(s.la + (int64_t)l * s.rank * s.K, (uint32_t)s.rank * (uint32_t)s.K * 2u);
+            const uint16_t* la = s.la + (int64_t)l * s.rank * s.K;
+            const uint32_t lmis = (uint32_t)(uintptr_t)la & 2u;
+            const __amdgpu_buffer_rsrc_t rl = make_rsrc((const uint8_t*)la - lmis, (uint32_t)s.rank * (uint32_t)s.K * 2u + lmis);
             f32x4 d[NB] = {};
-            for (int ks = ks0; ks < ks1; ++ks) {
-                const int k = kbeg + 32 * ks + 8 * lq;
-                const half8 x = piece8<false>(ra, arow, k, kend, ain);
+            auto steps_of = [&](auto count, int ks, auto&& piece) {
+                constexpr int N = decltype(count)::value;
+                half8 x[N], w[N][NB];
 #pragma unroll
-                for (int q = 0; q < NB; ++q) {
-                    const int r = kAdapterChunk * (c0 + q) + lrow;
-                    const half8 w = piece8<false>(rl, (uint32_t)r * (uint32_t)s.K, k, kend, r < s.rank);
-                    d[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, d[q], 0, 0, 0);
+                for (int i = 0; i < N; ++i) {
+                    const int k = kbeg + 32 * (ks + i) + 8 * lq;
+                    x[i] = piece(ra, arow, k, ain);
+#pragma unroll
+                    for (int q = 0; q < NB; ++q) {
+                        const int r = kAdapterChunk * (c0 + q) + lrow;
+                        w[i][q] = piece(rl, (uint32_t)r * (uint32_t)s.K + lmis / 2u, k, r < s.rank);
+                    }
                 }
-            }
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int q = 0; q < NB; ++q) d[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i][q], x[i], d[q], 0, 0, 0);
+            };
+            auto wide = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, int k, bool in) {
+                return __builtin_bit_cast(half8, load8_whole<2>(rs, (row + (uint32_t)k) * 2u, in));
+            };
+            auto narrow = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, int k, bool in) {
+                return piece8<false>(rs, row, k, kend, in);
+            };
+            int ks = ks0;
+            for (; ks + BATCH <= whole; ks += BATCH) steps_of(std::integral_constant<int, BATCH>{}, ks, wide);
+            for (; ks < whole; ++ks) steps_of(std::integral_constant<int, 1>{}, ks, wide);
+            for (; ks < ks1; ++ks) steps_of(std::integral_constant<int, 1>{}, ks, narrow);
 #pragma unroll
             for (int q = 0; q < NB; ++q)
 #pragma unroll
