@@ -133,6 +133,30 @@ def test_normal_inputs(gsr, shape, act):
         assert counters_zero(ws)
 
 
+@pytest.mark.parametrize("kind", ["mixed", "runs", "one"])
+@pytest.mark.parametrize("shape", [(65, 72, 10240, 5, 24), (100, 40, 9221, 3, 17), (400, 24, 9224, 2, 16),
+                                   (50, 40, 333, 5, 7), (90, 40, 333, 5, 7), (70, 33, 4097, 3, 5)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_inner_sums_of_long_and_odd_rows(gsr, shape, kind):
+    """The inner sums in parts of K above 64 rows, and rows of odd length, where
+    rows and adapters start at any 2-byte address: small sparse integers, whose
+    sums are exact: |t| <= 6 (K / 16 + 3) < 2^12 is kept whole in its two
+    halves, and |c| <= 9 * 643 + 24 * 2 * 2^12 < 2^18 in fp32."""
+    M, N, K, L, R = shape
+    a, b, la, lb = integer_case(M, N, K, L, R, seed=K)
+    keep = (torch.arange(K) % 16 == 0) | (torch.arange(K) >= K - 3)  # at most K / 16 + 3 values of K count
+    a, b, la = a * keep, b * keep[:, None], la * keep
+    for shift in (0, 1):  # every operand also from an address that is no multiple of 4
+        d = lambda t: torch.cat([torch.zeros(shift, dtype=t.dtype), t.flatten()]).to(DEV)[shift:].view(t.shape)
+        ids = ids_of(kind, M, L)
+        ws = workspace(gsr, M, N, K, R)
+        say(f"adapters long rows {shape} {kind} shift={shift}")
+        c = gsr.gemm_adapters(d(a), d(b), d(la), d(lb), torch.from_numpy(ids).to(DEV), ws, alpha=2.0 ** -7, activation="none")
+        ref, _ = reference(a, b, la, lb, ids, None, None, 2.0 ** -7, "none")
+        assert torch.equal(c.cpu(), torch.from_numpy(ref).half())
+        assert counters_zero(ws)
+
+
 @pytest.mark.parametrize("size", [1e-6, 1.0, 2000.0])
 def test_inner_sums_of_any_size(gsr, size):
     """Inner sums above fp16's range and below its normal numbers keep their value."""

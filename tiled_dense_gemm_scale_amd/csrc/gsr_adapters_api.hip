@@ -101,12 +101,21 @@ const Entry& stand_in(int id)
 
 int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// The shrink launch.  Up to kShrinkFewRows rows, a block of 16 spreads over
-// chunks of ranks, adapters and, while that makes fewer than kShrinkGrid
-// workgroups, parts of about kShrinkPart values of K; blocks count arrivals in the counters at the workspace's start.  More rows
-// take one workgroup per block and share of its adapters, as many shares as
-// the chip has room for.
-constexpr int64_t kShrinkFewRows = 64, kShrinkPart = 1024, kShrinkMaxParts = 16, kShrinkGrid = 512;
+// The shrink launch.  In a decode step (kShrinkMixedRows) a workgroup has one
+// block of 16 rows, one chunk of ranks, one of the block's adapters (the rows
+// are mixed) and, while that makes fewer than kShrinkGrid workgroups, one of
+// the parts of about kShrinkPart values of K; a block's workgroups count
+// arrivals in the counters at the workspace's start and the last adds up.
+// More rows have one workgroup per block and share of its adapters, for all
+// of K and all ranks, as many shares as the chip has room for.  In between,
+// where few blocks (times chunks: kShrinkFew) walk far (K times the passes
+// over the ranks: kShrinkDeep), the parts are the faster way: product and
+// sums, us, without and with: 256x4096x11008 rank 64 85 and 67, 230x10112x7808
+// rank 107 138 and 105, 512x4096x11008 rank 16 102 and 99; but
+// 256x4096x8192 rank 16 39 and 42, 256x4096x4096 23 and 28, and 1024 rows of
+// mixed adapters, K 11008, rank 64, 183 and 238.
+constexpr int64_t kShrinkMixedRows = 64, kShrinkPart = 1024, kShrinkMaxParts = 16, kShrinkGrid = 512, kShrinkFew = 128,
+                  kShrinkDeep = 9216;
 
 struct ShrinkPlan {
     int blocks, parts, kchunk;  // parts 0: all of K in one workgroup
@@ -117,15 +126,17 @@ ShrinkPlan shrink_plan(int64_t M, int64_t K, int64_t adapters, int64_t rank)
 {
     ShrinkPlan s{(int)cdiv(M, gsr::kShrinkRows), 0, (int)K, 1};
     const int64_t most = std::min<int64_t>({M, adapters, gsr::kShrinkRows});
-    if (M > kShrinkFewRows) {
+    int64_t wgs = (int64_t)s.blocks * cdiv(rank, gsr::kAdapterChunk);
+    if (M > kShrinkMixedRows &&
+        (wgs > kShrinkFew || s.blocks >= kSplitCounters || K * cdiv(rank, 4 * gsr::kAdapterChunk) < kShrinkDeep)) {
         s.slots = (int)std::max<int64_t>(1, std::min<int64_t>(most, 256 / s.blocks));
         return s;
     }
-    s.slots = (int)most;
-    const int64_t wgs = (int64_t)s.blocks * s.slots * cdiv(rank, gsr::kAdapterChunk);
+    if (M <= kShrinkMixedRows) s.slots = (int)most, wgs *= most;
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({kShrinkMaxParts, cdiv(K, kShrinkPart), kShrinkGrid / wgs}));
     s.kchunk = (int)(cdiv(cdiv(K, parts), 32) * 32);
     s.parts = (int)cdiv(K, s.kchunk);
+    if (M > kShrinkMixedRows) s.slots = (int)std::max<int64_t>(1, std::min<int64_t>(most, kShrinkGrid / (wgs * s.parts)));
     return s;
 }
 
@@ -248,7 +259,7 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     const ShrinkPlan sp = shrink_plan(M, K, adapters, rank);
     const int makers = sp.blocks * std::max(sp.parts, 1) * w.chunks * sp.slots;
     const bool shrink_vec = p.unit_a == 16 && load_unit(la, K) == 16;
-    const bool shared = sp.parts > 0 && vec && e.shared != nullptr && shrink_vec && makers <= kSharedMakers &&
+    const bool shared = M <= kShrinkMixedRows && sp.parts > 0 && vec && e.shared != nullptr && shrink_vec && makers <= kSharedMakers &&
                         (split.parts == 1 || tiles <= kSharedCounters);
     // a split leaves the makers their CUs
     while (shared && splits == 0 && split.parts > 1 && tiles * split.parts + makers > 256)
