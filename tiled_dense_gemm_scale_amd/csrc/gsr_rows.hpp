@@ -214,6 +214,13 @@ struct HalfVec<2> {
     }
 };
 
+template <bool STREAM, typename V>
+__device__ __forceinline__ V row_load(const V* p)
+{
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+
 struct RowArgs {
     const uint16_t* x;         // gather: the table; combine: y; backward: dout
     const uint16_t* y;         // backward: y
@@ -288,11 +295,20 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(RowArgs r)
 
 // The gradient of combine: dy[positions[t, j]] = w[t, j] dout[t] and
 // dw[t, j] = <dout[t], y[positions[t, j]]> (fp32, 0 for a dropped choice).
-// One wave per token: dout[t] comes from memory once and from the caches for
-// the later choices, each y row is read once and each dy row written once, and
-// the dot needs no LDS, only a sum over the lanes.  Rows of dy that no choice
-// names (rows[p] < 0) are set to zero by the same waves.
-template <int U>
+// One wave per token and J choices at a time, so dout[t] is read once for all
+// of them, each y row is read once and each dy row written once, and the dot
+// needs no LDS, only a sum over the lanes.  A wave requests S units per row
+// before it uses one: S follows the row's length (up to 64, 128, more and
+// from 512 units on: 1, 2, 4, 8; steps past a row's end cost their
+// instructions), J is 2 where two choices of 8 steps are all there is.  y of
+// kStreamBytes and more is read without a claim on the caches.  One choice at
+// a time and 4 steps, then this: 8192x2x4096 78 and 57 us (335 MB: 5.9 TB/s),
+// 16384x4x1024 57 and 51, 8192x4x512 16.3 and 14.2, 16384x8x256 59 and 31;
+// 8192x2x512 10.7 and 10.9.  Rows of dy that no choice names (rows[p] < 0)
+// are set to zero by the same waves.
+constexpr int64_t kStreamBytes = 64 << 20;
+
+template <int U, int J, int S, bool STREAM>
 __global__ void __launch_bounds__(256) combine_rows_backward_kernel(RowArgs r)
 {
     typedef typename RowUnit<U>::type V;
@@ -300,39 +316,53 @@ __global__ void __launch_bounds__(256) combine_rows_backward_kernel(RowArgs r)
     const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), nw = (int64_t)gridDim.x * 4;
     for (int64_t t = wid; t < r.T; t += nw) {
         const V* d = (const V*)r.x + t * r.units;
-        for (int j = 0; j < r.k; ++j) {
-            const int32_t q = r.positions[t * r.k + j];
-            const bool ok = (uint32_t)q < (uint32_t)r.P;
-            float dot = 0.0f;
-            if (ok) {
-                const float w = r.weights ? r.weights[t * r.k + j] : 1.0f;
-                const V* y = (const V*)r.y + (int64_t)q * r.units;
-                V* dy = (V*)r.out + (int64_t)q * r.units;
-                for (int u0 = lane; u0 < r.units; u0 += 256) {
-                    V dv[4], yv[4];
+        for (int j0 = 0; j0 < r.k; j0 += J) {
+            float dot[J], w[J];
+            bool ok[J];
+            const V* y[J];
+            V* dy[J];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = u0 + 64 * i < r.units;
-                        dv[i] = in ? d[u0 + 64 * i] : V{};
-                        yv[i] = (in && r.dweights) ? y[u0 + 64 * i] : V{};
-                    }
+            for (int j = 0; j < J; ++j) {
+                const int64_t at = t * r.k + j0 + j;
+                const int32_t q = j0 + j < r.k ? r.positions[at] : -1;
+                ok[j] = (uint32_t)q < (uint32_t)r.P;
+                w[j] = (ok[j] && r.weights) ? r.weights[at] : 1.0f;
+                y[j] = (const V*)r.y + (int64_t)(ok[j] ? q : 0) * r.units;
+                dy[j] = (V*)r.out + (int64_t)(ok[j] ? q : 0) * r.units;
+                dot[j] = 0.0f;
+            }
+            for (int u0 = lane; u0 < r.units; u0 += 64 * S) {
+                V dv[S], yv[J][S];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < S; ++i) {
+                    const bool in = u0 + 64 * i < r.units;
+                    dv[i] = in ? d[u0 + 64 * i] : V{};
+#pragma unroll
+                    for (int j = 0; j < J; ++j) yv[j][i] = (in && ok[j] && r.dweights) ? row_load<STREAM>(y[j] + u0 + 64 * i) : V{};
+                }
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (!ok[j]) continue;
+#pragma unroll
+                    for (int i = 0; i < S; ++i) {
                         float g[U / 2];
 #pragma unroll
                         for (int e = 0; e < U / 2; ++e) {
                             const float de = HalfVec<U>::at(dv[i], e);
-                            dot += de * HalfVec<U>::at(yv[i], e);
-                            g[e] = w * de;
+                            dot[j] += de * HalfVec<U>::at(yv[j][i], e);
+                            g[e] = w[j] * de;
                         }
-                        if (u0 + 64 * i < r.units) dy[u0 + 64 * i] = HalfVec<U>::pack(g);
+                        if (u0 + 64 * i < r.units) dy[j][u0 + 64 * i] = HalfVec<U>::pack(g);
                     }
                 }
             }
             if (r.dweights) {
 #pragma unroll
-                for (int s = 32; s > 0; s >>= 1) dot += __shfl_xor(dot, s);
-                if (lane == 0) r.dweights[t * r.k + j] = dot;
+                for (int j = 0; j < J; ++j) {
+#pragma unroll
+                    for (int x = 32; x > 0; x >>= 1) dot[j] += __shfl_xor(dot[j], x);
+                    if (lane == 0 && j0 + j < r.k) r.dweights[t * r.k + j0 + j] = dot[j];
+                }
             }
         }
     }

@@ -48,6 +48,26 @@ int lanes_log2_of(int64_t units)
 #define GSR_BY_UNIT(KERNEL, UNIT)                                                           \
     ((UNIT) == 16 ? gsr::KERNEL<16> : (UNIT) == 8 ? gsr::KERNEL<8> : (UNIT) == 4 ? gsr::KERNEL<4> : gsr::KERNEL<2>)
 
+// combine_rows_backward_kernel's form for rows of `units` units.
+typedef void (*rows_kernel)(gsr::RowArgs);
+template <int J, int S>
+rows_kernel backward16(bool stream)
+{
+    return stream ? gsr::combine_rows_backward_kernel<16, J, S, true> : gsr::combine_rows_backward_kernel<16, J, S, false>;
+}
+rows_kernel backward_kernel(int unit, int units, int k, bool stream)
+{
+    switch (unit) {
+    case 8: return gsr::combine_rows_backward_kernel<8, 4, 4, false>;
+    case 4: return gsr::combine_rows_backward_kernel<4, 4, 4, false>;
+    case 2: return gsr::combine_rows_backward_kernel<2, 4, 4, false>;
+    default: break;
+    }
+    if (units >= 512) return k <= 2 ? backward16<2, 8>(stream) : backward16<4, 8>(stream);
+    if (units > 128) return backward16<4, 4>(stream);
+    return units > 64 ? backward16<4, 2>(stream) : backward16<4, 1>(stream);
+}
+
 int status_of(hipError_t e) { return e == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH; }
 
 }  // namespace
@@ -211,8 +231,8 @@ int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_
     r.k = (int32_t)k;
     r.units = (int32_t)(width * 2 / unit);
     const int64_t waves = std::max<int64_t>({tokens, cdiv(rows_in, 64), 1});
-    return status_of(launch_kernel(GSR_BY_UNIT(combine_rows_backward_kernel, unit), dim3((unsigned)cdiv(waves, 4)),
-                                   dim3(256), (hipStream_t)stream, r));
+    return status_of(launch_kernel(backward_kernel(unit, r.units, r.k, weights != nullptr && rb >= (uint64_t)gsr::kStreamBytes),
+                                   dim3((unsigned)cdiv(waves, 4)), dim3(256), (hipStream_t)stream, r));
 }
 
 }  // extern "C"
