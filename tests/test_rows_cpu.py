@@ -34,8 +34,8 @@ def test_group_refusals(native, change, status):
 def test_group_workspace_bytes(native):
     assert native.group_workspace_bytes(0, 8) == 0
     assert native.group_workspace_bytes(8192, 1024) == 0
-    assert native.group_workspace_bytes(8193, 8) == 3 * 9 * 4
-    assert native.group_workspace_bytes(131072, 64) == 32 * 65 * 4
+    assert native.group_workspace_bytes(8193, 8) == 5 * 9 * 4  # blocks of 2048 slots
+    assert native.group_workspace_bytes(131072, 64) == 64 * 65 * 4
     # never more than 256 blocks
     assert native.group_workspace_bytes(2 ** 31 - 1, 1024) <= 256 * 1025 * 4
     for bad in ((-1, 8), (4, 0), (4, 1025)):

@@ -20,20 +20,28 @@ namespace gsr {
 // run per wave, and a run is walked 64 slots at a time.  Inside such a step
 // the lanes with the same key find each other with one ballot per key bit;
 // a lane's rank is the number of such lanes below it, and the lowest of them
-// adds their count to the wave's counter of that key.  Counting a whole run
-// first and walking it again with the counters turned into start positions
-// gives every slot its place in stable order.  Key `groups` collects the
-// dropped slots (ids outside [0, groups)), which so sort behind all others.
+// adds their count to the wave's counter of that key, whose value before is
+// where the step's slots of that key start within the wave.  Once all waves
+// have counted, the counters are turned into start positions, and every slot
+// has its place in stable order.  Runs of up to kGroupKept steps keep their
+// slots' keys and places in registers meanwhile, longer ones walk twice.  Key
+// `groups` collects the dropped slots (ids outside [0, groups)), which so sort
+// behind all others.
 //
 // Up to kGroupSingle slots one workgroup does all of it.  Above, one launch
 // counts per block and a second places: each of its blocks adds up the other
 // blocks' counts by itself, which costs blocks x (groups + 1) reads per block
 // (at most 256 blocks) but no third launch and no block waits for another.
 // The work is bound by latency: the passes of a step depend on each other.
+// 64 slots of 8 groups take 2.8 us, 8192 of 64 11.8 (walked twice: 15.8), and
+// both launches for 131072 of 64 groups 11.9 (blocks of 4096 slots: 13.7; of
+// 2048 and walked twice: 15.7), of 256 groups 16.7 (4096: 17.7, 1024: 20.1).
 constexpr int kGroupMax = 1024;       // groups
 constexpr int kGroupWaves = 16;       // waves of a full workgroup
 constexpr int kGroupSingle = 8192;    // slots one workgroup handles alone
-constexpr int kGroupChunk = 4096;     // smallest block of the two-launch form
+constexpr int kGroupChunk = 2048;     // smallest block of the two-launch form
+constexpr int kGroupCounts = 20000;   // counts per block from which blocks grow
+constexpr int kGroupKept = 8;         // steps whose keys and places a wave keeps
 constexpr int kGroupBlocks = 256;     // most blocks of it
 
 struct GroupArgs {
@@ -99,11 +107,27 @@ __global__ void __launch_bounds__(1024) group_place_kernel(GroupArgs g)
     const int run = ((end - beg + waves - 1) / waves + 63) & ~63;
     const int wbeg = beg + wave * run, wend = min(end, wbeg + run);
     uint32_t* const mine = cnt + wave * nb;
-    for (int i0 = wbeg; i0 < wend; i0 += 64) {
-        const int i = i0 + lane;
-        const int key = i < wend ? group_key<ID>(g, i) : -1;
+    // the place of this lane's slot of a step among the wave's slots of its key
+    auto place_of = [&](int key) {
         const uint64_t m = same_key(key, g.bits);
-        if (key >= 0 && lane == __ffsll((unsigned long long)m) - 1) atomicAdd(&mine[key], (uint32_t)__popcll(m));
+        const int leader = __ffsll((unsigned long long)m) - 1;
+        uint32_t first = 0;
+        if (key >= 0 && lane == leader) first = atomicAdd(&mine[key], (uint32_t)__popcll(m));
+        return (uint32_t)__shfl((int)first, key >= 0 ? leader : lane) + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
+    };
+    const bool kept = run <= 64 * kGroupKept;
+    int key[kGroupKept];
+    uint32_t place[kGroupKept];
+    if (kept) {
+#pragma unroll
+        for (int s = 0; s < kGroupKept; ++s) {
+            const int i = wbeg + 64 * s + lane;
+            key[s] = i < wend ? group_key<ID>(g, i) : -1;
+        }
+#pragma unroll
+        for (int s = 0; s < kGroupKept; ++s) place[s] = wbeg + 64 * s < wend ? place_of(key[s]) : 0u;
+    } else {
+        for (int i0 = wbeg; i0 < wend; i0 += 64) place_of(i0 + lane < wend ? group_key<ID>(g, i0 + lane) : -1);
     }
     if (g.blocks > 1) {
         // every block's count of key e, and those of the blocks before this one
@@ -152,19 +176,21 @@ __global__ void __launch_bounds__(1024) group_place_kernel(GroupArgs g)
         }
     }
     __syncthreads();
-    for (int i0 = wbeg; i0 < wend; i0 += 64) {
-        const int i = i0 + lane;
-        const int key = i < wend ? group_key<ID>(g, i) : -1;
-        const uint64_t m = same_key(key, g.bits);
-        const int leader = __ffsll((unsigned long long)m) - 1;
-        uint32_t first = 0;
-        if (key >= 0 && lane == leader) first = atomicAdd(&mine[key], (uint32_t)__popcll(m));
-        first = (uint32_t)__shfl((int)first, key >= 0 ? leader : lane);
-        if (key >= 0) {
-            const uint32_t at = prior[key] + first + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
-            const bool kept = key < g.groups;
-            g.rows[at] = kept ? (int32_t)(i / g.k) : -1;
-            g.positions[i] = kept ? (int32_t)at : -1;
+    auto put = [&](int i, int key, uint32_t at) {
+        if (key < 0) return;
+        const bool in = key < g.groups;
+        at += prior[key];
+        g.rows[at] = in ? (int32_t)(i / g.k) : -1;
+        g.positions[i] = in ? (int32_t)at : -1;
+    };
+    if (kept) {
+#pragma unroll
+        for (int s = 0; s < kGroupKept; ++s)
+            if (key[s] >= 0) put(wbeg + 64 * s + lane, key[s], mine[key[s]] + place[s]);
+    } else {
+        for (int i0 = wbeg; i0 < wend; i0 += 64) {
+            const int i = i0 + lane, k = i < wend ? group_key<ID>(g, i) : -1;
+            put(i, k, place_of(k));
         }
     }
 }

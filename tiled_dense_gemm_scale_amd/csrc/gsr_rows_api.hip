@@ -19,12 +19,15 @@ struct GroupPlan {
     int chunk, blocks;
 };
 
-// Up to kGroupSingle slots: one block.  Above: blocks of at least
-// kGroupChunk slots, kGroupBlocks of them at most.
-GroupPlan group_plan(int64_t n)
+// Up to kGroupSingle slots: one block.  Above, blocks of kGroupChunk slots or,
+// where the counts that each block has to read (blocks x groups) pass
+// kGroupCounts, of up to four times as many; kGroupBlocks blocks at most.
+GroupPlan group_plan(int64_t n, int64_t groups)
 {
     if (n <= gsr::kGroupSingle) return GroupPlan{(int)n, 1};
-    const int64_t chunk = std::max<int64_t>(gsr::kGroupChunk, cdiv(cdiv(n, gsr::kGroupBlocks), 1024) * 1024);
+    int64_t chunk = gsr::kGroupChunk;
+    while (chunk < 4 * gsr::kGroupChunk && cdiv(n, chunk) * (groups + 1) > gsr::kGroupCounts) chunk *= 2;
+    chunk = std::max(chunk, cdiv(cdiv(n, gsr::kGroupBlocks), 1024) * 1024);
     return GroupPlan{(int)chunk, (int)cdiv(n, chunk)};
 }
 
@@ -78,7 +81,7 @@ int64_t gsr_group_workspace_bytes(int64_t tokens, int64_t k, int64_t groups)
 {
     const int64_t n = slots_of(tokens, k);
     if (n < 0 || groups < 1 || groups > gsr::kGroupMax) return -1;
-    const GroupPlan plan = group_plan(n);
+    const GroupPlan plan = group_plan(n, groups);
     return plan.blocks > 1 ? (int64_t)plan.blocks * (groups + 1) * 4 : 0;
 }
 
@@ -108,7 +111,7 @@ int gsr_group_rows(int64_t tokens, int64_t k, int64_t groups, const void* ids, i
     }
     const int st = check_device();
     if (st != GSR_SUCCESS) return st;
-    const GroupPlan plan = group_plan(n);
+    const GroupPlan plan = group_plan(n, groups);
     gsr::GroupArgs g;
     g.ids = ids;
     g.offsets = offsets;
