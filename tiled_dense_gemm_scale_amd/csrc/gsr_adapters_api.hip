@@ -240,7 +240,7 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     p.unit_b = load_unit(B, N);
     p.unit_c = load_unit(C, N);
     const bool vec = p.unit_a == 16 && p.unit_b == 16 && (((uintptr_t)bias & 7u) == 0);
-    const int elem = elem_choice(config_id, (double)cdiv(M, 64) * (double)cdiv(N, 64), (double)cdiv(M, 128) * (double)cdiv(N, 128));
+    const int elem = elem_choice(config_id, K, (double)cdiv(M, 64) * (double)cdiv(N, 64), (double)cdiv(M, 128) * (double)cdiv(N, 128));
     p.tiles_m = (int)cdiv(M, vec ? e.bm : kElemTiles[elem].bm);
     p.tiles_n = (int)cdiv(N, vec ? e.bn : kElemTiles[elem].bn);
     const int tiles = p.tiles_m * p.tiles_n;

@@ -100,7 +100,12 @@ double tile_rows(int64_t P, int64_t used, int bm)
     return (double)used / (1.0 - std::exp(-(double)bm * (double)used / (double)P));
 }
 
-// The tile.  The estimate is the larger of two times plus a twentieth of the smaller: the
+// The tile.  Decode steps are bound by B's bytes (16 tokens, 2 of 8 experts,
+// 4096 -> 11008: 116 to 126 us, 5.5 TB/s and more of what the hit experts hold),
+// prefills by the matrix cores (8192 tokens: 1.22 ms, 1.21 PFLOP/s), and in
+// between it is whole rounds of tiles that count (1025 tokens, 11008 -> 4096:
+// 231 us, 0.80 PFLOP/s: 184 tiles of 256 x 256 on 256 CUs, 69 % of their rows
+// filled).  The estimate is the larger of two times plus a twentieth of the smaller: the
 // tiles' (the dense selector's time of one, in rounds of 256 workgroups, a
 // part-filled last round costing 0.6 + 0.4 fill) and that of reading B once
 // per tile row at 5.5 TB/s.  Its constants come from a grid search over the
@@ -197,7 +202,7 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
         const Entry& e = config_id >= 0 ? *entry_of(config_id) : select(P, groups, N, K);
         bm = e.bm, bn = e.bn, fn = e.vec;
     } else {
-        const int i = elem_choice(config_id, tile_rows(P, used, 64) * (double)cdiv(N, 64), tile_rows(P, used, 128) * (double)cdiv(N, 128));
+        const int i = elem_choice(config_id, K, tile_rows(P, used, 64) * (double)cdiv(N, 64), tile_rows(P, used, 128) * (double)cdiv(N, 128));
         bm = kElemTiles[i].bm, bn = kElemTiles[i].bn, fn = kElem[i];
     }
     p.tiles_n = (int)cdiv(N, bn);

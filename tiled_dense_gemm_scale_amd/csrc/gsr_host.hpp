@@ -71,16 +71,23 @@ constexpr int64_t kSplitCounters = 128;  // arrival counters at a workspace's st
 // The element-wise kernels of the grouped products and of those with adapters:
 // 0: 64x64 with four groups of waves on K, 1: 64x64, 2: 128x128.  For a forced
 // configuration id its tile's (the copy-wave K-split ones: 22 and 21); else by
-// the number of tiles the launch has of 64x64 and of 128x128.
+// the number of tiles the launch has of 64x64 and of 128x128, which fill the
+// chip from one per CU on (the 64x64 ones from two if K is deep).  In us, the
+// three in turn, K 517: 136 tiles of 64x64 12, 15 and 22, 264 tiles 24, 17 and
+// 22, 272 of 128x128 55, 33 and 25; K 10044: 136 tiles 85, 210 and 264, 264
+// tiles 198, 247 and 298, 528 tiles 296, 260 and 321, 272 of 128x128 423, 431
+// and 272.  Unaligned 16-byte loads go out at about one lane per clock, which
+// bounds all three.
 struct ElemTile {
     int bm, bn;
 };
 constexpr ElemTile kElemTiles[3] = {{64, 64}, {64, 64}, {128, 128}};
-constexpr int64_t kElemFull128 = 256, kElemFull64 = 512;
-inline int elem_choice(int config_id, double tiles64, double tiles128)
+constexpr int64_t kElemFull = 256, kElemDeep = 2048;
+inline int elem_choice(int config_id, int64_t K, double tiles64, double tiles128)
 {
     if (config_id >= 0) return config_id == 22 ? 0 : config_id == 21 ? 1 : 2;
-    return tiles128 >= (double)kElemFull128 ? 2 : tiles64 > (double)kElemFull64 ? 1 : 0;
+    if (tiles128 >= (double)kElemFull) return 2;
+    return tiles64 > (double)(K > kElemDeep ? 2 * kElemFull : kElemFull) ? 1 : 0;
 }
 
 }  // namespace host
