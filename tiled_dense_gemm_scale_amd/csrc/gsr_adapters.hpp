@@ -374,9 +374,9 @@ __global__ void __launch_bounds__(512) adapter_shrink_rows_kernel(ShrinkArgs s)
 // and every slots-th adapter, which meet in the workspace: the workgroup of a
 // block that arrives last adds the parts in part order and writes the records
 // (device-scope accesses and the arrival counter as in KsSum::split_sum_store,
-// so no order depends on timing and no workgroup waits).  Bound by latency: a
-// launch, a walk of K / parts and the meeting, 8 us for 16 rows of 16 adapters,
-// K 4096, rank 16.
+// so no order depends on timing and no workgroup waits).  Bound by latency (a
+// launch, a walk of K / parts, the meeting): 12.6 us for 16 rows of 16
+// adapters of rank 64, K 4096 (8.4 MB of La).
 typedef ShrinkCfg<1, 8, 8, 2> ShrinkParts;
 
 // The finished row of a block: `at` gives the thread's rank c of chunk j summed
@@ -610,8 +610,8 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t d) { return ((d & 0x7c00
 // loop over adapters (changing them with vector instructions there made the
 // register allocator spill them), so the rows of other adapters take part with
 // t = 0, and the rows' scales multiply all accumulators once at the end.
-// (4097 x 11008 x 4096 with 9 runs of rank 16 takes 316 us beside 285 without
-// adapters; the inner sums before it 13.)
+// (4097 x 11008 x 4096 with 9 runs of rank 16 takes 336 us in all beside 285
+// without adapters; 14 of them are the inner sums'.)
 // 0 * infinity and 0 * NaN would then reach those rows: fragments with such
 // values have them replaced by zeros, and the caller, told so by the returned
 // true, runs adapter_nonfinite16 after its epilogue.
