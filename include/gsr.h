@@ -292,7 +292,7 @@ int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_
  *   B        groups x K x N; bias NULL or groups x N
  *   offsets  groups + 1 values on the device, not decreasing, in [0, P] (the
  *            offsets of gsr_group_rows); a group may be empty.  Other values
- *            are clamped: they make wrong results, never an access outside.
+ *            make wrong or missing results, never an access outside.
  * Epilogue, precision, alignment, ownership and errors as gemm_scale_bias_act
  * (same kernels per tile, so a group's outputs are the bits of that call on
  * its rows with the same configuration).  GSR_ERROR_TOO_LARGE for P >= 2^31,

@@ -222,6 +222,23 @@ def test_less_aligned_c_and_a(gsr, off):
         assert bool((host[:o] == 3.0).all()) and bool((host[o + P * N:] == 3.0).all())
 
 
+@pytest.mark.parametrize("config", [-1, 21, 22, 28, 31, 32])
+@pytest.mark.parametrize("kind", ["overlapping", "decreasing", "outside", "far"])
+def test_offsets_out_of_order(gsr, config, kind):
+    """Offsets that no sort gives: the call ends and nothing outside the P rows
+    of c is written."""
+    P, E, K, N = 70, 130, 64, 72
+    offsets = {"overlapping": [0, P] * 66, "decreasing": list(range(E, -1, -1)), "outside": [-5, 10 ** 6] * 66,
+               "far": [-2 ** 31, 2 ** 31 - 1] * 66}[kind][:E + 1]
+    a, b = torch.zeros(P, K, dtype=torch.float16, device=DEV), torch.zeros(E, K, N, dtype=torch.float16, device=DEV)
+    c = torch.full((P + 300, N), 9.0, dtype=torch.float16, device=DEV)
+    say(f"grouped offsets {kind} config={config}")
+    gsr.gemm_grouped(a, b, torch.tensor(offsets, dtype=torch.int32, device=DEV), c=c[150:150 + P], activation="none",
+                     config_id=config)
+    torch.cuda.synchronize()
+    assert bool((c[:150] == 9.0).all()) and bool((c[150 + P:] == 9.0).all())
+
+
 def test_past_32_bit_offsets(gsr):
     """B and C of more than 2^31 bytes: the last group's weights, the last rows."""
     E, K, N = 40, 4096, 8192  # 2.7 GB

@@ -207,7 +207,8 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
     }
     p.tiles_n = (int)cdiv(N, bn);
     // tile rows: at most one part-filled tile for each group that has rows
-    const int64_t grid = (P + used * (bm - 1)) / bm * p.tiles_n;
+    p.tiles_m = (int)((P + used * (bm - 1)) / bm);
+    const int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (grid >= kLimit) return GSR_ERROR_TOO_LARGE;
     const hipError_t err = fn(p, (int)grid, s);
     return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;

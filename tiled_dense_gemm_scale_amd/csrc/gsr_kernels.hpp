@@ -355,11 +355,14 @@ __device__ __forceinline__ void tile_of(int pid, int nwg, const Problem& p, int&
 // groups.  The grid is an upper bound; false for the workgroups past the last
 // tile.  On true, `p` is that tile alone: its group's B and bias, its first
 // row's C (and A or rows), M its row count; bases are 64-bit, so only a tile
-// has to lie within 32-bit offsets.  Sizes are clamped to p.M rows in all,
-// so no offsets make it reach outside.
+// has to lie within 32-bit offsets.  Rows are clamped to 0 .. p.M - 1, and
+// groups that overlap so far that they have more tiles than any offsets in
+// order could (p.tiles_m tile rows; the sums stop at kMost, far above) are not
+// computed at all, so no offsets make it reach outside or search without end.
 template <int BM, int BN>
 __device__ __forceinline__ bool group_tile(Problem& p, int& n0)
 {
+    constexpr int kMost = 1 << 29;
     const int lane = threadIdx.x & 63;
     int lo = 0, n = 0, inc = 0;  // the lane's group: first row, rows, tiles up to and with it
     auto scan = [&](int e0) {
@@ -373,13 +376,14 @@ __device__ __forceinline__ bool group_tile(Problem& p, int& n0)
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int o = __shfl_up(inc, d);
-            if (lane >= d) inc += o;
+            if (lane >= d) inc = min(inc + o, kMost);
         }
         return __builtin_amdgcn_readlane(inc, 63);
     };
     int total = scan(0);
-    for (int e0 = 64; e0 < p.groups; e0 += 64) total += scan(e0);
-    const int nwg = total * p.tiles_n;
+    for (int e0 = 64; e0 < p.groups; e0 += 64) total = min(total + scan(e0), kMost);
+    if (total > p.tiles_m) return false;
+    const int nwg = total * p.tiles_n;  // at most the grid
     if ((int)blockIdx.x >= nwg) return false;
     Problem q = p;
     q.tiles_m = total;
