@@ -61,6 +61,17 @@ def test_group_rows(gsr, case, dtype):
         assert np.array_equal(g.cpu().numpy(), want), name
 
 
+@pytest.mark.parametrize("case", [(300001, 2, 1024), (1100001, 2, 5)], ids=lambda c: "x".join(map(str, c)))
+def test_group_rows_many(gsr, case):
+    """Larger blocks for many groups, and runs too long to keep in registers
+    (more than 256 blocks of 8192 slots)."""
+    T, k, E = case
+    ids = np.random.default_rng(E).integers(-1, E, (T, k), dtype=np.int32)
+    say(f"group many {case}")
+    for g, want in zip(gsr.group_rows(torch.from_numpy(ids).to(DEV), E), plan_of(ids, E)):
+        assert np.array_equal(g.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("fill", ["one", "none", "last"])
 @pytest.mark.parametrize("n", [64, 5000, 20000])
 def test_group_rows_lopsided(gsr, fill, n):
@@ -180,6 +191,38 @@ def test_combine_rows_backward(gsr, case, weighted):
     # a lane adds at most 8 ceil(H / 512) products, then six additions over the lanes
     terms = 8 * -(-H // 512) + 6
     within("dweights", dw.cpu().double().numpy(), refw, terms * 2.0 ** -24 * magw + 1e-37)
+
+
+@pytest.mark.parametrize("case", [(50, 3, 500), (50, 5, 1000), (50, 3, 2056), (50, 2, 4104), (50, 3, 4104), (50, 1, 8192),
+                                  (70000, 8, 64), (8400, 4, 1000), (4100, 4, 2056), (4100, 2, 4104), (2100, 4, 4096),
+                                  (8400, 1, 4096), (1400, 6, 4097)], ids=lambda c: "x".join(map(str, c)))
+def test_combine_rows_backward_by_length(gsr, case):
+    """Every form that the length of a row, the choices and the size of y
+    (above and below 64 MiB) select, against the formula in 64 bits on the
+    device."""
+    T, k, H = case
+    g = torch.Generator().manual_seed(T + H)
+    ids = torch.randint(-1, 8, (T, k), generator=g).to(DEV)
+    offsets, rows, positions = gsr.group_rows(ids, 8)
+    w = torch.randn(T, k, generator=g).to(DEV)
+    dg = torch.Generator(device=DEV).manual_seed(H)
+    y = torch.randn(T * k, H, device=DEV, generator=dg).half()
+    y[int(offsets[-1]):] = float("nan")
+    dout = torch.randn(T, H, device=DEV, generator=dg).half()
+    say(f"combine backward by length {case}")
+    dy, dw = gsr.combine_rows_backward(dout, y, positions, w, rows,
+                                       dy=torch.full((T * k, H), float("nan"), dtype=torch.float16, device=DEV))
+    assert bool((dy[int(offsets[-1]):] == 0).all())
+    for j in range(k):
+        at, ok = positions[:, j].long(), positions[:, j] >= 0
+        d, q = dout[ok].double(), at[ok]
+        ref = w[ok, j].double()[:, None] * d
+        assert bool(((dy[q].double() - ref).abs() <= (HALF16 + 2.0 ** -23) * ref.abs() + 2.0 ** -25).all())
+        prod = d * y[q].double()
+        # a lane adds at most 8 ceil(H / 512) products, then six additions over the lanes
+        slack = (8 * -(-H // 512) + 6) * 2.0 ** -24 * prod.abs().sum(1) + 1e-37
+        assert bool(((dw[ok, j].double() - prod.sum(1)).abs() <= slack).all())
+        assert bool((dw[~ok, j] == 0).all())
 
 
 def test_combine_gradient_by_differences(gsr):
