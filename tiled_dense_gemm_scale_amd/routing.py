@@ -100,7 +100,7 @@ def matrix(name: str, t, dtype, rank: int, index: Optional[int] = None) -> int:
 def output(name: str, t: Optional[torch.Tensor], dtype, shape, like: torch.Tensor) -> torch.Tensor:
     """`t` after need(), or a new tensor on `like`'s device."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     need(name, t, dtype, shape, like.get_device())
     return t
 
@@ -130,16 +130,18 @@ def group_rows(ids: torch.Tensor, groups: int, offsets: Optional[torch.Tensor] =
     n = T * k
 
     def go(s):
-        ws, wbytes, out = workspace, 0, [offsets, rows, positions]
-        if ws is None:
+        if workspace is not None:
+            wptr, wbytes = workspace_of(workspace, dev)
+        else:
             wbytes = group_workspace_bytes(n, groups)
-            ws = ids.new_empty(wbytes, dtype=torch.uint8) if wbytes else None
-        wptr, wbytes = workspace_of(ws, dev) if ws is not None else (0, 0)
-        for i, (name, want) in enumerate((("offsets", (max(groups, 0) + 1,)), ("rows", (n,)), ("positions", shape))):
-            out[i] = output(name, out[i], torch.int32, want, ids)
-        _native.check(_native.group_rows(T, k, groups, ids.data_ptr(), ids.element_size(), out[0].data_ptr(),
-                                         out[1].data_ptr(), out[2].data_ptr(), wptr, wbytes, s))
-        return tuple(out)
+            ws = torch.empty(wbytes, dtype=torch.uint8, device=ids.device) if wbytes else None
+            wptr = ws.data_ptr() if wbytes else 0
+        o = output("offsets", offsets, torch.int32, (max(groups, 0) + 1,), ids)
+        r = output("rows", rows, torch.int32, (n,), ids)
+        p = output("positions", positions, torch.int32, shape, ids)
+        _native.check(_native.group_rows(T, k, groups, ids.data_ptr(), ids.element_size(), o.data_ptr(), r.data_ptr(),
+                                         p.data_ptr(), wptr, wbytes, s))
+        return o, r, p
 
     return enqueue(dev, stream, go)
 
