@@ -134,7 +134,7 @@ def test_normal_inputs(gsr, shape, act):
 
 
 @pytest.mark.parametrize("kind", ["mixed", "runs", "one"])
-@pytest.mark.parametrize("shape", [(65, 72, 10240, 5, 24), (100, 40, 9221, 3, 17), (400, 24, 9224, 2, 16),
+@pytest.mark.parametrize("shape", [(65, 72, 10240, 5, 24), (100, 40, 9221, 3, 17), (400, 24, 9224, 2, 16), (1100, 24, 9224, 2, 16),
                                    (50, 40, 333, 5, 7), (90, 40, 333, 5, 7), (70, 33, 4097, 3, 5)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_inner_sums_of_long_and_odd_rows(gsr, shape, kind):
