@@ -510,6 +510,7 @@ __device__ __forceinline__ void shrink_announce(const ShrinkArgs& s, uint8_t* sm
     const uint32_t active = active_blocks(s);
     if (threadIdx.x == 0) {
         __hip_atomic_store(s.flags + wg % s.blocks, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the flag is set before whoever counts last clears it
         shrink_done(s, tiles, active);
     }
 }
