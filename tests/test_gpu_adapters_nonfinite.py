@@ -1,0 +1,117 @@
+"""GPU tests of the product with low-rank adapters where a factor is an
+infinity or a NaN: every output is what the formula makes of it in 64 bits, on
+every tile, and finite ones keep their value."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+CONFIGS = [-1, 21, 22, 28, 31, 32]
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def gsr(native):
+    import tiled_dense_gemm_scale_amd as g
+
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    return g
+
+
+def say(msg):
+    print("[gpu] " + msg, flush=True)
+
+
+def products(x, y):
+    """x @ y.T in 64 bits, product by product (0 * infinity is NaN, infinities
+    of two signs add up to NaN)."""
+    with np.errstate(invalid="ignore"):
+        return np.stack([(x * row[None, :]).sum(1) for row in y], 1)
+
+
+def formula(a, b, la, lb, ids, scales):
+    """alpha 1, no bias, no activation: c, the inner sums, and per value the
+    bound on what the fp32 sums, the split of the inner sum (2^-23 of its row's
+    largest value) and one fp16 rounding may be off by."""
+    u = 2.0 ** -24
+    a64, b64, la64, lb64 = (t.double().numpy() for t in (a, b, la, lb))
+    K, R = b64.shape[0], la64.shape[1]
+    mag = lambda x: np.where(np.isfinite(x), np.abs(x), 0.0)
+    v, t = products(a64, b64.T), np.zeros((len(a64), R))
+    off = (K + 2) * u * products(mag(a64), mag(b64).T)
+    with np.errstate(invalid="ignore"):
+        for m, l in enumerate(ids):
+            if 0 <= l < len(la64):
+                t[m] = scales[l] * products(a64[m:m + 1], la64[l])[0]
+                v[m] += products(t[m:m + 1], lb64[l])[0]
+                tmag = abs(scales[l]) * products(mag(a64[m:m + 1]), mag(la64[l]))[0]
+                terr = (K + 40) * u * tmag + 2.0 ** -23 * mag(t[m]).max()
+                off[m] += products((terr + (2 * R + 4) * u * mag(t[m]))[None], mag(lb64[l]))[0]
+    return v, t, off + 2.0 ** -11 * (mag(v) + off) + 2.0 ** -25
+
+
+def agree(got, want, slack):
+    """Infinities and NaN in the same places, finite values within `slack`."""
+    got = got.double().numpy()
+    for name, kind in (("+inf", np.isposinf), ("-inf", np.isneginf), ("NaN", np.isnan)):
+        assert np.array_equal(kind(got), kind(want)), f"{name}: {np.count_nonzero(kind(got) != kind(want))} values differ"
+    fin = np.isfinite(want)
+    assert np.all(np.abs(got[fin] - want[fin]) <= slack[fin])
+
+
+def inputs(shape, seed):
+    M, N, K, L, R = shape
+    g = torch.Generator().manual_seed(seed)
+    n = lambda std, *s: (torch.randn(*s, generator=g) * std).half()
+    ids = np.random.default_rng(seed).integers(-1, L + 1, M).astype(np.int32)
+    ids[:L] = np.arange(L)[:M]
+    return n(1.0, M, K), n(K ** -0.5, K, N), n(K ** -0.5, L, R, K), n(R ** -0.5, L, N, R), ids
+
+
+def calls(gsr, native, a, b, la, lb, ids, scales, act):
+    """The call by every configuration, split over K, and with inner sums that
+    the tiles make themselves; garbage in the workspace."""
+    (M, K), N, (L, R) = a.shape, b.shape[1], la.shape[:2]
+    d = [t.to(DEV) for t in (a, b, la, lb, torch.from_numpy(ids), torch.tensor(scales, dtype=torch.float32))]
+    for config in CONFIGS:
+        for splits, looks in [(0, -1)] + ([(3, -1), (1, 0)] if config in (21, 22) else []):
+            ws = gsr.new_workspace(gsr.adapter_workspace_bytes(M, N, K, R) + (4 << 20))
+            ws[512:] = 0xFF  # NaN patterns
+            c = torch.full((M, N), 9.0, dtype=torch.float16, device=DEV)
+            say(f"{M}x{N}x{K} of {L} rank {R} config={config} splits={splits} looks={looks}")
+            native.check(native.gemm_adapters_scale_bias_act(
+                M, N, K, d[0].data_ptr(), d[1].data_ptr(), 0, c.data_ptr(), L, R, d[2].data_ptr(), d[3].data_ptr(),
+                d[4].data_ptr(), d[5].data_ptr(), 1.0, {"relu": 0, "none": 2}[act], ws.data_ptr(), ws.numel(),
+                torch.cuda.current_stream().cuda_stream, config, splits, looks))
+            yield c.cpu()
+            assert bool((ws[:512] == 0).all())
+
+
+SHAPES = [(1, 64, 512, 1, 8), (16, 200, 1032, 4, 16), (40, 136, 264, 3, 40), (150, 264, 520, 5, 24), (300, 264, 136, 3, 16),
+          (33, 101, 77, 3, 5), (200, 301, 130, 4, 17)]
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("exact", [True, False], ids=["integers", "normal"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_infinite_lb(gsr, native, shape, exact, act):
+    """Infinities of either sign and NaN in Lb meet inner sums that are exact in
+    fp16 (zeros among them) and such whose two halves have one sign or two."""
+    M, N, K, L, R = shape
+    a, b, la, lb, ids = inputs(shape, seed=M + N)
+    if exact:
+        g = torch.Generator().manual_seed(K)
+        a, la = torch.randint(-1, 2, a.shape, generator=g).half(), torch.randint(-1, 2, la.shape, generator=g).half()
+    lb[0, 3, 0], lb[L - 1, 5, R - 1], lb[L - 1, N - 1, R // 2] = INF, -INF, INF
+    lb[L // 2, 7, 0], lb[L // 2, 7, R - 1] = INF, -INF  # infinities of one sign or two
+    lb[0, 9, R // 2] = float("nan")
+    scales = [1.0, -0.5, 2.0, 1.0, 0.25][:L]
+    want, t, slack = formula(a, b, la, lb, ids, scales)
+    assert exact or np.abs(t[(ids >= 0) & (ids < L)]).min() > 1e-6  # no sign in doubt
+    assert np.isposinf(want).any() and np.isneginf(want).any() or M == 1
+    if act == "relu":
+        want = np.where(want > 0, want, 0.0)
+    for got in calls(gsr, native, a, b, la, lb, ids, scales, act):
+        agree(got, want, slack)

@@ -598,6 +598,24 @@ __device__ __forceinline__ void mfma16_pinned(f32x4& acc, const half8& x, const 
 // Bits 15 and 31 set where a half of `d` is an infinity or a NaN.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t d) { return ((d & 0x7c007c00u) + 0x04000400u) & 0x80008000u; }
 
+// `seen`, all zeros at first, gets a NaN where v has an infinity or a NaN (one
+// packed instruction per two values); any_odd tells whether it has any.
+__device__ __forceinline__ half8 look_odd(half8 v, half8 seen) { return __builtin_elementwise_fma(v, (half8)(_Float16)0.0f, seen); }
+__device__ __forceinline__ bool any_odd(half8 seen)
+{
+    const u32x4 w = __builtin_bit_cast(u32x4, seen);
+    return (w[0] | w[1] | w[2] | w[3]) != 0u;
+}
+
+// v with zeros in the place of infinities and NaN.
+__device__ __forceinline__ half8 finite8(half8 v)
+{
+    u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] &= ~((nonfinite2(w[i]) >> 15) * 0xffffu);
+    return __builtin_bit_cast(half8, w);
+}
+
 // acc, all zeros, becomes t @ Lb^T on the 16x16x32 MFMA for FN x FM blocks
 // (n, m) of 16x16 at column n0, row m0 of the problem: lane l holds row
 // 16 b + l % 16 and columns 16 a + 4 (l / 16) + 0..3.  One MFMA per block and
@@ -678,15 +696,7 @@ __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[F
 #pragma unroll
                 for (int j = 0; j < CB; ++j)
 #pragma unroll
-                    for (int a = 0; a < FN; ++a) {
-                        u32x4 w = __builtin_bit_cast(u32x4, x[j][a]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t f = nonfinite2(w[i]);
-                            w[i] &= ~((f >> 15) * 0xffffu);
-                        }
-                        x[j][a] = __builtin_bit_cast(half8, w);
-                    }
+                    for (int a = 0; a < FN; ++a) x[j][a] = finite8(x[j][a]);
             }
 #pragma unroll
             for (int b = 0; b < FM; ++b) {
@@ -878,19 +888,29 @@ struct AdapterItems {
         }
     }
 
+    // Lb's infinities and NaN meet the hi half of t alone, which has the sign
+    // of t: with both, 0 * infinity, or halves of two signs, would make a NaN of
+    // what is an infinity.
     template <int B>
     __device__ __forceinline__ void apply(const Batch<B>& w, f32x16 (&acc)[TN][TM]) const
     {
 #pragma unroll
         for (int j = 0; j < B; ++j) {
             if (j >= w.n) break;
+            half8 seen = (half8)(_Float16)0.0f, low[TN];
+#pragma unroll
+            for (int a = 0; a < TN; ++a) low[a] = w.x[j][a], seen = look_odd(w.x[j][a], seen);
+            if (__ballot(any_odd(seen)) != 0) {
+#pragma unroll
+                for (int a = 0; a < TN; ++a) low[a] = finite8(low[a]);
+            }
 #pragma unroll
             for (int b = 0; b < TM; ++b) {
                 if (__ballot(id[b] == w.ls[j]) == 0) continue;
 #pragma unroll
                 for (int a = 0; a < TN; ++a) {
                     f32x16 d = {};
-                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.x[j][a], w.lo[j][b], d, 0, 0, 0);
+                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(low[a], w.lo[j][b], d, 0, 0, 0);
                     d = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.x[j][a], w.hi[j][b], d, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
