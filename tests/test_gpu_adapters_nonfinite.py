@@ -115,3 +115,26 @@ def test_infinite_lb(gsr, native, shape, exact, act):
         want = np.where(want > 0, want, 0.0)
     for got in calls(gsr, native, a, b, la, lb, ids, scales, act):
         agree(got, want, slack)
+
+
+def positive_inputs(shape, seed):
+    """Factors above zero, A of either sign: an infinite inner sum makes
+    infinities of one sign of its row."""
+    a, b, la, lb, ids = inputs(shape, seed)
+    return a, b.abs() + 2.0 ** -10, la.abs() + 2.0 ** -10, lb.abs() + 2.0 ** -10, ids
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 512, 1, 16), (16, 200, 1032, 4, 48), (150, 264, 520, 5, 16), (300, 264, 136, 3, 48),
+                                   (300, 136, 72, 2, 240)], ids=lambda s: "x".join(map(str, s)))
+def test_infinite_la(gsr, native, shape):
+    """An infinity in La makes an infinite inner sum in every row of its adapter,
+    whose chunk of ranks may be the last of an odd count."""
+    a, b, la, lb, ids = positive_inputs(shape, seed=shape[0] + 1)
+    a = torch.where(a == 0, torch.ones_like(a), a)
+    la[0, 2, 7] = INF
+    la[-1, shape[4] - 1, 9] = -INF
+    scales = [1.0, -0.5, 2.0, 1.0, 0.25][:shape[3]]
+    want, _, slack = formula(a, b, la, lb, ids, scales)
+    assert np.isinf(want).any()
+    for got in calls(gsr, native, a, b, la, lb, ids, scales, "none"):
+        agree(got, want, slack)

@@ -662,8 +662,9 @@ __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[F
         for (int j = 0; j < CB; ++j)
 #pragma unroll
             for (int b = 0; b < FM; ++b)
-                t[j][b] = __builtin_bit_cast(half8, __builtin_amdgcn_raw_buffer_load_b128(
-                    rt, (uint32_t)(16 * b + lrow) * rec_bytes + (uint32_t)min(c + j, p.chunks - 1) * 64u + 16u * (uint32_t)lq, 0, 0));
+                t[j][b] = __builtin_bit_cast(half8, __builtin_amdgcn_raw_buffer_load_b128(  // zeros past the last chunk
+                    rt, c + j < p.chunks ? (uint32_t)(16 * b + lrow) * rec_bytes + (uint32_t)(c + j) * 64u + 16u * (uint32_t)lq
+                                         : kOutOfRange, 0, 0));
         int todo = all;
         while (const uint64_t any = __ballot(todo != 0)) {
             const int src = __ffsll((unsigned long long)any) - 1;
