@@ -138,3 +138,20 @@ def test_infinite_la(gsr, native, shape):
     assert np.isinf(want).any()
     for got in calls(gsr, native, a, b, la, lb, ids, scales, "none"):
         agree(got, want, slack)
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 512, 1, 1), (16, 200, 1032, 4, 8), (40, 136, 264, 3, 24), (150, 264, 520, 5, 40),
+                                   (300, 136, 72, 2, 200), (33, 101, 77, 3, 5), (200, 301, 130, 4, 17)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_infinite_a(gsr, native, shape):
+    """An infinity in A, with a rank that fills no whole chunks: the ranks that
+    are not there add nothing."""
+    a, b, la, lb, ids = positive_inputs(shape, seed=shape[0] + 2)
+    a[0, 5] = INF
+    a[-1, 1] = INF if len(a) == 1 else -INF
+    a[len(a) // 2, shape[2] - 1] = INF
+    scales = [1.0, 0.5, 2.0, 1.0, 0.25][:shape[3]]
+    want, _, slack = formula(a, b, la, lb, ids, scales)
+    assert np.isinf(want).any() and not np.isnan(want).any()
+    for got in calls(gsr, native, a, b, la, lb, ids, scales, "none"):
+        agree(got, want, slack)

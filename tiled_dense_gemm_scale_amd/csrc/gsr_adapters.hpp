@@ -284,6 +284,13 @@ __device__ __forceinline__ float shrink_sum(const uint8_t* smem, int row, int q,
     return v;
 }
 
+// The scaled sum of rank c of chunk j: 0 past the last rank, where zeros in La's
+// place met whatever A and the scale hold (NaN for an infinity or a NaN).
+__device__ __forceinline__ float shrink_rank(const ShrinkArgs& s, int j, int c, float sum)
+{
+    return kAdapterChunk * j + c < s.rank ? sum : 0.0f;
+}
+
 // Writes the records of row `row` of t and t_scale: this thread holds ranks
 // c + 16 j of the row for j in v[], the 16 lanes around it the rest.  With
 // device-scope stores, for readers in the same launch.
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(512) adapter_shrink_rows_kernel(ShrinkArgs s)
         for (int j = 0; j < PER; ++j) {
             const int cq = q + QT * j;
             if (cq >= NB || i * NB + cq >= s.chunks) continue;
-            const float u = shrink_sum<T>(smem, row, cq, c) * scale;
+            const float u = shrink_rank(s, i * NB + cq, c, shrink_sum<T>(smem, row, cq, c) * scale);
             v[i * PER + j] = u;
             odd |= !(fabsf(u) <= 3.0e38f);
             big = fmaxf(big, fabsf(u));
@@ -382,14 +389,14 @@ typedef ShrinkCfg<1, 8, 8, 2> ShrinkParts;
 // The finished row of a block: `at` gives the thread's rank c of chunk j summed
 // over the parts; scaled, with the row's largest value.
 template <int N, class F>
-__device__ __forceinline__ float shrink_row(const ShrinkArgs& s, int l, float (&v)[N], F&& at)
+__device__ __forceinline__ float shrink_row(const ShrinkArgs& s, int l, int c, float (&v)[N], F&& at)
 {
     const float scale = (l >= 0 && s.scales != nullptr) ? s.scales[l] : 1.0f;
     float big = 0.0f;
     bool odd = false;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        v[j] = j < s.chunks ? at(j) * scale : 0.0f;
+        v[j] = j < s.chunks ? shrink_rank(s, j, c, at(j) * scale) : 0.0f;
         odd |= !(fabsf(v[j]) <= 3.0e38f);
         big = fmaxf(big, fabsf(v[j]));
     }
@@ -441,7 +448,7 @@ __device__ __forceinline__ bool shrink_part(const ShrinkArgs& s, uint8_t* smem, 
     if (tid == 0) __hip_atomic_store(s.count + block, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (tid < 256) {
         float v[kShrinkRounds];
-        const float big = shrink_row(s, l, v, [&](int j) {
+        const float big = shrink_row(s, l, c, v, [&](int j) {
             float sum = 0.0f;
             for (int g = 0; g < s.parts; g += 8) {
                 float u[8];
@@ -554,7 +561,7 @@ __device__ __forceinline__ void shrink_here(const ShrinkArgs& s, uint8_t* smem, 
                 shrink_sums<VEC, T>(s, smem, id, m0 + b0, j, g * s.kchunk, min(s.K, (g + 1) * s.kchunk), 0, 1);
                 v[0] += shrink_sum<T>(smem, row, 0, c);
             }
-            v[0] *= scale;
+            v[0] = shrink_rank(s, j, c, v[0] * scale);
             odd |= !(fabsf(v[0]) <= 3.0e38f);
             big = fmaxf(big, fabsf(v[0]));
             if (tid < 256) *(volatile float*)(wait + 64 * j) = v[0];
