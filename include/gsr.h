@@ -318,10 +318,10 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
  *   ids  M adapter indices in any order; an index outside [0, adapters) is a
  *        row without an adapter
  *   scales  adapters binary32 values, or NULL (ones)
- * The inner sum is binary32 and enters the second product with 22 bits of its
- * row's largest value; both sums, the scale, the bias and the activation are
- * binary32, with one narrowing to binary16.  An adapter's values reach its
- * own rows only, whatever they are.  rank is at most 256
+ * The inner sum is binary32 and enters the second product to within 2^-23 of
+ * its row's largest value, whatever that is; both sums, the scale, the bias and
+ * the activation are binary32, with one narrowing to binary16.  An adapter's
+ * values reach its own rows only, whatever they are.  rank is at most 256
  * (GSR_ERROR_TOO_LARGE); one adapter's La and Lb are below 2^31 bytes each
  * and the whole arrays may be larger.  adapters = 0 or rank = 0 is the product
  * alone.  Two kernels are enqueued, or, for at most 64 rows, one whose first

@@ -16,8 +16,8 @@
 // value is split into its fp16 rounding and the fp16 rounding of the rest,
 // which leaves at most 2^-23 of that largest value (hi has 11 bits, lo the 11
 // bits below, down to fp16's smallest step of 2^-24).  The product runs over
-// both halves and the power of two multiplies its fp32 result, so no
-// magnitude of t overflows or underflows.  Ranks go in chunks of 16: a chunk's
+// both halves and the power of two multiplies its fp32 result, so that holds
+// over all of fp32's range.  Ranks go in chunks of 16: a chunk's
 // record is its 16 hi values and then its 16 lo values, 64 bytes, the K = 32
 // operand of one 16x16x32 MFMA against the chunk of Lb taken twice.
 //
@@ -299,17 +299,17 @@ __device__ __forceinline__ void shrink_store(const ShrinkArgs& s, uint16_t* t, f
                                              int j0, int stride, const float (&v)[N], float big)
 {
     if (l < 0) return;
-    const bool odd = !(big <= 3.0e38f);
-    // 2^e <= big < 2^(e + 1); zeros, and rows with an infinity or a NaN, keep 2^0
+    const bool odd = !(big < __builtin_inff());
+    // 2^e <= big < 2^(e + 1), or the least normal number's 2^e; zeros, and rows
+    // with an infinity or a NaN, keep 2^0
     int e = 0;
-    if (!odd && big > 0.0f) e = min(max(__builtin_amdgcn_frexp_expf(big) - 1, -40), 100);
-    const float down = ldexpf(1.0f, -e);
+    if (!odd && big > 0.0f) e = max(__builtin_amdgcn_frexp_expf(big) - 1, -126);
     if (c == 0 && j0 == 0) __hip_atomic_store(t_scale + row, ldexpf(1.0f, e), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int j = j0 + i * stride;
         if (j >= s.chunks) break;
-        const float x = v[i] * down;
+        const float x = ldexpf(v[i], -e);
         const _Float16 hi = (_Float16)x;
         const _Float16 lo = odd ? (_Float16)0.0f : (_Float16)(x - (float)hi);
         uint16_t* rec = t + (row * s.chunks + j) * 32;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(512) adapter_shrink_rows_kernel(ShrinkArgs s)
             if (cq >= NB || i * NB + cq >= s.chunks) continue;
             const float u = shrink_rank(s, i * NB + cq, c, shrink_sum<T>(smem, row, cq, c) * scale);
             v[i * PER + j] = u;
-            odd |= !(fabsf(u) <= 3.0e38f);
+            odd |= !(fabsf(u) < __builtin_inff());
             big = fmaxf(big, fabsf(u));
         }
     }
@@ -397,7 +397,7 @@ __device__ __forceinline__ float shrink_row(const ShrinkArgs& s, int l, int c, f
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         v[j] = j < s.chunks ? shrink_rank(s, j, c, at(j) * scale) : 0.0f;
-        odd |= !(fabsf(v[j]) <= 3.0e38f);
+        odd |= !(fabsf(v[j]) < __builtin_inff());
         big = fmaxf(big, fabsf(v[j]));
     }
     big = odd ? __builtin_inff() : big;
@@ -562,7 +562,7 @@ __device__ __forceinline__ void shrink_here(const ShrinkArgs& s, uint8_t* smem, 
                 v[0] += shrink_sum<T>(smem, row, 0, c);
             }
             v[0] = shrink_rank(s, j, c, v[0] * scale);
-            odd |= !(fabsf(v[0]) <= 3.0e38f);
+            odd |= !(fabsf(v[0]) < __builtin_inff());
             big = fmaxf(big, fabsf(v[0]));
             if (tid < 256) *(volatile float*)(wait + 64 * j) = v[0];
         }
