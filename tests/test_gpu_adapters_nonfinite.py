@@ -155,3 +155,25 @@ def test_infinite_a(gsr, native, shape):
     assert np.isinf(want).any() and not np.isnan(want).any()
     for got in calls(gsr, native, a, b, la, lb, ids, scales, "none"):
         agree(got, want, slack)
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 512, 1, 16), (16, 200, 1032, 4, 8), (40, 136, 264, 3, 24), (150, 264, 520, 5, 40),
+                                   (300, 264, 136, 3, 16), (300, 136, 72, 2, 256), (33, 101, 77, 3, 5), (200, 301, 130, 4, 17)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_infinities_on_both_sides(gsr, native, shape):
+    """Infinite inner sums meet infinities of Lb, and infinite products of A and B
+    meet infinite ones of the adapter, of the same sign and of the other."""
+    a, b, la, lb, ids = positive_inputs(shape, seed=shape[0] + 3)
+    a[len(a) // 2, 1] = -INF
+    b[2, 11], b[3, 12] = INF, -INF
+    a[:, 2:4] = a[:, 2:4].abs() + 1.0  # B's infinities come through with their sign
+    a = torch.where(a == 0, torch.ones_like(a), a)
+    la[0, 0, 4] = INF
+    lb[0, 3, 0], lb[0, 5, shape[4] - 1] = INF, -INF
+    lb[-1, 11, 0], lb[-1, 12, 0], lb[-1, 13, 0] = INF, INF, -INF
+    scales = [1.0, 0.5, 2.0, 1.0, 0.25][:shape[3]]
+    want, t, slack = formula(a, b, la, lb, ids, scales)
+    fin = np.isfinite(t) & ((ids >= 0) & (ids < shape[3]))[:, None]
+    assert not fin.any() or np.abs(t[fin]).min() > 1e-6  # no sign in doubt
+    for got in calls(gsr, native, a, b, la, lb, ids, scales, "none"):
+        agree(got, want, slack)

@@ -300,11 +300,12 @@ __device__ __forceinline__ void shrink_store(const ShrinkArgs& s, uint16_t* t, f
 {
     if (l < 0) return;
     const bool odd = !(big < __builtin_inff());
-    // 2^e <= big < 2^(e + 1), or the least normal number's 2^e; zeros, and rows
-    // with an infinity or a NaN, keep 2^0
+    // 2^e <= big < 2^(e + 1), or the least normal number's 2^e; zeros keep 2^0
     int e = 0;
     if (!odd && big > 0.0f) e = max(__builtin_amdgcn_frexp_expf(big) - 1, -126);
-    if (c == 0 && j0 == 0) __hip_atomic_store(t_scale + row, ldexpf(1.0f, e), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // the power of two, negative for a row with an infinity or a NaN
+    if (c == 0 && j0 == 0)
+        __hip_atomic_store(t_scale + row, odd ? -1.0f : ldexpf(1.0f, e), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int j = j0 + i * stride;
@@ -638,9 +639,10 @@ __device__ __forceinline__ half8 finite8(half8 v)
 // t = 0, and the rows' scales multiply all accumulators once at the end.
 // (4097 x 11008 x 4096 with 9 runs of rank 16 takes 334 us in all beside 311
 // with no row's id an adapter's, 14 of them the inner sums'; rank 64 366, 22.)
-// 0 * infinity and 0 * NaN would then reach those rows: fragments with such
-// values have them replaced by zeros, and the caller, told so by the returned
-// true, runs adapter_nonfinite16 after its epilogue.
+// 0 * infinity and 0 * NaN would then reach those rows: infinities and NaN of Lb
+// have zeros in their place, rows of t with such values take no part, and the
+// caller, told so by the returned true, runs adapter_nonfinite16 before its
+// epilogue.
 template <int CB, bool VEC, int FN, int FM>
 __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0)
 {
@@ -651,6 +653,7 @@ __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[F
     const __amdgpu_buffer_rsrc_t rsc = make_rsrc(p.t_scale + m0, rows * 4u);
     const __amdgpu_buffer_rsrc_t rt = make_rsrc(p.t + (int64_t)m0 * p.chunks * 32, rows * rec_bytes);
     int id[FM], all = 0;
+    bool odd = false;
     float sc[FM];
 #pragma unroll
     for (int b = 0; b < FM; ++b) id[b] = (int)__builtin_amdgcn_raw_buffer_load_b32(rid, (uint32_t)(16 * b + lrow) * 4u, 0, 0);
@@ -659,10 +662,12 @@ __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[F
 #pragma unroll
     for (int b = 0; b < FM; ++b) {
         if ((uint32_t)(16 * b + lrow) >= rows || (uint32_t)id[b] >= (uint32_t)p.adapters) id[b] = -1, sc[b] = 1.0f;
+        odd |= sc[b] < 0.0f;
+        if (sc[b] < 0.0f) id[b] = -1, sc[b] = 1.0f;  // all of such a row is adapter_nonfinite16's
         all |= (id[b] >= 0 ? 1 : 0) << b;
     }
-    if (__ballot(all != 0) == 0) return false;
-    bool odd = false;
+    odd = __ballot(odd) != 0;
+    if (__ballot(all != 0) == 0) return odd;
     for (int c = 0; c < p.chunks; c += CB) {
         half8 t[CB][FM];
 #pragma unroll
@@ -692,14 +697,12 @@ __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[F
                     // value by value: one fragment at a time, for the registers' sake
                     if constexpr (!VEC) asm volatile("" : "+v"(x[j][a]));
                 }
-            uint32_t bad = 0;
+            half8 seen = (half8)(_Float16)0.0f;
 #pragma unroll
             for (int j = 0; j < CB; ++j)
 #pragma unroll
-                for (int a = 0; a < FN; ++a)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) bad |= nonfinite2(__builtin_bit_cast(u32x4, x[j][a])[i]);
-            if (__ballot(bad != 0) != 0) {
+                for (int a = 0; a < FN; ++a) seen = look_odd(x[j][a], seen);
+            if (__ballot(any_odd(seen)) != 0) {
                 odd = true;
 #pragma unroll
                 for (int j = 0; j < CB; ++j)
@@ -733,34 +736,50 @@ __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[F
     return odd;
 }
 
-// What adapter_start16 left out: outputs of the wave's WTM x WTN sub-tile whose
-// adapter has an infinity or a NaN in their column's Lb row become what that
-// makes of the sum (a NaN that is there already stays).  The wave has stored
-// the sub-tile itself.
-template <int WTM, int WTN>
-__device__ __forceinline__ void adapter_nonfinite16(const Problem& p, int m0, int n0)
+// What adapter_start16 left out: acc += what the infinities and NaN of t and Lb
+// make of each sum.  A sum with one is an infinity or a NaN, and which is
+// told by the hi half of t alone, which has the sign of t; finite sums are
+// left alone, and so are the rows of other adapters, which share the matrix
+// instructions.  Four blocks of columns at a time, for the registers' sake.
+template <bool VEC, int FN, int FM>
+__device__ __forceinline__ void adapter_nonfinite16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0)
 {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const int lane = threadIdx.x & 63;
-    for (int m = m0; m < min(m0 + WTM, p.M); ++m) {
-        const int l = p.ids[m];
-        if ((uint32_t)l >= (uint32_t)p.adapters) continue;
-        for (int n = n0 + lane; n < min(n0 + WTN, p.N); n += 64) {
-            const uint16_t* row = p.lb + ((int64_t)l * p.N + n) * p.rank;
-            const uint16_t* rec = p.t + (int64_t)m * p.chunks * 32;
-            float sum = 0.0f;
-            bool odd = false;
-            for (int r = 0; r < p.rank; ++r) {
-                if ((row[r] & 0x7c00u) != 0x7c00u) continue;
-                const uint16_t* h = rec + (r / kAdapterChunk) * 32 + r % kAdapterChunk;
-                const float t = (float)__builtin_bit_cast(_Float16, h[0]) + (float)__builtin_bit_cast(_Float16, h[16]);
-                sum += t * (float)__builtin_bit_cast(_Float16, row[r]);
-                odd = true;
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane), "+s"(m0), "+s"(n0));  // nothing of this is made before the product's loop and kept across it
+    const int lrow = lane & 15, lq = lane >> 4;
+    constexpr int GROUP = 4;
+    static_assert(FN % GROUP == 0, "blocks of columns");
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+        const int id = adapter_of(p.ids, m0 + 16 * b + lrow, p.M, p.adapters);
+        const uint16_t* const rec = p.t + (int64_t)(id >= 0 ? m0 + 16 * b + lrow : 0) * p.chunks * 32 + 8 * (lq & 1);
+#pragma unroll
+        for (int a0 = 0; a0 < FN; a0 += GROUP) {
+            f32x4 sum[GROUP] = {};
+            for_each_adapter(id, [&](int l) {
+                const __amdgpu_buffer_rsrc_t rl = lb_rsrc(p, l);
+#pragma unroll 1
+                for (int c = 0; c < p.chunks; ++c) {
+                    const bool hi = lq < 2;  // the MFMA's other half of K is zeros
+                    const half8 y = hi ? __builtin_bit_cast(half8, *(const u32x4*)(rec + 32 * c)) : (half8)(_Float16)0.0f;
+#pragma unroll
+                    for (int a = 0; a < GROUP; ++a) {
+                        const int n = n0 + 16 * (a0 + a) + lrow;
+                        const half8 x = piece8<VEC>(rl, (uint32_t)n * (uint32_t)p.rank, kAdapterChunk * c + 8 * (lq & 1), p.rank,
+                                                    hi && n < p.N);
+                        const f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, f32x4{}, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sum[a][i] += (id == l && !(fabsf(d[i]) < __builtin_inff())) ? d[i] : 0.0f;
+                    }
+                }
+            });
+#pragma unroll
+            for (int a = 0; a < GROUP; ++a) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[a0 + a][b][i] += sum[a][i];
+                asm volatile("" : "+a"(acc[a0 + a][b]));
             }
-            uint16_t* c = p.C + (int64_t)m * p.N + n;
-            if (!odd || (c[0] & 0x7fffu) > 0x7c00u) continue;
-            const float b = p.bias ? (float)__builtin_bit_cast(_Float16, p.bias[n]) : 0.0f;
-            c[0] = __builtin_bit_cast(uint16_t, (_Float16)activate(p.alpha * sum + b, p.act));
         }
     }
 }
@@ -922,7 +941,7 @@ struct AdapterItems {
                     d = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.x[j][a], w.hi[j][b], d, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[a][b][i] = id[b] == w.ls[j] ? acc[a][b][i] + sc[b] * d[i] : acc[a][b][i];
+                        acc[a][b][i] = id[b] == w.ls[j] ? acc[a][b][i] + fabsf(sc[b]) * d[i] : acc[a][b][i];
                 }
             }
         }

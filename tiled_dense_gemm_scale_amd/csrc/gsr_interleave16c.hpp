@@ -392,9 +392,9 @@ __global__ void __launch_bounds__(512) gemm_scale_relu_ilv16c_kernel(Problem p)
     // last of them the wait states a matrix result needs before other
     // instructions read it (64, well above the 16x16x32 requirement).
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-    ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
     if constexpr (ADAPT != kAdaptNone)
-        if (odd) adapter_nonfinite16<T::WTM, T::WTN>(p, m0 + wm * T::WTM, n0 + wn * T::WTN);
+        if (odd) adapter_nonfinite16<ADAPT == kAdaptVec>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
+    ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
 }
 
 }  // namespace gsr

@@ -393,9 +393,13 @@ gemm_scale_relu_ilv16d_kernel(Problem p)
     // last of them the wait states a matrix result needs before other
     // instructions read it (64, well above the 16x16x32 requirement).
     asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-    ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
     if constexpr (ADAPT != kAdaptNone)
-        if (odd) adapter_nonfinite16<T::WTM, T::WTN>(p, m0 + wm * T::WTM, n0 + wn * T::WTN);
+        if (odd) {  // a copy of the epilogue of its own: behind a common one, accumulators spilled on either way
+            adapter_nonfinite16<ADAPT == kAdaptVec>(p, acc, m0 + wm * T::WTM, n0 + wn * T::WTN);
+            ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
+            return;
+        }
+    ilv16_epilogue_t<T>(p, acc, smem, m0, n0, wm, wn, wave);
 }
 
 }  // namespace gsr

@@ -180,8 +180,8 @@ enum : int { kAdaptNone = 0, kAdaptVec = 1, kAdaptElem = 2, kAdaptShared = 3 };
 // gsr_adapters.hpp
 template <int CB, bool VEC, int FN, int FM>
 __device__ bool adapter_start16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0);
-template <int WTM, int WTN>
-__device__ void adapter_nonfinite16(const Problem& p, int m0, int n0);
+template <bool VEC, int FN, int FM>
+__device__ void adapter_nonfinite16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0);
 template <int TN, int TM, bool SHARED>
 struct AdapterItems;
 
