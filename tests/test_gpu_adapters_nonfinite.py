@@ -49,7 +49,11 @@ def formula(a, b, la, lb, ids, scales):
                 tmag = abs(scales[l]) * products(mag(a64[m:m + 1]), mag(la64[l]))[0]
                 terr = (K + 40) * u * tmag + 2.0 ** -23 * mag(t[m]).max()
                 off[m] += products((terr + (2 * R + 4) * u * mag(t[m]))[None], mag(lb64[l]))[0]
-    return v, t, off + 2.0 ** -11 * (mag(v) + off) + 2.0 ** -25
+    slack = off + 2.0 ** -11 * (mag(v) + off) + 2.0 ** -25
+    # finite sums from 65520 on are rounded to fp16's infinity; none is in doubt
+    past = np.isfinite(v) & (np.abs(v) >= 65520)
+    assert not (np.isfinite(v) & (np.abs(np.abs(v) - 65520) <= off)).any()
+    return np.where(past, np.copysign(np.inf, v), v), t, slack
 
 
 def agree(got, want, slack):
@@ -175,5 +179,30 @@ def test_infinities_on_both_sides(gsr, native, shape):
     want, t, slack = formula(a, b, la, lb, ids, scales)
     fin = np.isfinite(t) & ((ids >= 0) & (ids < shape[3]))[:, None]
     assert not fin.any() or np.abs(t[fin]).min() > 1e-6  # no sign in doubt
+    for got in calls(gsr, native, a, b, la, lb, ids, scales, "none"):
+        agree(got, want, slack)
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 512, 1, 16), (16, 200, 1032, 4, 8), (40, 136, 264, 3, 24), (150, 264, 520, 5, 40),
+                                   (300, 136, 72, 2, 256), (33, 101, 77, 3, 5), (200, 301, 130, 4, 17)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_inner_sums_of_unlike_size_keep_their_sign(gsr, native, shape):
+    """An inner sum of 2^-30 and less of its row's largest, which leaves finite
+    outputs alone, gives its sign to an infinity of Lb; and one far above fp16's
+    range in a row with an infinite one stays finite beside it."""
+    M, N, K, L, R = shape
+    a, b, la, lb, ids = positive_inputs(shape, seed=shape[0] + 4)
+    g = torch.Generator().manual_seed(K)
+    a = torch.randint(1, 3, a.shape, generator=g).half()
+    la[:, 0] = 100.0
+    la[:, R - 1] = torch.randint(0, 2, (L, K), generator=g).half() * 2.0 ** -23 - 2.0 ** -24  # +-2^-24
+    lb[:, 3, R - 1], lb[:, 6, R - 1] = INF, -INF
+    la[L - 1, 1, 2], la[L - 1, 2] = INF, 60000.0
+    lb[L - 1, :, 2] *= -1.0
+    scales = [1.0, -0.5, 2.0, 1.0, 0.25][:L]
+    want, t, slack = formula(a, b, la, lb, ids, scales)
+    ours = t[(ids >= 0) & (ids < L)]
+    assert (np.abs(ours[:, R - 1]) <= 2.0 ** -26 * np.nanmax(np.abs(np.where(np.isfinite(ours), ours, 0.0)), 1)).all()
+    assert np.isinf(want[ids == L - 1][:, 8:]).all()
     for got in calls(gsr, native, a, b, la, lb, ids, scales, "none"):
         agree(got, want, slack)

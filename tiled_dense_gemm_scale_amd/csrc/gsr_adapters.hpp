@@ -311,8 +311,18 @@ __device__ __forceinline__ void shrink_store(const ShrinkArgs& s, uint16_t* t, f
         const int j = j0 + i * stride;
         if (j >= s.chunks) break;
         const float x = ldexpf(v[i], -e);
-        const _Float16 hi = (_Float16)x;
-        const _Float16 lo = odd ? (_Float16)0.0f : (_Float16)(x - (float)hi);
+        // The hi half has the value's sign, for the products with infinities of Lb:
+        // fp16's smallest step where it would be zero.  In a row with an infinity
+        // or a NaN, which makes one of every sum, the other values are their signs
+        // alone (they may be past fp16's range).
+        const float sign = v[i] > 0.0f ? 1.0f : v[i] < 0.0f ? -1.0f : 0.0f;
+        _Float16 hi = (_Float16)x, lo = (_Float16)0.0f;
+        if (!odd) {
+            if (hi == (_Float16)0.0f) hi = (_Float16)(sign * 0x1p-24f);
+            lo = (_Float16)(x - (float)hi);
+        } else if (fabsf(v[i]) < __builtin_inff()) {
+            hi = (_Float16)sign;
+        }
         uint16_t* rec = t + (row * s.chunks + j) * 32;
         __hip_atomic_store(rec + c, __builtin_bit_cast(uint16_t, hi), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __hip_atomic_store(rec + 16 + c, __builtin_bit_cast(uint16_t, lo), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
