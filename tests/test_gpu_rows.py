@@ -338,3 +338,34 @@ def test_python_refusals_on_the_device(gsr):
     for bad in (lambda: gsr.gather_rows(h, r, out=h), lambda: gsr.group_rows(i32, 0), lambda: gsr.group_rows(i32, 1025)):
         with pytest.raises(gsr.GsrError):
             bad()
+
+
+def test_group_rows_of_the_largest_count(gsr):
+    """2^31 - 1 slots, whose last block ends at 2^31: every slot in its place."""
+    n, E, period = 2 ** 31 - 1, 7, 8  # slot i has id i mod 8; 7 is dropped
+    ids = torch.arange(n, dtype=torch.int32, device=DEV)
+    ids.remainder_(period)
+    offsets = torch.full((E + 1,), -7, dtype=torch.int32, device=DEV)
+    rows, positions = (torch.full((n,), -7, dtype=torch.int32, device=DEV) for _ in range(2))
+    say(f"group of {n} slots")
+    gsr.group_rows(ids, E, offsets=offsets, rows=rows, positions=positions)
+    torch.cuda.synchronize()
+    counts = [(n - e + period - 1) // period for e in range(E)]
+    starts = [sum(counts[:e]) for e in range(E + 1)]
+    assert offsets.tolist() == starts
+    say("group of the largest count: positions")
+    base = torch.tensor(starts[:E] + [0], device=DEV)
+    step = 1 << 27
+    for lo in range(0, n, step):
+        i = torch.arange(lo, min(lo + step, n), device=DEV)
+        want = torch.where(i % period < E, base[i % period] + i // period, -1)
+        assert torch.equal(positions[lo:lo + step].long(), want)
+    say("group of the largest count: rows")
+    for e in range(E):
+        for lo in range(0, counts[e], step):
+            i = torch.arange(lo, min(lo + step, counts[e]), device=DEV)
+            assert torch.equal(rows[starts[e] + lo:starts[e] + lo + i.numel()].long(), i * period + e)
+    for lo in range(starts[E], n, step):
+        assert bool((rows[lo:lo + step] == -1).all())
+    del ids, rows, positions
+    torch.cuda.empty_cache()

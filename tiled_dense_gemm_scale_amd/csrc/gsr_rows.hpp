@@ -10,6 +10,7 @@
 // so NaN or infinity there does not spread.
 #pragma once
 
+#include "gsr_group_plan.hpp"
 #include "gsr_kernels.hpp"
 
 namespace gsr {
@@ -36,13 +37,7 @@ namespace gsr {
 // 64 slots of 8 groups take 2.8 us, 8192 of 64 11.8 (walked twice: 15.8), and
 // both launches for 131072 of 64 groups 11.9 (blocks of 4096 slots: 13.7; of
 // 2048 and walked twice: 15.7), of 256 groups 16.7 (4096: 17.7, 1024: 20.1).
-constexpr int kGroupMax = 1024;       // groups
-constexpr int kGroupWaves = 16;       // waves of a full workgroup
-constexpr int kGroupSingle = 8192;    // slots one workgroup handles alone
-constexpr int kGroupChunk = 2048;     // smallest block of the two-launch form
-constexpr int kGroupCounts = 20000;   // counts per block from which blocks grow
-constexpr int kGroupKept = 8;         // steps whose keys and places a wave keeps
-constexpr int kGroupBlocks = 256;     // most blocks of it
+constexpr int kGroupKept = 8;  // steps whose keys and places a wave keeps
 
 struct GroupArgs {
     const void* ids;      // n ids of 4 or 8 bytes
@@ -80,11 +75,10 @@ __global__ void __launch_bounds__(1024) group_count_kernel(GroupArgs g)
     const int nb = g.groups + 1;
     for (int i = threadIdx.x; i < nb; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
-    const int beg = blockIdx.x * g.chunk, end = min(g.n, beg + g.chunk);
+    const GroupSpan all = group_block(g.n, g.chunk, blockIdx.x);
     const int lane = threadIdx.x & 63;
-    for (int i0 = beg + (int)(threadIdx.x & ~63u); i0 < end; i0 += blockDim.x) {
-        const int i = i0 + lane;
-        const int key = i < end ? group_key<ID>(g, i) : -1;
+    for (int at = (int)(threadIdx.x & ~63u); at < all.len; at += blockDim.x) {
+        const int key = at + lane < all.len ? group_key<ID>(g, all.beg + at + lane) : -1;
         const uint64_t m = same_key(key, g.bits);
         if (key >= 0 && lane == __ffsll((unsigned long long)m) - 1) atomicAdd(&cnt[key], (uint32_t)__popcll(m));
     }
@@ -103,9 +97,7 @@ __global__ void __launch_bounds__(1024) group_place_kernel(GroupArgs g)
     for (int i = tid; i < nb; i += nt) total[i] = prior[i] = 0;
     __syncthreads();
 
-    const int beg = blockIdx.x * g.chunk, end = min(g.n, beg + g.chunk);
-    const int run = ((end - beg + waves - 1) / waves + 63) & ~63;
-    const int wbeg = beg + wave * run, wend = min(end, wbeg + run);
+    const GroupSpan run = group_run(group_block(g.n, g.chunk, blockIdx.x), wave, waves);
     uint32_t* const mine = cnt + wave * nb;
     // the place of this lane's slot of a step among the wave's slots of its key
     auto place_of = [&](int key) {
@@ -115,19 +107,19 @@ __global__ void __launch_bounds__(1024) group_place_kernel(GroupArgs g)
         if (key >= 0 && lane == leader) first = atomicAdd(&mine[key], (uint32_t)__popcll(m));
         return (uint32_t)__shfl((int)first, key >= 0 ? leader : lane) + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
     };
-    const bool kept = run <= 64 * kGroupKept;
+    const bool kept = run.len <= 64 * kGroupKept;
     int key[kGroupKept];
     uint32_t place[kGroupKept];
     if (kept) {
 #pragma unroll
         for (int s = 0; s < kGroupKept; ++s) {
-            const int i = wbeg + 64 * s + lane;
-            key[s] = i < wend ? group_key<ID>(g, i) : -1;
+            const int at = 64 * s + lane;
+            key[s] = at < run.len ? group_key<ID>(g, run.beg + at) : -1;
         }
 #pragma unroll
-        for (int s = 0; s < kGroupKept; ++s) place[s] = wbeg + 64 * s < wend ? place_of(key[s]) : 0u;
+        for (int s = 0; s < kGroupKept; ++s) place[s] = 64 * s < run.len ? place_of(key[s]) : 0u;
     } else {
-        for (int i0 = wbeg; i0 < wend; i0 += 64) place_of(i0 + lane < wend ? group_key<ID>(g, i0 + lane) : -1);
+        for (int at = 0; at < run.len; at += 64) place_of(at + lane < run.len ? group_key<ID>(g, run.beg + at + lane) : -1);
     }
     if (g.blocks > 1) {
         // every block's count of key e, and those of the blocks before this one
@@ -186,10 +178,11 @@ __global__ void __launch_bounds__(1024) group_place_kernel(GroupArgs g)
     if (kept) {
 #pragma unroll
         for (int s = 0; s < kGroupKept; ++s)
-            if (key[s] >= 0) put(wbeg + 64 * s + lane, key[s], mine[key[s]] + place[s]);
+            if (key[s] >= 0) put(run.beg + 64 * s + lane, key[s], mine[key[s]] + place[s]);
     } else {
-        for (int i0 = wbeg; i0 < wend; i0 += 64) {
-            const int i = i0 + lane, k = i < wend ? group_key<ID>(g, i) : -1;
+        for (int at = 0; at < run.len; at += 64) {
+            const bool in = at + lane < run.len;
+            const int i = run.beg + at + (in ? lane : 0), k = in ? group_key<ID>(g, i) : -1;
             put(i, k, place_of(k));
         }
     }

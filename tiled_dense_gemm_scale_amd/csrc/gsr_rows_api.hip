@@ -13,23 +13,10 @@ namespace {
 
 using namespace gsr::host;
 
+using gsr::GroupPlan;
+using gsr::group_plan;
+
 constexpr int64_t kLimit = (int64_t)1 << 31;
-
-struct GroupPlan {
-    int chunk, blocks;
-};
-
-// Up to kGroupSingle slots: one block.  Above, blocks of kGroupChunk slots or,
-// where the counts that each block has to read (blocks x groups) pass
-// kGroupCounts, of up to four times as many; kGroupBlocks blocks at most.
-GroupPlan group_plan(int64_t n, int64_t groups)
-{
-    if (n <= gsr::kGroupSingle) return GroupPlan{(int)n, 1};
-    int64_t chunk = gsr::kGroupChunk;
-    while (chunk < 4 * gsr::kGroupChunk && cdiv(n, chunk) * (groups + 1) > gsr::kGroupCounts) chunk *= 2;
-    chunk = std::max(chunk, cdiv(cdiv(n, gsr::kGroupBlocks), 1024) * 1024);
-    return GroupPlan{(int)chunk, (int)cdiv(n, chunk)};
-}
 
 // slots = tokens * k, or -1 (invalid) / -2 (too large)
 int64_t slots_of(int64_t tokens, int64_t k)
