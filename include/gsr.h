@@ -226,7 +226,7 @@ int64_t gsr_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * [0, groups) is dropped.  Rows of fp16 values are row-major and contiguous,
  * `width` values each; any 2-byte alignment is accepted and the widest unit
  * (16, 8, 4 or 2 bytes) that the addresses and the width allow is used.
- * Counts are below 2^31 (GSR_ERROR_TOO_LARGE), matrices may be larger than
+ * Counts are below 2^31 and widths below 2^30 (GSR_ERROR_TOO_LARGE), matrices may be larger than
  * 2^31 bytes.  Outputs must not overlap inputs or each other
  * (GSR_ERROR_INVALID_VALUE).  No kernel here uses atomics on memory: equal
  * inputs give equal bits.  Ownership, streams and errors as above. */

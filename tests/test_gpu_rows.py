@@ -369,3 +369,34 @@ def test_group_rows_of_the_largest_count(gsr):
         assert bool((rows[lo:lo + step] == -1).all())
     del ids, rows, positions
     torch.cuda.empty_cache()
+
+
+def test_more_rows_than_a_grid_has_threads(gsr):
+    """Rows x 256 threads past 2^32: 2^24 + 3 rows of 129 odd values for gather and
+    combine, 2^26 + 5 tokens of one value for the gradient."""
+    n, H, T = (1 << 24) + 3, 129, 1000
+    x = torch.randint(-50, 50, (T, H), device=DEV).half()
+    rows = torch.arange(n, device=DEV).remainder_(T + 1).int()  # T itself is no row
+    padded = torch.cat([x, torch.zeros(1, H, dtype=torch.float16, device=DEV)])
+    for name, go in (("gather", lambda: gsr.gather_rows(x, rows)), ("combine", lambda: gsr.combine_rows(x, rows))):
+        say(f"{name} of {n} rows of {H}")
+        out = go()
+        for lo in range(0, n, 1 << 22):
+            assert torch.equal(out[lo:lo + (1 << 22)], padded[rows[lo:lo + (1 << 22)].long()])
+        del out
+    n = (1 << 26) + 5
+    say(f"gradient of {n} tokens")
+    dout = torch.arange(n, device=DEV).remainder_(2000).half()[:, None]
+    positions = torch.arange(n, device=DEV).flip(0).int()[:, None]
+    w = torch.full((n, 1), 0.5, device=DEV)
+    y = torch.full((n, 1), 2.0, dtype=torch.float16, device=DEV)
+    rows = positions.flatten().clone()
+    rows[7] = -1  # token n - 8's row, which then no choice names
+    positions[n - 8] = -1
+    dy, dw = gsr.combine_rows_backward(dout, y, positions, w, rows)
+    want = 0.5 * dout.flip(0)
+    want[7] = 0
+    assert torch.equal(dy, want)
+    want = 2.0 * dout.float()
+    want[n - 8] = 0
+    assert torch.equal(dw, want)

@@ -253,6 +253,13 @@ struct RowArgs {
     int32_t lanes_log2;        // threads per row
 };
 
+// A grid dimension holds fewer than 2^32 threads (a launch with more runs a part
+// of them and reports nothing), so from kRowBlocks workgroups on a launch has
+// several rows of so many, numbered one behind the other.  (Reading the grid's
+// size instead of the constant costs a small call 0.6 us.)
+constexpr int64_t kRowBlocks = 1 << 20;
+__device__ __forceinline__ int64_t row_block() { return (int64_t)blockIdx.y * kRowBlocks + blockIdx.x; }
+
 // out[p] = x[rows[p]], zeros where rows[p] names no row of x.  2^lanes_log2
 // threads walk a row; their loads of four units are in flight together.  It
 // runs at the rate of a copy: 4098 rows of 4096 (50 MB) in 10.8 us, 8192x2x4096
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(RowArgs r)
 {
     typedef typename RowUnit<U>::type V;
     const int tpr = 1 << r.lanes_log2;
-    const int64_t p = (int64_t)blockIdx.x * (256 >> r.lanes_log2) + (threadIdx.x >> r.lanes_log2);
+    const int64_t p = row_block() * (256 >> r.lanes_log2) + (threadIdx.x >> r.lanes_log2);
     if (p >= r.P) return;
     const int32_t t = r.index[p];
     const bool ok = (uint32_t)t < (uint32_t)r.T;
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(RowArgs r)
 {
     typedef typename RowUnit<U>::type V;
     const int tpr = 1 << r.lanes_log2;
-    const int64_t t = (int64_t)blockIdx.x * (256 >> r.lanes_log2) + (threadIdx.x >> r.lanes_log2);
+    const int64_t t = row_block() * (256 >> r.lanes_log2) + (threadIdx.x >> r.lanes_log2);
     if (t >= r.T) return;
     const int32_t* pos = r.index + t * r.k;
     const float* w = r.weights ? r.weights + t * r.k : nullptr;
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(256) combine_rows_backward_kernel(RowArgs r)
 {
     typedef typename RowUnit<U>::type V;
     const int lane = threadIdx.x & 63;
-    const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), nw = (int64_t)gridDim.x * 4;
+    const int64_t wid = row_block() * 4 + (threadIdx.x >> 6), nw = (int64_t)gridDim.x * gridDim.y * 4;
     for (int64_t t = wid; t < r.T; t += nw) {
         const V* d = (const V*)r.x + t * r.units;
         for (int j0 = 0; j0 < r.k; j0 += J) {

@@ -58,6 +58,11 @@ rows_kernel backward_kernel(int unit, int units, int k, bool stream)
     return units > 64 ? backward16<4, 2>(stream) : backward16<4, 1>(stream);
 }
 
+dim3 row_grid(int64_t blocks)
+{
+    return dim3((unsigned)std::min(blocks, gsr::kRowBlocks), (unsigned)cdiv(blocks, gsr::kRowBlocks));
+}
+
 int status_of(hipError_t e) { return e == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH; }
 
 }  // namespace
@@ -147,7 +152,7 @@ int gsr_gather_rows(int64_t rows_out, int64_t rows_in, int64_t width, const void
     r.units = (int32_t)(width * 2 / unit);
     r.lanes_log2 = lanes_log2_of(r.units);
     return status_of(launch_kernel(GSR_BY_UNIT(gather_rows_kernel, unit),
-                                   dim3((unsigned)cdiv(rows_out, 256 >> r.lanes_log2)), dim3(256), (hipStream_t)stream, r));
+                                   row_grid(cdiv(rows_out, 256 >> r.lanes_log2)), dim3(256), (hipStream_t)stream, r));
 }
 
 int gsr_combine_rows(int64_t tokens, int64_t k, int64_t rows_in, int64_t width, const void* y, const int32_t* positions,
@@ -178,7 +183,7 @@ int gsr_combine_rows(int64_t tokens, int64_t k, int64_t rows_in, int64_t width, 
     r.units = (int32_t)(width * 2 / unit);
     r.lanes_log2 = lanes_log2_of(r.units);
     return status_of(launch_kernel(GSR_BY_UNIT(combine_rows_kernel, unit),
-                                   dim3((unsigned)cdiv(tokens, 256 >> r.lanes_log2)), dim3(256), (hipStream_t)stream, r));
+                                   row_grid(cdiv(tokens, 256 >> r.lanes_log2)), dim3(256), (hipStream_t)stream, r));
 }
 
 int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_t width, const void* dout, const void* y,
@@ -222,7 +227,7 @@ int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_
     r.units = (int32_t)(width * 2 / unit);
     const int64_t waves = std::max<int64_t>({tokens, cdiv(rows_in, 64), 1});
     return status_of(launch_kernel(backward_kernel(unit, r.units, r.k, weights != nullptr && rb >= (uint64_t)gsr::kStreamBytes),
-                                   dim3((unsigned)cdiv(waves, 4)), dim3(256), (hipStream_t)stream, r));
+                                   row_grid(cdiv(waves, 4)), dim3(256), (hipStream_t)stream, r));
 }
 
 }  // extern "C"
