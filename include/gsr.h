@@ -43,7 +43,8 @@ enum gsr_status {
      * nonzero; C's byte range overlapping A's or B's; alpha not finite */
     GSR_ERROR_INVALID_VALUE = 1,
     /* a dimension >= 2^31, or a matrix of 2^31 bytes or more (the kernels
-     * use 32-bit byte offsets) */
+     * use 32-bit byte offsets), or so many tiles that a launch would have
+     * 2^32 threads */
     GSR_ERROR_TOO_LARGE = 2,
     GSR_ERROR_NO_DEVICE = 3,          /* no HIP device is visible */
     GSR_ERROR_UNSUPPORTED_DEVICE = 4, /* the current device is not gfx950 */
@@ -297,9 +298,10 @@ int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_
  * (same kernels per tile, so a group's outputs are the bits of that call on
  * its rows with the same configuration).  GSR_ERROR_TOO_LARGE for P >= 2^31,
  * more than 1024 groups, K or N >= 2^22, one group's B of 2^31 bytes or more,
- * or, with rows, an A of 2^31 bytes or more; P x N, P x K and the whole B may
- * be larger.  config_id: -1, or one of 21, 22, 28, 31 and 32 (forced tile;
- * others GSR_ERROR_INVALID_CONFIG). */
+ * or, with rows, an A of 2^31 bytes or more, and where a launch would have
+ * 2^32 threads (a forced 64 x 64 tile: from P of about 2^29); P x N, P x K and
+ * the whole B may be larger.  config_id: -1, or one of 21, 22, 28, 31 and 32
+ * (forced tile; others GSR_ERROR_INVALID_CONFIG). */
 int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
                                 const void* A, int64_t a_rows, const int32_t* rows,
                                 const void* B, const void* bias, void* C, const int32_t* offsets,
@@ -322,10 +324,10 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
  * its row's largest value, whatever that is; both sums, the scale, the bias and
  * the activation are binary32, with one narrowing to binary16.  An adapter's
  * values reach its own rows only, whatever they are.  rank is at most 256
- * (GSR_ERROR_TOO_LARGE); one adapter's La and Lb are below 2^31 bytes each
- * and the whole arrays may be larger.  adapters = 0 or rank = 0 is the product
- * alone.  Two kernels are enqueued, or, for at most 64 rows, one whose first
- * workgroups make the inner sums.
+ * and M at most 2^27 - 16 (GSR_ERROR_TOO_LARGE); one adapter's La and Lb are
+ * below 2^31 bytes each and the whole arrays may be larger.  adapters = 0 or
+ * rank = 0 is the product alone.  Two kernels are enqueued, or, for at most 64
+ * rows, one whose first workgroups make the inner sums.
  *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its
  *              first 512 bytes zero before the first call and again after
  *              each), of gsr_adapter_workspace_bytes(M, N, K, rank) bytes;

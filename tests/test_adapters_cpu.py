@@ -60,3 +60,14 @@ def test_python_refusals():
         gsr.gemm_adapters(a.float(), b, la, lb, ids, ws)
     with pytest.raises(ValueError, match="device"):
         gsr.gemm_adapters(a, b, la, lb, ids, ws)
+
+
+def test_more_rows_than_a_launch_has_threads(native):
+    """From 2^27 - 15 rows on the inner sums' launch would have 2^32 threads."""
+    far = dict(N=1, K=1, A=FAKE, B=FAKE + GB, bias=0, C=FAKE + 2 * GB, ws=FAKE + 20 * GB, wsb=100 * GB, la=FAKE + 10 * GB,
+               lb=FAKE + 11 * GB, ids=FAKE + 12 * GB, scales=0)
+    for M in (2 ** 27 - 15, 2 ** 27, 2 ** 29):
+        assert call(native, M=M, **far) == 2
+        with pytest.raises(native.GsrError):
+            native.adapter_workspace_bytes(M, 1, 1, 8)
+    assert native.adapter_workspace_bytes(2 ** 27 - 16, 1, 1, 8) > 0

@@ -46,3 +46,13 @@ def test_python_refusals():
         gsr.gemm_grouped(a.float(), b, o)
     with pytest.raises(ValueError, match="device"):
         gsr.gemm_grouped(a, b, o)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(P=2 ** 29, config_id=21), 2), (dict(P=2 ** 28, config_id=22), 2), (dict(P=2 ** 30, config_id=31), 2),
+    (dict(P=2 ** 31 - 1, K=1, N=1, config_id=28), 2),  # 2^24 tiles of 256 threads
+])
+def test_launches_of_too_many_threads(native, change, status):
+    """2^32 threads and more, of which a launch would run a part."""
+    far = dict(groups=1, a_rows=0, rows=0, N=8, K=8, C=FAKE + 100 * GB, B=FAKE + 200 * GB, bias=0, offsets=FAKE + 201 * GB)
+    assert call(native, **{**far, **change}) == status

@@ -66,16 +66,16 @@ const launch_fn kElem[] = {launch_staged<64, 64, 4>, launch_staged<64, 64, 1>, l
 // The tiles with an adapter form, under the ids of their dense forms.
 struct Entry {
     int id;
-    int bm, bn;
+    int bm, bn, threads;
     launch_fn vec, split;
     hipError_t (*shared)(const Problem&, const ShrinkArgs&, int makers, int grid, hipStream_t);  // both steps, or null
 };
 const Entry kTable[] = {
-    {21, 64, 64, launch_kspec<64, 64, 4, 2, false>, launch_kspec<64, 64, 4, 2, true>, launch_shared<64, 64, 4, 2>},
-    {22, 32, 64, launch_kspec<32, 64, 4, 2, false>, launch_kspec<32, 64, 4, 2, true>, launch_shared<32, 64, 4, 2>},
-    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, nullptr, nullptr},
-    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>, nullptr, nullptr},
-    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>, nullptr, nullptr},
+    {21, 64, 64, 512, launch_kspec<64, 64, 4, 2, false>, launch_kspec<64, 64, 4, 2, true>, launch_shared<64, 64, 4, 2>},
+    {22, 32, 64, 512, launch_kspec<32, 64, 4, 2, false>, launch_kspec<32, 64, 4, 2, true>, launch_shared<32, 64, 4, 2>},
+    {28, 256, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>, nullptr, nullptr},
+    {31, 128, 256, 512, launch_ilv16c<gsr::Ilv16CCfg>, nullptr, nullptr},
+    {32, 128, 128, 512, launch_ilv16c<gsr::Ilv16QCCfg>, nullptr, nullptr},
 };
 
 const Entry* entry_of(int id)
@@ -175,6 +175,7 @@ int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ran
 {
     if (M < 0 || N < 0 || K < 0 || rank < 0 || M >= kLimit || N >= kLimit || K >= kLimit || rank > kMaxRank) return -1;
     if (M == 0 || N == 0 || K == 0 || rank == 0) return 0;
+    if (!grid_fits(cdiv(M, gsr::kShrinkRows), 512)) return -1;
     const Entry& e = stand_in(dense_launch(M, N, K).id);
     const int64_t split = e.split ? dense_split(M, N, K, cdiv(M, e.bm) * cdiv(N, e.bn), e.bm, e.bn, 0).partial_bytes : 0;
     return layout_of(M, K, rank).split + split;
@@ -241,8 +242,11 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     p.unit_c = load_unit(C, N);
     const bool vec = p.unit_a == 16 && p.unit_b == 16 && (((uintptr_t)bias & 7u) == 0);
     const int elem = elem_choice(config_id, K, (double)cdiv(M, 64) * (double)cdiv(N, 64), (double)cdiv(M, 128) * (double)cdiv(N, 128));
-    p.tiles_m = (int)cdiv(M, vec ? e.bm : kElemTiles[elem].bm);
-    p.tiles_n = (int)cdiv(N, vec ? e.bn : kElemTiles[elem].bn);
+    const int64_t tiles_m = cdiv(M, vec ? e.bm : kElemTiles[elem].bm), tiles_n = cdiv(N, vec ? e.bn : kElemTiles[elem].bn);
+    if (!grid_fits(tiles_m * tiles_n, vec ? e.threads : kElemTiles[elem].threads) || !grid_fits(cdiv(M, gsr::kShrinkRows), 512))
+        return GSR_ERROR_TOO_LARGE;
+    p.tiles_m = (int)tiles_m;
+    p.tiles_n = (int)tiles_n;
     const int tiles = p.tiles_m * p.tiles_n;
 
     const Layout w = layout_of(M, K, rank);
@@ -305,7 +309,7 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     }
     hipStream_t s = (hipStream_t)stream;
     if (shared)
-        return e.shared(p, a, makers, makers + tiles * split.parts, s) == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+        return status_of(e.shared(p, a, makers, makers + tiles * split.parts, s));
     hipError_t err;
     if (sp.parts > 0)
         err = launch_kernel(shrink_vec ? gsr::adapter_shrink_parts_kernel<true> : gsr::adapter_shrink_parts_kernel<false>,
@@ -318,10 +322,10 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
         err = launch_kernel(shrink_vec ? gsr::adapter_shrink_rows_kernel<true, gsr::ShrinkRows4>
                                        : gsr::adapter_shrink_rows_kernel<false, gsr::ShrinkRows4>,
                             dim3((unsigned)sp.blocks, 1, (unsigned)sp.slots), dim3(512), s, a);
-    if (err != hipSuccess) return GSR_ERROR_LAUNCH;
+    if (err != hipSuccess) return status_of(err);
     if (split.parts > 1) err = e.split(p, tiles * split.parts, s);
     else err = (vec ? e.vec : kElem[elem])(p, tiles, s);
-    return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+    return status_of(err);
 }
 
 }  // extern "C"

@@ -522,7 +522,7 @@ int run(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const voi
         const int grid = (int)std::min<int64_t>(cdiv(count, 256), 4096);
         const hipError_t err = launch_kernel(gsr::fill_epilogue_kernel, dim3(grid), dim3(256), s, (uint16_t*)C,
                                              (uint32_t)M, (uint32_t)N, (const uint16_t*)bias, alpha, (int)activation);
-        return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+        return status_of(err);
     }
 
     const Launch l = (forced == -2) ? given : resolve(M, N, K, forced);
@@ -576,10 +576,10 @@ int run(int64_t M, int64_t N, int64_t K, const void* A, const void* B, const voi
         p.ws_count = (uint32_t*)workspace;
         p.ws_part = (float*)((uint8_t*)workspace + split_count_bytes(tiles));
         const hipError_t err = e.split(p, tiles * plan.parts, s);
-        return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+        return status_of(err);
     }
     const hipError_t err = (vec ? e.vec : e.elem)(p, tiles, s);
-    return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+    return status_of(err);
 }
 
 }  // namespace

@@ -73,15 +73,15 @@ const launch_fn kElem[] = {launch_staged<64, 64, 4>, launch_staged<64, 64, 1>, l
 // forms.
 struct Entry {
     int id;
-    int bm, bn;
+    int bm, bn, threads;
     launch_fn vec;
 };
 const Entry kTable[] = {
-    {21, 64, 64, launch_kspec<64, 64, 4, 2>},
-    {22, 32, 64, launch_kspec<32, 64, 4, 2>},
-    {28, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>},
-    {31, 128, 256, launch_ilv16c<gsr::Ilv16CCfg>},
-    {32, 128, 128, launch_ilv16c<gsr::Ilv16QCCfg>},
+    {21, 64, 64, 512, launch_kspec<64, 64, 4, 2>},
+    {22, 32, 64, 512, launch_kspec<32, 64, 4, 2>},
+    {28, 256, 256, 256, launch_ilv16d<gsr::Ilv16DCfg>},
+    {31, 128, 256, 512, launch_ilv16c<gsr::Ilv16CCfg>},
+    {32, 128, 128, 512, launch_ilv16c<gsr::Ilv16QCCfg>},
 };
 
 const Entry* entry_of(int id)
@@ -99,6 +99,10 @@ double tile_rows(int64_t P, int64_t used, int bm)
 {
     return (double)used / (1.0 - std::exp(-(double)bm * (double)used / (double)P));
 }
+
+// The tile rows of a launch, at most: one part-filled tile for each group that
+// has rows.
+int64_t most_tile_rows(int64_t P, int64_t used, int bm) { return (P + used * (bm - 1)) / bm; }
 
 // The tile.  Decode steps are bound by B's bytes (16 tokens, 2 of 8 experts,
 // 4096 -> 11008: 116 to 126 us, 5.5 TB/s and more of what the hit experts hold),
@@ -121,6 +125,8 @@ const Entry& select(int64_t P, int64_t groups, int64_t N, int64_t K)
     const Entry* best = nullptr;
     double best_t = 1e300;
     for (const Entry& e : kTable) {
+        // (the tile with the fewest threads per output stays in any case)
+        if (e.id != 28 && !grid_fits(most_tile_rows(P, used, e.bm) * cdiv(N, e.bn), e.threads)) continue;
         const double rows = tile_rows(P, used, e.bm);
         const double rounds = std::ceil(rows * (double)cdiv(N, e.bn)) / 256.0;
         const double full = std::floor(rounds), fill = rounds - full;
@@ -165,9 +171,6 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
         (rows != nullptr && overlaps(C, cb, rows, (uint64_t)P * 4u)) ||
         (bias != nullptr && overlaps(C, cb, bias, (uint64_t)groups * (uint64_t)N * 2u)))
         return GSR_ERROR_INVALID_VALUE;
-    const int st = check_device();
-    if (st != GSR_SUCCESS) return st;
-
     Problem p{};
     p.A = (const uint16_t*)A;
     p.B = (const uint16_t*)B;
@@ -188,30 +191,27 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
     p.unit_a = load_unit(A, K);
     p.unit_b = load_unit(B, N);
     p.unit_c = load_unit(C, N);
-    hipStream_t s = (hipStream_t)stream;
-    if (K == 0) {
-        const hipError_t err = launch_kernel(gsr::fill_grouped_kernel, dim3((unsigned)groups), dim3(256), s, p);
-        return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
-    }
     const bool vec = p.unit_a == 16 && p.unit_b == 16 && (((uintptr_t)bias & 7u) == 0);
     const int64_t used = std::min(groups, P);
-    int bm, bn;
+    int bm, bn, threads;
     launch_fn fn;
     p.group_m = 4;
     if (vec) {
         const Entry& e = config_id >= 0 ? *entry_of(config_id) : select(P, groups, N, K);
-        bm = e.bm, bn = e.bn, fn = e.vec;
+        bm = e.bm, bn = e.bn, threads = e.threads, fn = e.vec;
     } else {
         const int i = elem_choice(config_id, K, tile_rows(P, used, 64) * (double)cdiv(N, 64), tile_rows(P, used, 128) * (double)cdiv(N, 128));
-        bm = kElemTiles[i].bm, bn = kElemTiles[i].bn, fn = kElem[i];
+        bm = kElemTiles[i].bm, bn = kElemTiles[i].bn, threads = kElemTiles[i].threads, fn = kElem[i];
     }
-    p.tiles_n = (int)cdiv(N, bn);
-    // tile rows: at most one part-filled tile for each group that has rows
-    p.tiles_m = (int)((P + used * (bm - 1)) / bm);
-    const int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
-    if (grid >= kLimit) return GSR_ERROR_TOO_LARGE;
-    const hipError_t err = fn(p, (int)grid, s);
-    return err == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH;
+    const int64_t tiles_n = cdiv(N, bn), tiles_m = most_tile_rows(P, used, bm);
+    if (K > 0 && !grid_fits(tiles_m * tiles_n, threads)) return GSR_ERROR_TOO_LARGE;
+    const int st = check_device();
+    if (st != GSR_SUCCESS) return st;
+    hipStream_t s = (hipStream_t)stream;
+    if (K == 0) return status_of(launch_kernel(gsr::fill_grouped_kernel, dim3((unsigned)groups), dim3(256), s, p));
+    p.tiles_n = (int)tiles_n;
+    p.tiles_m = (int)tiles_m;
+    return status_of(fn(p, (int)(tiles_m * tiles_n), s));
 }
 
 }  // extern "C"

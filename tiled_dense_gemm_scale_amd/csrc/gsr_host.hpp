@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gsr.h"
+
 namespace gsr {
 namespace host {
 
@@ -13,6 +15,11 @@ struct as_is {
     using type = T;
 };
 
+// Whether `blocks` workgroups of `threads` threads fit a dimension of a grid,
+// which holds fewer than 2^32 threads.  The runtime refuses 2^32 itself, but of
+// more it runs a part and reports nothing.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks * threads < (int64_t)1 << 32; }
+
 // Enqueues `kernel` and returns the status of this launch alone.  The status
 // comes from hipLaunchKernel's return value, not from hipGetLastError: an
 // error that an earlier, unrelated HIP call left pending on the calling
@@ -20,8 +27,14 @@ struct as_is {
 template <typename... P>
 hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, typename as_is<P>::type... args)
 {
+    if (!grid_fits(grid.x, block.x)) return hipErrorInvalidConfiguration;
     void* argv[] = {(void*)&args...};
     return hipLaunchKernel((const void*)kernel, grid, block, argv, 0, s);
+}
+
+inline int status_of(hipError_t e)
+{
+    return e == hipSuccess ? GSR_SUCCESS : e == hipErrorInvalidConfiguration ? GSR_ERROR_TOO_LARGE : GSR_ERROR_LAUNCH;
 }
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -79,9 +92,9 @@ constexpr int64_t kSplitCounters = 128;  // arrival counters at a workspace's st
 // and 272.  Unaligned 16-byte loads go out at about one lane per clock, which
 // bounds all three.
 struct ElemTile {
-    int bm, bn;
+    int bm, bn, threads;
 };
-constexpr ElemTile kElemTiles[3] = {{64, 64}, {64, 64}, {128, 128}};
+constexpr ElemTile kElemTiles[3] = {{64, 64, 1024}, {64, 64, 256}, {128, 128, 256}};
 constexpr int64_t kElemFull = 256, kElemDeep = 2048;
 inline int elem_choice(int config_id, int64_t K, double tiles64, double tiles128)
 {

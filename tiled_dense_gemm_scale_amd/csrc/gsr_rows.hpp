@@ -253,8 +253,8 @@ struct RowArgs {
     int32_t lanes_log2;        // threads per row
 };
 
-// A grid dimension holds fewer than 2^32 threads (a launch with more runs a part
-// of them and reports nothing), so from kRowBlocks workgroups on a launch has
+// A grid dimension holds fewer than 2^32 threads (of more, a part runs and nothing
+// is reported), so from kRowBlocks workgroups on a launch has
 // several rows of so many, numbered one behind the other.  (Reading the grid's
 // size instead of the constant costs a small call 0.6 us.)
 constexpr int64_t kRowBlocks = 1 << 20;

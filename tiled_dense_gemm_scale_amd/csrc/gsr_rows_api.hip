@@ -63,8 +63,6 @@ dim3 row_grid(int64_t blocks)
     return dim3((unsigned)std::min(blocks, gsr::kRowBlocks), (unsigned)cdiv(blocks, gsr::kRowBlocks));
 }
 
-int status_of(hipError_t e) { return e == hipSuccess ? GSR_SUCCESS : GSR_ERROR_LAUNCH; }
-
 }  // namespace
 
 extern "C" {
@@ -122,7 +120,7 @@ int gsr_group_rows(int64_t tokens, int64_t k, int64_t groups, const void* ids, i
     if (plan.blocks > 1) {
         const hipError_t err = launch_kernel(wide ? gsr::group_count_kernel<int64_t> : gsr::group_count_kernel<int32_t>,
                                              dim3((unsigned)plan.blocks), dim3(1024), s, g);
-        if (err != hipSuccess) return GSR_ERROR_LAUNCH;
+        if (err != hipSuccess) return status_of(err);
     }
     const int waves = (int)std::min<int64_t>(gsr::kGroupWaves, std::max<int64_t>(1, cdiv(plan.chunk, 64)));
     return status_of(launch_kernel(wide ? gsr::group_place_kernel<int64_t> : gsr::group_place_kernel<int32_t>,
