@@ -52,3 +52,8 @@ def test_dense_rows_past_a_grid(gsr, native):
         st = native.gemm_scale_bias_act(M, 1, 1, a.data_ptr(), b.data_ptr(), 0, c.data_ptr(), 1.0, 2, 0, config)
         torch.cuda.synchronize()
         assert st == 2 or (st == 0 and torch.equal(a, c))
+
+
+def test_grouped_of_the_largest_count(gsr):
+    """2^31 - 1 rows in one group: its tiles' count passes no 2^31 on the way."""
+    grouped_identity(gsr, 2 ** 31 - 1)

@@ -347,6 +347,10 @@ __device__ __forceinline__ void tile_of(int pid, int nwg, const Problem& p, int&
     tn = within / gs;
 }
 
+// Tiles of BM rows that n rows take; n + BM - 1 could pass 2^31.
+template <int BM>
+__device__ __forceinline__ int cdiv_rows(int n) { return n / BM + (n % BM != 0 ? 1 : 0); }
+
 // The tile of a grouped product that this workgroup computes: every group's
 // rows are cut into tiles of BM by themselves, the tiles of all groups are
 // numbered one behind the other as tile rows, and tile_of orders them as it
@@ -372,7 +376,7 @@ __device__ __forceinline__ bool group_tile(Problem& p, int& n0)
             lo = min(max(p.offsets[e], 0), p.M);
             n = max(min(p.offsets[e + 1], p.M) - lo, 0);
         }
-        inc = (n + BM - 1) / BM;
+        inc = cdiv_rows<BM>(n);
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int o = __shfl_up(inc, d);
@@ -401,7 +405,7 @@ __device__ __forceinline__ bool group_tile(Problem& p, int& n0)
     const int at = __ffsll((unsigned long long)__ballot(before + inc > tm)) - 1;  // the lane whose group holds tile row tm
     const int e = e0 + at;
     const int rows = __builtin_amdgcn_readlane(n, at);
-    const int skip = (tm - (before + __builtin_amdgcn_readlane(inc, at) - (rows + BM - 1) / BM)) * BM;
+    const int skip = (tm - (before + __builtin_amdgcn_readlane(inc, at) - cdiv_rows<BM>(rows))) * BM;
     const int row0 = __builtin_amdgcn_readlane(lo, at) + skip;
     p.M = min(BM, rows - skip);
     p.B += (int64_t)e * p.K * p.N;
