@@ -295,8 +295,9 @@ int gsr_combine_rows_backward(int64_t tokens, int64_t k, int64_t rows_in, int64_
  *            offsets of gsr_group_rows); a group may be empty.  Other values
  *            make wrong or missing results, never an access outside.
  * Epilogue, precision, alignment, ownership and errors as gemm_scale_bias_act
- * (same kernels per tile, so a group's outputs are the bits of that call on
- * its rows with the same configuration).  GSR_ERROR_TOO_LARGE for P >= 2^31,
+ * (same sums per tile, so with a forced configuration a group's outputs are the
+ * bits of that call on its rows with the same one; without one, operands off the
+ * 128-bit path may be summed over four runs of K).  GSR_ERROR_TOO_LARGE for P >= 2^31,
  * more than 1024 groups, K or N >= 2^22, one group's B of 2^31 bytes or more,
  * or, with rows, an A of 2^31 bytes or more, and where a launch would have
  * 2^32 threads (a forced 64 x 64 tile: from P of about 2^29); P x N, P x K and

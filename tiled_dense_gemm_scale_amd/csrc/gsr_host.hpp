@@ -83,7 +83,8 @@ constexpr int64_t kSplitCounters = 128;  // arrival counters at a workspace's st
 
 // The element-wise kernels of the grouped products and of those with adapters:
 // 0: 64x64 with four groups of waves on K, 1: 64x64, 2: 128x128.  For a forced
-// configuration id its tile's (the copy-wave K-split ones: 22 and 21); else by
+// configuration id one whose sums are those of its dense form, bit for bit (1
+// for the copy-wave K-split ones, 21 and 22; 0 adds up four runs of K); else by
 // the number of tiles the launch has of 64x64 and of 128x128, which fill the
 // chip from one per CU on (the 64x64 ones from two if K is deep).  In us, the
 // three in turn, K 517: 136 tiles of 64x64 12, 15 and 22, 264 tiles 24, 17 and
@@ -98,7 +99,7 @@ constexpr ElemTile kElemTiles[3] = {{64, 64, 1024}, {64, 64, 256}, {128, 128, 25
 constexpr int64_t kElemFull = 256, kElemDeep = 2048;
 inline int elem_choice(int config_id, int64_t K, double tiles64, double tiles128)
 {
-    if (config_id >= 0) return config_id == 22 ? 0 : config_id == 21 ? 1 : 2;
+    if (config_id >= 0) return config_id == 21 || config_id == 22 ? 1 : 2;
     if (tiles128 >= (double)kElemFull) return 2;
     return tiles64 > (double)(K > kElemDeep ? 2 * kElemFull : kElemFull) ? 1 : 0;
 }
