@@ -327,8 +327,9 @@ int gemm_grouped_scale_bias_act(int64_t P, int64_t N, int64_t K, int64_t groups,
  * values reach its own rows only, whatever they are.  rank is at most 256
  * and M at most 2^27 - 16 (GSR_ERROR_TOO_LARGE); one adapter's La and Lb are
  * below 2^31 bytes each and the whole arrays may be larger.  adapters = 0 or
- * rank = 0 is the product alone.  Two kernels are enqueued, or, for at most 64
- * rows, one whose first workgroups make the inner sums.
+ * rank = 0 is the product alone (gemm_scale_bias_act_ws).  Two kernels are
+ * enqueued, or, for at most 64 rows, one whose first workgroups make the inner
+ * sums.
  *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its
  *              first 512 bytes zero before the first call and again after
  *              each), of gsr_adapter_workspace_bytes(M, N, K, rank) bytes;

@@ -383,3 +383,21 @@ def test_refusals_on_the_device(gsr):
         with pytest.raises(gsr.GsrError) as e:
             bad()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("L,R", [(0, 16), (3, 0)])
+def test_no_adapters_keep_the_split(gsr, L, R):
+    """Without adapters a decode call splits K as the call with a workspace does."""
+    M, N, K = 16, 4096, 11008
+    g = torch.Generator().manual_seed(12)
+    a, b = torch.randn(M, K, generator=g).half().to(DEV), (torch.randn(K, N, generator=g) * K ** -0.5).half().to(DEV)
+    h = dict(dtype=torch.float16, device=DEV)
+    ids = torch.zeros(M, dtype=torch.int32, device=DEV)
+    ws = gsr.new_workspace(gsr.adapter_workspace_bytes(M, N, K, R))
+    say(f"adapters: {L} of rank {R}, split")
+    want = gsr.gemm_scale_bias_act_ws(a, b, gsr.new_workspace(gsr.workspace_bytes(M, N, K)), None, 0.5, "gelu")
+    assert not torch.equal(want, gsr.gemm_scale_bias_act(a, b, None, 0.5, "gelu"))  # it is a split's sum
+    for _ in range(2):
+        c = gsr.gemm_adapters(a, b, torch.empty(L, R, K, **h), torch.empty(L, N, R, **h), ids, ws, alpha=0.5, activation="gelu")
+        assert torch.equal(c.view(torch.int16), want.view(torch.int16))
+        assert counters_zero(ws)

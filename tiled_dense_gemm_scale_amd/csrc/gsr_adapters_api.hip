@@ -174,7 +174,8 @@ extern "C" {
 int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank)
 {
     if (M < 0 || N < 0 || K < 0 || rank < 0 || M >= kLimit || N >= kLimit || K >= kLimit || rank > kMaxRank) return -1;
-    if (M == 0 || N == 0 || K == 0 || rank == 0) return 0;
+    if (M == 0 || N == 0 || K == 0) return 0;
+    if (rank == 0) return gsr_workspace_bytes(M, N, K);
     if (!grid_fits(cdiv(M, gsr::kShrinkRows), 512)) return -1;
     const Entry& e = stand_in(dense_launch(M, N, K).id);
     const int64_t split = e.split ? dense_split(M, N, K, cdiv(M, e.bm) * cdiv(N, e.bn), e.bm, e.bn, 0).partial_bytes : 0;
@@ -191,7 +192,7 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
     if (M < 0 || N < 0 || K < 0 || adapters < 0 || rank < 0 || splits < 0 || splits > kSplitMaxParts || workspace_bytes < 0)
         return GSR_ERROR_INVALID_VALUE;
     if (adapters == 0 || rank == 0 || M == 0 || N == 0 || K == 0)  // the product alone
-        return gemm_scale_bias_act_ex(M, N, K, A, B, bias, C, alpha, activation, stream, config_id);
+        return gemm_scale_bias_act_ws(M, N, K, A, B, bias, C, alpha, activation, workspace, workspace_bytes, stream, config_id, splits);
     if (M >= kLimit || N >= kLimit || K >= kLimit || adapters >= kLimit || rank > kMaxRank) return GSR_ERROR_TOO_LARGE;
     // 32-bit byte offsets within a matrix and within one adapter
     if (M * K * 2 >= kLimit || K * N * 2 >= kLimit || M * N * 2 >= kLimit || N * rank * 2 >= kLimit || K * rank * 2 >= kLimit)
