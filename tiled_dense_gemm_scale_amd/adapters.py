@@ -1,5 +1,6 @@
 """The fused product with low-rank adapters: a batch whose rows belong to
-requests with adapters of their own, against one shared weight matrix."""
+requests with adapters of their own, against one shared weight matrix.  For
+serving: autograd records nothing, and there is no gradient here."""
 from __future__ import annotations
 
 from typing import Optional

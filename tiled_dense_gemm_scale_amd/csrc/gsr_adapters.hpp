@@ -3,7 +3,7 @@
 // (rows whose id names no adapter: W = B).
 //
 // The sum over K is taken first, the rank last:
-//   1. adapter_shrink_kernel: t[m, r] = s_l * sum_k A[m, k] La_l[r, k], fp32;
+//   1. the adapter_shrink kernels: t[m, r] = s_l * sum_k A[m, k] La_l[r, k], fp32;
 //   2. the product's own kernels add sum_r t[m, r] Lb_l[n, r] to their fp32
 //      sums, so the adapter costs no pass over C and is scaled, biased and
 //      activated with the sum it belongs to.
@@ -647,8 +647,8 @@ __device__ __forceinline__ half8 finite8(half8 v)
 // loop over adapters (changing them with vector instructions there made the
 // register allocator spill them), so the rows of other adapters take part with
 // t = 0, and the rows' scales multiply all accumulators once at the end.
-// (4097 x 11008 x 4096 with 9 runs of rank 16 takes 334 us in all beside 311
-// with no row's id an adapter's, 14 of them the inner sums'; rank 64 366, 22.)
+// (4097 x 11008 x 4096 with 9 runs of rank 16 takes 318 us in all beside 294
+// with no row's id an adapter's, 14 of them the inner sums'; rank 64 350, 22.)
 // 0 * infinity and 0 * NaN would then reach those rows: infinities and NaN of Lb
 // have zeros in their place, rows of t with such values take no part, and the
 // caller, told so by the returned true, runs adapter_nonfinite16 before its
@@ -750,7 +750,9 @@ __device__ __forceinline__ bool adapter_start16(const Problem& p, f32x4 (&acc)[F
 // make of each sum.  A sum with one is an infinity or a NaN, and which is
 // told by the hi half of t alone, which has the sign of t; finite sums are
 // left alone, and so are the rows of other adapters, which share the matrix
-// instructions.  Four blocks of columns at a time, for the registers' sake.
+// instructions.  Four blocks of columns at a time, for the registers' sake, and
+// behind the product's loop: in front of it the 256x256 tile spilled 55 registers
+// instead of 29.
 template <bool VEC, int FN, int FM>
 __device__ __forceinline__ void adapter_nonfinite16(const Problem& p, f32x4 (&acc)[FN][FM], int m0, int n0)
 {

@@ -73,8 +73,9 @@ struct Ilv16DCfg : Ilv16Cfg {
     static constexpr int BAR = 6;                       // wait + barrier slot of substep 1
     static constexpr int BC0 = 4, BCD = 8;              // B copies in substep 0: first slot, stride
     static constexpr int AC0 = 8, ACD = 7;              // A copies in substep 1: first slot, stride
-    // chunks of ranks at a time in adapter_start16 (two spill, and were 12 %
-    // slower over the whole call at rank 16, 17 % at 64)
+    // chunks of ranks at a time in adapter_start16.  One spills 29 registers
+    // outside the product's loop already (96 bytes of scratch per lane); two
+    // spill more, and were 12 % slower over the whole call at rank 16, 17 % at 64.
     static constexpr int ADAPTER_CHUNKS = 1;
 };
 

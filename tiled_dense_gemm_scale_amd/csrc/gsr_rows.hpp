@@ -264,7 +264,7 @@ __device__ __forceinline__ int64_t row_block() { return (int64_t)blockIdx.y * kR
 // threads walk a row; their loads of four units are in flight together.  It
 // runs at the rate of a copy: 4098 rows of 4096 (50 MB) in 10.8 us, 8192x2x4096
 // (201 MB) in 39 us (5.2 TB/s); rows of odd length go 2 bytes at a time, 2331
-// of 1001 in 4 us.
+// of 1001 in 3.4 us, 8192x2x4095 in 41.
 template <int U>
 __global__ void __launch_bounds__(256) gather_rows_kernel(RowArgs r)
 {
@@ -288,8 +288,11 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(RowArgs r)
 
 // out[t] = sum_j w[t, j] y[positions[t, j]], fp32 in order of j from +0,
 // rounded once to fp16.  Four choices' units are requested before the first
-// is used.  Bound by the bytes of y: 8192x2x4096 (195 MB) in 33.5 us; a decode
-// step's 16x8x4096 takes 5.5 us, of which 2.8 are an empty launch's.
+// is used.  Bound by the bytes of y: 8192x2x4096 (195 MB) in 30 us.  A decode
+// step is bound by latency: 16x8x4096 is 16 workgroups whose threads walk two
+// units and, in each, two batches of four choices one behind the other, 5.3 us
+// beside an empty launch's 2.3.  Rows of odd length go 2 bytes at a time, which
+// issues eight times the loads: 8192x2x4095 90 us.
 template <int U>
 __global__ void __launch_bounds__(256) combine_rows_kernel(RowArgs r)
 {
@@ -334,7 +337,8 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(RowArgs r)
 // kStreamBytes and more is read without a claim on the caches.  One choice at
 // a time and 4 steps, then this: 8192x2x4096 78 and 57 us (335 MB: 5.9 TB/s),
 // 16384x4x1024 57 and 51, 8192x4x512 16.3 and 14.2, 16384x8x256 59 and 31;
-// 8192x2x512 10.7 and 10.9.  Rows of dy that no choice names (rows[p] < 0)
+// 8192x2x512 10.7 and 10.9.  Units of 8, 4 and 2 bytes have one form (J = S =
+// 4), bound by the loads' issue: 8192x2x4095 198 us.  Rows of dy that no choice names (rows[p] < 0)
 // are set to zero by the same waves.
 constexpr int64_t kStreamBytes = 64 << 20;
 

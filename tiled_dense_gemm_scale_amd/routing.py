@@ -4,7 +4,11 @@ rows copied into group order (gather_rows) and summed back with their weights
 (combine_rows and its gradient), and the whole layer (expert_mlp).
 
 Every function enqueues on `stream` (default: the current stream of the
-inputs' device); what it allocates itself is allocated for that stream.
+inputs' device); what it allocates itself is allocated for that stream.  As
+with every call of this package autograd records nothing: outputs carry no
+gradient, whatever the inputs require.  combine_rows and combine_rows_backward
+are the gradients of gather_rows and combine_rows; the grouped product has none
+here.
 """
 from __future__ import annotations
 
