@@ -927,34 +927,78 @@ struct AdapterItems {
         }
     }
 
-    // Lb's infinities and NaN meet the hi half of t alone, which has the sign
-    // of t: with both, 0 * infinity, or halves of two signs, would make a NaN of
-    // what is an infinity.
+    // Lb's infinities and NaN must not meet both halves of t: 0 * infinity, or
+    // halves of two signs, would make a NaN of what is an infinity.  A batch with
+    // such values has zeros in their place, and in t's, and nonfinite() adds what
+    // they make of the sums.  One look per batch costs 1 % of 256x4096x4096 with
+    // 64 mixed adapters of rank 64 (84.9 us); a look, and Lb's fragments twice, per
+    // item cost 3 %.
     template <int B>
-    __device__ __forceinline__ void apply(const Batch<B>& w, f32x16 (&acc)[TN][TM]) const
+    __device__ __forceinline__ void apply(const Problem& p, Batch<B>& w, f32x16 (&acc)[TN][TM]) const
     {
+        half8 seen = (half8)(_Float16)0.0f;
 #pragma unroll
         for (int j = 0; j < B; ++j) {
             if (j >= w.n) break;
-            half8 seen = (half8)(_Float16)0.0f, low[TN];
 #pragma unroll
-            for (int a = 0; a < TN; ++a) low[a] = w.x[j][a], seen = look_odd(w.x[j][a], seen);
-            if (__ballot(any_odd(seen)) != 0) {
+            for (int a = 0; a < TN; ++a) seen = look_odd(w.x[j][a], seen);
+        }
+        const bool odd = __ballot(any_odd(seen)) != 0;
+        if (odd) {
 #pragma unroll
-                for (int a = 0; a < TN; ++a) low[a] = finite8(low[a]);
+            for (int j = 0; j < B; ++j) {
+#pragma unroll
+                for (int a = 0; a < TN; ++a) w.x[j][a] = finite8(w.x[j][a]);
+#pragma unroll
+                for (int b = 0; b < TM; ++b) w.hi[j][b] = finite8(w.hi[j][b]);
             }
+        }
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            if (j >= w.n) break;
 #pragma unroll
             for (int b = 0; b < TM; ++b) {
                 if (__ballot(id[b] == w.ls[j]) == 0) continue;
 #pragma unroll
                 for (int a = 0; a < TN; ++a) {
                     f32x16 d = {};
-                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(low[a], w.lo[j][b], d, 0, 0, 0);
+                    d = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.x[j][a], w.lo[j][b], d, 0, 0, 0);
                     d = __builtin_amdgcn_mfma_f32_32x32x16_f16(w.x[j][a], w.hi[j][b], d, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         acc[a][b][i] = id[b] == w.ls[j] ? acc[a][b][i] + fabsf(sc[b]) * d[i] : acc[a][b][i];
                 }
+            }
+        }
+        if (odd) {
+#pragma unroll 1
+            for (int j = 0; j < w.n; ++j) {
+                int ol = w.ls[0], oc = w.ch[0];
+#pragma unroll
+                for (int i = 1; i < B; ++i) ol = j == i ? w.ls[i] : ol, oc = j == i ? w.ch[i] : oc;
+                nonfinite(p, ol, oc, acc);
+            }
+        }
+    }
+
+    // Adds the sums of adapter ol's chunk oc that are an infinity or a NaN, in the
+    // lanes whose row is the adapter's; the hi half of t alone, which has the sign
+    // of t, tells which.
+    __device__ __forceinline__ void nonfinite(const Problem& p, int ol, int oc, f32x16 (&acc)[TN][TM]) const
+    {
+        const int lane = threadIdx.x & 63, frow = lane & 31, fhi = lane >> 5;
+        const __amdgpu_buffer_rsrc_t rl = lb_rsrc(p, ol);
+#pragma unroll
+        for (int b = 0; b < TM; ++b) {
+            const int r = id[b] >= 0 ? row_of(b) - t_row : 0;
+            half8 y = piece(t + ((int64_t)r * p.chunks + oc) * 32 + 8 * fhi);
+#pragma unroll
+            for (int a = 0; a < TN; ++a) {
+                half8 x = lb_piece(p, rl, n0 + 32 * a + frow, kAdapterChunk * oc + 8 * fhi);
+                asm volatile("" : "+v"(x), "+v"(y));  // a block at a time, for the registers' sake
+                const f32x16 d = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, f32x16{}, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[a][b][i] += (id[b] == ol && !(fabsf(d[i]) < __builtin_inff())) ? d[i] : 0.0f;
             }
         }
     }
@@ -967,7 +1011,7 @@ struct AdapterItems {
         do {
             load_lb(p, w);
             load_t(p, w);
-            apply(w, acc);
+            apply(p, w, acc);
         } while (w.n == B);
     }
 };

@@ -291,7 +291,7 @@ __device__ __forceinline__ void kspec_tile(Problem p, uint8_t* smem, int* last, 
             }
         }
         if constexpr (ADAPT != kAdaptNone) {
-            items.apply(batch, acc);
+            items.apply(p, batch, acc);
             if (batch.n == kFirst) items.template rest<kRest>(p, acc);
         }
 
