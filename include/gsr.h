@@ -56,7 +56,8 @@ enum gsr_status {
 enum gsr_activation {
     GSR_ACT_RELU = 0, /* max(v, 0); non-positive results are +0 */
     GSR_ACT_GELU = 1, /* v/2 * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) */
-    GSR_ACT_NONE = 2  /* v itself */
+    GSR_ACT_NONE = 2, /* v itself */
+    GSR_ACT_SILU = 3  /* v / (1 + exp(-v)); gsr_expert_mlp_few only */
 };
 
 /* One compiled tile configuration.  A workgroup of waves_m*waves_n wave64s
@@ -351,6 +352,102 @@ int gemm_adapters_scale_bias_act(int64_t M, int64_t N, int64_t K,
 /* The bytes gemm_adapters_scale_bias_act needs (0: none); -1 for sizes it
  * rejects.  Host only. */
 int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t rank);
+
+/* ---- a few rows against weights in 4 bits, and a whole layer for a few tokens ---
+ * 4-bit weights of a K x N matrix (or `matrices` of them, one behind the other):
+ *
+ *     w[k,n] = (q[k,n] - zeros[k / group, n]) * scales[k / group, n]
+ *
+ *   codes   ceil(K / 8) x N 32-bit words (4-byte aligned): bits 4i .. 4i + 3 of
+ *           word (r, n) are q[8r + i, n], 0..15; those of rows past K are ignored
+ *   scales  ceil(K / group) x N binary16 values
+ *   zeros   ceil(K / group) x N 8-bit values (0..255), or NULL: 8 everywhere
+ *   group   a power of two from 32 to 2^30; the last group may be short
+ * K and N are below 2^22 (GSR_ERROR_TOO_LARGE). */
+
+/* codes, scales and (zeros not NULL) zeros of the binary16 values B, column by
+ * column and group by group, in binary32:
+ *   zeros NULL  scale = binary16(max|b| / 7), q = clamp(rint(b / scale), -8, 7) + 8
+ *   else        lo = min(b, 0), hi = max(b, 0), scale = binary16((hi - lo) / 15),
+ *               zero = clamp(rint(-lo / scale), 0, 15),
+ *               q = clamp(rint(b / scale) + zero, 0, 15)
+ * rint rounds ties to even.  A scale of zero has codes and zero 8; a group with
+ * an infinity or a NaN gets the scale NaN.  Codes past K are those of zeros. */
+int gsr_quantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group, const void* B,
+                    uint32_t* codes, void* scales, uint8_t* zeros, void* stream);
+
+/* B = the weights' values, each rounded once to binary16. */
+int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group,
+                      const uint32_t* codes, const void* scales, const uint8_t* zeros, void* B,
+                      void* stream);
+
+/* The fused product with such weights, made for few rows:
+ *
+ *     C[m,n] = act( alpha * sum_k A[m,k] * w[k,n] + bias[n] )
+ *
+ * A, bias, C, alpha and the activation as gemm_scale_bias_act's, at any 2-byte
+ * alignment; matrices may be larger than 2^31 bytes, M is below 2^31.  The
+ * products A[m,k] (q - zero) are summed exactly as written in binary32, group by
+ * group, and the scale multiplies a group's sum: the weights are not rounded.
+ * A scale that is not finite makes its column's outputs not finite.
+ *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its first
+ *              512 bytes zero before the first call and again after each), of
+ *              gsr_w4_workspace_bytes(M, N, K) bytes; with less or NULL K is
+ *              not split across workgroups
+ * Ownership, streams and errors as gemm_scale_bias_act_ws. */
+int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
+                           int64_t group, const uint32_t* codes, const void* scales, const uint8_t* zeros,
+                           const void* bias, void* C, float alpha, int32_t activation,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The bytes gemm_w4_scale_bias_act can use (0: none); -1 for sizes it rejects.
+ * Host only. */
+int64_t gsr_w4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* One of a layer's matrices: `experts` of K x N binary16 values (group 0, scales
+ * and zeros NULL) or of 4-bit weights (group as above, data the codes), and
+ * experts x N binary16 values of bias, or NULL. */
+typedef struct gsr_weights {
+    const void* data;
+    const void* scales;
+    const uint8_t* zeros;
+    const void* bias;
+    int64_t group;
+} gsr_weights;
+
+/* A whole layer of routed experts for at most 64 tokens, in two launches.  With
+ * e = ids[t,j] (T x k, 4 or 8 bytes each; an id outside [0, experts) has no
+ * term, and an expert may be named more than once):
+ *
+ *     h[t,j,f] = act( sum_i x[t,i] * up[e,i,f] + bias_up[e,f] )               gate NULL
+ *     h[t,j,f] = act( sum_i x[t,i] * gate[e,i,f] + bias_gate[e,f] )
+ *                * ( sum_i x[t,i] * up[e,i,f] + bias_up[e,f] )                otherwise
+ *     out[t,o] = sum_j weights[t,j] * ( sum_f h[t,j,f] * down[e,f,o] + bias_down[e,o] )
+ *
+ *   x        T x H;  up, gate  experts of H x F;  down  experts of F x O
+ *   weights  T x k binary32, or NULL (ones)
+ *   activation  any gsr_activation
+ * Sums, biases, activation, gate and weights are binary32; h is rounded to
+ * binary16 between the launches and out once at the end.  j is added in
+ * ascending order: equal inputs give equal bits.  Either all matrices are
+ * binary16 or all are 4-bit, gate and up of one group.  Values are row-major at
+ * any 2-byte alignment (codes 4).  T <= 64, T k <= 1024, experts <= 1024, widths
+ * below 2^22 (GSR_ERROR_TOO_LARGE); for more tokens there are gsr_group_rows and
+ * the grouped products.
+ *   workspace  gsr_expert_few_workspace_bytes(T, k, experts, F, O) bytes,
+ *              16-byte aligned, counters as gemm_scale_bias_act_ws's (its first
+ *              512 bytes zero before the first call and again after each), one
+ *              per call that may run at the same time; GSR_ERROR_INVALID_VALUE
+ *              if smaller
+ * out must not overlap anything else.  Ownership, streams and errors as above. */
+int gsr_expert_mlp_few(int64_t tokens, int64_t k, int64_t experts, int64_t H, int64_t F, int64_t O,
+                       const void* x, const void* ids, int32_t id_bytes, const float* weights,
+                       const gsr_weights* up, const gsr_weights* gate, const gsr_weights* down,
+                       int32_t activation, void* out, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The bytes gsr_expert_mlp_few needs (with 4-bit weights or without); -1 for
+ * sizes it rejects.  Host only. */
+int64_t gsr_expert_few_workspace_bytes(int64_t tokens, int64_t k, int64_t experts, int64_t F, int64_t O);
 
 /* Tuning table: exact problem shapes mapped to a launch, consulted before the
  * built-in selector (by every entry point called with config id -1, and by

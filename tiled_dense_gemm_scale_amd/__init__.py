@@ -27,6 +27,8 @@ from . import _native
 from ._native import (GsrError, clear_tuning, config_ids, get_config, load_tuning, num_configs, select_config,
                       status_string, tuning_entries, version, workspace_bytes)
 from .adapters import adapter_workspace_bytes, gemm_adapters
+from .few import expert_few_workspace_bytes, expert_mlp_few
+from .quantized import W4, dequantize_w4, gemm_w4, quantize_w4, w4_workspace_bytes
 from .routing import (combine_rows, combine_rows_backward, expert_mlp, gather_rows, gemm_grouped, group_rows,
                       group_workspace_bytes)
 
@@ -34,6 +36,8 @@ __all__ = ["gemm_scale_relu", "gemm_scale_relu_ex", "gemm_scale_bias_act", "gemm
            "gemm_scale_relu_ws", "gemm_scale_bias_act_ws", "workspace_bytes", "new_workspace",
            "group_rows", "group_workspace_bytes", "gather_rows", "combine_rows", "combine_rows_backward",
            "gemm_grouped", "expert_mlp", "gemm_adapters", "adapter_workspace_bytes",
+           "W4", "quantize_w4", "dequantize_w4", "gemm_w4", "w4_workspace_bytes",
+           "expert_mlp_few", "expert_few_workspace_bytes",
            "select_config", "get_config", "num_configs", "config_ids", "status_string", "version", "configs",
            "ACTIVATIONS",
            "load_tuning", "clear_tuning", "tuning_entries"]

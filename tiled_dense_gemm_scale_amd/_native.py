@@ -23,6 +23,7 @@ GSR_ERROR_INVALID_CONFIG = 6
 GSR_ACT_RELU = 0
 GSR_ACT_GELU = 1
 GSR_ACT_NONE = 2
+GSR_ACT_SILU = 3
 
 
 class GsrConfig(ctypes.Structure):
@@ -42,6 +43,17 @@ class GsrConfig(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {name: int(getattr(self, name)) for name, _ in self._fields_}
+
+
+class GsrWeights(ctypes.Structure):
+    """Mirror of struct gsr_weights."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("group", ctypes.c_int64),
+    ]
 
 
 class GsrError(RuntimeError):
@@ -103,6 +115,20 @@ def lib() -> ctypes.CDLL:
             L.gemm_adapters_scale_bias_act.restype = ctypes.c_int
             L.gsr_adapter_workspace_bytes.argtypes = [i64, i64, i64, i64]
             L.gsr_adapter_workspace_bytes.restype = i64
+            L.gsr_quantize_w4.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, vp]
+            L.gsr_quantize_w4.restype = ctypes.c_int
+            L.gsr_dequantize_w4.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, vp]
+            L.gsr_dequantize_w4.restype = ctypes.c_int
+            L.gemm_w4_scale_bias_act.argtypes = [i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, f32, i32, vp, i64, vp]
+            L.gemm_w4_scale_bias_act.restype = ctypes.c_int
+            L.gsr_w4_workspace_bytes.argtypes = [i64, i64, i64]
+            L.gsr_w4_workspace_bytes.restype = i64
+            wp = ctypes.POINTER(GsrWeights)
+            L.gsr_expert_mlp_few.argtypes = [i64, i64, i64, i64, i64, i64, vp, vp, i32, vp, wp, wp, wp, i32, vp, vp, i64,
+                                             vp]
+            L.gsr_expert_mlp_few.restype = ctypes.c_int
+            L.gsr_expert_few_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+            L.gsr_expert_few_workspace_bytes.restype = i64
             L.gsr_load_tuning.argtypes = [ctypes.c_char_p]
             L.gsr_load_tuning.restype = ctypes.c_int
             L.gsr_clear_tuning.argtypes = []
@@ -252,6 +278,54 @@ def gemm_adapters_scale_bias_act(M: int, N: int, K: int, A: int, B: int, bias: i
 def adapter_workspace_bytes(M: int, N: int, K: int, rank: int) -> int:
     """Workspace bytes that the product with adapters of `rank` needs."""
     got = int(lib().gsr_adapter_workspace_bytes(int(M), int(N), int(K), int(rank)))
+    if got < 0:
+        raise GsrError(GSR_ERROR_INVALID_VALUE, status_string(GSR_ERROR_INVALID_VALUE))
+    return got
+
+
+def quantize_w4(matrices: int, K: int, N: int, group: int, B: int, codes: int, scales: int, zeros: int,
+                stream: int) -> int:
+    return lib().gsr_quantize_w4(matrices, K, N, group, B or None, codes or None, scales or None, zeros or None,
+                                 stream or None)
+
+
+def dequantize_w4(matrices: int, K: int, N: int, group: int, codes: int, scales: int, zeros: int, B: int,
+                  stream: int) -> int:
+    return lib().gsr_dequantize_w4(matrices, K, N, group, codes or None, scales or None, zeros or None, B or None,
+                                   stream or None)
+
+
+def gemm_w4_scale_bias_act(M: int, N: int, K: int, A: int, group: int, codes: int, scales: int, zeros: int, bias: int,
+                           C: int, alpha: float, activation: int, workspace: int, workspace_bytes: int,
+                           stream: int) -> int:
+    """Raw entry point of the product with 4-bit weights.  Returns the
+    gsr_status."""
+    return lib().gemm_w4_scale_bias_act(M, N, K, A or None, group, codes or None, scales or None, zeros or None,
+                                        bias or None, C or None, float(alpha), int(activation), workspace or None,
+                                        int(workspace_bytes), stream or None)
+
+
+def w4_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes that the product with 4-bit weights can use (0: none)."""
+    got = int(lib().gsr_w4_workspace_bytes(int(M), int(N), int(K)))
+    if got < 0:
+        raise GsrError(GSR_ERROR_INVALID_VALUE, status_string(GSR_ERROR_INVALID_VALUE))
+    return got
+
+
+def expert_mlp_few(tokens: int, k: int, experts: int, H: int, F: int, O: int, x: int, ids: int, id_bytes: int,
+                   weights: int, up: GsrWeights, gate, down: GsrWeights, activation: int, out: int, workspace: int,
+                   workspace_bytes: int, stream: int) -> int:
+    """Raw entry point of the few-token layer (gate None: none).  Returns the
+    gsr_status."""
+    return lib().gsr_expert_mlp_few(tokens, k, experts, H, F, O, x or None, ids or None, int(id_bytes), weights or None,
+                                    up, gate, down, int(activation), out or None, workspace or None,
+                                    int(workspace_bytes), stream or None)
+
+
+def expert_few_workspace_bytes(tokens: int, k: int, experts: int, F: int, O: int) -> int:
+    """Workspace bytes that the few-token layer needs."""
+    got = int(lib().gsr_expert_few_workspace_bytes(int(tokens), int(k), int(experts), int(F), int(O)))
     if got < 0:
         raise GsrError(GSR_ERROR_INVALID_VALUE, status_string(GSR_ERROR_INVALID_VALUE))
     return got

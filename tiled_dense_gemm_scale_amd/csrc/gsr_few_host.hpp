@@ -1,0 +1,67 @@
+// gsr_few_host.hpp -- host helpers of the few-token entry points: operands as
+// ranges of bytes, 4-bit weights, and K (or F) cut into parts.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+#include <initializer_list>
+
+#include "gsr_host.hpp"
+#include "gsr_stream.hpp"
+
+namespace gsr {
+namespace host {
+
+struct Span {
+    const void* p;
+    uint64_t bytes;
+    uintptr_t unit;  // alignment
+};
+
+// Whether a range that has bytes is null or misaligned.
+inline bool unusable(std::initializer_list<Span> spans)
+{
+    for (const Span& s : spans)
+        if (s.bytes > 0 && (s.p == nullptr || misaligned(s.p, s.unit))) return true;
+    return false;
+}
+
+inline bool clash(const Span& out, std::initializer_list<Span> others)
+{
+    for (const Span& s : others)
+        if (overlaps(out.p, out.bytes, s.p, s.bytes)) return true;
+    return false;
+}
+
+// log2 of a group size (a power of two from 32 on), or -1.
+inline int group_log2(int64_t group)
+{
+    if (group < 32 || group > ((int64_t)1 << 30) || (group & (group - 1)) != 0) return -1;
+    int l = 5;
+    while (((int64_t)1 << l) < group) ++l;
+    return l;
+}
+
+inline uint64_t w4_code_bytes(uint64_t matrices, int64_t K, int64_t N) { return matrices * (uint64_t)cdiv(K, 8) * (uint64_t)N * 4u; }
+inline uint64_t w4_scale_count(uint64_t matrices, int64_t K, int64_t N, int64_t group)
+{
+    return matrices * (uint64_t)cdiv(K, group) * (uint64_t)N;
+}
+
+// Widths from here on are refused: a step's rows are addressed by 32-bit offsets.
+constexpr int64_t kStreamWidth = (int64_t)1 << 22;
+
+// `units` of K over parts so that `tiles` column blocks make about two
+// workgroups per CU, each wave keeping `least` units.
+struct Parts {
+    int parts, chunk;
+};
+inline Parts stream_parts(int64_t tiles, int64_t units, int64_t least)
+{
+    const int64_t want = std::min<int64_t>({16, 512 / std::max<int64_t>(tiles, 1), units / (least * kStreamWaves)});
+    const int64_t chunk = cdiv(std::max<int64_t>(units, 1), std::max<int64_t>(want, 1));
+    return Parts{(int)std::max<int64_t>(1, cdiv(units, chunk)), (int)chunk};
+}
+
+}  // namespace host
+}  // namespace gsr
