@@ -25,31 +25,29 @@ bool large_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F, int64_t 
 }
 
 struct Plan {
-    int most, blocks, parts, chunk, per;
+    int blocks_up, grid_up, blocks, groups, per;
     int64_t hidden_wide, part_wide, hidden_bytes, bytes;
 };
 
-template <class S>
-Plan plan_for(int64_t T, int64_t k, int64_t E, int64_t F, int64_t O, int64_t least)
-{
-    Plan g;
-    const int64_t slots = T * k;
-    g.most = (int)std::max<int64_t>(1, std::min(E, slots));
-    g.blocks = (int)cdiv(O, S::CB);
-    const Parts p = stream_parts((int64_t)g.most * g.blocks, cdiv(F, S::UNIT), least);
-    g.parts = p.parts;
-    g.chunk = p.chunk;
-    g.per = (int)cdiv(g.blocks, gsr::kMeetCounters);
-    g.hidden_wide = cdiv(F, 8) * 8;
-    g.part_wide = (int64_t)g.blocks * S::CB;
-    g.hidden_bytes = slots * g.hidden_wide * 2;
-    g.bytes = gsr::kMeetBytes + g.hidden_bytes + g.parts * slots * g.part_wide * 4;
-    return g;
-}
+// Workgroups of a launch: one to a CU, which is what their registers allow.
+constexpr int64_t kFewGrid = 256;
 
 Plan plan_of(bool w4, int64_t T, int64_t k, int64_t E, int64_t F, int64_t O)
 {
-    return w4 ? plan_for<gsr::W4Stream<1, 1>>(T, k, E, F, O, 1) : plan_for<gsr::HalfStream<1>>(T, k, E, F, O, 2);
+    const int64_t CB = w4 ? gsr::W4Stream<1, 1>::CB : gsr::HalfStream<1, true>::CB;
+    Plan g;
+    const int64_t slots = T * k, most = std::max<int64_t>(1, std::min(E, slots));
+    g.blocks_up = (int)cdiv(F, CB);
+    g.grid_up = (int)std::min(kFewGrid, g.blocks_up * most);
+    g.blocks = (int)cdiv(O, CB);
+    // a job is an expert and 256 rows of F at least, eight to a workgroup
+    g.groups = (int)std::max<int64_t>(1, std::min({(int64_t)16, kFewGrid / std::max(g.blocks, 1), cdiv(most * cdiv(F, 256), gsr::kStreamWaves)}));
+    g.per = (int)cdiv(g.blocks, gsr::kMeetCounters);
+    g.hidden_wide = cdiv(F, 8) * 8;
+    g.part_wide = g.blocks * CB;
+    g.hidden_bytes = slots * g.hidden_wide * 2;
+    g.bytes = gsr::kMeetBytes + g.hidden_bytes + (g.groups > 1 ? g.groups * T * g.part_wide * 4 : 0);
+    return g;
 }
 
 // The ranges of `E` matrices of K x N; false where a pointer or the group is bad.
@@ -84,22 +82,22 @@ typedef void (*few_kernel)(gsr::FewArgs);
 struct Kernels {
     few_kernel up, gated, down;
 };
-template <int FMT, int MT, int FL>
-Kernels kernels_for()
+// One tile of rows per expert up to 16 tokens (choices that name an expert twice
+// are further tiles), two above.
+template <int FORM>
+Kernels kernels_of(int64_t T)
 {
-    return Kernels{gsr::few_up_kernel<FMT, MT, FL, false>, gsr::few_up_kernel<FMT, MT, FL, true>,
-                   gsr::few_down_kernel<FMT, MT, FL>};
+    if (T <= 16) return Kernels{gsr::few_up_kernel<FORM, 1, false>, gsr::few_up_kernel<FORM, 1, true>, gsr::few_down_kernel<FORM, 1, 1>};
+    return Kernels{gsr::few_up_kernel<FORM, 2, false>, gsr::few_up_kernel<FORM, 2, true>, gsr::few_down_kernel<FORM, 2, 4>};
 }
-template <int MT>
-Kernels kernels_of(int64_t group)
+// For matrices of `w` (and `w2`, or null) of N columns.
+Kernels kernels_at(int64_t T, const gsr_weights* w, const gsr_weights* w2, int64_t N)
 {
-    return group == 0 ? kernels_for<0, MT, 1>() : group == 32 ? kernels_for<1, MT, 1>()
-                                              : group == 64   ? kernels_for<1, MT, 2>()
-                                                              : kernels_for<1, MT, 4>();
-}
-Kernels kernels_at(int64_t T, int64_t group)
-{
-    return T <= 16 ? kernels_of<1>(group) : T <= 32 ? kernels_of<2>(group) : kernels_of<4>(group);
+    if (w->group == 0) {
+        const bool dwords = N % 2 == 0 && !misaligned(w->data, 4) && (w2 == nullptr || !misaligned(w2->data, 4));
+        return dwords ? kernels_of<gsr::kFewHalf>(T) : kernels_of<gsr::kFewHalfAny>(T);
+    }
+    return w->group == 32 ? kernels_of<gsr::kFewW4x1>(T) : w->group == 64 ? kernels_of<gsr::kFewW4x2>(T) : kernels_of<gsr::kFewW4x4>(T);
 }
 
 }  // namespace
@@ -160,25 +158,21 @@ int gsr_expert_mlp_few(int64_t tokens, int64_t k, int64_t experts, int64_t H, in
     p.H = (int)H;
     p.F = (int)F;
     p.O = (int)O;
-    p.most = g.most;
     p.hidden_wide = (int)g.hidden_wide;
     p.part_wide = (int)g.part_wide;
     p.act = activation;
     p.wide_ids = id_bytes == 8;
+    p.blocks_up = g.blocks_up;
     p.blocks = g.blocks;
-    p.parts = g.parts;
-    p.chunk = g.chunk;
+    p.groups = g.groups;
     p.per = g.per;
     hipStream_t s = (hipStream_t)stream;
-    const int CB = w4 ? gsr::W4Stream<1, 1>::CB : gsr::HalfStream<1>::CB;
-    const int64_t grid_up = cdiv(F, CB) * g.most, grid_down = (int64_t)g.blocks * g.parts * g.most;
-    if (!grid_fits(grid_up, gsr::kStreamThreads) || !grid_fits(grid_down, gsr::kStreamThreads)) return GSR_ERROR_TOO_LARGE;
     if (F > 0 && slots > 0) {
-        const Kernels f = kernels_at(tokens, up->group);
-        const hipError_t err = launch_kernel(gate != nullptr ? f.gated : f.up, dim3((unsigned)grid_up), dim3(gsr::kStreamThreads), s, p);
+        const Kernels f = kernels_at(tokens, up, gate, F);
+        const hipError_t err = launch_kernel(gate != nullptr ? f.gated : f.up, dim3((unsigned)g.grid_up), dim3(gsr::kStreamThreads), s, p);
         if (err != hipSuccess) return status_of(err);
     }
-    return status_of(launch_kernel(kernels_at(tokens, down->group).down, dim3((unsigned)grid_down), dim3(gsr::kStreamThreads), s, p));
+    return status_of(launch_kernel(kernels_at(tokens, down, nullptr, O).down, dim3((unsigned)(g.blocks * g.groups)), dim3(gsr::kStreamThreads), s, p));
 }
 
 }  // extern "C"

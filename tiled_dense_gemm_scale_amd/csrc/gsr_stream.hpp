@@ -55,22 +55,23 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 
 constexpr int kStep = 32;  // k per MFMA
 
-// The rows of A that a lane reads: row l of each of MT tiles of 16 (null: none,
-// zeros).
+// The rows of A that a lane reads: row l of each of MT tiles of 16.  Rows past
+// the last are that one again, whose sums nobody takes: no load is masked, and
+// lanes with one address are one access.
 template <int MT>
 struct StreamRows {
     const uint16_t* p[MT];
-    __device__ __forceinline__ u32x4 full(int mt, int k) const
-    {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (p[mt] != nullptr) v = *(const u32x4_at2*)(p[mt] + k);
-        return v;
-    }
-    __device__ __forceinline__ u32x4 part(int mt, int k, int K) const
-    {
-        return p[mt] != nullptr ? load8_first(p[mt] + k, K - k) : u32x4{0u, 0u, 0u, 0u};
-    }
+    __device__ __forceinline__ u32x4 full(int t, int k) const { return *(const u32x4_at2*)(p[t] + k); }
+    __device__ __forceinline__ u32x4 part(int t, int k, int K) const { return load8_first(p[t] + k, K - k); }
 };
+
+// A descriptor of the rows k0 and on of a matrix of `rows` rows of `pitch` bytes
+// (whole dwords): loads behind the last row are zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, int rows, int k0, uint32_t pitch)
+{
+    const uint64_t left = (uint64_t)max(rows - k0, 0) * pitch;  // none: nothing is read
+    return make_rsrc((const uint8_t*)base + (size_t)k0 * pitch, (uint32_t)min(left, (uint64_t)0x7fffffffu));
+}
 
 // The column where lane l's CPL columns of the block from n0 start.
 template <int CPL>
@@ -93,128 +94,150 @@ struct StreamSums {
     }
 };
 
+// multiply(b[i]) for n > 0 units in turn, DEPTH - 1 units' loads in flight: load(b,
+// i) is called for units past the last too, and has to be one that reads nothing
+// new there, so that no wait depends on which way a branch went.
+template <int DEPTH, class Batch, class Load, class Multiply>
+__device__ __forceinline__ void stream_ring(int n, Load&& load, Multiply&& multiply)
+{
+    Batch b[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH - 1; ++i) load(b[i], i);
+    for (int i = 0;; i += DEPTH) {
+#pragma unroll
+        for (int j = 0; j < DEPTH; ++j) {
+            load(b[(j + DEPTH - 1) % DEPTH], i + j + DEPTH - 1);
+            multiply(b[j]);
+            if (i + j + 1 >= n) return;
+        }
+    }
+}
+
 // ---- fp16 weights ------------------------------------------------------------
 struct HalfMatrix {
     const uint16_t* b;  // K x N
 };
 
-template <int MT>
+// DW: every row starts on a dword (N even, b on one).
+template <int MT, bool DW>
 struct HalfStream {
-    static constexpr int CPL = 8, CB = 16 * CPL, UNIT = kStep;  // UNIT: k of the smallest run
+    static constexpr int CPL = 8, CB = 16 * CPL, UNIT = kStep, DEPTH = 2;  // UNIT: k of the smallest run
     typedef StreamSums<CPL, MT> Sums;
 
     struct Step {
         u32x4 b[8];
         u32x4 a[MT];
     };
+    struct Place {
+        const uint16_t* b;
+        int K, N, c, g;
+        uint32_t off[DW ? 8 : 1];  // bytes from a step's first row
+    };
 
-    __device__ static __forceinline__ void load(Step& s, const uint16_t* B, int N, uint32_t voff, const StreamRows<MT>& rows,
-                                                int tiles, int k0, int g)
+    // Unit u of a run of units before `end` (from there on nothing is read anew).
+    template <bool TAIL>
+    __device__ static __forceinline__ void load(Step& s, const Place& p, const StreamRows<MT>& rows, int u, int end)
     {
-        const uint16_t* base = B + (size_t)k0 * N;
+        const int k0 = min(u, end - 1) * kStep;
+        if (TAIL && p.N < CPL) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {  // one row in flight, for the registers' sake
+                const int k = k0 + 8 * p.g + i;
+                const u32x4 v = load8_first(p.b + (size_t)min(k, p.K - 1) * p.N + p.c, k < p.K ? p.N - p.c : 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s.b[i] = *(const u32x4_at2*)(base + (size_t)i * N + voff);
+                for (int x = 0; x < 8; ++x) s.b[x] = x == i ? v : s.b[x];
+            }
+        } else if constexpr (DW) {
+            const __amdgpu_buffer_rsrc_t rs = rows_rsrc(p.b, u < end ? p.K : 0, k0, 2u * (uint32_t)p.N);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-            if (t < tiles) s.a[t] = rows.full(t, k0 + 8 * g);
-    }
-
-    __device__ static __forceinline__ void load_part(Step& s, const uint16_t* B, int N, int K, int c,
-                                                     const StreamRows<MT>& rows, int tiles, int k0, int g)
-    {
+            for (int i = 0; i < 8; ++i) s.b[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, p.off[i], 0, 0);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int k = k0 + 8 * g + i;
-            s.b[i] = load8_first(B + (size_t)min(k, K - 1) * N + c, k < K ? N - c : 0);
+            for (int i = 0; i < 8; ++i) {
+                const int k = k0 + 8 * p.g + i;
+                s.b[i] = *(const u32x4_at2*)(p.b + (size_t)(TAIL ? min(k, p.K - 1) : k) * p.N + p.c);
+                if (TAIL && k >= p.K) s.b[i] = u32x4{0u, 0u, 0u, 0u};
+            }
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-            if (t < tiles) s.a[t] = rows.part(t, k0 + 8 * g, K);
+        for (int t = 0; t < MT; ++t) s.a[t] = TAIL ? rows.part(t, k0 + 8 * p.g, p.K) : rows.full(t, k0 + 8 * p.g);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
-    __device__ static __forceinline__ void multiply(const Step& s, int tiles, Sums& acc)
+    __device__ static __forceinline__ void multiply(const Step& s, Sums& acc)
     {
-        u32x4 o[8];
-        transpose8x8(s.b, o);
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-            if (t < tiles) {
+        for (int d = 0; d < 4; ++d) {  // columns 2d and 2d + 1
+            u32x4 even, odd;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc.v[j][t] = mfma16(s.a[t], o[j], acc.v[j][t]);
+            for (int e = 0; e < 4; ++e) {
+                even[e] = pack_lo(s.b[2 * e][d], s.b[2 * e + 1][d]);
+                odd[e] = pack_hi(s.b[2 * e][d], s.b[2 * e + 1][d]);
             }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                acc.v[2 * d][t] = mfma16(s.a[t], even, acc.v[2 * d][t]);
+                acc.v[2 * d + 1][t] = mfma16(s.a[t], odd, acc.v[2 * d + 1][t]);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // a pair's values live no longer than it
+        }
     }
 
     // acc += A[:, k] B[k, :] over the units u0 <= u < u1 of 32 k
     __device__ static __forceinline__ void run(const HalfMatrix& m, int K, int N, int n0, const StreamRows<MT>& rows,
-                                               int tiles, int u0, int u1, Sums& acc)
+                                               int u0, int u1, Sums& acc)
     {
-        const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-        const int c = stream_column<CPL>(n0, l, N);
-        const uint32_t voff = (uint32_t)(8 * g) * (uint32_t)N + (uint32_t)c;
-        const int full = N >= CPL ? min(u1, K / kStep) : u0;
-        Step s0, s1;
-        int u = u0;
-        if (u < full) {
-            load(s0, m.b, N, voff, rows, tiles, u * kStep, g);
-            for (; u + 2 < full; u += 2) {
-                load(s1, m.b, N, voff, rows, tiles, (u + 1) * kStep, g);
-                multiply(s0, tiles, acc);
-                load(s0, m.b, N, voff, rows, tiles, (u + 2) * kStep, g);
-                multiply(s1, tiles, acc);
-            }
-            if (u + 1 < full) {
-                load(s1, m.b, N, voff, rows, tiles, (u + 1) * kStep, g);
-                multiply(s0, tiles, acc);
-                multiply(s1, tiles, acc);
-                u += 2;
-            } else {
-                multiply(s0, tiles, acc);
-                u += 1;
-            }
-        }
-        for (u = max(u, u0); u < u1; ++u) {
-            load_part(s0, m.b, N, K, c, rows, tiles, u * kStep, g);
-            multiply(s0, tiles, acc);
+        const int lane = threadIdx.x & 63;
+        Place p;
+        p.b = m.b;
+        p.K = K;
+        p.N = N;
+        p.g = lane >> 4;
+        p.c = stream_column<CPL>(n0, lane & 15, N);
+        if constexpr (DW)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p.off[i] = 2u * ((uint32_t)(8 * p.g + i) * (uint32_t)N + (uint32_t)p.c);
+        const int full = N >= CPL ? max(u0, min(u1, K / kStep)) : u0;
+        if (u0 < full)
+            stream_ring<DEPTH, Step>(
+                full - u0, [&](Step& s, int i) { load<false>(s, p, rows, u0 + i, full); }, [&](const Step& s) { multiply(s, acc); });
+        for (int u = full; u < u1; ++u) {
+            Step s{};
+            load<true>(s, p, rows, u, u1);
+            multiply(s, acc);
         }
     }
 };
 
 // ---- the sum over waves ---------------------------------------------------------
-// Tile t (16 rows x CB columns) of every wave's sums goes to LDS; f(row, q, sum,
-// sum of the second set) is called for every four consecutive positions 4q of
-// a row, in wave order from +0.  With SETS = 2 the first half of the waves
-// is one sum and the second half another.
+// Each of a workgroup's waves has a slice of LDS for one tile (16 rows x CB
+// columns) of its sums, row-major.
 constexpr int kStreamWaves = 8, kStreamThreads = kWave * kStreamWaves;
 
-template <int CPL, int MT, int SETS, class F>
-__device__ __forceinline__ void stream_reduce(float* lds, const StreamSums<CPL, MT>& acc, int tiles, F&& f)
+template <int CPL, int MT>
+__device__ __forceinline__ void stream_put(float* slice, const StreamSums<CPL, MT>& acc, int t)
 {
-    constexpr int CB = 16 * CPL, QUADS = CB / 4, W = kStreamWaves / SETS;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        if (t >= tiles) break;
-        __syncthreads();
+    for (int r = 0; r < 4; ++r) {
+        f32x4* to = (f32x4*)(slice + (4 * g + r) * 16 * CPL + CPL * l);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            f32x4* to = (f32x4*)(lds + (size_t)(wave * 16 + 4 * g + r) * CB + CPL * l);
-#pragma unroll
-            for (int j = 0; j < CPL / 4; ++j)
-                to[j] = f32x4{acc.v[4 * j][t][r], acc.v[4 * j + 1][t][r], acc.v[4 * j + 2][t][r], acc.v[4 * j + 3][t][r]};
-        }
-        __syncthreads();
-        for (int u = tid; u < 16 * QUADS; u += kStreamThreads) {
-            const int m = u / QUADS, q = u % QUADS;
-            f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-            for (int w = 0; w < kStreamWaves; ++w) {
-                const f32x4 v = *(const f32x4*)(lds + (size_t)(w * 16 + m) * CB + 4 * q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[w / W][i] += v[i];
-            }
-            f(16 * t + m, q, s[0], s[1]);
-        }
+        for (int j = 0; j < CPL / 4; ++j)
+            to[j] = f32x4{acc.v[4 * j][t][r], acc.v[4 * j + 1][t][r], acc.v[4 * j + 2][t][r], acc.v[4 * j + 3][t][r]};
     }
+}
+
+// Positions 4q .. 4q + 3 of row m, summed over `waves` slices in order from +0.
+template <int CPL>
+__device__ __forceinline__ f32x4 stream_sum(const float* slices, int waves, int m, int q)
+{
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int w = 0; w < waves; ++w) {
+        const f32x4 v = *(const f32x4*)(slices + (size_t)(w * 16 + m) * 16 * CPL + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += v[i];
+    }
+    return s;
 }
 
 // The column of position 4q of the block from n0 (the first of four), or -1

@@ -18,19 +18,30 @@ struct W4Matrix {
 
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 
+// (w & mask) | base in one instruction: the mask in a scalar register, the base
+// in a vector one, as the encoding has room for one constant of neither.
+__device__ __forceinline__ half2v and_or(uint32_t w, uint32_t mask, uint32_t base)
+{
+    uint32_t d;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(w), "s"(mask), "v"(base));
+    return __builtin_bit_cast(half2v, d);
+}
+
 // The eight values q - z of a word as an MFMA operand: dword i holds rows i and
 // i + 4.  A code behind the bits of 1024 in fp16 is 1024 + q, four bits higher
 // 1024 + 16 q, and the differences below are whole numbers of at most 9 bits,
-// so every value is exact.  lo: -(1024 + z), hi: -(64 + z), twice each.
+// so every value is exact.  lo: -(1024 + z), hi: -(64 + z), twice each.  Nine
+// instructions for eight weights; the loop is bound by them where the weights'
+// bytes come fast enough.
 __device__ __forceinline__ u32x4 w4_values(uint32_t w, half2v lo, half2v hi)
 {
     constexpr uint32_t kBase = 0x64006400u;
     const half2v sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
     const uint32_t t = w >> 8;
-    const half2v a = __builtin_bit_cast(half2v, (w & 0x000f000fu) | kBase) + lo;
-    const half2v b = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (w & 0x00f000f0u) | kBase), sixteenth, hi);
-    const half2v c = __builtin_bit_cast(half2v, (t & 0x000f000fu) | kBase) + lo;
-    const half2v d = __builtin_elementwise_fma(__builtin_bit_cast(half2v, (t & 0x00f000f0u) | kBase), sixteenth, hi);
+    const half2v a = and_or(w, 0x000f000fu, kBase) + lo;
+    const half2v b = __builtin_elementwise_fma(and_or(w, 0x00f000f0u, kBase), sixteenth, hi);
+    const half2v c = and_or(t, 0x000f000fu, kBase) + lo;
+    const half2v d = __builtin_elementwise_fma(and_or(t, 0x00f000f0u, kBase), sixteenth, hi);
     return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
                  __builtin_bit_cast(uint32_t, d)};
 }
@@ -47,7 +58,7 @@ __device__ __forceinline__ u32x4 w4_order(u32x4 a)
 // the weights are never rounded.  FL: steps between such ends (1, 2 or 4).
 template <int MT, int FL>
 struct W4Stream {
-    static constexpr int CPL = 4, CB = 16 * CPL, STEPS = 4, UNIT = STEPS * kStep, ENDS = STEPS / FL;
+    static constexpr int CPL = 4, CB = 16 * CPL, STEPS = 4, UNIT = STEPS * kStep, ENDS = STEPS / FL, DEPTH = 2;
     typedef StreamSums<CPL, MT> Sums;
 
     struct Batch {
@@ -56,132 +67,138 @@ struct W4Stream {
         u32x2 s[ENDS];
         uint32_t z[ENDS];
     };
+    struct Place {
+        W4Matrix m;
+        const uint8_t* zeros;  // m.zeros, or any readable bytes of that many
+        int K, N, c, g;
+        uint32_t off[STEPS];   // bytes from a unit's first row of words
+    };
 
-    __device__ static __forceinline__ void load(Batch& t, const W4Matrix& m, int N, uint32_t voff, int c,
-                                                const StreamRows<MT>& rows, int tiles, int u, int g)
+    // Unit u of a run of units before `end` (from there on nothing is read anew).
+    __device__ static __forceinline__ void load(Batch& t, const Place& p, const StreamRows<MT>& rows, int u, int end)
     {
-        const int k0 = u * UNIT;
+        const int k0 = min(u, end - 1) * UNIT;
+        const __amdgpu_buffer_rsrc_t rs = rows_rsrc(p.m.codes, u < end ? (p.K + 7) / 8 : 0, k0 / 8, 4u * (uint32_t)p.N);
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-            t.w[i] = *(const u32x4_at4*)(m.codes + (size_t)(k0 / 8 + 4 * i) * N + voff);
+        for (int i = 0; i < STEPS; ++i) t.w[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, p.off[i], 0, 0);
 #pragma unroll
         for (int e = 0; e < ENDS; ++e) {
-            const size_t row = (size_t)((k0 + e * FL * kStep) >> m.glog2) * N;
-            t.s[e] = *(const u32x2_at2*)(m.scales + row + (uint32_t)c);
-            t.z[e] = m.zeros ? *(const u32_at1*)(m.zeros + row + (uint32_t)c) : 0x08080808u;
+            const size_t row = (size_t)((k0 + e * FL * kStep) >> p.m.glog2) * p.N;
+            t.s[e] = *(const u32x2_at2*)(p.m.scales + row + p.c);
+            t.z[e] = *(const u32_at1*)(p.zeros + row + p.c);
         }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-            for (int x = 0; x < MT; ++x)
-                if (x < tiles) t.a[i][x] = rows.full(x, k0 + i * kStep + 8 * g);
+            for (int x = 0; x < MT; ++x) t.a[i][x] = rows.full(x, k0 + i * kStep + 8 * p.g);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
-    __device__ static __forceinline__ void load_part(Batch& t, const W4Matrix& m, int K, int N, int c,
-                                                     const StreamRows<MT>& rows, int tiles, int u, int g)
+    // The scale and the zero point's two forms of a lane's columns.
+    struct Scale {
+        half2v lo[CPL], hi[CPL];
+        float s[CPL];
+    };
+    __device__ static __forceinline__ void scale_of(Scale& v, u32x2 s, uint32_t zeros, bool have)
     {
-        const int k0 = u * UNIT, words = (K + 7) / 8;
+        const uint32_t all = have ? zeros : 0x08080808u;
+        const half2v shift = {(_Float16)960.0f, (_Float16)960.0f};
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int r = k0 / 8 + 4 * i + g;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) t.w[i][j] = (r < words && c + j < N) ? m.codes[(size_t)r * N + c + j] : 0u;
+        for (int j = 0; j < CPL; ++j) {
+            // the bits of -(1024 + z) are 0xe400 + z
+            const uint32_t pick = 0x04000400u | (uint32_t)j * 0x00010001u;
+            v.lo[j] = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0xe4e4e4e4u, all, pick));
+            v.hi[j] = v.lo[j] + shift;
+            v.s[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(s[j / 2] >> (16 * (j & 1))));
         }
-#pragma unroll
-        for (int e = 0; e < ENDS; ++e) {
-            const int k = k0 + e * FL * kStep;
-            const size_t row = (size_t)(k >> m.glog2) * N;
-            uint16_t s[CPL];
-            t.z[e] = 0u;
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const bool in = k < K && c + j < N;
-                s[j] = in ? m.scales[row + c + j] : (uint16_t)0;
-                t.z[e] |= (uint32_t)(in && m.zeros ? m.zeros[row + c + j] : (uint8_t)8) << (8 * j);
-            }
-            t.s[e] = u32x2{join16(s[0], s[1]), join16(s[2], s[3])};
-        }
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-            for (int x = 0; x < MT; ++x)
-                if (x < tiles) t.a[i][x] = rows.part(x, k0 + i * kStep + 8 * g, K);
     }
 
-    // `ends`: how many of the batch's ends there are (fewer in the last batch of K)
-    __device__ static __forceinline__ void multiply(const Batch& t, int tiles, int ends, Sums& acc)
+    __device__ static __forceinline__ void multiply(const Batch& t, const Place& p, Sums& acc)
     {
 #pragma unroll
         for (int e = 0; e < ENDS; ++e) {
-            if (e >= ends) break;
-            half2v lo[CPL], hi[CPL];
-            float s[CPL];
-#pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const _Float16 z = (_Float16)(float)((t.z[e] >> (8 * j)) & 0xffu);
-                const _Float16 l = (_Float16)-1024.0f - z, h = (_Float16)-64.0f - z;
-                lo[j] = half2v{l, l};
-                hi[j] = half2v{h, h};
-                s[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(t.s[e][j / 2] >> (16 * (j & 1))));
-            }
+            Scale v;
+            scale_of(v, t.s[e], t.z[e], p.m.zeros != nullptr);
             f32x4 sum[CPL][MT];
 #pragma unroll
             for (int i = 0; i < FL; ++i) {
-                u32x4 b[CPL];
+                u32x4 a[MT];
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) b[j] = w4_values(t.w[e * FL + i][j], lo[j], hi[j]);
+                for (int x = 0; x < MT; ++x) a[x] = w4_order(t.a[e * FL + i][x]);
 #pragma unroll
-                for (int x = 0; x < MT; ++x)
-                    if (x < tiles) {
-                        const u32x4 a = w4_order(t.a[e * FL + i][x]);
+                for (int j = 0; j < CPL; ++j) {
+                    const u32x4 b = w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]);
 #pragma unroll
-                        for (int j = 0; j < CPL; ++j)
-                            sum[j][x] = mfma16(a, b[j], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j][x]);
-                    }
+                    for (int x = 0; x < MT; ++x)
+                        sum[j][x] = mfma16(a[x], b, i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j][x]);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // a step's values live no longer than it
             }
 #pragma unroll
-            for (int x = 0; x < MT; ++x)
-                if (x < tiles) {
+            for (int j = 0; j < CPL; ++j)
 #pragma unroll
-                    for (int j = 0; j < CPL; ++j)
+                for (int x = 0; x < MT; ++x)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc.v[j][x][r] = fmaf(s[j], sum[j][x][r], acc.v[j][x][r]);
-                }
+                    for (int r = 0; r < 4; ++r) acc.v[j][x][r] = fmaf(v.s[j], sum[j][x][r], acc.v[j][x][r]);
         }
+    }
+
+    // One step of 32 rows, any of which may lie past K, of a matrix of any
+    // width: value by value and scaled by itself.
+    __device__ static __forceinline__ void step(const Place& p, const StreamRows<MT>& rows, int k0, Sums& acc)
+    {
+        const int r = k0 / 8 + p.g, words = (p.K + 7) / 8;
+        const size_t row = (size_t)(k0 >> p.m.glog2) * p.N;
+        Scale v;
+        u32x4 w;
+        uint16_t s[CPL];
+        uint32_t zeros = 0u;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const bool in = p.c + j < p.N;
+            w[j] = r < words && in ? p.m.codes[(size_t)r * p.N + p.c + j] : 0u;
+            s[j] = in ? p.m.scales[row + p.c + j] : (uint16_t)0;
+            zeros |= (uint32_t)(in ? p.zeros[row + p.c + j] : (uint8_t)0) << (8 * j);
+        }
+        scale_of(v, u32x2{join16(s[0], s[1]), join16(s[2], s[3])}, zeros, p.m.zeros != nullptr);
+#pragma unroll
+        for (int x = 0; x < MT; ++x) {
+            const u32x4 a = w4_order(rows.part(x, k0 + 8 * p.g, p.K));
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                const f32x4 sum = mfma16(a, w4_values(w[j], v.lo[j], v.hi[j]), f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) acc.v[j][x][r4] = fmaf(v.s[j], sum[r4], acc.v[j][x][r4]);
+            }
+        }
+    }
+
+    __device__ static __forceinline__ Place place(const W4Matrix& m, int K, int N, int n0)
+    {
+        const int lane = threadIdx.x & 63;
+        Place p;
+        p.m = m;
+        p.zeros = m.zeros ? m.zeros : (const uint8_t*)m.scales;  // without zeros its loads are not looked at
+        p.K = K;
+        p.N = N;
+        p.g = lane >> 4;
+        p.c = stream_column<CPL>(n0, lane & 15, N);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) p.off[i] = 4u * ((uint32_t)(4 * i + p.g) * (uint32_t)N + (uint32_t)p.c);
+        return p;
     }
 
     // acc += A[:, k] w[k, :] over the units u0 <= u < u1 of 128 k
     __device__ static __forceinline__ void run(const W4Matrix& m, int K, int N, int n0, const StreamRows<MT>& rows,
-                                               int tiles, int u0, int u1, Sums& acc)
+                                               int u0, int u1, Sums& acc)
     {
-        const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-        const int c = stream_column<CPL>(n0, l, N);
-        const uint32_t voff = (uint32_t)g * (uint32_t)N + (uint32_t)c;
-        const int full = N >= CPL ? min(u1, K / UNIT) : u0;
-        Batch b0, b1;
-        int u = u0;
-        if (u < full) {
-            load(b0, m, N, voff, c, rows, tiles, u, g);
-            for (; u + 2 < full; u += 2) {
-                load(b1, m, N, voff, c, rows, tiles, u + 1, g);
-                multiply(b0, tiles, ENDS, acc);
-                load(b0, m, N, voff, c, rows, tiles, u + 2, g);
-                multiply(b1, tiles, ENDS, acc);
-            }
-            if (u + 1 < full) {
-                load(b1, m, N, voff, c, rows, tiles, u + 1, g);
-                multiply(b0, tiles, ENDS, acc);
-                multiply(b1, tiles, ENDS, acc);
-                u += 2;
-            } else {
-                multiply(b0, tiles, ENDS, acc);
-                u += 1;
-            }
-        }
-        for (u = max(u, u0); u < u1; ++u) {
-            load_part(b0, m, K, N, c, rows, tiles, u, g);
-            multiply(b0, tiles, min(ENDS, (K - u * UNIT + FL * kStep - 1) / (FL * kStep)), acc);
-        }
+        const Place p = place(m, K, N, n0);
+        const int full = N >= CPL ? max(u0, min(u1, K / UNIT)) : u0;
+        if (u0 < full)
+            stream_ring<DEPTH, Batch>(
+                full - u0, [&](Batch& t, int i) { load(t, p, rows, u0 + i, full); }, [&](const Batch& t) { multiply(t, p, acc); });
+#pragma unroll 1
+        for (int k0 = full * UNIT; k0 < min(K, u1 * UNIT); k0 += kStep) step(p, rows, k0, acc);
     }
 };
 

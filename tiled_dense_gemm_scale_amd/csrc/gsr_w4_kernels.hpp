@@ -24,7 +24,7 @@ struct W4Gemm {
 // With more than one part the sums meet in the workspace and the last workgroup
 // of a counter's blocks adds them in part order.
 template <int MT, int FL>
-__global__ void __launch_bounds__(kStreamThreads) w4_gemm_kernel(W4Gemm p)
+__global__ void __launch_bounds__(kStreamThreads, 2) w4_gemm_kernel(W4Gemm p)
 {
     using S = W4Stream<MT, FL>;
     constexpr int CPL = S::CPL, CB = S::CB, QUADS = CB / 4;
@@ -33,17 +33,16 @@ __global__ void __launch_bounds__(kStreamThreads) w4_gemm_kernel(W4Gemm p)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 15;
     const int part = blockIdx.x % p.parts, tile = blockIdx.x / p.parts, nb = tile % p.blocks_n;
     const int m0 = tile / p.blocks_n * 16 * MT, n0 = nb * CB, rows_here = min(16 * MT, p.M - m0);
-    const int tiles = (rows_here + 15) / 16;
 
     StreamRows<MT> rows;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) rows.p[t] = 16 * t + l < rows_here ? p.a + (size_t)(m0 + 16 * t + l) * p.K : nullptr;
+    for (int t = 0; t < MT; ++t) rows.p[t] = p.a + (size_t)(m0 + min(16 * t + l, rows_here - 1)) * p.K;
     const int units = (p.K + S::UNIT - 1) / S::UNIT;
     const int first = part * p.chunk, here = max(0, min(p.chunk, units - first));
     const int u0 = first + here * wave / kStreamWaves, u1 = first + here * (wave + 1) / kStreamWaves;
     typename S::Sums acc;
     acc.clear();
-    S::run(p.w, p.K, p.N, n0, rows, tiles, u0, u1, acc);
+    S::run(p.w, p.K, p.N, n0, rows, u0, u1, acc);
 
     auto finish = [&](int m, int q, int at, f32x4 s) {
         const int col = stream_position<CPL>(at, q, p.N);
@@ -53,16 +52,19 @@ __global__ void __launch_bounds__(kStreamThreads) w4_gemm_kernel(W4Gemm p)
         for (int i = 0; i < 4; ++i)
             if (col + i < p.N) to[i] = to_half(activate(s[i] * p.alpha + (p.bias ? half_at(p.bias + col + i) : 0.0f), p.act));
     };
-    if (p.parts == 1) {
-        stream_reduce<CPL, MT, 1>(lds, acc, tiles, [&](int m, int q, f32x4 s, f32x4) {
-            if (m < rows_here) finish(m0 + m, q, n0, s);
-        });
-        return;
-    }
     const size_t wide = (size_t)p.blocks_n * CB;
-    stream_reduce<CPL, MT, 1>(lds, acc, tiles, [&](int m, int q, f32x4 s, f32x4) {
-        if (m < rows_here) meet_store(p.part + ((size_t)part * p.M + m0 + m) * wide + n0 + 4 * q, s);
-    });
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        __syncthreads();
+        stream_put<CPL, MT>(lds + wave * 16 * CB, acc, t);
+        __syncthreads();
+        const int m = 16 * t + threadIdx.x / QUADS, q = threadIdx.x % QUADS;
+        if (threadIdx.x >= 16 * QUADS || m >= rows_here) continue;
+        const f32x4 s = stream_sum<CPL>(lds, kStreamWaves, m - 16 * t, q);
+        if (p.parts == 1) finish(m0 + m, q, n0, s);
+        else meet_store(p.part + ((size_t)part * p.M + m0 + m) * wide + n0 + 4 * q, s);
+    }
+    if (p.parts == 1) return;
     const int b0 = nb / p.per * p.per, b1 = min(b0 + p.per, p.blocks_n);
     if (!meet_last(p.count + nb / p.per, (uint32_t)((b1 - b0) * p.parts), &flag)) return;
     for (int b = b0; b < b1; ++b)
