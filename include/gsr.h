@@ -387,13 +387,16 @@ int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group,
  *
  * A, bias, C, alpha and the activation as gemm_scale_bias_act's, at any 2-byte
  * alignment; matrices may be larger than 2^31 bytes, M is below 2^31.  The
- * products A[m,k] (q - zero) are summed exactly as written in binary32, group by
- * group, and the scale multiplies a group's sum: the weights are not rounded.
+ * products A[m,k] (q - zero) are summed in binary32, group by group, and the
+ * scale multiplies a group's sum: the weights are not rounded.  Where many rows
+ * make it faster (more than 16, commonly from 150 on) and the workspace holds K x N
+ * binary16 values, the weights are first written there as gsr_dequantize_w4 gives
+ * them, each rounded once to binary16, and multiplied by the dense kernels.
  * A scale that is not finite makes its column's outputs not finite.
  *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its first
  *              512 bytes zero before the first call and again after each), of
  *              gsr_w4_workspace_bytes(M, N, K) bytes; with less or NULL K is
- *              not split across workgroups
+ *              not split across workgroups, and the weights are not written out
  * Ownership, streams and errors as gemm_scale_bias_act_ws. */
 int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
                            int64_t group, const uint32_t* codes, const void* scales, const uint8_t* zeros,

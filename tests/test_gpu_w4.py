@@ -170,7 +170,9 @@ def test_product(gsr, case, act):
     a64 = a.astype(np.float64)
     top = alpha * (np.abs(a64) @ np.abs(f)) + np.abs(bias.astype(np.float64))
     v = alpha * (a64 @ f) + bias.astype(np.float64)
-    slack = ref.act_slack(ref.sum_slack(K + -(-K // group) + 2, top), v, act)
+    # many rows take weights rounded to fp16: half a step each
+    rounded = alpha * (np.abs(a64) @ ref.half_step(f)) if M > 16 else 0.0
+    slack = ref.act_slack(ref.sum_slack(K + -(-K // group) + 2, top) + rounded, v, act)
     want = ref.act64(v, act)
     say(f"w4 {case} {act}")
     ws = gsr.new_workspace(gsr.w4_workspace_bytes(M, N, K))
@@ -180,6 +182,31 @@ def test_product(gsr, case, act):
     say(f"w4 {case} {act}: worst {float((err / bound).max()):.3f} of its bound, "
         f"{float(err.max() / np.abs(want).max()):.1e} of the largest output")
     assert (err <= bound).all()
+
+
+@pytest.mark.parametrize("case", [(1025, 2048, 1024, 128), (700, 1000, 4096, 64), (4000, 333, 1001, 32)], ids=lambda c: "x".join(map(str, c)))
+def test_product_of_many_rows(gsr, case):
+    """Many rows: the bits of the dense product with the weights' values, and the
+    formula's within one more rounding; a workspace too small for the values keeps
+    the weights as they are."""
+    M, N, K, group = case
+    rng = np.random.default_rng(M)
+    q, s, z = weights(rng, K, N, group, True, False)
+    w = handle(gsr, q, s, z, K, group)
+    a, bias = torch.randn(M, K, device=DEV).half(), torch.randn(N, device=DEV).half()
+    nbytes = gsr.w4_workspace_bytes(M, N, K)
+    assert nbytes == 512 + 2 * K * N
+    say(f"w4 many rows {case}")
+    got = gsr.gemm_w4(a, w, gsr.new_workspace(nbytes), bias=bias, alpha=0.5, activation="gelu")
+    assert torch.equal(got, gsr.gemm_scale_bias_act(a, gsr.dequantize_w4(w), bias, 0.5, "gelu"))
+    f, a64 = ref.values(q, s, z, group), a.cpu().numpy().astype(np.float64)
+    b64 = bias.cpu().numpy().astype(np.float64)
+    v, top = 0.5 * (a64 @ f) + b64, 0.5 * (np.abs(a64) @ np.abs(f)) + np.abs(b64)
+    for work, rounded in ((gsr.new_workspace(nbytes), 0.5 * (np.abs(a64) @ ref.half_step(f))), (gsr.new_workspace(nbytes - 1), 0.0)):
+        slack = ref.act_slack(ref.sum_slack(K + -(-K // group) + 2, top) + rounded, v, "gelu")
+        want = ref.act64(v, "gelu")
+        err = np.abs(gsr.gemm_w4(a, w, work, bias=bias, alpha=0.5, activation="gelu").cpu().numpy().astype(np.float64) - want)
+        assert (err <= slack + ref.half_step(np.abs(want) + slack)).all()
 
 
 @pytest.mark.parametrize("shape", [(1, 4096, 512, 128), (9, 130, 300, 64), (40, 77, 333, 32), (70, 77, 333, 32)],

@@ -236,7 +236,7 @@ const Candidate kCandidates[] = {
 };
 constexpr double kPartMin = 0.80, kPartA = 0.35;  // a part-filled last wave: max(kPartMin, kPartA + (1 - kPartA) * fill)
 
-int select(int64_t M, int64_t N, int64_t K)
+int select(int64_t M, int64_t N, int64_t K, double* time = nullptr)
 {
     const double cus = 256.0;
     int best = 28;
@@ -255,6 +255,7 @@ int select(int64_t M, int64_t N, int64_t K)
             best = c.id;
         }
     }
+    if (time != nullptr) *time = best_t;
     return best;
 }
 
@@ -268,6 +269,13 @@ double gsr::host::tile_time(int id, int64_t K)
             return 2.0 * g.block_m * g.block_n * (double)K / (c.tflops_per_cu * 1e6) + c.tile_us;
         }
     return 0.0;
+}
+
+double gsr::host::dense_time(int64_t M, int64_t N, int64_t K)
+{
+    double t = 0.0;
+    select(M, N, K, &t);
+    return t;
 }
 
 namespace {

@@ -51,15 +51,16 @@ struct FewArgs {
     int act;
     bool wide_ids;
     int blocks_up;         // column blocks of the first launch
+    int waves_log2;        // its waves (a power of two)
     int blocks, groups;    // of the second: column blocks, workgroups to each
     int per;               // column blocks per counter
 };
 
-// The stream of a form of weights: fp16 with rows on dwords, fp16 at any
-// address, 4 bits with groups of 32, 64, and 128 or more rows.
-enum : int { kFewHalf = 0, kFewHalfAny = 1, kFewW4x1 = 2, kFewW4x2 = 3, kFewW4x4 = 4 };
-template <int FORM, int MT>
-struct FewStream : W4Stream<MT, FORM == kFewW4x1 ? 1 : FORM == kFewW4x2 ? 2 : 4> {
+// The stream of a form of weights: fp16, 4 bits with groups of 32, 64, and 128 or
+// more rows.  DW: every row of fp16 weights and of A starts on a dword.
+enum : int { kFewHalf = 0, kFewW4x1 = 1, kFewW4x2 = 2, kFewW4x4 = 3 };
+template <int FORM, int MT, bool DW>
+struct FewStream : W4Stream<MT, FORM == kFewW4x1 ? 1 : FORM == kFewW4x2 ? 2 : 4, DW> {
     __device__ static __forceinline__ W4Matrix matrix(const FewWeights& w, int e, int K, int N)
     {
         const size_t words = (size_t)((K + 7) / 8) * N, groups = (size_t)((((int64_t)K - 1) >> w.glog2) + 1) * N;
@@ -67,15 +68,8 @@ struct FewStream : W4Stream<MT, FORM == kFewW4x1 ? 1 : FORM == kFewW4x2 ? 2 : 4>
                         w.glog2};
     }
 };
-template <int MT>
-struct FewStream<kFewHalf, MT> : HalfStream<MT, true> {
-    __device__ static __forceinline__ HalfMatrix matrix(const FewWeights& w, int e, int K, int N)
-    {
-        return HalfMatrix{(const uint16_t*)w.data + (size_t)e * K * N};
-    }
-};
-template <int MT>
-struct FewStream<kFewHalfAny, MT> : HalfStream<MT, false> {
+template <int MT, bool DW>
+struct FewStream<kFewHalf, MT, DW> : HalfStream<MT, DW> {
     __device__ static __forceinline__ HalfMatrix matrix(const FewWeights& w, int e, int K, int N)
     {
         return HalfMatrix{(const uint16_t*)w.data + (size_t)e * K * N};
@@ -99,7 +93,7 @@ __device__ __forceinline__ void wave_fence()
 // the wave's set of experts; returns how many are hit.
 __device__ __forceinline__ int few_keys(FewWave& s, int16_t* key, const FewArgs& p)
 {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, words = (p.experts + 31) / 32;
     if (lane < kFewExperts / 32) s.hit[lane] = 0u;
     wave_fence();
     for (int i = lane; i < p.slots; i += kWave) {
@@ -109,29 +103,26 @@ __device__ __forceinline__ int few_keys(FewWave& s, int16_t* key, const FewArgs&
         if (in) atomicOr(&s.hit[(int)id >> 5], 1u << ((int)id & 31));
     }
     wave_fence();
-    int n = lane < kFewExperts / 32 ? __popc(s.hit[lane]) : 0;
-#pragma unroll
-    for (int x = 1; x < kFewExperts / 32; x <<= 1) n += __shfl_xor(n, x);
-    return __builtin_amdgcn_readfirstlane(n);
+    const uint32_t w = s.hit[lane & (kFewExperts / 32 - 1)];
+    int n = 0;
+    for (int i = 0; i < words; ++i) n += __popc(__builtin_amdgcn_readlane(w, i));
+    return n;
 }
 
 // The d-th expert that is hit, ascending (d below their number).
 __device__ __forceinline__ int few_expert(const FewWave& s, int d)
 {
-    const int lane = threadIdx.x & 63;
-    const uint32_t w = lane < kFewExperts / 32 ? s.hit[lane] : 0u;
-    const int mine = __popc(w);
-    int upto = mine;
-#pragma unroll
-    for (int x = 1; x < kFewExperts / 32; x <<= 1) {
-        const int o = __shfl_up(upto, x);
-        if (lane >= x) upto += o;
+    const uint32_t w = s.hit[threadIdx.x & (kFewExperts / 32 - 1)];
+    int i = 0;
+    uint32_t bits;
+    for (;; ++i) {
+        bits = __builtin_amdgcn_readlane(w, i);
+        const int n = __popc(bits);
+        if (d < n) break;
+        d -= n;
     }
-    const int word = __ffsll((unsigned long long)__ballot(d < upto)) - 1;  // the lowest lane of these holds it
-    uint32_t bits = __builtin_amdgcn_readlane(w, word);
-    int left = d - (__builtin_amdgcn_readlane(upto, word) - __popc(bits));
-    for (; left > 0; --left) bits &= bits - 1u;
-    return __builtin_amdgcn_readfirstlane(32 * word + __ffs((int)bits) - 1);
+    for (; d > 0; --d) bits &= bits - 1u;
+    return 32 * i + __ffs((int)bits) - 1;
 }
 
 // The slots m0 .. m0 + 2 kFewRows - 1 of expert e into s.slot; how many it has in all.
@@ -152,39 +143,37 @@ __device__ __forceinline__ int few_rows(FewWave& s, const int16_t* key, int slot
 }
 
 // acc of MT tiles from `left` rows: streams one tile where that is all.
-template <int FORM, int MT>
-__device__ __forceinline__ void few_stream(const FewWeights& w, int e, int K, int N, int n0, const StreamRows<MT>& rows, int left,
-                                           int u0, int u1, typename FewStream<FORM, MT>::Sums& acc)
+template <int FORM, int MT, bool DW>
+__device__ __forceinline__ void few_stream(const FewWeights& w, int e, int K, int N, int n0, const StreamRows<MT, DW>& rows, int left,
+                                           int u0, int u1, typename FewStream<FORM, MT, DW>::Sums& acc)
 {
     acc.clear();
     if (MT > 1 && left <= kFewRows) {
-        using S = FewStream<FORM, 1>;
-        StreamRows<1> one;
-        one.p[0] = rows.p[0];
+        using S = FewStream<FORM, 1, DW>;
         typename S::Sums sums;
         sums.clear();
-        S::run(S::matrix(w, e, K, N), K, N, n0, one, u0, u1, sums);
+        S::run(S::matrix(w, e, K, N), K, N, n0, StreamRows<1, DW>(rows), u0, u1, sums);
 #pragma unroll
         for (int j = 0; j < S::CPL; ++j) acc.v[j][0] = sums.v[j][0];
     } else {
-        using S = FewStream<FORM, MT>;
+        using S = FewStream<FORM, MT, DW>;
         S::run(S::matrix(w, e, K, N), K, N, n0, rows, u0, u1, acc);
     }
 }
 
-// How many of a workgroup's waves split an item's K of `units` (`least` at
-// least): the count for which the grid's rounds, each `fixed` units longer than
-// its share of K, are shortest.
-__device__ __forceinline__ int few_split(int items, int workgroups, int units, int fixed, int least)
+// log2 of how many of a workgroup's waves split an item's K of `units` (2^least
+// at least): the count for which the rounds of `waves` (a power of two) waves,
+// each `fixed` units longer than its share of K, are shortest.
+__device__ __forceinline__ int few_split(int items, int waves_log2, int units, int fixed, int least)
 {
-    int best = least;
-    int64_t shortest = INT64_MAX;
-    for (int kg = least; kg <= kStreamWaves; kg *= 2) {
-        const int64_t rounds = ((int64_t)items * kg + workgroups * kStreamWaves - 1) / (workgroups * kStreamWaves);
-        const int64_t cost = rounds * ((units * least + kg - 1) / kg + fixed);
+    int best = least, shortest = INT32_MAX;
+    for (int s = least; s <= 3; ++s) {
+        const int rounds = (int)((((int64_t)items << s) + (1 << waves_log2) - 1) >> waves_log2);
+        const int share = units >> (s - least);  // of 2^22 / 32 units at most; rounded down, as it is an estimate
+        const int64_t cost = (int64_t)rounds * (share + fixed);
         if (cost < shortest) {
-            shortest = cost;
-            best = kg;
+            shortest = (int)cost;
+            best = s;
         }
     }
     return best;
@@ -192,11 +181,11 @@ __device__ __forceinline__ int few_split(int items, int workgroups, int units, i
 
 // h of the experts' slots.  With a gate the first half of an item's waves
 // streams the gate and the second half up.
-template <int FORM, int MT, bool GATED>
+template <int FORM, int MT, bool DW, bool GATED>
 __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
 {
-    using S = FewStream<FORM, MT>;
-    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, QUADS = CB / 4, EACH = 16 * QUADS, SETS = GATED ? 2 : 1;
+    using S = FewStream<FORM, MT, DW>;
+    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, SETS = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ FewWave waves[kStreamWaves];
     __shared__ int16_t key[kFewSlots];
@@ -204,25 +193,24 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 15;
     FewWave& mine = waves[wave];
     const int hits = few_keys(mine, key, p), items = hits * p.blocks_up, units = (p.H + UNIT - 1) / UNIT;
-    const int kg = few_split(items, gridDim.x, units, 256 / UNIT, SETS), cg = kStreamWaves / kg;
-    const int turn = wave % kg, half = kg / SETS;  // the waves of one matrix
+    const int kl = few_split(items, p.waves_log2, units, 256 / UNIT, SETS - 1), kg = 1 << kl, cg = kStreamWaves >> kl;
+    const int turn = wave & (kg - 1), half = kg / SETS;  // the waves of one matrix
     const FewWeights& w = GATED && turn < half ? p.gate : p.up;
-    const int u0 = (int)((int64_t)units * (turn % half) / half), u1 = (int)((int64_t)units * (turn % half + 1) / half);
+    const int u0 = units * (turn & (half - 1)) / half, u1 = units * ((turn & (half - 1)) + 1) / half;
 
     for (int first = blockIdx.x * cg; first < items; first += gridDim.x * cg) {
-        const int item = first + wave / kg, n0 = item % p.blocks_up * CB;
+        const int item = first + (wave >> kl), d = item / p.blocks_up, n0 = (item - d * p.blocks_up) * CB;
         const bool have = item < items;
-        const int e = have ? few_expert(mine, item / p.blocks_up) : -1;
+        const int e = have ? few_expert(mine, d) : -1;
         int count = 0, m0 = 0;
         do {
             if (have) count = few_rows(mine, key, p.slots, e, m0);
             typename S::Sums acc;
             if (m0 < count) {
-                StreamRows<MT> rows;
+                typename S::Rows rows(p.x, (uint64_t)p.T * (uint32_t)p.H * 2u);
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    rows.p[t] = p.x + (size_t)(mine.slot[min(16 * t + l, count - 1 - m0)] / p.k) * p.H;
-                few_stream<FORM, MT>(w, e, p.H, p.F, n0, rows, count - m0, u0, u1, acc);
+                for (int t = 0; t < MT; ++t) rows.row(t, (uint32_t)mine.slot[min(16 * t + l, count - 1 - m0)] / (uint32_t)p.k * (uint32_t)p.H);
+                few_stream<FORM, MT, DW>(w, e, p.H, p.F, n0, rows, count - m0, u0, u1, acc);
             }
             if ((threadIdx.x & 63) == 0) {
                 experts[wave] = e;
@@ -234,25 +222,22 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
                 if (m0 + 16 * t < count) stream_put<CPL, MT>(lds + wave * 16 * CB, acc, t);
                 __syncthreads();
 #pragma unroll 1
-                for (int u = threadIdx.x; u < cg * EACH; u += kStreamThreads) {
-                    const int c = u / EACH, m = u % EACH / QUADS, q = u % QUADS;
-                    const int col = stream_position<CPL>((first + c) % p.blocks_up * CB, q, p.F);
-                    if (m0 + 16 * t + m >= counts[c * kg] || col < 0) continue;
-                    const f32x4 s = stream_sum<CPL>(lds + (c * kg + kg - half) * 16 * CB, half, m, q);
-                    f32x4 gate = {0.f, 0.f, 0.f, 0.f};
-                    if constexpr (GATED) gate = stream_sum<CPL>(lds + c * kg * 16 * CB, half, m, q);
-                    uint16_t* to = p.hidden + (size_t)waves[c * kg].slot[16 * t + m] * p.hidden_wide + col;
-                    const size_t b = (size_t)experts[c * kg] * p.F + col;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if (col + x >= p.F) break;
-                        const float v = s[x] + (p.up.bias ? half_at(p.up.bias + b + x) : 0.0f);
+                for (int c = 0; c < cg; ++c) {
+                    const int at_n0 = (first + c) % p.blocks_up * CB, ex = experts[c << kl], here = min(16, counts[c << kl] - m0 - 16 * t);
+                    const float* slices = lds + (c << kl) * 16 * CB;
+#pragma unroll 1
+                    for (int u = threadIdx.x; u < here * CB; u += kStreamThreads) {
+                        const int m = u / CB, at = u % CB, col = stream_position<CPL>(at_n0, at, p.F);
+                        if (col < 0) continue;
+                        const size_t b = (size_t)ex * p.F + col;
+                        float v = stream_sum<CPL>(slices + (kg - half) * 16 * CB, half, m, at) + (p.up.bias ? half_at(p.up.bias + b) : 0.0f);
                         if constexpr (GATED) {
-                            const float g = gate[x] + (p.gate.bias ? half_at(p.gate.bias + b + x) : 0.0f);
-                            to[x] = to_half(stream_activate(g, p.act) * v);
+                            const float g = stream_sum<CPL>(slices, half, m, at) + (p.gate.bias ? half_at(p.gate.bias + b) : 0.0f);
+                            v *= stream_activate(g, p.act);
                         } else {
-                            to[x] = to_half(stream_activate(v, p.act));
+                            v = stream_activate(v, p.act);
                         }
+                        p.hidden[(size_t)waves[c << kl].slot[16 * t + m] * p.hidden_wide + col] = to_half(v);
                     }
                 }
             }
@@ -261,58 +246,61 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
     }
 }
 
-// out of a block of columns.  T is at most 16 NT.
-template <int FORM, int MT, int NT>
+// out of a block of columns.  T is at most 16 NT.  A tile's rows are weighed and
+// added to their tokens' sums in LDS: per token a mask of the waves that have
+// rows of it (two masks in turn, one cleared while the other is read), and its
+// first row in each; the rows of a token lie behind each other.
+template <int FORM, int MT, int NT, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
 {
-    using S = FewStream<FORM, MT>;
-    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, QUADS = CB / 4, UNITS = (16 * NT * QUADS + kStreamThreads - 1) / kStreamThreads;
+    using S = FewStream<FORM, MT, DW>;
+    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, TOKENS = 16 * NT;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
+    __shared__ float sums[TOKENS * CB];
     __shared__ FewWave waves[kStreamWaves];
     __shared__ int16_t key[kFewSlots];
-    __shared__ int8_t row_of[kStreamWaves][kFewTokens];  // a token's first row of a wave's tile, or -1
-    __shared__ int8_t token_of[kStreamWaves][kFewRows + 1];
+    __shared__ uint32_t mask[2][TOKENS];
+    __shared__ int8_t row_of[kStreamWaves][TOKENS], token_of[kStreamWaves][kFewRows + 1];
     __shared__ float weight_of[kStreamWaves][kFewRows];
-    __shared__ int bias_of[kStreamWaves];                // the expert whose bias a wave's rows get, or -1
+    __shared__ int bias_of[kStreamWaves];  // the expert whose bias a wave's rows get, or -1
     __shared__ int flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 15;
-    const int group = blockIdx.x % p.groups, nb = blockIdx.x / p.groups, n0 = nb * CB;
+    const int nb = blockIdx.x / p.groups, group = blockIdx.x - nb * p.groups, n0 = nb * CB;
     FewWave& mine = waves[wave];
     const int hits = few_keys(mine, key, p), units = (p.F + UNIT - 1) / UNIT;
     // every wave of the block has a job where that leaves each 256 rows of F
     const int parts = max(1, min(p.groups * kStreamWaves / max(hits, 1), units * UNIT / 256)), jobs = hits * parts;
-    const int j0 = (int)((int64_t)jobs * group / p.groups), j1 = (int)((int64_t)jobs * (group + 1) / p.groups);
+    const int j0 = jobs * group / p.groups, j1 = jobs * (group + 1) / p.groups;
+    for (int i = tid; i < p.T * CB; i += kStreamThreads) sums[i] = 0.0f;
+    if (tid < TOKENS) mask[0][tid] = mask[1][tid] = 0u;
 
-    f32x4 sum[UNITS];
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int turn = 0;
     for (int first = j0; first < j1; first += kStreamWaves) {
-        const int job = first + wave, part = job % parts;
+        const int job = first + wave, d = job / parts, part = job - d * parts;
         const bool have = job < j1;
-        const int e = have ? few_expert(mine, job / parts) : -1;
+        const int e = have ? few_expert(mine, d) : -1;
         const int u0 = (int)((int64_t)units * part / parts), u1 = (int)((int64_t)units * (part + 1) / parts);
         int count = 0, m0 = 0;
         do {
             if (have) count = few_rows(mine, key, p.slots, e, m0);
             typename S::Sums acc;
             if (m0 < count) {
-                StreamRows<MT> rows;
+                typename S::Rows rows(p.hidden, (uint64_t)p.slots * (uint32_t)p.hidden_wide * 2u);
 #pragma unroll
-                for (int t = 0; t < MT; ++t) rows.p[t] = p.hidden + (size_t)mine.slot[min(16 * t + l, count - 1 - m0)] * p.hidden_wide;
-                few_stream<FORM, MT>(p.down, e, p.F, p.O, n0, rows, count - m0, u0, u1, acc);
+                for (int t = 0; t < MT; ++t) rows.row(t, (uint32_t)mine.slot[min(16 * t + l, count - 1 - m0)] * (uint32_t)p.hidden_wide);
+                few_stream<FORM, MT, DW>(p.down, e, p.F, p.O, n0, rows, count - m0, u0, u1, acc);
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 __syncthreads();
                 const int here = min(16, count - m0 - 16 * t);
-                row_of[wave][lane] = -1;
-                wave_fence();
                 if (here > 0) {
                     if (lane < here) {
                         const int slot = mine.slot[16 * t + lane], token = slot / p.k;
                         token_of[wave][lane] = (int8_t)token;
                         weight_of[wave][lane] = p.weights ? p.weights[slot] : 1.0f;
                         if (lane == 0 || mine.slot[16 * t + lane - 1] / p.k != token) row_of[wave][token] = (int8_t)lane;
+                        atomicOr(&mask[turn][token], 1u << wave);
                     }
                     if (lane == 0) {
                         token_of[wave][here] = -1;
@@ -321,57 +309,46 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
                     stream_put<CPL, MT>(lds + wave * 16 * CB, acc, t);
                 }
                 __syncthreads();
-#pragma unroll
-                for (int i = 0; i < UNITS; ++i) {
-                    const int u = tid + i * kStreamThreads, token = u / QUADS, q = u % QUADS;
-                    if (token >= p.T) continue;
-                    for (int w = 0; w < kStreamWaves; ++w) {
+#pragma unroll 1
+                for (int u = tid; u < p.T * CB; u += kStreamThreads) {
+                    const int token = u / CB, at = u % CB;
+                    uint32_t from = mask[turn][token];
+                    if (from == 0u) continue;
+                    const int col = stream_position<CPL>(n0, at, p.O);
+                    float s = sums[u];
+                    do {
+                        const int w = __ffs((int)from) - 1;
+                        from &= from - 1u;
+                        const float b = bias_of[w] >= 0 && col >= 0 ? half_at(p.down.bias + (size_t)bias_of[w] * p.O + col) : 0.0f;
                         int r = row_of[w][token];
-                        if (r < 0) continue;
-                        const int col = stream_position<CPL>(n0, q, p.O);
-                        f32x4 b = {0.f, 0.f, 0.f, 0.f};
-                        if (bias_of[w] >= 0 && col >= 0)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) b[x] = col + x < p.O ? half_at(p.down.bias + (size_t)bias_of[w] * p.O + col + x) : 0.0f;
-                        do {
-                            const f32x4 y = *(const f32x4*)(lds + (w * 16 + r) * CB + 4 * q);
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) sum[i][x] = fmaf(weight_of[w][r], y[x] + b[x], sum[i][x]);
-                        } while (token_of[w][++r] == token);
-                    }
+                        do s = fmaf(weight_of[w][r], lds[(w * 16 + r) * CB + at] + b, s);
+                        while (token_of[w][++r] == token);
+                    } while (from != 0u);
+                    sums[u] = s;
                 }
+                turn ^= 1;
+                if (tid < TOKENS) mask[turn][tid] = 0u;  // read before the barriers above
             }
             m0 += 16 * MT;
         } while (__syncthreads_or(m0 < count));
     }
+    __syncthreads();
 
-    auto finish = [&](int u, int at, const f32x4& s) {
-        const int col = stream_position<CPL>(at, u % QUADS, p.O);
-        if (col < 0) return;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (col + x < p.O) p.out[(size_t)(u / QUADS) * p.O + col + x] = to_half(s[x]);
+    auto finish = [&](int u, int n_block, float s) {
+        const int col = stream_position<CPL>(n_block, u % CB, p.O);
+        if (col >= 0) p.out[(size_t)(u / CB) * p.O + col] = to_half(s);
     };
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-        const int u = tid + i * kStreamThreads;
-        if (u >= p.T * QUADS) continue;
-        if (p.groups == 1) finish(u, n0, sum[i]);
-        else meet_store(p.part + ((size_t)group * p.T + u / QUADS) * p.part_wide + n0 + 4 * (u % QUADS), sum[i]);
+    for (int u = tid; u < p.T * CB; u += kStreamThreads) {
+        if (p.groups == 1) finish(u, n0, sums[u]);
+        else meet_store(p.part + ((size_t)group * p.T + u / CB) * p.part_wide + n0 + u % CB, sums[u]);
     }
     if (p.groups == 1) return;
     const int b0 = nb / p.per * p.per, b1 = min(b0 + p.per, p.blocks);
     if (!meet_last(p.count + nb / p.per, (uint32_t)((b1 - b0) * p.groups), &flag)) return;
     for (int b = b0; b < b1; ++b)
-        for (int u = tid; u < p.T * QUADS; u += kStreamThreads) {
-            f32x4 s = {0.f, 0.f, 0.f, 0.f};
-            for (int g = 0; g < p.groups; ++g) {
-                const f32x4 v = meet_load(p.part + ((size_t)g * p.T + u / QUADS) * p.part_wide + b * CB + 4 * (u % QUADS));
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s[x] += v[x];
-            }
-            finish(u, b * CB, s);
-        }
+#pragma unroll 1
+        for (int u = tid; u < p.T * CB; u += kStreamThreads)
+            finish(u, b * CB, meet_sum(p.part + (size_t)(u / CB) * p.part_wide + b * CB + u % CB, p.groups, (size_t)p.T * p.part_wide));
 }
 
 }  // namespace gsr

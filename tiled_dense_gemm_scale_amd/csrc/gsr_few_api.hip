@@ -21,11 +21,11 @@ bool bad_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F, int64_t O)
 bool large_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F, int64_t O)
 {
     return T > gsr::kFewTokens || k > gsr::kFewSlots || T * k > gsr::kFewSlots || E > gsr::kFewExperts ||
-           H >= kStreamWidth || F >= kStreamWidth || O >= kStreamWidth;
+           H >= kStreamWidth || F >= kStreamWidth || O >= kStreamWidth || T * k * F >= ((int64_t)1 << 30);
 }
 
 struct Plan {
-    int blocks_up, grid_up, blocks, groups, per;
+    int blocks_up, grid_up, waves_log2, blocks, groups, per;
     int64_t hidden_wide, part_wide, hidden_bytes, bytes;
 };
 
@@ -34,11 +34,12 @@ constexpr int64_t kFewGrid = 256;
 
 Plan plan_of(bool w4, int64_t T, int64_t k, int64_t E, int64_t F, int64_t O)
 {
-    const int64_t CB = w4 ? gsr::W4Stream<1, 1>::CB : gsr::HalfStream<1, true>::CB;
+    const int64_t CB = w4 ? gsr::W4Stream<1, 1, true>::CB : gsr::HalfStream<1, true>::CB;
     Plan g;
     const int64_t slots = T * k, most = std::max<int64_t>(1, std::min(E, slots));
     g.blocks_up = (int)cdiv(F, CB);
-    g.grid_up = (int)std::min(kFewGrid, g.blocks_up * most);
+    // as many workgroups as items, up to a power of two of them
+    for (g.grid_up = 1, g.waves_log2 = 3; g.grid_up < kFewGrid && g.grid_up < g.blocks_up * most; g.grid_up *= 2) ++g.waves_log2;
     g.blocks = (int)cdiv(O, CB);
     // a job is an expert and 256 rows of F at least, eight to a workgroup
     g.groups = (int)std::max<int64_t>(1, std::min({(int64_t)16, kFewGrid / std::max(g.blocks, 1), cdiv(most * cdiv(F, 256), gsr::kStreamWaves)}));
@@ -84,20 +85,26 @@ struct Kernels {
 };
 // One tile of rows per expert up to 16 tokens (choices that name an expert twice
 // are further tiles), two above.
-template <int FORM>
+template <int FORM, bool DW>
 Kernels kernels_of(int64_t T)
 {
-    if (T <= 16) return Kernels{gsr::few_up_kernel<FORM, 1, false>, gsr::few_up_kernel<FORM, 1, true>, gsr::few_down_kernel<FORM, 1, 1>};
-    return Kernels{gsr::few_up_kernel<FORM, 2, false>, gsr::few_up_kernel<FORM, 2, true>, gsr::few_down_kernel<FORM, 2, 4>};
+    if (T <= 16)
+        return Kernels{gsr::few_up_kernel<FORM, 1, DW, false>, gsr::few_up_kernel<FORM, 1, DW, true>,
+                       gsr::few_down_kernel<FORM, 1, 1, DW || FORM != gsr::kFewHalf>};
+    return Kernels{gsr::few_up_kernel<FORM, 2, DW, false>, gsr::few_up_kernel<FORM, 2, DW, true>,
+                   gsr::few_down_kernel<FORM, 2, 4, DW || FORM != gsr::kFewHalf>};
 }
-// For matrices of `w` (and `w2`, or null) of N columns.
-Kernels kernels_at(int64_t T, const gsr_weights* w, const gsr_weights* w2, int64_t N)
+// For matrices of `w` (and `w2`, or null) of N columns, and rows of A of K values.
+Kernels kernels_at(int64_t T, const gsr_weights* w, const gsr_weights* w2, const void* a, int64_t K, int64_t N)
 {
-    if (w->group == 0) {
-        const bool dwords = N % 2 == 0 && !misaligned(w->data, 4) && (w2 == nullptr || !misaligned(w2->data, 4));
-        return dwords ? kernels_of<gsr::kFewHalf>(T) : kernels_of<gsr::kFewHalfAny>(T);
+    bool dwords = K % 2 == 0 && !misaligned(a, 4);
+    if (w->group == 0) dwords = dwords && N % 2 == 0 && !misaligned(w->data, 4) && (w2 == nullptr || !misaligned(w2->data, 4));
+    switch (w->group) {
+    case 0: return dwords ? kernels_of<gsr::kFewHalf, true>(T) : kernels_of<gsr::kFewHalf, false>(T);
+    case 32: return dwords ? kernels_of<gsr::kFewW4x1, true>(T) : kernels_of<gsr::kFewW4x1, false>(T);
+    case 64: return dwords ? kernels_of<gsr::kFewW4x2, true>(T) : kernels_of<gsr::kFewW4x2, false>(T);
+    default: return dwords ? kernels_of<gsr::kFewW4x4, true>(T) : kernels_of<gsr::kFewW4x4, false>(T);
     }
-    return w->group == 32 ? kernels_of<gsr::kFewW4x1>(T) : w->group == 64 ? kernels_of<gsr::kFewW4x2>(T) : kernels_of<gsr::kFewW4x4>(T);
 }
 
 }  // namespace
@@ -163,16 +170,17 @@ int gsr_expert_mlp_few(int64_t tokens, int64_t k, int64_t experts, int64_t H, in
     p.act = activation;
     p.wide_ids = id_bytes == 8;
     p.blocks_up = g.blocks_up;
+    p.waves_log2 = g.waves_log2;
     p.blocks = g.blocks;
     p.groups = g.groups;
     p.per = g.per;
     hipStream_t s = (hipStream_t)stream;
     if (F > 0 && slots > 0) {
-        const Kernels f = kernels_at(tokens, up, gate, F);
+        const Kernels f = kernels_at(tokens, up, gate, x, H, F);
         const hipError_t err = launch_kernel(gate != nullptr ? f.gated : f.up, dim3((unsigned)g.grid_up), dim3(gsr::kStreamThreads), s, p);
         if (err != hipSuccess) return status_of(err);
     }
-    return status_of(launch_kernel(kernels_at(tokens, down, nullptr, O).down, dim3((unsigned)(g.blocks * g.groups)), dim3(gsr::kStreamThreads), s, p));
+    return status_of(launch_kernel(kernels_at(tokens, down, nullptr, p.hidden, p.hidden_wide, O).down, dim3((unsigned)(g.blocks * g.groups)), dim3(gsr::kStreamThreads), s, p));
 }
 
 }  // extern "C"

@@ -65,6 +65,10 @@ __attribute__((visibility("hidden"))) int check_device();
 // (gsr_api.hip; 0 for an id that is no candidate of it).
 __attribute__((visibility("hidden"))) double tile_time(int id, int64_t K);
 
+// The selector's time of the whole dense product on the 128-bit path, in us
+// (gsr_api.hip).
+__attribute__((visibility("hidden"))) double dense_time(int64_t M, int64_t N, int64_t K);
+
 // The dense product's launch for a shape (the tuning table, else the
 // selector), and the library's K split of it on bm x bn tiles: `parts` parts
 // of kchunk values of K (parts 1: none) whose fp32 partial tiles take

@@ -55,15 +55,65 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 
 constexpr int kStep = 32;  // k per MFMA
 
-// The rows of A that a lane reads: row l of each of MT tiles of 16.  Rows past
-// the last are that one again, whose sums nobody takes: no load is masked, and
-// lanes with one address are one access.
-template <int MT>
+// Eight fp16 values at byte `off` of a buffer whose base lies on a dword: one
+// 16-byte load at the dword below, one of the dword behind, shifted together
+// (a 16-byte load at an odd element goes out at about a lane per clock, one on a
+// dword whole).
+__device__ __forceinline__ u32x4 load8_shifted(__amdgpu_buffer_rsrc_t rs, uint32_t off)
+{
+    const uint32_t o = off & ~3u, sh = (off & 2u) << 3;
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+    const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(rs, o + 16u, 0, 0);
+    return u32x4{__builtin_amdgcn_alignbit(v[1], v[0], sh), __builtin_amdgcn_alignbit(v[2], v[1], sh),
+                 __builtin_amdgcn_alignbit(v[3], v[2], sh), __builtin_amdgcn_alignbit(w, v[3], sh)};
+}
+
+// A descriptor of `bytes` bytes from `at`, from the dword that holds its first
+// to the one that holds its last; what `at` lies behind that base.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t dword_rsrc(const void* at, uint64_t bytes, uint32_t& behind)
+{
+    behind = (uint32_t)(uintptr_t)at & 2u;
+    return make_rsrc((const uint8_t*)at - behind, (uint32_t)min((bytes + behind + 3u) & ~(uint64_t)3, (uint64_t)0x7ffffffcu));
+}
+
+// The rows of A that a lane reads: row l of each of MT tiles of 16, of a table of
+// less than 2^31 bytes.  Rows past the last are that one again, whose sums nobody
+// takes, and loads behind the table are zeros: no load is masked, and lanes with
+// one address are one access.  DW: every row starts on a dword.
+template <int MT, bool DW>
 struct StreamRows {
-    const uint16_t* p[MT];
-    __device__ __forceinline__ u32x4 full(int t, int k) const { return *(const u32x4_at2*)(p[t] + k); }
-    __device__ __forceinline__ u32x4 part(int t, int k, int K) const { return load8_first(p[t] + k, K - k); }
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t off[MT];
+
+    __device__ __forceinline__ StreamRows(const uint16_t* table, uint64_t bytes)
+    {
+        uint32_t behind;
+        rs = dword_rsrc(table, bytes, behind);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) off[t] = behind;
+    }
+    template <int MORE>
+    __device__ __forceinline__ explicit StreamRows(const StreamRows<MORE, DW>& r) : rs(r.rs)  // the first of its tiles
+    {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) off[t] = r.off[t];
+    }
+    __device__ __forceinline__ void row(int t, uint32_t at) { off[t] += 2u * at; }  // `at` values into the table
+    __device__ __forceinline__ u32x4 load(int t, int k) const
+    {
+        const uint32_t o = off[t] + 2u * (uint32_t)k;
+        if constexpr (DW) return __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+        else return load8_shifted(rs, o);
+    }
 };
+
+// The first n of eight values, zeros for the others.
+__device__ __forceinline__ u32x4 first8(u32x4 v, int n)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = n >= 2 * i + 2 ? v[i] : n == 2 * i + 1 ? v[i] & 0xffffu : 0u;
+    return v;
+}
 
 // A descriptor of the rows k0 and on of a matrix of `rows` rows of `pitch` bytes
 // (whole dwords): loads behind the last row are zeros.
@@ -94,20 +144,19 @@ struct StreamSums {
     }
 };
 
-// multiply(b[i]) for n > 0 units in turn, DEPTH - 1 units' loads in flight: load(b,
-// i) is called for units past the last too, and has to be one that reads nothing
-// new there, so that no wait depends on which way a branch went.
-template <int DEPTH, class Batch, class Load, class Multiply>
+// multiply(b, i) for n > 0 units in turn, the next one's loads in flight: load(b,
+// i) is called for the unit past the last too, and has to be one that reads
+// nothing new there, so that no wait depends on which way a branch went.
+template <class Batch, class Load, class Multiply>
 __device__ __forceinline__ void stream_ring(int n, Load&& load, Multiply&& multiply)
 {
-    Batch b[DEPTH];
+    Batch b[2];
+    load(b[0], 0);
+    for (int i = 0;; i += 2) {
 #pragma unroll
-    for (int i = 0; i < DEPTH - 1; ++i) load(b[i], i);
-    for (int i = 0;; i += DEPTH) {
-#pragma unroll
-        for (int j = 0; j < DEPTH; ++j) {
-            load(b[(j + DEPTH - 1) % DEPTH], i + j + DEPTH - 1);
-            multiply(b[j]);
+        for (int j = 0; j < 2; ++j) {
+            load(b[j ^ 1], i + j + 1);
+            multiply(b[j], i + j);
             if (i + j + 1 >= n) return;
         }
     }
@@ -118,11 +167,12 @@ struct HalfMatrix {
     const uint16_t* b;  // K x N
 };
 
-// DW: every row starts on a dword (N even, b on one).
+// DW: every row starts on a dword (N even, b on one), and every row of A.
 template <int MT, bool DW>
 struct HalfStream {
-    static constexpr int CPL = 8, CB = 16 * CPL, UNIT = kStep, DEPTH = 2;  // UNIT: k of the smallest run
+    static constexpr int CPL = 8, CB = 16 * CPL, UNIT = kStep;  // UNIT: k of the smallest run
     typedef StreamSums<CPL, MT> Sums;
+    typedef StreamRows<MT, DW> Rows;
 
     struct Step {
         u32x4 b[8];
@@ -131,41 +181,44 @@ struct HalfStream {
     struct Place {
         const uint16_t* b;
         int K, N, c, g;
-        uint32_t off[DW ? 8 : 1];  // bytes from a step's first row
+        uint32_t off[8];  // bytes from a step's first row
     };
 
     // Unit u of a run of units before `end` (from there on nothing is read anew).
-    template <bool TAIL>
-    __device__ static __forceinline__ void load(Step& s, const Place& p, const StreamRows<MT>& rows, int u, int end)
+    __device__ static __forceinline__ void load(Step& s, const Place& p, const Rows& rows, int u, int end)
     {
         const int k0 = min(u, end - 1) * kStep;
-        if (TAIL && p.N < CPL) {
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {  // one row in flight, for the registers' sake
-                const int k = k0 + 8 * p.g + i;
-                const u32x4 v = load8_first(p.b + (size_t)min(k, p.K - 1) * p.N + p.c, k < p.K ? p.N - p.c : 0);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) s.b[x] = x == i ? v : s.b[x];
-            }
-        } else if constexpr (DW) {
+        if constexpr (DW) {
             const __amdgpu_buffer_rsrc_t rs = rows_rsrc(p.b, u < end ? p.K : 0, k0, 2u * (uint32_t)p.N);
 #pragma unroll
             for (int i = 0; i < 8; ++i) s.b[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, p.off[i], 0, 0);
         } else {
+            uint32_t behind;
+            const __amdgpu_buffer_rsrc_t rs =
+                dword_rsrc(p.b + (size_t)k0 * p.N, u < end ? (uint64_t)(p.K - k0) * (uint32_t)p.N * 2u : 0u, behind);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int k = k0 + 8 * p.g + i;
-                s.b[i] = *(const u32x4_at2*)(p.b + (size_t)(TAIL ? min(k, p.K - 1) : k) * p.N + p.c);
-                if (TAIL && k >= p.K) s.b[i] = u32x4{0u, 0u, 0u, 0u};
-            }
+            for (int i = 0; i < 8; ++i) s.b[i] = load8_shifted(rs, p.off[i] + behind);
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t) s.a[t] = TAIL ? rows.part(t, k0 + 8 * p.g, p.K) : rows.full(t, k0 + 8 * p.g);
+        for (int t = 0; t < MT; ++t) s.a[t] = rows.load(t, k0 + 8 * p.g);
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    __device__ static __forceinline__ void multiply(const Step& s, Sums& acc)
+    // Zeros for what lies past K on both sides (behind a row of A lies the next
+    // one, and the last row of B may share its last dword with other values).
+    __device__ static __forceinline__ void cut(Step& s, const Place& p, int k0)
     {
+        const int n = p.K - k0 - 8 * p.g;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) s.a[t] = first8(s.a[t], n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= n) s.b[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+
+    __device__ static __forceinline__ void multiply(Step& s, const Place& p, int u, Sums& acc)
+    {
+        if ((u + 1) * kStep > p.K) cut(s, p, u * kStep);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {  // columns 2d and 2d + 1
             u32x4 even, odd;
@@ -184,8 +237,8 @@ struct HalfStream {
     }
 
     // acc += A[:, k] B[k, :] over the units u0 <= u < u1 of 32 k
-    __device__ static __forceinline__ void run(const HalfMatrix& m, int K, int N, int n0, const StreamRows<MT>& rows,
-                                               int u0, int u1, Sums& acc)
+    __device__ static __forceinline__ void run(const HalfMatrix& m, int K, int N, int n0, const Rows& rows, int u0, int u1,
+                                               Sums& acc)
     {
         const int lane = threadIdx.x & 63;
         Place p;
@@ -194,17 +247,28 @@ struct HalfStream {
         p.N = N;
         p.g = lane >> 4;
         p.c = stream_column<CPL>(n0, lane & 15, N);
-        if constexpr (DW)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p.off[i] = 2u * ((uint32_t)(8 * p.g + i) * (uint32_t)N + (uint32_t)p.c);
-        const int full = N >= CPL ? max(u0, min(u1, K / kStep)) : u0;
-        if (u0 < full)
-            stream_ring<DEPTH, Step>(
-                full - u0, [&](Step& s, int i) { load<false>(s, p, rows, u0 + i, full); }, [&](const Step& s) { multiply(s, acc); });
-        for (int u = full; u < u1; ++u) {
+        for (int i = 0; i < 8; ++i) p.off[i] = 2u * ((uint32_t)(8 * p.g + i) * (uint32_t)N + (uint32_t)p.c);
+        if (u0 >= u1) return;
+        if (N >= CPL) {
+            stream_ring<Step>(
+                u1 - u0, [&](Step& s, int i) { load(s, p, rows, u0 + i, u1); },
+                [&](Step& s, int i) { multiply(s, p, u0 + i, acc); });
+            return;
+        }
+#pragma unroll 1
+        for (int u = u0; u < u1; ++u) {  // fewer columns than a lane's: value by value
             Step s{};
-            load<true>(s, p, rows, u, u1);
-            multiply(s, acc);
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int k = u * kStep + 8 * p.g + i;
+                const u32x4 v = load8_first(p.b + (size_t)min(k, K - 1) * N + p.c, k < K ? N - p.c : 0);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) s.b[x] = x == i ? v : s.b[x];
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) s.a[t] = rows.load(t, u * kStep + 8 * p.g);
+            multiply(s, p, u, acc);
         }
     }
 };
@@ -227,26 +291,23 @@ __device__ __forceinline__ void stream_put(float* slice, const StreamSums<CPL, M
     }
 }
 
-// Positions 4q .. 4q + 3 of row m, summed over `waves` slices in order from +0.
+// Position `at` of row m, summed over `waves` slices in order from +0.
 template <int CPL>
-__device__ __forceinline__ f32x4 stream_sum(const float* slices, int waves, int m, int q)
+__device__ __forceinline__ float stream_sum(const float* slices, int waves, int m, int at)
 {
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    for (int w = 0; w < waves; ++w) {
-        const f32x4 v = *(const f32x4*)(slices + (size_t)(w * 16 + m) * 16 * CPL + 4 * q);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += v[i];
-    }
+    float s = 0.0f;
+#pragma unroll 4
+    for (int w = 0; w < waves; ++w) s += slices[(w * 16 + m) * 16 * CPL + at];
     return s;
 }
 
-// The column of position 4q of the block from n0 (the first of four), or -1
-// where the position's lane lies past N.
+// The column of a position of the block from n0, or -1 where the position's lane
+// lies past N.
 template <int CPL>
-__device__ __forceinline__ int stream_position(int n0, int q, int N)
+__device__ __forceinline__ int stream_position(int n0, int at, int N)
 {
-    const int l = 4 * q / CPL;
-    return n0 + CPL * l < N ? stream_column<CPL>(n0, l, N) + 4 * q % CPL : -1;
+    const int l = at / CPL, col = stream_column<CPL>(n0, l, N) + at % CPL;
+    return n0 + CPL * l < N && col < N ? col : -1;
 }
 
 // ---- sums that meet in a workspace ---------------------------------------------------
@@ -255,20 +316,24 @@ __device__ __forceinline__ int stream_position(int n0, int q, int N)
 // stale line.  Whoever counts last has every other's sums: each wave waits for
 // its stores before the barrier in front of the count, and reads only after the
 // count has returned.
-__device__ __forceinline__ void meet_store(float* to, f32x4 v)
+__device__ __forceinline__ void meet_store(float* to, float v)
 {
-    const u32x4 w = __builtin_bit_cast(u32x4, v);
-    uint64_t* d = (uint64_t*)to;
-    __hip_atomic_store(d, w[0] | (uint64_t)w[1] << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(d + 1, w[2] | (uint64_t)w[3] << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__device__ __forceinline__ f32x4 meet_load(const float* from)
+// The sum of `n` values `stride` apart, in order from +0, eight in flight.
+__device__ __forceinline__ float meet_sum(const float* from, int n, size_t stride)
 {
-    const uint64_t* s = (const uint64_t*)from;
-    const uint64_t a = __hip_atomic_load(s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const uint64_t b = __hip_atomic_load(s + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return __builtin_bit_cast(f32x4, u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)});
+    float s = 0.0f;
+    for (int g = 0; g < n; g += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = __hip_atomic_load(from + (size_t)min(g + i, n - 1) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += g + i < n ? v[i] : 0.0f;
+    }
+    return s;
 }
 
 // Counts this workgroup in; true in the one that completes `all`, whose counter

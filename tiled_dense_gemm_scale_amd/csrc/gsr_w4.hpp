@@ -55,11 +55,13 @@ __device__ __forceinline__ u32x4 w4_order(u32x4 a)
 // A wave's share: 64 columns, four per lane, one word of each per step.  Runs
 // are cut at multiples of 128 rows; a group's sum of products is kept apart and
 // scaled in fp32 when the group (or, of larger ones, 128 rows of it) ends, so
-// the weights are never rounded.  FL: steps between such ends (1, 2 or 4).
-template <int MT, int FL>
+// the weights are never rounded.  FL: steps between such ends (1, 2 or 4).  DW: every row of A starts on a
+// dword.
+template <int MT, int FL, bool DW>
 struct W4Stream {
     static constexpr int CPL = 4, CB = 16 * CPL, STEPS = 4, UNIT = STEPS * kStep, ENDS = STEPS / FL, DEPTH = 2;
     typedef StreamSums<CPL, MT> Sums;
+    typedef StreamRows<MT, DW> Rows;
 
     struct Batch {
         u32x4 w[STEPS];
@@ -75,7 +77,7 @@ struct W4Stream {
     };
 
     // Unit u of a run of units before `end` (from there on nothing is read anew).
-    __device__ static __forceinline__ void load(Batch& t, const Place& p, const StreamRows<MT>& rows, int u, int end)
+    __device__ static __forceinline__ void load(Batch& t, const Place& p, const Rows& rows, int u, int end)
     {
         const int k0 = min(u, end - 1) * UNIT;
         const __amdgpu_buffer_rsrc_t rs = rows_rsrc(p.m.codes, u < end ? (p.K + 7) / 8 : 0, k0 / 8, 4u * (uint32_t)p.N);
@@ -83,14 +85,14 @@ struct W4Stream {
         for (int i = 0; i < STEPS; ++i) t.w[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, p.off[i], 0, 0);
 #pragma unroll
         for (int e = 0; e < ENDS; ++e) {
-            const size_t row = (size_t)((k0 + e * FL * kStep) >> p.m.glog2) * p.N;
+            const size_t row = (size_t)(min(k0 + e * FL * kStep, p.K - 1) >> p.m.glog2) * p.N;
             t.s[e] = *(const u32x2_at2*)(p.m.scales + row + p.c);
             t.z[e] = *(const u32_at1*)(p.zeros + row + p.c);
         }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-            for (int x = 0; x < MT; ++x) t.a[i][x] = rows.full(x, k0 + i * kStep + 8 * p.g);
+            for (int x = 0; x < MT; ++x) t.a[i][x] = rows.load(x, k0 + i * kStep + 8 * p.g);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -113,24 +115,32 @@ struct W4Stream {
         }
     }
 
-    __device__ static __forceinline__ void multiply(const Batch& t, const Place& p, Sums& acc)
+    __device__ static __forceinline__ void multiply(Batch& t, const Place& p, int u, Sums& acc)
     {
+        const int left = p.K - u * UNIT;
+        if (left < UNIT) {  // behind a row of A lies the next one
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                for (int x = 0; x < MT; ++x) t.a[i][x] = first8(t.a[i][x], left - i * kStep - 8 * p.g);
+        }
 #pragma unroll
         for (int e = 0; e < ENDS; ++e) {
+            if (e * FL * kStep >= left) break;  // no such group
             Scale v;
             scale_of(v, t.s[e], t.z[e], p.m.zeros != nullptr);
             f32x4 sum[CPL][MT];
 #pragma unroll
             for (int i = 0; i < FL; ++i) {
-                u32x4 a[MT];
+                u32x4 b[CPL];
 #pragma unroll
-                for (int x = 0; x < MT; ++x) a[x] = w4_order(t.a[e * FL + i][x]);
+                for (int j = 0; j < CPL; ++j) b[j] = w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]);
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    const u32x4 b = w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]);
+                for (int x = 0; x < MT; ++x) {
+                    const u32x4 a = w4_order(t.a[e * FL + i][x]);
 #pragma unroll
-                    for (int x = 0; x < MT; ++x)
-                        sum[j][x] = mfma16(a[x], b, i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j][x]);
+                    for (int j = 0; j < CPL; ++j)
+                        sum[j][x] = mfma16(a, b[j], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j][x]);
                 }
                 __builtin_amdgcn_sched_barrier(0);  // a step's values live no longer than it
             }
@@ -143,9 +153,9 @@ struct W4Stream {
         }
     }
 
-    // One step of 32 rows, any of which may lie past K, of a matrix of any
-    // width: value by value and scaled by itself.
-    __device__ static __forceinline__ void step(const Place& p, const StreamRows<MT>& rows, int k0, Sums& acc)
+    // One step of 32 rows of a matrix of any width: value by value and scaled by
+    // itself.
+    __device__ static __forceinline__ void step(const Place& p, const Rows& rows, int k0, Sums& acc)
     {
         const int r = k0 / 8 + p.g, words = (p.K + 7) / 8;
         const size_t row = (size_t)(k0 >> p.m.glog2) * p.N;
@@ -163,7 +173,7 @@ struct W4Stream {
         scale_of(v, u32x2{join16(s[0], s[1]), join16(s[2], s[3])}, zeros, p.m.zeros != nullptr);
 #pragma unroll
         for (int x = 0; x < MT; ++x) {
-            const u32x4 a = w4_order(rows.part(x, k0 + 8 * p.g, p.K));
+            const u32x4 a = w4_order(first8(rows.load(x, k0 + 8 * p.g), p.K - k0 - 8 * p.g));
 #pragma unroll
             for (int j = 0; j < CPL; ++j) {
                 const f32x4 sum = mfma16(a, w4_values(w[j], v.lo[j], v.hi[j]), f32x4{0.f, 0.f, 0.f, 0.f});
@@ -189,16 +199,19 @@ struct W4Stream {
     }
 
     // acc += A[:, k] w[k, :] over the units u0 <= u < u1 of 128 k
-    __device__ static __forceinline__ void run(const W4Matrix& m, int K, int N, int n0, const StreamRows<MT>& rows,
+    __device__ static __forceinline__ void run(const W4Matrix& m, int K, int N, int n0, const Rows& rows,
                                                int u0, int u1, Sums& acc)
     {
         const Place p = place(m, K, N, n0);
-        const int full = N >= CPL ? max(u0, min(u1, K / UNIT)) : u0;
-        if (u0 < full)
-            stream_ring<DEPTH, Batch>(
-                full - u0, [&](Batch& t, int i) { load(t, p, rows, u0 + i, full); }, [&](const Batch& t) { multiply(t, p, acc); });
+        if (u0 >= u1) return;
+        if (N >= CPL) {
+            stream_ring<Batch>(
+                u1 - u0, [&](Batch& t, int i) { load(t, p, rows, u0 + i, u1); },
+                [&](Batch& t, int i) { multiply(t, p, u0 + i, acc); });
+            return;
+        }
 #pragma unroll 1
-        for (int k0 = full * UNIT; k0 < min(K, u1 * UNIT); k0 += kStep) step(p, rows, k0, acc);
+        for (int k0 = u0 * UNIT; k0 < min(K, u1 * UNIT); k0 += kStep) step(p, rows, k0, acc);
     }
 };
 

@@ -37,33 +37,52 @@ gsr::W4Convert convert_args(int64_t matrices, int64_t K, int64_t N, int64_t grou
 constexpr int64_t kGridY = 32768;
 
 struct GemmPlan {
-    int mt, parts, chunk, blocks_n, per;
-    int64_t row_blocks, bytes;
+    bool dense;  // the weights' values in the workspace, then the dense product
+    int parts, chunk, per;
+    int64_t blocks_m, blocks_n, bytes;
 };
 
-GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int64_t bytes)
+// Many rows are bound by the matrix cores, whose tiles of 256 rows the stream does
+// not have: there the values are written out once, 2.5 bytes to and from memory
+// per weight, and the dense kernels multiply them.  In us, the stream, and both
+// steps: 11008 x 4096 with 64 rows 25 and 44, 128 rows 47 and 53, 256 rows 84 and
+// 54, 1025 rows 334 and 113.  The stream's rounds of 256 workgroups take 2.5 and
+// 0.165 per unit of K; the values 4.6 TB/s; the dense products their selector's
+// time, off the 128-bit path 17 ns per K or 340 TFLOP/s.
+bool dense_pays(int64_t M, int64_t N, int64_t K, bool vec)
 {
-    constexpr int CB = gsr::W4Stream<1, 1>::CB, UNIT = gsr::W4Stream<1, 1>::UNIT;
+    const double mnk = 2.0 * (double)M * (double)N * (double)K;
+    const double stream = std::max(1.0, (double)cdiv(M, 16) * (double)cdiv(N, 64) / 256.0) * (2.5 + 0.165 * (double)cdiv(K, 128));
+    const double dense = vec ? dense_time(M, N, K) : std::max(0.017 * (double)K, mnk * 1e-6 / 340.0);
+    return 4.0 + 2.5 * (double)K * (double)N * 1e-6 / 4.6 + dense < stream;
+}
+
+// aligned: A and C let the dense product take its 128-bit path.
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int64_t bytes, bool aligned)
+{
+    constexpr int CB = gsr::W4Stream<1, 1, true>::CB, UNIT = gsr::W4Stream<1, 1, true>::UNIT;
     GemmPlan g;
-    g.mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    g.blocks_n = (int)cdiv(N, CB);
-    g.row_blocks = cdiv(M, 16 * g.mt);
-    const int64_t units = cdiv(K, UNIT);
-    Parts p = g.row_blocks == 1 ? stream_parts(g.blocks_n, units, 1) : Parts{1, (int)std::max<int64_t>(units, 1)};
+    const int64_t units = cdiv(K, UNIT), values = gsr::kMeetBytes + 2 * K * N;
+    g.blocks_m = cdiv(M, 16);
+    g.blocks_n = cdiv(N, CB);
+    const int64_t tiles = g.blocks_m * g.blocks_n;
+    g.dense = M > 16 && K > 0 && values < kLimit && (bytes < 0 || values <= bytes) &&
+              dense_pays(M, N, K, aligned && K % 8 == 0 && N % 8 == 0);
+    Parts p = stream_parts(tiles, units, gsr::kStreamWaves, 256);
     auto need = [&](int parts) { return parts > 1 ? gsr::kMeetBytes + (int64_t)parts * M * g.blocks_n * CB * 4 : 0; };
     if (bytes >= 0 && need(p.parts) > bytes) p = Parts{1, (int)std::max<int64_t>(units, 1)};
     g.parts = p.parts;
     g.chunk = p.chunk;
-    g.per = (int)cdiv(g.blocks_n, gsr::kMeetCounters);
-    g.bytes = need(p.parts);
+    g.per = (int)cdiv(tiles, gsr::kMeetCounters);
+    g.bytes = g.dense ? values : need(p.parts);
     return g;
 }
 
 typedef void (*gemm_kernel)(gsr::W4Gemm);
-template <int MT>
-gemm_kernel gemm_form(int glog2)
+template <bool DW>
+gemm_kernel gemm_form(int64_t group)
 {
-    return glog2 == 5 ? gsr::w4_gemm_kernel<MT, 1> : glog2 == 6 ? gsr::w4_gemm_kernel<MT, 2> : gsr::w4_gemm_kernel<MT, 4>;
+    return group == 32 ? gsr::w4_rows_kernel<1, DW> : group == 64 ? gsr::w4_rows_kernel<2, DW> : gsr::w4_rows_kernel<4, DW>;
 }
 
 }  // namespace
@@ -87,8 +106,13 @@ int gsr_quantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group, const
     p.codes = codes;
     p.scales = (uint16_t*)scales;
     p.zeros = zeros;
-    const dim3 grid((unsigned)cdiv(N, 256), (unsigned)std::min(matrices * p.groups, kGridY));
-    return status_of(launch_kernel(gsr::w4_quantize_kernel, grid, dim3(256), (hipStream_t)stream, p));
+    if (N < 4)
+        return status_of(launch_kernel(gsr::w4_quantize_narrow_kernel, dim3((unsigned)std::min(cdiv(matrices * p.groups * N, 256), kGridY)),
+                                       dim3(256), (hipStream_t)stream, p));
+    const bool longer = group > 128;
+    const dim3 grid((unsigned)cdiv(N, 256), (unsigned)std::min(matrices * (longer ? p.groups : cdiv(K, 128)), kGridY));
+    return status_of(launch_kernel(longer ? gsr::w4_quantize_kernel<true> : gsr::w4_quantize_kernel<false>, grid, dim3(256),
+                                   (hipStream_t)stream, p));
 }
 
 int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group, const uint32_t* codes, const void* scales,
@@ -108,14 +132,17 @@ int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group, con
     p.codes = const_cast<uint32_t*>(codes);
     p.scales = (uint16_t*)const_cast<void*>(scales);
     p.zeros = const_cast<uint8_t*>(zeros);
-    const dim3 grid((unsigned)cdiv(N, 256), (unsigned)std::min(matrices * cdiv(K, 8), kGridY));
+    if (N < 4)
+        return status_of(launch_kernel(gsr::w4_dequantize_narrow_kernel, dim3((unsigned)std::min(cdiv(matrices * cdiv(K, 8) * N, 256), kGridY)),
+                                       dim3(256), (hipStream_t)stream, p));
+    const dim3 grid((unsigned)cdiv(N, 256), (unsigned)std::min(cdiv(matrices * cdiv(K, 32), 4), kGridY));
     return status_of(launch_kernel(gsr::w4_dequantize_kernel, grid, dim3(256), (hipStream_t)stream, p));
 }
 
 int64_t gsr_w4_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (M < 0 || N < 0 || K < 0 || M >= kLimit || N >= gsr::host::kStreamWidth || K >= gsr::host::kStreamWidth) return -1;
-    return M == 0 || N == 0 ? 0 : gemm_plan(M, N, K, -1).bytes;
+    return M == 0 || N == 0 ? 0 : std::max(gemm_plan(M, N, K, -1, true).bytes, gemm_plan(M, N, K, -1, false).bytes);
 }
 
 int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, int64_t group, const uint32_t* codes,
@@ -136,7 +163,17 @@ int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, int64
         return GSR_ERROR_INVALID_VALUE;
     st = check_device();
     if (st != GSR_SUCCESS) return st;
-    const GemmPlan g = gemm_plan(M, N, K, (int64_t)w.bytes);
+    const GemmPlan g = gemm_plan(M, N, K, (int64_t)w.bytes, !misaligned(A, 16) && !misaligned(bias, 8));
+    if (g.dense) {
+        void* values = (uint8_t*)workspace + gsr::kMeetBytes;
+        st = gsr_dequantize_w4(1, K, N, group, codes, scales, zeros, values, stream);
+        // the dense product's matrices are below 2^31 bytes
+        const int64_t rows = (kLimit - 1) / (2 * std::max(K, N)) / 256 * 256;
+        for (int64_t m = 0; m < M && st == GSR_SUCCESS; m += rows)
+            st = gemm_scale_bias_act(std::min(rows, M - m), N, K, (const uint8_t*)A + 2 * m * K, values, bias, (uint8_t*)C + 2 * m * N,
+                                     alpha, activation, stream);
+        return st;
+    }
     gsr::W4Gemm p{};
     p.a = (const uint16_t*)A;
     p.w = gsr::W4Matrix{codes, (const uint16_t*)scales, zeros, group_log2(group)};
@@ -147,15 +184,16 @@ int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, int64
     p.K = (int)K;
     p.act = activation;
     p.alpha = alpha;
-    p.blocks_n = g.blocks_n;
+    p.blocks_m = (int)g.blocks_m;
+    p.blocks_n = (int)g.blocks_n;
     p.parts = g.parts;
     p.chunk = g.chunk;
     p.per = g.per;
     p.count = (uint32_t*)workspace;
     p.part = (float*)((uint8_t*)workspace + gsr::kMeetBytes);
-    const int64_t grid = g.row_blocks * g.blocks_n * g.parts;
+    const int64_t grid = cdiv(g.blocks_m * g.blocks_n * g.parts, 8) * 8;
     if (!grid_fits(grid, gsr::kStreamThreads)) return GSR_ERROR_TOO_LARGE;
-    const gemm_kernel f = g.mt == 1 ? gemm_form<1>(p.w.glog2) : g.mt == 2 ? gemm_form<2>(p.w.glog2) : gemm_form<4>(p.w.glog2);
+    const gemm_kernel f = K % 2 == 0 && !misaligned(A, 4) ? gemm_form<true>(group) : gemm_form<false>(group);
     return status_of(launch_kernel(f, dim3((unsigned)grid), dim3(gsr::kStreamThreads), (hipStream_t)stream, p));
 }
 

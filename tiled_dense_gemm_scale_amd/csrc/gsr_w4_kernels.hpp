@@ -1,5 +1,5 @@
 // gsr_w4_kernels.hpp -- kernels on weights held in 4 bits (gsr_w4.hpp): the
-// product of a few rows, quantizing, and the values back.
+// product, quantizing, and the values back.
 #pragma once
 
 #include "gsr_w4.hpp"
@@ -14,29 +14,35 @@ struct W4Gemm {
     uint16_t* c;        // M x N
     int M, N, K, act;
     float alpha;
-    int blocks_n, parts, chunk;  // column blocks; parts of K, of `chunk` units each
-    int per;                     // column blocks per counter
-    float* part;                 // parts x M x (blocks_n CB)
+    int blocks_m, blocks_n;  // tiles of the launch
+    int parts, chunk;        // parts of K, of `chunk` units each
+    int per;                 // tiles per counter
+    float* part;             // parts x M x (blocks_n CB)
     uint32_t* count;
 };
 
-// Workgroup (block of 16 MT rows, column block, part of K), parts fastest.
-// With more than one part the sums meet in the workspace and the last workgroup
-// of a counter's blocks adds them in part order.
-template <int MT, int FL>
-__global__ void __launch_bounds__(kStreamThreads, 2) w4_gemm_kernel(W4Gemm p)
+// A tile of 16 rows and 64 columns, whose workgroup's waves split its K, or a
+// part of it: then the tile's sums meet in the workspace and the workgroup that
+// comes last of a counter's tiles adds them.  One block of rows is bound by the
+// codes' bytes and the chain of launch, loads and sums; more of them run beside
+// each other and read the codes again, from the caches.
+template <int FL, bool DW>
+__global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 {
-    using S = W4Stream<MT, FL>;
-    constexpr int CPL = S::CPL, CB = S::CB, QUADS = CB / 4;
+    using S = W4Stream<1, FL, DW>;
+    constexpr int CPL = S::CPL, CB = S::CB;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ int flag;
+    // neighbouring tiles on one XCD: they share a block of columns
+    const int all = p.blocks_m * p.blocks_n * p.parts, per_xcd = (all + 7) / 8;
+    const int id = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
+    if (id >= all) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 15;
-    const int part = blockIdx.x % p.parts, tile = blockIdx.x / p.parts, nb = tile % p.blocks_n;
-    const int m0 = tile / p.blocks_n * 16 * MT, n0 = nb * CB, rows_here = min(16 * MT, p.M - m0);
+    const int part = id % p.parts, tile = id / p.parts;
+    const int m0 = tile % p.blocks_m * 16, n0 = tile / p.blocks_m * CB, rows_here = min(16, p.M - m0);
 
-    StreamRows<MT> rows;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) rows.p[t] = p.a + (size_t)(m0 + min(16 * t + l, rows_here - 1)) * p.K;
+    typename S::Rows rows(p.a + (size_t)m0 * p.K, (uint64_t)rows_here * (uint32_t)p.K * 2u);
+    rows.row(0, (uint32_t)min(l, rows_here - 1) * (uint32_t)p.K);
     const int units = (p.K + S::UNIT - 1) / S::UNIT;
     const int first = part * p.chunk, here = max(0, min(p.chunk, units - first));
     const int u0 = first + here * wave / kStreamWaves, u1 = first + here * (wave + 1) / kStreamWaves;
@@ -44,45 +50,36 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_gemm_kernel(W4Gemm p)
     acc.clear();
     S::run(p.w, p.K, p.N, n0, rows, u0, u1, acc);
 
-    auto finish = [&](int m, int q, int at, f32x4 s) {
-        const int col = stream_position<CPL>(at, q, p.N);
-        if (col < 0 || m >= p.M) return;
-        uint16_t* to = p.c + (size_t)m * p.N + col;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (col + i < p.N) to[i] = to_half(activate(s[i] * p.alpha + (p.bias ? half_at(p.bias + col + i) : 0.0f), p.act));
+    auto finish = [&](int m, int n_block, int at, float s) {
+        const int col = stream_position<CPL>(n_block, at, p.N);
+        if (col < 0) return;
+        const float b = p.bias ? half_at(p.bias + col) : 0.0f;
+        p.c[(size_t)m * p.N + col] = to_half(activate(s * p.alpha + b, p.act));
     };
+    stream_put<CPL, 1>(lds + wave * 16 * CB, acc, 0);
+    __syncthreads();
     const size_t wide = (size_t)p.blocks_n * CB;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        __syncthreads();
-        stream_put<CPL, MT>(lds + wave * 16 * CB, acc, t);
-        __syncthreads();
-        const int m = 16 * t + threadIdx.x / QUADS, q = threadIdx.x % QUADS;
-        if (threadIdx.x >= 16 * QUADS || m >= rows_here) continue;
-        const f32x4 s = stream_sum<CPL>(lds, kStreamWaves, m - 16 * t, q);
-        if (p.parts == 1) finish(m0 + m, q, n0, s);
-        else meet_store(p.part + ((size_t)part * p.M + m0 + m) * wide + n0 + 4 * q, s);
+#pragma unroll 1
+    for (int u = threadIdx.x; u < rows_here * CB; u += kStreamThreads) {
+        const int m = u / CB, at = u % CB;
+        const float s = stream_sum<CPL>(lds, kStreamWaves, m, at);
+        if (p.parts > 1) meet_store(p.part + ((size_t)part * p.M + m0 + m) * wide + n0 + at, s);
+        else finish(m0 + m, n0, at, s);
     }
     if (p.parts == 1) return;
-    const int b0 = nb / p.per * p.per, b1 = min(b0 + p.per, p.blocks_n);
-    if (!meet_last(p.count + nb / p.per, (uint32_t)((b1 - b0) * p.parts), &flag)) return;
-    for (int b = b0; b < b1; ++b)
-        for (int u = threadIdx.x; u < rows_here * QUADS; u += kStreamThreads) {
-            const int m = u / QUADS, q = u % QUADS;
-            f32x4 s = {0.f, 0.f, 0.f, 0.f};
-            for (int g = 0; g < p.parts; ++g) {
-                const f32x4 v = meet_load(p.part + ((size_t)g * p.M + m0 + m) * wide + b * CB + 4 * q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] += v[i];
-            }
-            finish(m0 + m, q, b * CB, s);
+    const int t0 = tile / p.per * p.per, t1 = min(t0 + p.per, p.blocks_m * p.blocks_n);
+    if (!meet_last(p.count + tile / p.per, (uint32_t)((t1 - t0) * p.parts), &flag)) return;
+    for (int t = t0; t < t1; ++t) {
+        const int tm0 = t % p.blocks_m * 16, tn0 = t / p.blocks_m * CB;
+#pragma unroll 1
+        for (int u = threadIdx.x; u < min(16, p.M - tm0) * CB; u += kStreamThreads) {
+            const int m = tm0 + u / CB, at = u % CB;
+            finish(m, tn0, at, meet_sum(p.part + (size_t)m * wide + tn0 + at, p.parts, (size_t)p.M * wide));
         }
+    }
 }
 
 // ---- quantizing --------------------------------------------------------------------
-// One thread per column and group; the group is read twice, the second time
-// from the caches.
 struct W4Convert {
     const uint16_t* b;    // matrices x K x N
     uint16_t* values;     // the same, written by dequantize
@@ -93,60 +90,209 @@ struct W4Convert {
     int64_t matrices;
 };
 
+// What a group's values make of its scale and zero point, and a code of them.
+struct W4Step {
+    float s, r;
+    int z;
+    uint16_t bits;
+    bool live;
+    __device__ __forceinline__ W4Step(float lo, float hi, bool odd, bool zeros)
+    {
+        const float step = zeros ? (hi - lo) / 15.0f : fmaxf(-lo, hi) / 7.0f;
+        bits = odd ? (uint16_t)0x7e00 : to_half(step);
+        s = (float)__builtin_bit_cast(_Float16, bits);
+        live = s > 0.0f;
+        r = live ? 1.0f / s : 0.0f;
+        z = zeros && live ? (int)fminf(fmaxf(rintf(quotient(-lo)), 0.0f), 15.0f) : 8;
+    }
+    // v / s rounded as a division would be wherever that decides a code: from a
+    // quotient off by an ulp or two one correction, exact where v / s is half a
+    // whole number (then v - t s is the error itself); any other quotient of two
+    // fp16 values lies 2^-16 of itself away from those.
+    __device__ __forceinline__ float quotient(float v) const
+    {
+        const float t = v * r;
+        return fmaf(fmaf(-t, s, v), r, t);
+    }
+    __device__ __forceinline__ uint32_t code(float v) const
+    {
+        const int q = (int)rintf(quotient(v)) + z;
+        return live ? (uint32_t)min(max(q, 0), 15) : (uint32_t)z;
+    }
+};
+
+// A wave has 256 columns, four per lane, and 32 rows of a group, in registers;
+// the four waves of a workgroup have 128 rows, one to four groups, and tell each
+// other their largest values through LDS.  Larger groups are walked 128 rows at
+// a time, twice (LONG).
+template <bool LONG>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
 {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= p.N) return;
+    __shared__ u32x4 least[4][64], most[4][64];  // four columns: lo, hi as floats
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int words = (p.K + 7) / 8;
-    const int64_t all = p.matrices * p.groups;
-    for (int64_t eg = blockIdx.y; eg < all; eg += gridDim.y) {
-        const int64_t e = eg / p.groups;
-        const int64_t begin = (eg % p.groups) << p.glog2;
-        const int k0 = (int)begin, k1 = (int)min((int64_t)p.K, begin + ((int64_t)1 << p.glog2));
+    const bool live = ((int)blockIdx.x * 64 + lane) * 4 < p.N;
+    const int c = min(((int)blockIdx.x * 64 + lane) * 4, p.N - 4);
+    const int spans = LONG ? p.groups : (p.K + 127) / 128;  // of 128 rows or a longer group
+    const int64_t all = p.matrices * spans;
+    for (int64_t es = blockIdx.y; es < all; es += gridDim.y) {
+        const int64_t e = es / spans, span = es % spans;
+        const uint16_t* b = p.b + (size_t)e * p.K * p.N;
+        const int64_t k_span = LONG ? span << p.glog2 : span * 128;
+        const int64_t k_end = LONG ? min((int64_t)p.K, k_span + ((int64_t)1 << p.glog2)) : min((int64_t)p.K, k_span + 128);
+        u32x2 v[32];
+        auto load = [&](int64_t k0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int64_t k = k0 + 32 * wave + i;
+                v[i] = *(const u32x2_at2*)(b + (size_t)min(k, (int64_t)p.K - 1) * p.N + c);
+                if (k >= k_end) v[i] = u32x2{0u, 0u};
+            }
+        };
+        float lo[4] = {}, hi[4] = {};
+        bool odd[4] = {};
+        for (int64_t k0 = k_span; k0 < k_end; k0 += 128) {
+            load(k0);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint16_t h = (uint16_t)(v[i][j / 2] >> (16 * (j & 1)));
+                    const float x = (float)__builtin_bit_cast(_Float16, h);
+                    odd[j] |= (h & 0x7c00u) == 0x7c00u;
+                    lo[j] = fminf(lo[j], x);
+                    hi[j] = fmaxf(hi[j], x);
+                }
+        }
+        __syncthreads();  // the last span's values are read
+        u32x4 put_lo, put_hi;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // an infinity or a NaN travels as a NaN
+            put_lo[j] = odd[j] ? 0x7fc00000u : __builtin_bit_cast(uint32_t, lo[j]);
+            put_hi[j] = __builtin_bit_cast(uint32_t, hi[j]);
+        }
+        least[wave][lane] = put_lo;
+        most[wave][lane] = put_hi;
+        __syncthreads();
+        // the waves of this wave's group
+        const int share = LONG ? 4 : max(1, min(4, (1 << p.glog2) / 32)), w0 = wave / share * share;
+        float glo[4] = {}, ghi[4] = {};
+        bool godd[4] = {};
+        for (int w = w0; w < w0 + share; ++w) {
+            const u32x4 a = least[w][lane], d = most[w][lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = __builtin_bit_cast(float, (uint32_t)a[j]);
+                godd[j] |= x != x;
+                glo[j] = fminf(glo[j], x);
+                ghi[j] = fmaxf(ghi[j], __builtin_bit_cast(float, (uint32_t)d[j]));
+            }
+        }
+        const W4Step st[4] = {{glo[0], ghi[0], godd[0], p.zeros != nullptr}, {glo[1], ghi[1], godd[1], p.zeros != nullptr},
+                              {glo[2], ghi[2], godd[2], p.zeros != nullptr}, {glo[3], ghi[3], godd[3], p.zeros != nullptr}};
+        const int64_t group = (LONG ? k_span : k_span + 32 * wave) >> p.glog2;
+        if (live && wave == w0 && group < p.groups) {
+            const size_t at = ((size_t)e * p.groups + group) * p.N + c;
+            *(u32x2_at2*)(p.scales + at) = u32x2{join16(st[0].bits, st[1].bits), join16(st[2].bits, st[3].bits)};
+            if (p.zeros)
+                *(u32_at1*)(p.zeros + at) = (uint32_t)st[0].z | (uint32_t)st[1].z << 8 | (uint32_t)st[2].z << 16 | (uint32_t)st[3].z << 24;
+        }
+        for (int64_t k0 = k_span; k0 < k_end; k0 += 128) {
+            if (LONG) load(k0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint16_t h = (uint16_t)(v[8 * x + i][j / 2] >> (16 * (j & 1)));
+                        w[j] |= st[j].code((float)__builtin_bit_cast(_Float16, h)) << (4 * i);
+                    }
+                const int64_t row = k0 / 8 + 4 * wave + x;
+                if (live && row < words) *(u32x4_at4*)(p.codes + ((size_t)e * words + row) * p.N + c) = w;
+            }
+        }
+    }
+}
+
+// 32 rows of four columns per lane, which are of one group.
+__global__ void __launch_bounds__(256) w4_dequantize_kernel(W4Convert p)
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int words = (p.K + 7) / 8, strips = (p.K + 31) / 32;
+    const int c0 = ((int)blockIdx.x * 64 + lane) * 4, c = min(c0, p.N - 4);
+    if (c0 >= p.N) return;
+    const int64_t all = p.matrices * strips;
+    for (int64_t es = (int64_t)blockIdx.y * 4 + wave; es < all; es += (int64_t)gridDim.y * 4) {
+        const int64_t e = es / strips;
+        const int k0 = (int)(es % strips) * 32;
+        const size_t at = ((size_t)e * p.groups + (k0 >> p.glog2)) * p.N + c;
+        const u32x2 sb = *(const u32x2_at2*)(p.scales + at);
+        const uint32_t zb = p.zeros ? *(const u32_at1*)(p.zeros + at) : 0x08080808u;
+        u32x4 w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            w[x] = *(const u32x4_at4*)(p.codes + ((size_t)e * words + min(k0 / 8 + x, words - 1)) * p.N + c);
+        float s[4], z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(sb[j / 2] >> (16 * (j & 1))));
+            z[j] = (float)((zb >> (8 * j)) & 0xffu);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (k0 + i >= p.K) break;
+            uint16_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = to_half(((float)((w[i / 8][j] >> (4 * (i % 8))) & 15u) - z[j]) * s[j]);
+            *(u32x2_at2*)(p.values + ((size_t)e * p.K + k0 + i) * p.N + c) = u32x2{join16(h[0], h[1]), join16(h[2], h[3])};
+        }
+    }
+}
+
+// Both for fewer than four columns: one thread per column and group, and per
+// column and word.
+__global__ void __launch_bounds__(256) w4_quantize_narrow_kernel(W4Convert p)
+{
+    const int words = (p.K + 7) / 8;
+    const int64_t all = p.matrices * p.groups * p.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int n = (int)(i % p.N);
+        const int64_t eg = i / p.N, e = eg / p.groups, k0 = (eg % p.groups) << p.glog2, k1 = min((int64_t)p.K, k0 + ((int64_t)1 << p.glog2));
         const uint16_t* b = p.b + (size_t)e * p.K * p.N + n;
         float lo = 0.0f, hi = 0.0f;
-        bool odd = false;  // an infinity or a NaN
-        for (int k = k0; k < k1; ++k) {
+        bool odd = false;
+        for (int64_t k = k0; k < k1; ++k) {
             const float v = half_at(b + (size_t)k * p.N);
             odd |= !(fabsf(v) <= 65504.0f);
             lo = fminf(lo, v);
             hi = fmaxf(hi, v);
         }
-        const float step = p.zeros ? (hi - lo) / 15.0f : fmaxf(-lo, hi) / 7.0f;
-        const uint16_t sb = odd ? (uint16_t)0x7e00 : to_half(step);
-        const float s = (float)__builtin_bit_cast(_Float16, sb);
-        const bool live = s > 0.0f;
-        const float z = p.zeros && live ? fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f) : 8.0f;
-        const size_t at = (size_t)eg * p.N + n;
-        p.scales[at] = sb;
-        if (p.zeros) p.zeros[at] = (uint8_t)z;
-        for (int k = k0; k < k1; k += 8) {
+        const W4Step st(lo, hi, odd, p.zeros != nullptr);
+        p.scales[i] = st.bits;
+        if (p.zeros) p.zeros[i] = (uint8_t)st.z;
+        for (int64_t k = k0; k < k1; k += 8) {
             uint32_t w = 0;
-            for (int i = 0; i < 8; ++i) {
-                const float v = k + i < k1 ? half_at(b + (size_t)(k + i) * p.N) : 0.0f;
-                const float q = live ? fminf(fmaxf(rintf(v / s) + z, 0.0f), 15.0f) : z;
-                w |= (uint32_t)q << (4 * i);
-            }
+            for (int x = 0; x < 8; ++x) w |= st.code(k + x < k1 ? half_at(b + (size_t)(k + x) * p.N) : 0.0f) << (4 * x);
             p.codes[((size_t)e * words + k / 8) * p.N + n] = w;
         }
     }
 }
 
-// One thread per word.
-__global__ void __launch_bounds__(256) w4_dequantize_kernel(W4Convert p)
+__global__ void __launch_bounds__(256) w4_dequantize_narrow_kernel(W4Convert p)
 {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= p.N) return;
     const int words = (p.K + 7) / 8;
-    const int64_t all = p.matrices * words;
-    for (int64_t er = blockIdx.y; er < all; er += gridDim.y) {
-        const int64_t e = er / words;
+    const int64_t all = p.matrices * words * p.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int n = (int)(i % p.N);
+        const int64_t er = i / p.N, e = er / words;
         const int r = (int)(er % words);
-        const uint32_t w = p.codes[(size_t)er * p.N + n];
+        const uint32_t w = p.codes[i];
         const size_t at = ((size_t)e * p.groups + ((8 * r) >> p.glog2)) * p.N + n;
         const float s = half_at(p.scales + at), z = p.zeros ? (float)p.zeros[at] : 8.0f;
-        for (int i = 0; i < 8 && 8 * r + i < p.K; ++i)
-            p.values[((size_t)e * p.K + 8 * r + i) * p.N + n] = to_half(((float)((w >> (4 * i)) & 15u) - z) * s);
+        for (int x = 0; x < 8 && 8 * r + x < p.K; ++x)
+            p.values[((size_t)e * p.K + 8 * r + x) * p.N + n] = to_half(((float)((w >> (4 * x)) & 15u) - z) * s);
     }
 }
 

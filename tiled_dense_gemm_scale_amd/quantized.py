@@ -101,8 +101,10 @@ def gemm_w4(a: torch.Tensor, w: W4, workspace: Optional[torch.Tensor] = None, bi
     """c = act(alpha * a @ w + bias) for a (M, K) fp16, w a W4 of one (K, N)
     matrix, bias (N,) fp16 or None, act "relu", "gelu" (tanh form) or "none".
     Products are summed in fp32 and scaled group by group; the weights are not
-    rounded.  workspace: new_workspace(w4_workspace_bytes(M, N, K)), one per call
-    that may run at the same time; with less, or None, K is not split across
+    rounded, but where many rows make it faster they are written to the workspace
+    as dequantize_w4 gives them and multiplied by the dense kernels.  workspace:
+    new_workspace(w4_workspace_bytes(M, N, K)), one per call that may run at the
+    same time; with less, or None, neither that is done nor K split across
     workgroups.  Returns c (M, N)."""
     matrix("a", a, torch.float16, 2)
     (M, K), dev = a.shape, a.get_device()
