@@ -21,7 +21,7 @@ bool bad_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F, int64_t O)
 bool large_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F, int64_t O)
 {
     return T > gsr::kFewTokens || k > gsr::kFewSlots || T * k > gsr::kFewSlots || E > gsr::kFewExperts ||
-           H >= kStreamWidth || F >= kStreamWidth || O >= kStreamWidth || T * k * F >= ((int64_t)1 << 30);
+           H >= kStreamWidth || F >= kStreamWidth || O >= kStreamWidth || T * k * (cdiv(F, 8) * 8) >= ((int64_t)1 << 30);
 }
 
 struct Plan {
@@ -34,14 +34,15 @@ constexpr int64_t kFewGrid = 256;
 
 Plan plan_of(bool w4, int64_t T, int64_t k, int64_t E, int64_t F, int64_t O)
 {
-    const int64_t CB = w4 ? gsr::W4Stream<1, 1, true>::CB : gsr::HalfStream<1, true>::CB;
+    const int64_t CB = w4 ? gsr::W4Stream<1, true>::CB : gsr::HalfStream<true>::CB;
     Plan g;
-    const int64_t slots = T * k, most = std::max<int64_t>(1, std::min(E, slots));
+    // tiles at most: one per expert that is hit, and one for each 16 slots more
+    const int64_t slots = T * k, most = std::max<int64_t>(1, std::min(slots, std::min(E, slots) + slots / gsr::kFewRows));
     g.blocks_up = (int)cdiv(F, CB);
     // as many workgroups as items, up to a power of two of them
     for (g.grid_up = 1, g.waves_log2 = 3; g.grid_up < kFewGrid && g.grid_up < g.blocks_up * most; g.grid_up *= 2) ++g.waves_log2;
     g.blocks = (int)cdiv(O, CB);
-    // a job is an expert and 256 rows of F at least, eight to a workgroup
+    // a job is a tile and 256 rows of F at least, eight to a workgroup
     g.groups = (int)std::max<int64_t>(1, std::min({(int64_t)16, kFewGrid / std::max(g.blocks, 1), cdiv(most * cdiv(F, 256), gsr::kStreamWaves)}));
     g.per = (int)cdiv(g.blocks, gsr::kMeetCounters);
     g.hidden_wide = cdiv(F, 8) * 8;
@@ -83,16 +84,13 @@ typedef void (*few_kernel)(gsr::FewArgs);
 struct Kernels {
     few_kernel up, gated, down;
 };
-// One tile of rows per expert up to 16 tokens (choices that name an expert twice
-// are further tiles), two above.
+// The second launch keeps its tokens' sums in LDS: 16 of them, or 64.
 template <int FORM, bool DW>
 Kernels kernels_of(int64_t T)
 {
-    if (T <= 16)
-        return Kernels{gsr::few_up_kernel<FORM, 1, DW, false>, gsr::few_up_kernel<FORM, 1, DW, true>,
-                       gsr::few_down_kernel<FORM, 1, 1, DW || FORM != gsr::kFewHalf>};
-    return Kernels{gsr::few_up_kernel<FORM, 2, DW, false>, gsr::few_up_kernel<FORM, 2, DW, true>,
-                   gsr::few_down_kernel<FORM, 2, 4, DW || FORM != gsr::kFewHalf>};
+    constexpr bool DD = DW || FORM != gsr::kFewHalf;  // its rows of A are h's, which lie on dwords
+    return Kernels{gsr::few_up_kernel<FORM, DW, false>, gsr::few_up_kernel<FORM, DW, true>,
+                   T <= 16 ? gsr::few_down_kernel<FORM, 16, DD> : gsr::few_down_kernel<FORM, gsr::kFewTokens, DD>};
 }
 // For matrices of `w` (and `w2`, or null) of N columns, and rows of A of K values.
 Kernels kernels_at(int64_t T, const gsr_weights* w, const gsr_weights* w2, const void* a, int64_t K, int64_t N)

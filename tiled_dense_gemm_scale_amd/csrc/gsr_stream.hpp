@@ -1,5 +1,5 @@
 // gsr_stream.hpp -- products of a few rows with weights read once: a wave's
-// share of C (16 MT rows x CB columns) over a run of K, operands from memory
+// share of C (16 rows x CB columns) over a run of K, operands from memory
 // straight into registers.
 //
 // Such products are bound by the weights' bytes, so nothing stands between the
@@ -76,32 +76,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dword_rsrc(const void* at, uin
     return make_rsrc((const uint8_t*)at - behind, (uint32_t)min((bytes + behind + 3u) & ~(uint64_t)3, (uint64_t)0x7ffffffcu));
 }
 
-// The rows of A that a lane reads: row l of each of MT tiles of 16, of a table of
-// less than 2^31 bytes.  Rows past the last are that one again, whose sums nobody
-// takes, and loads behind the table are zeros: no load is masked, and lanes with
-// one address are one access.  DW: every row starts on a dword.
-template <int MT, bool DW>
+// The row of A that a lane reads, the l-th of 16, of a table of less than 2^31
+// bytes.  Rows past the last are that one again, whose sums nobody takes, and
+// loads behind the table are zeros: no load is masked, and lanes with one address
+// are one access.  DW: every row starts on a dword.
+template <bool DW>
 struct StreamRows {
     __amdgpu_buffer_rsrc_t rs;
-    uint32_t off[MT];
+    uint32_t off;
 
-    __device__ __forceinline__ StreamRows(const uint16_t* table, uint64_t bytes)
+    __device__ __forceinline__ StreamRows(const uint16_t* table, uint64_t bytes) { rs = dword_rsrc(table, bytes, off); }
+    __device__ __forceinline__ void row(uint32_t at) { off += 2u * at; }  // `at` values into the table
+    __device__ __forceinline__ u32x4 load(int k) const
     {
-        uint32_t behind;
-        rs = dword_rsrc(table, bytes, behind);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) off[t] = behind;
-    }
-    template <int MORE>
-    __device__ __forceinline__ explicit StreamRows(const StreamRows<MORE, DW>& r) : rs(r.rs)  // the first of its tiles
-    {
-#pragma unroll
-        for (int t = 0; t < MT; ++t) off[t] = r.off[t];
-    }
-    __device__ __forceinline__ void row(int t, uint32_t at) { off[t] += 2u * at; }  // `at` values into the table
-    __device__ __forceinline__ u32x4 load(int t, int k) const
-    {
-        const uint32_t o = off[t] + 2u * (uint32_t)k;
+        const uint32_t o = off + 2u * (uint32_t)k;
         if constexpr (DW) return __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
         else return load8_shifted(rs, o);
     }
@@ -131,16 +119,14 @@ __device__ __forceinline__ int stream_column(int n0, int l, int N)
     return N >= CPL ? min(c, N - CPL) : c;
 }
 
-// acc[j][t]: columns c + j of lane l (its 16 lanes' columns), rows 16 t + 4 g + r.
-template <int CT, int MT>
+// v[j]: column c + j of lane l (its 16 lanes' columns), rows 4 g + r.
+template <int CT>
 struct StreamSums {
-    f32x4 v[CT][MT];
+    f32x4 v[CT];
     __device__ __forceinline__ void clear()
     {
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) v[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < CT; ++j) v[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 };
 
@@ -168,15 +154,15 @@ struct HalfMatrix {
 };
 
 // DW: every row starts on a dword (N even, b on one), and every row of A.
-template <int MT, bool DW>
+template <bool DW>
 struct HalfStream {
     static constexpr int CPL = 8, CB = 16 * CPL, UNIT = kStep;  // UNIT: k of the smallest run
-    typedef StreamSums<CPL, MT> Sums;
-    typedef StreamRows<MT, DW> Rows;
+    typedef StreamSums<CPL> Sums;
+    typedef StreamRows<DW> Rows;
 
     struct Step {
         u32x4 b[8];
-        u32x4 a[MT];
+        u32x4 a;
     };
     struct Place {
         const uint16_t* b;
@@ -199,8 +185,7 @@ struct HalfStream {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s.b[i] = load8_shifted(rs, p.off[i] + behind);
         }
-#pragma unroll
-        for (int t = 0; t < MT; ++t) s.a[t] = rows.load(t, k0 + 8 * p.g);
+        s.a = rows.load(k0 + 8 * p.g);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -209,8 +194,7 @@ struct HalfStream {
     __device__ static __forceinline__ void cut(Step& s, const Place& p, int k0)
     {
         const int n = p.K - k0 - 8 * p.g;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) s.a[t] = first8(s.a[t], n);
+        s.a = first8(s.a, n);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i >= n) s.b[i] = u32x4{0u, 0u, 0u, 0u};
@@ -227,11 +211,8 @@ struct HalfStream {
                 even[e] = pack_lo(s.b[2 * e][d], s.b[2 * e + 1][d]);
                 odd[e] = pack_hi(s.b[2 * e][d], s.b[2 * e + 1][d]);
             }
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                acc.v[2 * d][t] = mfma16(s.a[t], even, acc.v[2 * d][t]);
-                acc.v[2 * d + 1][t] = mfma16(s.a[t], odd, acc.v[2 * d + 1][t]);
-            }
+            acc.v[2 * d] = mfma16(s.a, even, acc.v[2 * d]);
+            acc.v[2 * d + 1] = mfma16(s.a, odd, acc.v[2 * d + 1]);
             __builtin_amdgcn_sched_barrier(0);  // a pair's values live no longer than it
         }
     }
@@ -266,20 +247,19 @@ struct HalfStream {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) s.b[x] = x == i ? v : s.b[x];
             }
-#pragma unroll
-            for (int t = 0; t < MT; ++t) s.a[t] = rows.load(t, u * kStep + 8 * p.g);
+            s.a = rows.load(u * kStep + 8 * p.g);
             multiply(s, p, u, acc);
         }
     }
 };
 
 // ---- the sum over waves ---------------------------------------------------------
-// Each of a workgroup's waves has a slice of LDS for one tile (16 rows x CB
-// columns) of its sums, row-major.
+// Each of a workgroup's waves has a slice of LDS for its sums, 16 rows x CB
+// columns, row-major.
 constexpr int kStreamWaves = 8, kStreamThreads = kWave * kStreamWaves;
 
-template <int CPL, int MT>
-__device__ __forceinline__ void stream_put(float* slice, const StreamSums<CPL, MT>& acc, int t)
+template <int CPL>
+__device__ __forceinline__ void stream_put(float* slice, const StreamSums<CPL>& acc)
 {
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
 #pragma unroll
@@ -287,7 +267,7 @@ __device__ __forceinline__ void stream_put(float* slice, const StreamSums<CPL, M
         f32x4* to = (f32x4*)(slice + (4 * g + r) * 16 * CPL + CPL * l);
 #pragma unroll
         for (int j = 0; j < CPL / 4; ++j)
-            to[j] = f32x4{acc.v[4 * j][t][r], acc.v[4 * j + 1][t][r], acc.v[4 * j + 2][t][r], acc.v[4 * j + 3][t][r]};
+            to[j] = f32x4{acc.v[4 * j][r], acc.v[4 * j + 1][r], acc.v[4 * j + 2][r], acc.v[4 * j + 3][r]};
     }
 }
 

@@ -57,15 +57,15 @@ __device__ __forceinline__ u32x4 w4_order(u32x4 a)
 // scaled in fp32 when the group (or, of larger ones, 128 rows of it) ends, so
 // the weights are never rounded.  FL: steps between such ends (1, 2 or 4).  DW: every row of A starts on a
 // dword.
-template <int MT, int FL, bool DW>
+template <int FL, bool DW>
 struct W4Stream {
     static constexpr int CPL = 4, CB = 16 * CPL, STEPS = 4, UNIT = STEPS * kStep, ENDS = STEPS / FL, DEPTH = 2;
-    typedef StreamSums<CPL, MT> Sums;
-    typedef StreamRows<MT, DW> Rows;
+    typedef StreamSums<CPL> Sums;
+    typedef StreamRows<DW> Rows;
 
     struct Batch {
         u32x4 w[STEPS];
-        u32x4 a[STEPS][MT];
+        u32x4 a[STEPS];
         u32x2 s[ENDS];
         uint32_t z[ENDS];
     };
@@ -90,9 +90,7 @@ struct W4Stream {
             t.z[e] = *(const u32_at1*)(p.zeros + row + p.c);
         }
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-            for (int x = 0; x < MT; ++x) t.a[i][x] = rows.load(x, k0 + i * kStep + 8 * p.g);
+        for (int i = 0; i < STEPS; ++i) t.a[i] = rows.load(k0 + i * kStep + 8 * p.g);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -120,36 +118,26 @@ struct W4Stream {
         const int left = p.K - u * UNIT;
         if (left < UNIT) {  // behind a row of A lies the next one
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-                for (int x = 0; x < MT; ++x) t.a[i][x] = first8(t.a[i][x], left - i * kStep - 8 * p.g);
+            for (int i = 0; i < STEPS; ++i) t.a[i] = first8(t.a[i], left - i * kStep - 8 * p.g);
         }
 #pragma unroll
         for (int e = 0; e < ENDS; ++e) {
             if (e * FL * kStep >= left) break;  // no such group
             Scale v;
             scale_of(v, t.s[e], t.z[e], p.m.zeros != nullptr);
-            f32x4 sum[CPL][MT];
+            f32x4 sum[CPL];
 #pragma unroll
             for (int i = 0; i < FL; ++i) {
-                u32x4 b[CPL];
+                const u32x4 a = w4_order(t.a[e * FL + i]);
 #pragma unroll
-                for (int j = 0; j < CPL; ++j) b[j] = w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]);
-#pragma unroll
-                for (int x = 0; x < MT; ++x) {
-                    const u32x4 a = w4_order(t.a[e * FL + i][x]);
-#pragma unroll
-                    for (int j = 0; j < CPL; ++j)
-                        sum[j][x] = mfma16(a, b[j], i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j][x]);
-                }
+                for (int j = 0; j < CPL; ++j)
+                    sum[j] = mfma16(a, w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]), i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j]);
                 __builtin_amdgcn_sched_barrier(0);  // a step's values live no longer than it
             }
 #pragma unroll
             for (int j = 0; j < CPL; ++j)
 #pragma unroll
-                for (int x = 0; x < MT; ++x)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc.v[j][x][r] = fmaf(v.s[j], sum[j][x][r], acc.v[j][x][r]);
+                for (int r = 0; r < 4; ++r) acc.v[j][r] = fmaf(v.s[j], sum[j][r], acc.v[j][r]);
         }
     }
 
@@ -171,15 +159,12 @@ struct W4Stream {
             zeros |= (uint32_t)(in ? p.zeros[row + p.c + j] : (uint8_t)0) << (8 * j);
         }
         scale_of(v, u32x2{join16(s[0], s[1]), join16(s[2], s[3])}, zeros, p.m.zeros != nullptr);
+        const u32x4 a = w4_order(first8(rows.load(k0 + 8 * p.g), p.K - k0 - 8 * p.g));
 #pragma unroll
-        for (int x = 0; x < MT; ++x) {
-            const u32x4 a = w4_order(first8(rows.load(x, k0 + 8 * p.g), p.K - k0 - 8 * p.g));
+        for (int j = 0; j < CPL; ++j) {
+            const f32x4 sum = mfma16(a, w4_values(w[j], v.lo[j], v.hi[j]), f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
-                const f32x4 sum = mfma16(a, w4_values(w[j], v.lo[j], v.hi[j]), f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) acc.v[j][x][r4] = fmaf(v.s[j], sum[r4], acc.v[j][x][r4]);
-            }
+            for (int x = 0; x < 4; ++x) acc.v[j][x] = fmaf(v.s[j], sum[x], acc.v[j][x]);
         }
     }
 

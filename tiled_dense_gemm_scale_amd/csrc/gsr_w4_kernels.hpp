@@ -29,7 +29,7 @@ struct W4Gemm {
 template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 {
-    using S = W4Stream<1, FL, DW>;
+    using S = W4Stream<FL, DW>;
     constexpr int CPL = S::CPL, CB = S::CB;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ int flag;
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
     const int m0 = tile % p.blocks_m * 16, n0 = tile / p.blocks_m * CB, rows_here = min(16, p.M - m0);
 
     typename S::Rows rows(p.a + (size_t)m0 * p.K, (uint64_t)rows_here * (uint32_t)p.K * 2u);
-    rows.row(0, (uint32_t)min(l, rows_here - 1) * (uint32_t)p.K);
+    rows.row((uint32_t)min(l, rows_here - 1) * (uint32_t)p.K);
     const int units = (p.K + S::UNIT - 1) / S::UNIT;
     const int first = part * p.chunk, here = max(0, min(p.chunk, units - first));
     const int u0 = first + here * wave / kStreamWaves, u1 = first + here * (wave + 1) / kStreamWaves;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
         const float b = p.bias ? half_at(p.bias + col) : 0.0f;
         p.c[(size_t)m * p.N + col] = to_half(activate(s * p.alpha + b, p.act));
     };
-    stream_put<CPL, 1>(lds + wave * 16 * CB, acc, 0);
+    stream_put<CPL>(lds + wave * 16 * CB, acc);
     __syncthreads();
     const size_t wide = (size_t)p.blocks_n * CB;
 #pragma unroll 1
