@@ -122,18 +122,23 @@ __device__ __forceinline__ int few_plan(FewPlan& s, const FewArgs& p)
     return p.experts > 0 ? __builtin_amdgcn_readfirstlane(s.upto[p.experts - 1]) : 0;
 }
 
-// The expert of tile d (below their number), and which of its tiles that is.
-__device__ __forceinline__ int few_expert(const FewPlan& s, int experts, int d, int& tile)
+// Each tile stands `times` times in the waves' items, those of an expert of more
+// than one next to each other: item i is the `turn`-th of its tile.
+struct FewItem {
+    int e, tile, turn;
+};
+__device__ __forceinline__ FewItem few_item(const FewPlan& s, int experts, int i, int times)
 {
-    const int lane = threadIdx.x & 63;
-    for (int e0 = 0;; e0 += kWave) {
-        const uint64_t m = __ballot(e0 + lane < experts && s.upto[e0 + lane] > d);
-        if (m != 0) {
-            const int e = e0 + __ffsll((unsigned long long)m) - 1;
-            tile = d - (e > 0 ? __builtin_amdgcn_readfirstlane(s.upto[e - 1]) : 0);
-            return e;
-        }
-    }
+    const int lane = threadIdx.x & 63, d = (int)((uint32_t)i / (uint32_t)times);
+    int e0 = 0;
+    uint64_t m;
+    while ((m = __ballot(e0 + lane < experts && s.upto[e0 + lane] > d)) == 0) e0 += kWave;
+    const int e = e0 + __ffsll((unsigned long long)m) - 1;
+    const int before = e > 0 ? __builtin_amdgcn_readfirstlane(s.upto[e - 1]) : 0;
+    const int n = __builtin_amdgcn_readfirstlane(s.upto[e]) - before, at = i - before * times;
+    if (n == 1) return FewItem{e, 0, at};
+    const int turn = (int)((uint32_t)at / (uint32_t)n);
+    return FewItem{e, at - turn * n, turn};
 }
 
 // The slots of expert e's tile into this wave's list; how many there are.
@@ -159,10 +164,11 @@ __device__ __forceinline__ int few_rows(int16_t* list, const int16_t* key, int s
 __device__ __forceinline__ int few_split(int items, int waves_log2, int units, int fixed, int least)
 {
     int best = least;
-    int64_t shortest = INT64_MAX;
+    float shortest = 1e30f;
+#pragma unroll 1
     for (int s = least; s <= 3; ++s) {
-        const int rounds = (int)((((int64_t)items << s) + (1 << waves_log2) - 1) >> waves_log2);
-        const int64_t cost = (int64_t)rounds * ((units >> (s - least)) + fixed);
+        const int rounds = ((items << s) + (1 << waves_log2) - 1) >> waves_log2;  // items are below 2^27
+        const float cost = (float)rounds * (float)((units >> (s - least)) + fixed);
         if (cost < shortest) {
             shortest = cost;
             best = s;
@@ -177,53 +183,58 @@ template <int FORM, bool DW, bool GATED>
 __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
 {
     using S = FewStream<FORM, DW>;
-    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, SETS = GATED ? 2 : 1;
+    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, QUADS = CB / 4, SETS = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ FewPlan plan;
-    __shared__ int expert_of[kStreamWaves], count_of[kStreamWaves];
+    __shared__ int expert_of[kStreamWaves], block_of[kStreamWaves], count_of[kStreamWaves];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 15;
     const int items = few_plan(plan, p) * p.blocks_up, units = (p.H + UNIT - 1) / UNIT;
     const int kl = few_split(items, p.waves_log2, units, 256 / UNIT, SETS - 1), kg = 1 << kl, cg = kStreamWaves >> kl;
     const int turn = wave & (kg - 1), half = kg / SETS;  // the waves of one matrix
     const FewWeights& w = GATED && turn < half ? p.gate : p.up;
-    const int u0 = units * (turn & (half - 1)) / half, u1 = units * ((turn & (half - 1)) + 1) / half;
+    const int hl = kl - (SETS - 1), u0 = (units * (turn & (half - 1))) >> hl, u1 = (units * ((turn & (half - 1)) + 1)) >> hl;
 
     for (int first = blockIdx.x * cg; first < items; first += gridDim.x * cg) {
-        const int item = first + (wave >> kl), d = item / p.blocks_up, n0 = (item - d * p.blocks_up) * CB;
-        int e = -1, count = 0;
+        const int item = first + (wave >> kl);
+        FewItem at{-1, 0, 0};
+        int count = 0;
         typename S::Sums acc;
         if (item < items) {
-            int tile;
-            e = few_expert(plan, p.experts, d, tile);
-            count = few_rows(plan.slot[wave], plan.key, p.slots, e, tile);
+            at = few_item(plan, p.experts, item, p.blocks_up);
+            count = few_rows(plan.slot[wave], plan.key, p.slots, at.e, at.tile);
             typename S::Rows rows(p.x, (uint64_t)p.T * (uint32_t)p.H * 2u);
             rows.row((uint32_t)plan.slot[wave][min(l, count - 1)] / (uint32_t)p.k * (uint32_t)p.H);
             acc.clear();
-            S::run(S::matrix(w, e, p.H, p.F), p.H, p.F, n0, rows, u0, u1, acc);
+            S::run(S::matrix(w, at.e, p.H, p.F), p.H, p.F, at.turn * CB, rows, u0, u1, acc);
         }
         if ((threadIdx.x & 63) == 0) {
-            expert_of[wave] = e;
+            expert_of[wave] = at.e;
+            block_of[wave] = at.turn * CB;
             count_of[wave] = count;
         }
         if (count > 0) stream_put<CPL>(lds + wave * 16 * CB, acc);
         __syncthreads();
 #pragma unroll 1
         for (int c = 0; c < cg; ++c) {
-            const int at_n0 = (first + c) % p.blocks_up * CB, ex = expert_of[c << kl], here = count_of[c << kl];
+            const int n0 = block_of[c << kl], ex = expert_of[c << kl], here = count_of[c << kl];
             const float* slices = lds + (c << kl) * 16 * CB;
 #pragma unroll 1
-            for (int u = threadIdx.x; u < here * CB; u += kStreamThreads) {
-                const int m = u / CB, at = u % CB, col = stream_position<CPL>(at_n0, at, p.F);
+            for (int u = threadIdx.x; u < here * QUADS; u += kStreamThreads) {
+                const int m = u / QUADS, q = u % QUADS, col = stream_position<CPL>(n0, q, p.F);
                 if (col < 0) continue;
-                const size_t b = (size_t)ex * p.F + col;
-                float v = stream_sum<CPL>(slices + (kg - half) * 16 * CB, half, m, at) + (p.up.bias ? half_at(p.up.bias + b) : 0.0f);
+                const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+                f32x4 v = add4(stream_sum<CPL>(slices + (kg - half) * 16 * CB, half, m, q),
+                               p.up.bias ? half4_at(p.up.bias + (size_t)ex * p.F, col, p.F) : none);
                 if constexpr (GATED) {
-                    const float g = stream_sum<CPL>(slices, half, m, at) + (p.gate.bias ? half_at(p.gate.bias + b) : 0.0f);
-                    v *= stream_activate(g, p.act);
+                    const f32x4 g = add4(stream_sum<CPL>(slices, half, m, q),
+                                         p.gate.bias ? half4_at(p.gate.bias + (size_t)ex * p.F, col, p.F) : none);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] *= stream_activate(g[i], p.act);
                 } else {
-                    v = stream_activate(v, p.act);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = stream_activate(v[i], p.act);
                 }
-                p.hidden[(size_t)plan.slot[c << kl][m] * p.hidden_wide + col] = to_half(v);
+                put_half4(p.hidden + (size_t)plan.slot[c << kl][m] * p.hidden_wide, col, p.F, v);
             }
         }
         __syncthreads();
@@ -238,9 +249,9 @@ template <int FORM, int TOKENS, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
 {
     using S = FewStream<FORM, DW>;
-    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT;
+    constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, QUADS = CB / 4;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
-    __shared__ float sums[TOKENS * CB];
+    __shared__ f32x4 sums[TOKENS * QUADS];
     __shared__ FewPlan plan;
     __shared__ uint32_t mask[2][TOKENS];
     __shared__ int8_t row_of[kStreamWaves][TOKENS], token_of[kStreamWaves][kFewRows + 1];
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
     __shared__ int flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 15;
     const int nb = blockIdx.x / p.groups, group = blockIdx.x - nb * p.groups, n0 = nb * CB;
-    for (int i = tid; i < p.T * CB; i += kStreamThreads) sums[i] = 0.0f;
+    for (int i = tid; i < p.T * QUADS; i += kStreamThreads) sums[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (tid < TOKENS) mask[0][tid] = mask[1][tid] = 0u;
     const int tiles = few_plan(plan, p), units = (p.F + UNIT - 1) / UNIT;
     // every wave of the block has a job where that leaves each 256 rows of F
@@ -258,13 +269,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
 
     int turn = 0;
     for (int first = j0; first < j1; first += kStreamWaves) {
-        const int job = first + wave, d = job / parts, part = job - d * parts;
-        int e = -1, count = 0;
+        const int job = first + wave;
         typename S::Sums acc;
         if (job < j1) {
-            int tile;
-            e = few_expert(plan, p.experts, d, tile);
-            count = few_rows(plan.slot[wave], plan.key, p.slots, e, tile);
+            const FewItem it = few_item(plan, p.experts, job, parts);
+            const int e = it.e, part = it.turn, count = few_rows(plan.slot[wave], plan.key, p.slots, e, it.tile);
             if (lane < count) {
                 const int slot = plan.slot[wave][lane], token = slot / p.k;
                 token_of[wave][lane] = (int8_t)token;
@@ -279,25 +288,29 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
             typename S::Rows rows(p.hidden, (uint64_t)p.slots * (uint32_t)p.hidden_wide * 2u);
             rows.row((uint32_t)plan.slot[wave][min(l, count - 1)] * (uint32_t)p.hidden_wide);
             acc.clear();
-            S::run(S::matrix(p.down, e, p.F, p.O), p.F, p.O, n0, rows, (int)((int64_t)units * part / parts),
-                   (int)((int64_t)units * (part + 1) / parts), acc);
+            S::run(S::matrix(p.down, e, p.F, p.O), p.F, p.O, n0, rows, (int)((uint32_t)(units * part) / (uint32_t)parts),
+                   (int)((uint32_t)(units * (part + 1)) / (uint32_t)parts), acc);  // 2^17 units, 2^7 parts at most
             stream_put<CPL>(lds + wave * 16 * CB, acc);
         }
         __syncthreads();
 #pragma unroll 1
-        for (int u = tid; u < p.T * CB; u += kStreamThreads) {
-            const int token = u / CB, at = u % CB;
+        for (int u = tid; u < p.T * QUADS; u += kStreamThreads) {
+            const int token = u / QUADS, q = u % QUADS;
             uint32_t from = mask[turn][token];
             if (from == 0u) continue;
-            const int col = stream_position<CPL>(n0, at, p.O);
-            float s = sums[u];
+            const int col = stream_position<CPL>(n0, q, p.O);
+            f32x4 s = sums[u];
             do {
                 const int w = __ffs((int)from) - 1;
                 from &= from - 1u;
-                const float b = bias_of[w] >= 0 && col >= 0 ? half_at(p.down.bias + (size_t)bias_of[w] * p.O + col) : 0.0f;
+                f32x4 b = {0.f, 0.f, 0.f, 0.f};
+                if (bias_of[w] >= 0 && col >= 0) b = half4_at(p.down.bias + (size_t)bias_of[w] * p.O, col, p.O);
                 int r = row_of[w][token];
-                do s = fmaf(weight_of[w][r], lds[(w * 16 + r) * CB + at] + b, s);
-                while (token_of[w][++r] == token);
+                do {
+                    const f32x4 y = *(const f32x4*)(lds + (w * 16 + r) * CB + 4 * q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i] = fmaf(weight_of[w][r], y[i] + b[i], s[i]);
+                } while (token_of[w][++r] == token);
             } while (from != 0u);
             sums[u] = s;
         }
@@ -306,22 +319,20 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
         __syncthreads();
     }
 
-    auto finish = [&](int u, int n_block, float s) {
-        const int col = stream_position<CPL>(n_block, u % CB, p.O);
-        if (col >= 0) p.out[(size_t)(u / CB) * p.O + col] = to_half(s);
+    auto finish = [&](int u, int n_block, f32x4 s) {
+        const int col = stream_position<CPL>(n_block, u % QUADS, p.O);
+        if (col >= 0) put_half4(p.out + (size_t)(u / QUADS) * p.O, col, p.O, s);
     };
-#pragma unroll 1
-    for (int u = tid; u < p.T * CB; u += kStreamThreads) {
+    for (int u = tid; u < p.T * QUADS; u += kStreamThreads) {
         if (p.groups == 1) finish(u, n0, sums[u]);
-        else meet_store(p.part + ((size_t)group * p.T + u / CB) * p.part_wide + n0 + u % CB, sums[u]);
+        else meet_store(p.part + ((size_t)group * p.T + u / QUADS) * p.part_wide + n0 + 4 * (u % QUADS), sums[u]);
     }
     if (p.groups == 1) return;
     const int b0 = nb / p.per * p.per, b1 = min(b0 + p.per, p.blocks);
     if (!meet_last(p.count + nb / p.per, (uint32_t)((b1 - b0) * p.groups), &flag)) return;
     for (int b = b0; b < b1; ++b)
-#pragma unroll 1
-        for (int u = tid; u < p.T * CB; u += kStreamThreads)
-            finish(u, b * CB, meet_sum(p.part + (size_t)(u / CB) * p.part_wide + b * CB + u % CB, p.groups, (size_t)p.T * p.part_wide));
+        for (int u = tid; u < p.T * QUADS; u += kStreamThreads)
+            finish(u, b * CB, meet_sum(p.part + (size_t)(u / QUADS) * p.part_wide + b * CB + 4 * (u % QUADS), p.groups, (size_t)p.T * p.part_wide));
 }
 
 }  // namespace gsr

@@ -48,6 +48,8 @@ __device__ __forceinline__ u32x4 load8_first(const uint16_t* p, int n)
     return v;
 }
 
+__device__ __forceinline__ f32x4 add4(f32x4 a, f32x4 b) { return f32x4{a[0] + b[0], a[1] + b[1], a[2] + b[2], a[3] + b[3]}; }
+
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
@@ -271,23 +273,38 @@ __device__ __forceinline__ void stream_put(float* slice, const StreamSums<CPL>& 
     }
 }
 
-// Position `at` of row m, summed over `waves` slices in order from +0.
+// Positions 4q .. 4q + 3 of row m, summed over `waves` slices in order from +0.
 template <int CPL>
-__device__ __forceinline__ float stream_sum(const float* slices, int waves, int m, int at)
+__device__ __forceinline__ f32x4 stream_sum(const float* slices, int waves, int m, int q)
 {
-    float s = 0.0f;
-#pragma unroll 4
-    for (int w = 0; w < waves; ++w) s += slices[(w * 16 + m) * 16 * CPL + at];
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int w = 0; w < waves; ++w) s = add4(s, *(const f32x4*)(slices + (w * 16 + m) * 16 * CPL + 4 * q));
     return s;
 }
 
-// The column of a position of the block from n0, or -1 where the position's lane
-// lies past N.
+// The column of position 4q of the block from n0 (three more lie behind it; those
+// from N on are none), or -1 where the position's lane lies past N.
 template <int CPL>
-__device__ __forceinline__ int stream_position(int n0, int at, int N)
+__device__ __forceinline__ int stream_position(int n0, int q, int N)
 {
-    const int l = at / CPL, col = stream_column<CPL>(n0, l, N) + at % CPL;
-    return n0 + CPL * l < N && col < N ? col : -1;
+    const int l = 4 * q / CPL;
+    return n0 + CPL * l < N ? stream_column<CPL>(n0, l, N) + 4 * q % CPL : -1;
+}
+
+// Four fp16 values of a row of N from column `col` on (zeros past N), and back.
+__device__ __forceinline__ f32x4 half4_at(const uint16_t* row, int col, int N)
+{
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = col + i < N ? (float)__builtin_bit_cast(_Float16, row[col + i]) : 0.0f;
+    return v;
+}
+__device__ __forceinline__ void put_half4(uint16_t* row, int col, int N, f32x4 v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (col + i < N) row[col + i] = __builtin_bit_cast(uint16_t, (_Float16)v[i]);
 }
 
 // ---- sums that meet in a workspace ---------------------------------------------------
@@ -296,22 +313,31 @@ __device__ __forceinline__ int stream_position(int n0, int at, int N)
 // stale line.  Whoever counts last has every other's sums: each wave waits for
 // its stores before the barrier in front of the count, and reads only after the
 // count has returned.
-__device__ __forceinline__ void meet_store(float* to, float v)
+__device__ __forceinline__ void meet_store(float* to, f32x4 v)
 {
-    __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const u32x4 w = __builtin_bit_cast(u32x4, v);
+    uint64_t* d = (uint64_t*)to;
+    __hip_atomic_store(d, w[0] | (uint64_t)w[1] << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(d + 1, w[2] | (uint64_t)w[3] << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The sum of `n` values `stride` apart, in order from +0, eight in flight.
-__device__ __forceinline__ float meet_sum(const float* from, int n, size_t stride)
+// The sum of `n` quads `stride` values apart, in order from +0, eight in flight.
+__device__ __forceinline__ f32x4 meet_sum(const float* from, int n, size_t stride)
 {
-    float s = 0.0f;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
     for (int g = 0; g < n; g += 8) {
-        float v[8];
+        uint64_t v[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t* p = (const uint64_t*)(from + (size_t)min(g + i, n - 1) * stride);
+            v[i][0] = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v[i][1] = __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = __hip_atomic_load(from + (size_t)min(g + i, n - 1) * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += g + i < n ? v[i] : 0.0f;
+            if (g + i < n)
+                s = add4(s, __builtin_bit_cast(f32x4, u32x4{(uint32_t)v[i][0], (uint32_t)(v[i][0] >> 32), (uint32_t)v[i][1],
+                                                            (uint32_t)(v[i][1] >> 32)}));
     }
     return s;
 }

@@ -30,7 +30,7 @@ template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 {
     using S = W4Stream<FL, DW>;
-    constexpr int CPL = S::CPL, CB = S::CB;
+    constexpr int CPL = S::CPL, CB = S::CB, QUADS = CB / 4;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ int flag;
     // neighbouring tiles on one XCD: they share a block of columns
@@ -50,32 +50,30 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
     acc.clear();
     S::run(p.w, p.K, p.N, n0, rows, u0, u1, acc);
 
-    auto finish = [&](int m, int n_block, int at, float s) {
-        const int col = stream_position<CPL>(n_block, at, p.N);
+    auto finish = [&](int m, int n_block, int q, f32x4 s) {
+        const int col = stream_position<CPL>(n_block, q, p.N);
         if (col < 0) return;
-        const float b = p.bias ? half_at(p.bias + col) : 0.0f;
-        p.c[(size_t)m * p.N + col] = to_half(activate(s * p.alpha + b, p.act));
+        const f32x4 b = p.bias ? half4_at(p.bias, col, p.N) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = activate(s[i] * p.alpha + b[i], p.act);
+        put_half4(p.c + (size_t)m * p.N, col, p.N, s);
     };
     stream_put<CPL>(lds + wave * 16 * CB, acc);
     __syncthreads();
     const size_t wide = (size_t)p.blocks_n * CB;
-#pragma unroll 1
-    for (int u = threadIdx.x; u < rows_here * CB; u += kStreamThreads) {
-        const int m = u / CB, at = u % CB;
-        const float s = stream_sum<CPL>(lds, kStreamWaves, m, at);
-        if (p.parts > 1) meet_store(p.part + ((size_t)part * p.M + m0 + m) * wide + n0 + at, s);
-        else finish(m0 + m, n0, at, s);
+    const int m = threadIdx.x / QUADS, q = threadIdx.x % QUADS;
+    if (m < rows_here) {
+        const f32x4 s = stream_sum<CPL>(lds, kStreamWaves, m, q);
+        if (p.parts > 1) meet_store(p.part + ((size_t)part * p.M + m0 + m) * wide + n0 + 4 * q, s);
+        else finish(m0 + m, n0, q, s);
     }
     if (p.parts == 1) return;
     const int t0 = tile / p.per * p.per, t1 = min(t0 + p.per, p.blocks_m * p.blocks_n);
     if (!meet_last(p.count + tile / p.per, (uint32_t)((t1 - t0) * p.parts), &flag)) return;
     for (int t = t0; t < t1; ++t) {
         const int tm0 = t % p.blocks_m * 16, tn0 = t / p.blocks_m * CB;
-#pragma unroll 1
-        for (int u = threadIdx.x; u < min(16, p.M - tm0) * CB; u += kStreamThreads) {
-            const int m = tm0 + u / CB, at = u % CB;
-            finish(m, tn0, at, meet_sum(p.part + (size_t)m * wide + tn0 + at, p.parts, (size_t)p.M * wide));
-        }
+        if (tm0 + m < p.M && m < 16)
+            finish(tm0 + m, tn0, q, meet_sum(p.part + (size_t)(tm0 + m) * wide + tn0 + 4 * q, p.parts, (size_t)p.M * wide));
     }
 }
 
