@@ -215,27 +215,25 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
         if (count > 0) stream_put<CPL>(lds + wave * 16 * CB, acc);
         __syncthreads();
 #pragma unroll 1
-        for (int c = 0; c < cg; ++c) {
-            const int n0 = block_of[c << kl], ex = expert_of[c << kl], here = count_of[c << kl];
-            const float* slices = lds + (c << kl) * 16 * CB;
-#pragma unroll 1
-            for (int u = threadIdx.x; u < here * QUADS; u += kStreamThreads) {
-                const int m = u / QUADS, q = u % QUADS, col = stream_position<CPL>(n0, q, p.F);
-                if (col < 0) continue;
-                const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-                f32x4 v = add4(stream_sum<CPL>(slices + (kg - half) * 16 * CB, half, m, q),
-                               p.up.bias ? half4_at(p.up.bias + (size_t)ex * p.F, col, p.F) : none);
-                if constexpr (GATED) {
-                    const f32x4 g = add4(stream_sum<CPL>(slices, half, m, q),
-                                         p.gate.bias ? half4_at(p.gate.bias + (size_t)ex * p.F, col, p.F) : none);
+        for (int u = threadIdx.x; u < cg * 16 * QUADS; u += kStreamThreads) {
+            const int c = u / (16 * QUADS) << kl, m = u / QUADS % 16, q = u % QUADS;
+            if (m >= count_of[c]) continue;
+            const int ex = expert_of[c], col = stream_position<CPL>(block_of[c], q, p.F);
+            const float* slices = lds + c * 16 * CB;
+            if (col < 0) continue;
+            const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+            f32x4 v = add4(stream_sum<CPL>(slices + (kg - half) * 16 * CB, half, m, q),
+                           p.up.bias ? half4_at(p.up.bias + (size_t)ex * p.F, col, p.F) : none);
+            if constexpr (GATED) {
+                const f32x4 g = add4(stream_sum<CPL>(slices, half, m, q),
+                                     p.gate.bias ? half4_at(p.gate.bias + (size_t)ex * p.F, col, p.F) : none);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] *= stream_activate(g[i], p.act);
-                } else {
+                for (int i = 0; i < 4; ++i) v[i] *= stream_activate(g[i], p.act);
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = stream_activate(v[i], p.act);
-                }
-                put_half4(p.hidden + (size_t)plan.slot[c << kl][m] * p.hidden_wide, col, p.F, v);
+                for (int i = 0; i < 4; ++i) v[i] = stream_activate(v[i], p.act);
             }
+            put_half4(p.hidden + (size_t)plan.slot[c][m] * p.hidden_wide, col, p.F, v);
         }
         __syncthreads();
     }

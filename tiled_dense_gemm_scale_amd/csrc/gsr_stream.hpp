@@ -292,19 +292,32 @@ __device__ __forceinline__ int stream_position(int n0, int q, int N)
     return n0 + CPL * l < N ? stream_column<CPL>(n0, l, N) + 4 * q % CPL : -1;
 }
 
-// Four fp16 values of a row of N from column `col` on (zeros past N), and back.
+// Four fp16 values of a row of N from column `col` on (zeros past N), and back;
+// one access where N is a multiple of four, as `col` is then too.
 __device__ __forceinline__ f32x4 half4_at(const uint16_t* row, int col, int N)
 {
-    f32x4 v;
+    u32x2 w = {0u, 0u};
+    if ((N & 3) == 0) {
+        w = *(const u32x2_at2*)(row + col);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = col + i < N ? (float)__builtin_bit_cast(_Float16, row[col + i]) : 0.0f;
-    return v;
+        for (int i = 0; i < 4; ++i)
+            if (col + i < N) w[i / 2] |= (uint32_t)row[col + i] << (16 * (i & 1));
+    }
+    const half4 h = __builtin_bit_cast(half4, w);
+    return f32x4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
 }
 __device__ __forceinline__ void put_half4(uint16_t* row, int col, int N, f32x4 v)
 {
+    const half4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    const u32x2 w = __builtin_bit_cast(u32x2, h);
+    if ((N & 3) == 0) {
+        *(u32x2_at2*)(row + col) = w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (col + i < N) row[col + i] = __builtin_bit_cast(uint16_t, (_Float16)v[i]);
+        for (int i = 0; i < 4; ++i)
+            if (col + i < N) row[col + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
 }
 
 // ---- sums that meet in a workspace ---------------------------------------------------
