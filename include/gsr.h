@@ -430,12 +430,13 @@ typedef struct gsr_weights {
  *   x        T x H;  up, gate  experts of H x F;  down  experts of F x O
  *   weights  T x k binary32, or NULL (ones)
  *   activation  any gsr_activation
- * Sums, biases, activation, gate and weights are binary32; h is rounded to
- * binary16 between the launches and out once at the end.  j is added in
- * ascending order: equal inputs give equal bits.  Either all matrices are
+ * Sums, biases, activation, gate and weights are binary32; h is kept to within
+ * 2^-22 between the launches (an infinity beyond binary16's range) and out rounded
+ * once.  A token's choices are added in an order that the ids alone decide: equal
+ * inputs give equal bits.  Either all matrices are
  * binary16 or all are 4-bit, gate and up of one group.  Values are row-major at
  * any 2-byte alignment (codes 4).  T <= 64, T k <= 1024, experts <= 1024, widths
- * below 2^22 (GSR_ERROR_TOO_LARGE); for more tokens there are gsr_group_rows and
+ * below 2^22, T k F below 2^29 with F in whole eights (GSR_ERROR_TOO_LARGE); for more tokens there are gsr_group_rows and
  * the grouped products.
  *   workspace  gsr_expert_few_workspace_bytes(T, k, experts, F, O) bytes,
  *              16-byte aligned, counters as gemm_scale_bias_act_ws's (its first

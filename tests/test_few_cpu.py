@@ -93,7 +93,7 @@ W4DOWN = (FAKE + 5 * MB, FAKE + 6 * MB, 0, 0, 64)
     (dict(tokens=-1), 1), (dict(k=-1), 1), (dict(experts=-1), 1), (dict(H=-1), 1), (dict(F=-1), 1), (dict(O=-1), 1),
     (dict(id_bytes=2), 1), (dict(activation=4), 1), (dict(activation=-1), 1), (dict(wsb=-1), 1), (dict(wsb=512), 1),
     (dict(tokens=65), 2), (dict(k=257), 2), (dict(experts=1025), 2), (dict(H=2 ** 22), 2), (dict(F=2 ** 22), 2),
-    (dict(O=2 ** 22), 2), (dict(k=2 ** 62), 2), (dict(k=256, F=2 ** 20), 2), (dict(x=0), 1), (dict(ids=0), 1), (dict(out=0), 1), (dict(ws=0), 1),
+    (dict(O=2 ** 22), 2), (dict(k=2 ** 62), 2), (dict(k=256, F=2 ** 19), 2), (dict(x=0), 1), (dict(ids=0), 1), (dict(out=0), 1), (dict(ws=0), 1),
     (dict(up=(0, 0, 0, 0, 0)), 1), (dict(down=(0, 0, 0, 0, 0)), 1), (dict(gate=(0, 0, 0, 0, 0)), 1),
     (dict(x=FAKE + 1), 1), (dict(ids=FAKE + MB + 2), 1), (dict(ids=FAKE + MB + 4, id_bytes=8), 1),
     (dict(weights=FAKE + 2 * MB + 2), 1), (dict(out=FAKE + 7 * MB + 1), 1), (dict(ws=FAKE + 8 * MB + 8), 1),

@@ -1,6 +1,6 @@
 """GPU tests of the few-token layer of routed experts against its definition in
 64 bits on the host: whole numbers bit for bit, normal values within the bound
-of their sums and of the hidden values' rounding."""
+of their sums."""
 import numpy as np
 import pytest
 import torch

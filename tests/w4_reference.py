@@ -106,7 +106,8 @@ def layer(x, ids, weights, up, gate, down, biases, act):
                 g, dg = product(gate, "gate")
                 a, da = act64(g, act), act_slack(dg, g, act)
                 h, dh = a * u, da * np.abs(u) + du * np.abs(a) + da * du + 2.0 ** -24 * np.abs(a * u)
-            dh = dh + half_step(np.abs(h) + dh)
+            # h travels as two fp16 values: 2^-22 of it, 2^-25 at least
+            dh = dh + np.maximum((np.abs(h) + dh) * 2.0 ** -22, 2.0 ** -25)
             hidden.append(h)
             w = 1.0 if weights is None else float(weights[t, j])
             b = np.zeros(O) if biases.get("down") is None else biases["down"][e]

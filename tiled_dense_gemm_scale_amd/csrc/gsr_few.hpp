@@ -19,7 +19,8 @@
 //    part of F, weigh their rows and add them per token in LDS, in order of the
 //    experts.  The workgroups of a block meet in the workspace and the last one
 //    adds their sums in order, so equal inputs give equal bits.
-// h is rounded to fp16 between the launches, as the fp16 matrix cores take it.
+// Between the launches h is two fp16 values, rounded and what that lost, as the
+// matrix cores take it: one rounding to fp16 would be as large as that of out.
 #pragma once
 
 #include "gsr_stream.hpp"
@@ -45,7 +46,7 @@ struct FewArgs {
     const float* weights;  // T x k, or null (ones)
     FewWeights up, gate, down;
     uint16_t* out;         // T x O
-    uint16_t* hidden;      // slots x hidden_wide
+    uint16_t* hidden;      // slots x 2 x hidden_wide
     float* part;           // groups x T x part_wide
     uint32_t* count;
     int T, k, slots, experts, H, F, O;
@@ -61,8 +62,8 @@ struct FewArgs {
 // The stream of a form of weights: fp16, 4 bits with groups of 32, 64, and 128 or
 // more rows.  DW: every row of fp16 weights and of A starts on a dword.
 enum : int { kFewHalf = 0, kFewW4x1 = 1, kFewW4x2 = 2, kFewW4x4 = 3 };
-template <int FORM, bool DW>
-struct FewStream : W4Stream<FORM == kFewW4x1 ? 1 : FORM == kFewW4x2 ? 2 : 4, DW> {
+template <int FORM, bool DW, bool SPLIT>
+struct FewStream : W4Stream<FORM == kFewW4x1 ? 1 : FORM == kFewW4x2 ? 2 : 4, DW, SPLIT> {
     __device__ static __forceinline__ W4Matrix matrix(const FewWeights& w, int e, int K, int N)
     {
         const size_t words = (size_t)((K + 7) / 8) * N, groups = (size_t)((((int64_t)K - 1) >> w.glog2) + 1) * N;
@@ -70,8 +71,8 @@ struct FewStream : W4Stream<FORM == kFewW4x1 ? 1 : FORM == kFewW4x2 ? 2 : 4, DW>
                         w.glog2};
     }
 };
-template <bool DW>
-struct FewStream<kFewHalf, DW> : HalfStream<DW> {
+template <bool DW, bool SPLIT>
+struct FewStream<kFewHalf, DW, SPLIT> : HalfStream<DW, SPLIT> {
     __device__ static __forceinline__ HalfMatrix matrix(const FewWeights& w, int e, int K, int N)
     {
         return HalfMatrix{(const uint16_t*)w.data + (size_t)e * K * N};
@@ -182,7 +183,7 @@ __device__ __forceinline__ int few_split(int items, int waves_log2, int units, i
 template <int FORM, bool DW, bool GATED>
 __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
 {
-    using S = FewStream<FORM, DW>;
+    using S = FewStream<FORM, DW, false>;
     constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, QUADS = CB / 4, SETS = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ FewPlan plan;
@@ -233,7 +234,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = stream_activate(v[i], p.act);
             }
-            put_half4(p.hidden + (size_t)plan.slot[c][m] * p.hidden_wide, col, p.F, v);
+            uint16_t* row = p.hidden + (size_t)plan.slot[c][m] * 2 * p.hidden_wide;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < p.F) {
+                    const StreamHalves h = stream_split(v[i]);
+                    row[S::order(col + i)] = h.hi;
+                    row[p.hidden_wide + S::order(col + i)] = h.lo;
+                }
+            if (col + 4 >= p.F)  // zeros up to the width
+                for (int i = p.F; i < p.hidden_wide; ++i) row[S::order(i)] = row[p.hidden_wide + S::order(i)] = (uint16_t)0;
         }
         __syncthreads();
     }
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
 template <int FORM, int TOKENS, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
 {
-    using S = FewStream<FORM, DW>;
+    using S = FewStream<FORM, DW, true>;
     constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, QUADS = CB / 4;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ f32x4 sums[TOKENS * QUADS];
@@ -283,8 +293,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
                 token_of[wave][count] = -1;
                 bias_of[wave] = p.down.bias && part == 0 ? e : -1;
             }
-            typename S::Rows rows(p.hidden, (uint64_t)p.slots * (uint32_t)p.hidden_wide * 2u);
-            rows.row((uint32_t)plan.slot[wave][min(l, count - 1)] * (uint32_t)p.hidden_wide);
+            typename S::Rows rows(p.hidden, (uint64_t)p.slots * (uint32_t)p.hidden_wide * 4u);
+            rows.wide = p.hidden_wide;
+            rows.row((uint32_t)plan.slot[wave][min(l, count - 1)] * 2u * (uint32_t)p.hidden_wide);
             acc.clear();
             S::run(S::matrix(p.down, e, p.F, p.O), p.F, p.O, n0, rows, (int)((uint32_t)(units * part) / (uint32_t)parts),
                    (int)((uint32_t)(units * (part + 1)) / (uint32_t)parts), acc);  // 2^17 units, 2^7 parts at most

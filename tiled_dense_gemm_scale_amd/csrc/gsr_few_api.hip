@@ -21,7 +21,7 @@ bool bad_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F, int64_t O)
 bool large_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F, int64_t O)
 {
     return T > gsr::kFewTokens || k > gsr::kFewSlots || T * k > gsr::kFewSlots || E > gsr::kFewExperts ||
-           H >= kStreamWidth || F >= kStreamWidth || O >= kStreamWidth || T * k * (cdiv(F, 8) * 8) >= ((int64_t)1 << 30);
+           H >= kStreamWidth || F >= kStreamWidth || O >= kStreamWidth || T * k * (cdiv(F, 8) * 8) >= ((int64_t)1 << 29);
 }
 
 struct Plan {
@@ -34,7 +34,7 @@ constexpr int64_t kFewGrid = 256;
 
 Plan plan_of(bool w4, int64_t T, int64_t k, int64_t E, int64_t F, int64_t O)
 {
-    const int64_t CB = w4 ? gsr::W4Stream<1, true>::CB : gsr::HalfStream<true>::CB;
+    const int64_t CB = w4 ? gsr::W4Stream<1, true, false>::CB : gsr::HalfStream<true, false>::CB;
     Plan g;
     // tiles at most: one per expert that is hit, and one for each 16 slots more
     const int64_t slots = T * k, most = std::max<int64_t>(1, std::min(slots, std::min(E, slots) + slots / gsr::kFewRows));
@@ -47,7 +47,7 @@ Plan plan_of(bool w4, int64_t T, int64_t k, int64_t E, int64_t F, int64_t O)
     g.per = (int)cdiv(g.blocks, gsr::kMeetCounters);
     g.hidden_wide = cdiv(F, 8) * 8;
     g.part_wide = g.blocks * CB;
-    g.hidden_bytes = slots * g.hidden_wide * 2;
+    g.hidden_bytes = slots * g.hidden_wide * 4;  // two halves
     g.bytes = gsr::kMeetBytes + g.hidden_bytes + (g.groups > 1 ? g.groups * T * g.part_wide * 4 : 0);
     return g;
 }

@@ -81,11 +81,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dword_rsrc(const void* at, uin
 // The row of A that a lane reads, the l-th of 16, of a table of less than 2^31
 // bytes.  Rows past the last are that one again, whose sums nobody takes, and
 // loads behind the table are zeros: no load is masked, and lanes with one address
-// are one access.  DW: every row starts on a dword.
+// are one access.  DW: every row starts on a dword.  A table can also hold
+// values as two halves, the value rounded and what that lost (stream_split); each
+// of a row's halves is `wide` values long, zeros at the end, the second behind the
+// first, and in the order of k that the stream multiplies in.
 template <bool DW>
 struct StreamRows {
     __amdgpu_buffer_rsrc_t rs;
     uint32_t off;
+    int wide = 0;
 
     __device__ __forceinline__ StreamRows(const uint16_t* table, uint64_t bytes) { rs = dword_rsrc(table, bytes, off); }
     __device__ __forceinline__ void row(uint32_t at) { off += 2u * at; }  // `at` values into the table
@@ -96,6 +100,18 @@ struct StreamRows {
         else return load8_shifted(rs, o);
     }
 };
+
+// v as two fp16 values whose sum is within 2^-22 of it (an infinity alone).
+struct StreamHalves {
+    uint16_t hi, lo;
+};
+__device__ __forceinline__ StreamHalves stream_split(float v)
+{
+    const _Float16 hi = (_Float16)v;
+    const float rest = v - (float)hi;
+    return StreamHalves{__builtin_bit_cast(uint16_t, hi),
+                        __builtin_bit_cast(uint16_t, (_Float16)(fabsf((float)hi) <= 65504.0f ? rest : 0.0f))};
+}
 
 // The first n of eight values, zeros for the others.
 __device__ __forceinline__ u32x4 first8(u32x4 v, int n)
@@ -156,15 +172,17 @@ struct HalfMatrix {
 };
 
 // DW: every row starts on a dword (N even, b on one), and every row of A.
-template <bool DW>
+// SPLIT: A in halves.
+template <bool DW, bool SPLIT>
 struct HalfStream {
+    static __device__ __forceinline__ int order(int k) { return k; }  // where k lies in a row of halves
     static constexpr int CPL = 8, CB = 16 * CPL, UNIT = kStep;  // UNIT: k of the smallest run
     typedef StreamSums<CPL> Sums;
     typedef StreamRows<DW> Rows;
 
     struct Step {
         u32x4 b[8];
-        u32x4 a;
+        u32x4 a[SPLIT ? 2 : 1];
     };
     struct Place {
         const uint16_t* b;
@@ -187,24 +205,26 @@ struct HalfStream {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s.b[i] = load8_shifted(rs, p.off[i] + behind);
         }
-        s.a = rows.load(k0 + 8 * p.g);
+        s.a[0] = rows.load(k0 + 8 * p.g);
+        if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + k0 + 8 * p.g);
         __builtin_amdgcn_sched_barrier(0);
     }
 
     // Zeros for what lies past K on both sides (behind a row of A lies the next
     // one, and the last row of B may share its last dword with other values).
-    __device__ static __forceinline__ void cut(Step& s, const Place& p, int k0)
+    __device__ static __forceinline__ void cut(Step& s, const Place& p, const Rows& rows, int k0)
     {
         const int n = p.K - k0 - 8 * p.g;
-        s.a = first8(s.a, n);
+#pragma unroll
+        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) s.a[h] = first8(s.a[h], SPLIT ? rows.wide - k0 - 8 * p.g : n);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i >= n) s.b[i] = u32x4{0u, 0u, 0u, 0u};
     }
 
-    __device__ static __forceinline__ void multiply(Step& s, const Place& p, int u, Sums& acc)
+    __device__ static __forceinline__ void multiply(Step& s, const Place& p, const Rows& rows, int u, Sums& acc, Sums& low)
     {
-        if ((u + 1) * kStep > p.K) cut(s, p, u * kStep);
+        if ((u + 1) * kStep > p.K) cut(s, p, rows, u * kStep);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {  // columns 2d and 2d + 1
             u32x4 even, odd;
@@ -213,8 +233,12 @@ struct HalfStream {
                 even[e] = pack_lo(s.b[2 * e][d], s.b[2 * e + 1][d]);
                 odd[e] = pack_hi(s.b[2 * e][d], s.b[2 * e + 1][d]);
             }
-            acc.v[2 * d] = mfma16(s.a, even, acc.v[2 * d]);
-            acc.v[2 * d + 1] = mfma16(s.a, odd, acc.v[2 * d + 1]);
+            acc.v[2 * d] = mfma16(s.a[0], even, acc.v[2 * d]);
+            acc.v[2 * d + 1] = mfma16(s.a[0], odd, acc.v[2 * d + 1]);
+            if constexpr (SPLIT) {
+                low.v[2 * d] = mfma16(s.a[1], even, low.v[2 * d]);
+                low.v[2 * d + 1] = mfma16(s.a[1], odd, low.v[2 * d + 1]);
+            }
             __builtin_amdgcn_sched_barrier(0);  // a pair's values live no longer than it
         }
     }
@@ -233,14 +257,15 @@ struct HalfStream {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p.off[i] = 2u * ((uint32_t)(8 * p.g + i) * (uint32_t)N + (uint32_t)p.c);
         if (u0 >= u1) return;
+        Sums low;
+        low.clear();
         if (N >= CPL) {
             stream_ring<Step>(
                 u1 - u0, [&](Step& s, int i) { load(s, p, rows, u0 + i, u1); },
-                [&](Step& s, int i) { multiply(s, p, u0 + i, acc); });
-            return;
+                [&](Step& s, int i) { multiply(s, p, rows, u0 + i, acc, low); });
         }
 #pragma unroll 1
-        for (int u = u0; u < u1; ++u) {  // fewer columns than a lane's: value by value
+        for (int u = N >= CPL ? u1 : u0; u < u1; ++u) {  // fewer columns than a lane's: value by value
             Step s{};
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
@@ -249,9 +274,18 @@ struct HalfStream {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) s.b[x] = x == i ? v : s.b[x];
             }
-            s.a = rows.load(u * kStep + 8 * p.g);
-            multiply(s, p, u, acc);
+            s.a[0] = rows.load(u * kStep + 8 * p.g);
+            if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + u * kStep + 8 * p.g);
+            multiply(s, p, rows, u, acc, low);
         }
+        // The second halves' sums apart: where a weight is infinite the first
+        // halves' alone are the formula's (zero times infinity, and halves of
+        // two signs, would make NaN of them).
+        if constexpr (SPLIT)
+#pragma unroll
+            for (int j = 0; j < CPL; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc.v[j][r] += fabsf(acc.v[j][r]) < __builtin_inff() ? low.v[j][r] : 0.0f;
     }
 };
 

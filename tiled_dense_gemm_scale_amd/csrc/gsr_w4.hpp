@@ -56,16 +56,18 @@ __device__ __forceinline__ u32x4 w4_order(u32x4 a)
 // are cut at multiples of 128 rows; a group's sum of products is kept apart and
 // scaled in fp32 when the group (or, of larger ones, 128 rows of it) ends, so
 // the weights are never rounded.  FL: steps between such ends (1, 2 or 4).  DW: every row of A starts on a
-// dword.
-template <int FL, bool DW>
+// dword.  SPLIT: A in halves, which lie in the codes' order.
+template <int FL, bool DW, bool SPLIT>
 struct W4Stream {
+    static __device__ __forceinline__ int order(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
+    static __device__ __forceinline__ u32x4 ordered(u32x4 a) { return SPLIT ? a : w4_order(a); }
     static constexpr int CPL = 4, CB = 16 * CPL, STEPS = 4, UNIT = STEPS * kStep, ENDS = STEPS / FL, DEPTH = 2;
     typedef StreamSums<CPL> Sums;
     typedef StreamRows<DW> Rows;
 
     struct Batch {
         u32x4 w[STEPS];
-        u32x4 a[STEPS];
+        u32x4 a[SPLIT ? 2 : 1][STEPS];
         u32x2 s[ENDS];
         uint32_t z[ENDS];
     };
@@ -90,7 +92,10 @@ struct W4Stream {
             t.z[e] = *(const u32_at1*)(p.zeros + row + p.c);
         }
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) t.a[i] = rows.load(k0 + i * kStep + 8 * p.g);
+        for (int i = 0; i < STEPS; ++i) {
+            t.a[0][i] = rows.load(k0 + i * kStep + 8 * p.g);
+            if constexpr (SPLIT) t.a[1][i] = rows.load(rows.wide + k0 + i * kStep + 8 * p.g);
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -113,12 +118,15 @@ struct W4Stream {
         }
     }
 
-    __device__ static __forceinline__ void multiply(Batch& t, const Place& p, int u, Sums& acc)
+    __device__ static __forceinline__ void multiply(Batch& t, const Place& p, const Rows& rows, int u, Sums& acc)
     {
         const int left = p.K - u * UNIT;
         if (left < UNIT) {  // behind a row of A lies the next one
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) t.a[i] = first8(t.a[i], left - i * kStep - 8 * p.g);
+            for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                for (int h = 0; h < (SPLIT ? 2 : 1); ++h)
+                    t.a[h][i] = first8(t.a[h][i], (SPLIT ? rows.wide - u * UNIT : left) - i * kStep - 8 * p.g);
         }
 #pragma unroll
         for (int e = 0; e < ENDS; ++e) {
@@ -128,10 +136,13 @@ struct W4Stream {
             f32x4 sum[CPL];
 #pragma unroll
             for (int i = 0; i < FL; ++i) {
-                const u32x4 a = w4_order(t.a[e * FL + i]);
+                const u32x4 a = ordered(t.a[0][e * FL + i]);
 #pragma unroll
-                for (int j = 0; j < CPL; ++j)
-                    sum[j] = mfma16(a, w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]), i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j]);
+                for (int j = 0; j < CPL; ++j) {
+                    const u32x4 b = w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]);
+                    sum[j] = mfma16(a, b, i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j]);
+                    if constexpr (SPLIT) sum[j] = mfma16(t.a[1][e * FL + i], b, sum[j]);
+                }
                 __builtin_amdgcn_sched_barrier(0);  // a step's values live no longer than it
             }
 #pragma unroll
@@ -159,10 +170,15 @@ struct W4Stream {
             zeros |= (uint32_t)(in ? p.zeros[row + p.c + j] : (uint8_t)0) << (8 * j);
         }
         scale_of(v, u32x2{join16(s[0], s[1]), join16(s[2], s[3])}, zeros, p.m.zeros != nullptr);
-        const u32x4 a = w4_order(first8(rows.load(k0 + 8 * p.g), p.K - k0 - 8 * p.g));
+        const int n = (SPLIT ? rows.wide : p.K) - k0 - 8 * p.g;
+        const u32x4 a = ordered(first8(rows.load(k0 + 8 * p.g), n));
+        u32x4 a2 = {0u, 0u, 0u, 0u};
+        if constexpr (SPLIT) a2 = first8(rows.load(rows.wide + k0 + 8 * p.g), n);
 #pragma unroll
         for (int j = 0; j < CPL; ++j) {
-            const f32x4 sum = mfma16(a, w4_values(w[j], v.lo[j], v.hi[j]), f32x4{0.f, 0.f, 0.f, 0.f});
+            const u32x4 b = w4_values(w[j], v.lo[j], v.hi[j]);
+            f32x4 sum = mfma16(a, b, f32x4{0.f, 0.f, 0.f, 0.f});
+            if constexpr (SPLIT) sum = mfma16(a2, b, sum);
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc.v[j][x] = fmaf(v.s[j], sum[x], acc.v[j][x]);
         }
@@ -192,7 +208,7 @@ struct W4Stream {
         if (N >= CPL) {
             stream_ring<Batch>(
                 u1 - u0, [&](Batch& t, int i) { load(t, p, rows, u0 + i, u1); },
-                [&](Batch& t, int i) { multiply(t, p, u0 + i, acc); });
+                [&](Batch& t, int i) { multiply(t, p, rows, u0 + i, acc); });
             return;
         }
 #pragma unroll 1

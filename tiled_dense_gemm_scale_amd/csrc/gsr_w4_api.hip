@@ -60,7 +60,7 @@ bool dense_pays(int64_t M, int64_t N, int64_t K, bool vec)
 // aligned: A and C let the dense product take its 128-bit path.
 GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int64_t bytes, bool aligned)
 {
-    constexpr int CB = gsr::W4Stream<1, true>::CB, UNIT = gsr::W4Stream<1, true>::UNIT;
+    constexpr int CB = gsr::W4Stream<1, true, false>::CB, UNIT = gsr::W4Stream<1, true, false>::UNIT;
     GemmPlan g;
     const int64_t units = cdiv(K, UNIT), values = gsr::kMeetBytes + 2 * K * N;
     g.blocks_m = cdiv(M, 16);

@@ -29,7 +29,7 @@ struct W4Gemm {
 template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 {
-    using S = W4Stream<FL, DW>;
+    using S = W4Stream<FL, DW, false>;
     constexpr int CPL = S::CPL, CB = S::CB, QUADS = CB / 4;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ int flag;
