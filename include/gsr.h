@@ -376,7 +376,8 @@ int64_t gsr_adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t ran
 int gsr_quantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group, const void* B,
                     uint32_t* codes, void* scales, uint8_t* zeros, void* stream);
 
-/* B = the weights' values, each rounded once to binary16. */
+/* B = the weights' values, each rounded once to binary16 (an infinity beyond its
+ * range: 65504 in a group comes back as one, its scale 65504 / 7 being rounded up). */
 int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group,
                       const uint32_t* codes, const void* scales, const uint8_t* zeros, void* B,
                       void* stream);
@@ -433,11 +434,11 @@ typedef struct gsr_weights {
  * Sums, biases, activation, gate and weights are binary32; h is kept to within
  * 2^-22 between the launches (an infinity beyond binary16's range) and out rounded
  * once.  A token's choices are added in an order that the ids alone decide: equal
- * inputs give equal bits.  Either all matrices are
- * binary16 or all are 4-bit, gate and up of one group.  Values are row-major at
- * any 2-byte alignment (codes 4).  T <= 64, T k <= 1024, experts <= 1024, widths
- * below 2^22, T k F below 2^29 with F in whole eights (GSR_ERROR_TOO_LARGE); for more tokens there are gsr_group_rows and
- * the grouped products.
+ * inputs give equal bits.  Either all matrices are binary16 or all are 4-bit, gate
+ * and up of one group.  Values are row-major at any 2-byte alignment (codes 4).
+ * T <= 64, T k <= 1024, experts <= 1024, widths below 2^22, T k F below 2^29 with F
+ * in whole eights (GSR_ERROR_TOO_LARGE); for more tokens there are gsr_group_rows
+ * and the grouped products.
  *   workspace  gsr_expert_few_workspace_bytes(T, k, experts, F, O) bytes,
  *              16-byte aligned, counters as gemm_scale_bias_act_ws's (its first
  *              512 bytes zero before the first call and again after each), one

@@ -23,7 +23,7 @@ def test_reference_packing():
 
 QUANT = dict(matrices=1, K=64, N=16, group=32, B=FAKE, codes=FAKE + MB, scales=FAKE + 2 * MB, zeros=FAKE + 3 * MB)
 BAD = [(dict(matrices=-1), 1), (dict(K=-1), 1), (dict(N=-1), 1), (dict(group=0), 1), (dict(group=16), 1), (dict(group=48), 1),
-       (dict(group=2 ** 31), 1), (dict(matrices=2 ** 31), 2), (dict(K=2 ** 22), 2), (dict(N=2 ** 22), 2), (dict(B=0), 1),
+       (dict(group=2 ** 31), 1), (dict(matrices=2 ** 31), 2), (dict(matrices=2 ** 22, K=2 ** 21, N=2 ** 21), 2), (dict(K=2 ** 22), 2), (dict(N=2 ** 22), 2), (dict(B=0), 1),
        (dict(codes=0), 1), (dict(scales=0), 1), (dict(B=FAKE + 1), 1), (dict(codes=FAKE + MB + 2), 1),
        (dict(scales=FAKE + 2 * MB + 1), 1), (dict(codes=FAKE + 2044), 1), (dict(scales=FAKE + 2046), 1),
        (dict(zeros=FAKE + 2047), 1),

@@ -299,8 +299,8 @@ def test_agrees_with_the_layer_for_many_tokens(gsr):
     ws = gsr.new_workspace(gsr.expert_few_workspace_bytes(T, k, E, F, H))
     say("few beside expert_mlp")
     a, b = gsr.expert_mlp_few(x, ids, score, up, down, ws), gsr.expert_mlp(x, ids, score, up, down)
-    # both round h to fp16 from sums in other orders (one step of h, 2^-10) and the
-    # output once (half a step each); h's share of the output adds up over F
+    # the other one rounds h to fp16 (half a step, 2^-11, whose share of the output
+    # adds up over F), and both the output (half a step each)
     assert float((a - b).float().norm() / b.float().norm()) < 2.0 ** -10
     wu, wd, wp = gsr.quantize_w4(up), gsr.quantize_w4(down, 64, zeros=True), gsr.quantize_w4(proj, 32)
     y = gsr.gemm_w4(x, wp, ws, activation="none")
@@ -311,3 +311,95 @@ def test_agrees_with_the_layer_for_many_tokens(gsr):
     # independent roundings keeps; three products and the rounding of y and h
     assert float((y - y2).float().norm() / y2.float().norm()) < 2.0 ** -10
     assert float((z - z2).float().norm() / z2.float().norm()) < 2.0 ** -8
+
+
+def test_hidden_values_past_fp16(gsr):
+    """An h that fp16 does not hold becomes an infinity, of its own token's slot
+    alone; one just below stays, its rounding's rest with it."""
+    H, F, O = 8, 40, 24
+    x = torch.zeros(3, H, dtype=torch.float16, device=DEV)
+    x[0, 0], x[1, 0], x[2, 0] = 60000.0, 64000.0, -64000.0
+    up = torch.zeros(1, H, F, dtype=torch.float16, device=DEV)
+    up[0, 0, 0], up[0, 0, 1] = 1.0009765625, 1.0
+    down = torch.zeros(1, F, O, dtype=torch.float16, device=DEV)
+    down[0, 0], down[0, 1] = 2.0 ** -4, -(2.0 ** -4)
+    ids = torch.zeros(3, 1, dtype=torch.int32, device=DEV)
+    up[0, 0, 2] = 1.125  # 67500, 72000, -72000
+    ws = gsr.new_workspace(gsr.expert_few_workspace_bytes(3, 1, 1, F, O))
+    say("few past fp16")
+    got = gsr.expert_mlp_few(x, ids, None, up, down, ws, activation="none").cpu().numpy()
+    # the row of the overflowed h is zero in down: infinity times zero
+    assert np.isnan(got).all()
+    up[0, 0, 2] = 0.0
+    got = gsr.expert_mlp_few(x, ids, None, up, down, ws, activation="none").cpu().numpy()
+    # h0 - h1 = x 2^-10, a multiple of h's last bit only with the second half
+    want = np.array([60000.0, 64000.0, -64000.0]) * 2.0 ** -14
+    assert np.array_equal(got, np.repeat(want.astype(np.float16)[:, None], O, 1))
+
+
+@pytest.mark.parametrize("form", ["fp16", "w4z"])
+def test_two_layers_at_once(gsr, form):
+    """Calls on two streams with a workspace each, many times over."""
+    case, other = (16, 4, 12, 264, 1100, 520, 0.1, 64), (3, 2, 8, 64, 700, 300, 0.0, 32)
+    calls = []
+    for c in (case, other):
+        x, ids, w, hs, fs, biases = case_inputs(gsr, c, form, False, True, True, seed=4)
+        T, k, E, H, F, O, drop, group = c
+        X, I, W, B = dev(x), dev(ids.astype(np.int64)), dev(w), {n: dev(b) for n, b in biases.items()}
+        ws, out, s = workspace(gsr, c), torch.empty(T, O, dtype=torch.float16, device=DEV), torch.cuda.Stream()
+        calls.append((lambda X=X, I=I, W=W, hs=hs, B=B, ws=ws, out=out, s=s: gsr.expert_mlp_few(
+            X, I, W, hs["up"], hs["down"], ws, gate=hs["gate"], bias_up=B["up"], bias_gate=B["gate"], bias_down=B["down"],
+            activation="silu", out=out, stream=s), out, s))
+    say(f"few two streams {form}")
+    wants = []
+    for go, out, s in calls:
+        go()
+        torch.cuda.synchronize()
+        wants.append(out.clone())
+    for _ in range(5):
+        for go, out, s in calls:
+            with torch.cuda.stream(s):
+                out.fill_(9.0)
+        for _ in range(20):
+            for go, out, s in calls:
+                go()
+        torch.cuda.synchronize()
+        for (go, out, s), want in zip(calls, wants):
+            assert torch.equal(out, want)
+
+
+def test_every_expert_and_slot(gsr):
+    """1024 slots of 1024 experts, and one token of 1024 choices."""
+    for case in ((64, 16, 1024, 24, 33, 40, 0.0, 32), (1, 1024, 1024, 24, 40, 33, 0.0, 32)):
+        x, ids, w, hs, fs, biases = case_inputs(gsr, case, "w4z", True, False, False)
+        w[:] = 2.0 ** -3 if case[0] == 1 else w  # keeps the output in fp16's whole numbers
+        out, _, _ = ref.layer(x.astype(np.float64), ids, w, fs["up"], None, fs["down"], {}, "none")
+        say(f"few every expert {case}")
+        got = call(gsr, x, ids, w, hs, biases, "none", workspace(gsr, case)).cpu().numpy()
+        with np.errstate(over="ignore"):
+            assert np.array_equal(got, out.astype(np.float16))
+
+
+def test_matrices_past_32_bits(gsr):
+    """A stack of more than 2^33 values: quantized, given back and multiplied, its
+    matrices' bits are those of the same matrices by themselves."""
+    E, K, N, O = 700, 4096, 4096, 64
+    b = torch.empty(E, K, N, dtype=torch.float16, device=DEV).normal_()
+    down = torch.empty(E, N, O, dtype=torch.float16, device=DEV).normal_()
+    say("few past 32 bits: quantize")
+    w, wd = gsr.quantize_w4(b, 64, zeros=True), gsr.quantize_w4(down, 32)
+    back = gsr.dequantize_w4(w)
+    pick = [333, 699]
+    few, fewd = b[pick].contiguous(), down[pick].contiguous()
+    v, vd = gsr.quantize_w4(few, 64, zeros=True), gsr.quantize_w4(fewd, 32)
+    for i, e in enumerate(pick):
+        assert torch.equal(w.codes[e], v.codes[i]) and torch.equal(w.scales[e], v.scales[i]) and torch.equal(w.zeros[e], v.zeros[i])
+        assert torch.equal(back[e], gsr.dequantize_w4(gsr.W4(v.codes[i], v.scales[i], v.zeros[i], K, 64)))
+    x = torch.randn(1, K, device=DEV).half() * K ** -0.5
+    ids, near = torch.tensor([pick], dtype=torch.int32, device=DEV), torch.tensor([[0, 1]], dtype=torch.int32, device=DEV)
+    ws = gsr.new_workspace(gsr.expert_few_workspace_bytes(1, 2, E, N, O))
+    for big, bigd, small, smalld in ((b, down, few, fewd), (w, wd, v, vd)):
+        say("few past 32 bits: layer")
+        got = gsr.expert_mlp_few(x, ids, None, big, bigd, ws, gate=big, activation="silu")
+        want = gsr.expert_mlp_few(x, near, None, small, smalld, ws, gate=small, activation="silu")
+        assert torch.equal(got, want) and bool(torch.isfinite(got).all()) and bool(got.count_nonzero())

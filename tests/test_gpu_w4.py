@@ -300,6 +300,56 @@ def test_empty_products(gsr):
     assert tuple(gsr.gemm_w4(torch.empty(0, 40, dtype=torch.float16, device=DEV), handle(gsr, q, s, z, 40, 32)).shape) == (0, 5)
 
 
+def test_output_past_2_31_bytes(gsr):
+    """C of more than 2^31 bytes, with the weights' values in the workspace (the
+    rows then in runs below that) and without a workspace: whole numbers."""
+    M, N, K, group = 70001, 16384, 64, 32
+    rng = np.random.default_rng(2)
+    q, s, z = weights(rng, K, N, group, True, True)
+    w = handle(gsr, q, s, z, K, group)
+    a = torch.randint(-2, 3, (M, K), device=DEV).half()
+    f = torch.from_numpy(ref.values(q, s, z, group)).to(DEV).float()
+    nbytes = gsr.w4_workspace_bytes(M, N, K)
+    assert nbytes == 512 + 2 * K * N
+    c = torch.empty(M, N, dtype=torch.float16, device=DEV)
+    for ws in (gsr.new_workspace(nbytes), None):
+        say(f"w4 large output workspace={ws is not None}")
+        c.fill_(9.0)
+        gsr.gemm_w4(a, w, ws, alpha=0.5, activation="none", c=c)
+        for m in range(0, M, 10000):
+            want = ((a[m:m + 10000].float() @ f) * 0.5).half()
+            assert torch.equal(c[m:m + 10000], want), m
+
+
+def test_captured_product_of_many_rows(gsr):
+    """The weights' values and the dense product in a graph, replayed on new rows
+    and new weights beside eager calls in the same workspace."""
+    M, N, K, group = 600, 2048, 1024, 128
+    rng = np.random.default_rng(5)
+    q, s, z = weights(rng, K, N, group, True, False)
+    w = handle(gsr, q, s, z, K, group)
+    ws = gsr.new_workspace(max(gsr.w4_workspace_bytes(M, N, K), gsr.w4_workspace_bytes(4, N, K)))
+    a, c = torch.randn(M, K, device=DEV).half(), torch.empty(M, N, dtype=torch.float16, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gsr.gemm_w4(a, w, ws, c=c, activation="gelu", alpha=0.1, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    say("w4 capture of many rows")
+    with torch.cuda.graph(graph, stream=side):
+        gsr.gemm_w4(a, w, ws, c=c, activation="gelu", alpha=0.1)
+    for i in range(4):
+        a.copy_(torch.randn(M, K, device=DEV).half())
+        w.codes.random_(-2 ** 31, 2 ** 31 - 1)
+        want = gsr.gemm_w4(a, w, ws, activation="gelu", alpha=0.1)
+        gsr.gemm_w4(a[:4].contiguous(), w, ws)
+        c.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c, want), i
+    assert int(ws[:512].count_nonzero()) == 0
+
+
 def test_streams_graphs_and_shared_workspace(gsr):
     """A captured call replays with the eager bits on new inputs, beside eager
     calls of other shapes and of the split product in the same workspace."""

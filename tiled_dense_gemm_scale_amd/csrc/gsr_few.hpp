@@ -56,7 +56,6 @@ struct FewArgs {
     int blocks_up;         // column blocks of the first launch
     int waves_log2;        // its waves (a power of two)
     int blocks, groups;    // of the second: column blocks, workgroups to each
-    int per;               // column blocks per counter
 };
 
 // The stream of a form of weights: fp16, 4 bits with groups of 32, 64, and 128 or
@@ -328,20 +327,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
         __syncthreads();
     }
 
-    auto finish = [&](int u, int n_block, f32x4 s) {
-        const int col = stream_position<CPL>(n_block, u % QUADS, p.O);
+    auto finish = [&](int u, f32x4 s) {
+        const int col = stream_position<CPL>(n0, u % QUADS, p.O);
         if (col >= 0) put_half4(p.out + (size_t)(u / QUADS) * p.O, col, p.O, s);
     };
     for (int u = tid; u < p.T * QUADS; u += kStreamThreads) {
-        if (p.groups == 1) finish(u, n0, sums[u]);
+        if (p.groups == 1) finish(u, sums[u]);
         else meet_store(p.part + ((size_t)group * p.T + u / QUADS) * p.part_wide + n0 + 4 * (u % QUADS), sums[u]);
     }
     if (p.groups == 1) return;
-    const int b0 = nb / p.per * p.per, b1 = min(b0 + p.per, p.blocks);
-    if (!meet_last(p.count + nb / p.per, (uint32_t)((b1 - b0) * p.groups), &flag)) return;
-    for (int b = b0; b < b1; ++b)
-        for (int u = tid; u < p.T * QUADS; u += kStreamThreads)
-            finish(u, b * CB, meet_sum(p.part + (size_t)(u / QUADS) * p.part_wide + b * CB + 4 * (u % QUADS), p.groups, (size_t)p.T * p.part_wide));
+    if (!meet_last(p.count + nb, (uint32_t)p.groups, &flag)) return;
+    for (int u = tid; u < p.T * QUADS; u += kStreamThreads)
+        finish(u, meet_sum(p.part + (size_t)(u / QUADS) * p.part_wide + n0 + 4 * (u % QUADS), p.groups, (size_t)p.T * p.part_wide));
 }
 
 }  // namespace gsr

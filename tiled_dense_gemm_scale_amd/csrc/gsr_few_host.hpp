@@ -52,7 +52,8 @@ inline uint64_t w4_scale_count(uint64_t matrices, int64_t K, int64_t N, int64_t 
 constexpr int64_t kStreamWidth = (int64_t)1 << 22;
 
 // `units` of K over parts so that `tiles` tiles make about `workgroups`, each
-// keeping `least` units.
+// keeping `least` units.  With 256 workgroups tiles of more than one part are at
+// most 128, one to a counter.
 struct Parts {
     int parts, chunk;
 };

@@ -404,8 +404,7 @@ __device__ __forceinline__ bool meet_last(uint32_t* count, uint32_t all, int* fl
     return *flag != 0;
 }
 
-// Column blocks share the 128 counters that every workspace starts with: block
-// b counts in b / per, per blocks to a counter.
+// Every workspace starts with 128 counters.
 constexpr int kMeetCounters = 128;
 constexpr int64_t kMeetBytes = 4 * kMeetCounters;
 

@@ -19,7 +19,9 @@ constexpr int64_t kLimit = (int64_t)1 << 31;
 int check_matrix(int64_t matrices, int64_t K, int64_t N, int64_t group)
 {
     if (matrices < 0 || K < 0 || N < 0 || group_log2(group) < 0) return GSR_ERROR_INVALID_VALUE;
-    if (matrices >= kLimit || K >= gsr::host::kStreamWidth || N >= gsr::host::kStreamWidth) return GSR_ERROR_TOO_LARGE;
+    if (matrices >= kLimit || K >= gsr::host::kStreamWidth || N >= gsr::host::kStreamWidth ||
+        (K > 0 && N > 0 && matrices > ((int64_t)1 << 56) / (K * N)))
+        return GSR_ERROR_TOO_LARGE;
     return GSR_SUCCESS;
 }
 
@@ -38,7 +40,7 @@ constexpr int64_t kGridY = 32768;
 
 struct GemmPlan {
     bool dense;  // the weights' values in the workspace, then the dense product
-    int parts, chunk, per;
+    int parts, chunk;
     int64_t blocks_m, blocks_n, bytes;
 };
 
@@ -73,7 +75,6 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int64_t bytes, bool aligned)
     if (bytes >= 0 && need(p.parts) > bytes) p = Parts{1, (int)std::max<int64_t>(units, 1)};
     g.parts = p.parts;
     g.chunk = p.chunk;
-    g.per = (int)cdiv(tiles, gsr::kMeetCounters);
     g.bytes = g.dense ? values : need(p.parts);
     return g;
 }
@@ -188,7 +189,6 @@ int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, int64
     p.blocks_n = (int)g.blocks_n;
     p.parts = g.parts;
     p.chunk = g.chunk;
-    p.per = g.per;
     p.count = (uint32_t*)workspace;
     p.part = (float*)((uint8_t*)workspace + gsr::kMeetBytes);
     const int64_t grid = cdiv(g.blocks_m * g.blocks_n * g.parts, 8) * 8;

@@ -16,14 +16,13 @@ struct W4Gemm {
     float alpha;
     int blocks_m, blocks_n;  // tiles of the launch
     int parts, chunk;        // parts of K, of `chunk` units each
-    int per;                 // tiles per counter
     float* part;             // parts x M x (blocks_n CB)
     uint32_t* count;
 };
 
 // A tile of 16 rows and 64 columns, whose workgroup's waves split its K, or a
 // part of it: then the tile's sums meet in the workspace and the workgroup that
-// comes last of a counter's tiles adds them.  One block of rows is bound by the
+// comes last adds them.  One block of rows is bound by the
 // codes' bytes and the chain of launch, loads and sums; more of them run beside
 // each other and read the codes again, from the caches.
 template <int FL, bool DW>
@@ -50,31 +49,27 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
     acc.clear();
     S::run(p.w, p.K, p.N, n0, rows, u0, u1, acc);
 
-    auto finish = [&](int m, int n_block, int q, f32x4 s) {
-        const int col = stream_position<CPL>(n_block, q, p.N);
+    const int m = threadIdx.x / QUADS, q = threadIdx.x % QUADS;
+    auto finish = [&](f32x4 s) {
+        const int col = stream_position<CPL>(n0, q, p.N);
         if (col < 0) return;
         const f32x4 b = p.bias ? half4_at(p.bias, col, p.N) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = activate(s[i] * p.alpha + b[i], p.act);
-        put_half4(p.c + (size_t)m * p.N, col, p.N, s);
+        put_half4(p.c + (size_t)(m0 + m) * p.N, col, p.N, s);
     };
     stream_put<CPL>(lds + wave * 16 * CB, acc);
     __syncthreads();
     const size_t wide = (size_t)p.blocks_n * CB;
-    const int m = threadIdx.x / QUADS, q = threadIdx.x % QUADS;
+    float* meet = p.part + (size_t)(m0 + m) * wide + n0 + 4 * q;
     if (m < rows_here) {
         const f32x4 s = stream_sum<CPL>(lds, kStreamWaves, m, q);
-        if (p.parts > 1) meet_store(p.part + ((size_t)part * p.M + m0 + m) * wide + n0 + 4 * q, s);
-        else finish(m0 + m, n0, q, s);
+        if (p.parts > 1) meet_store(meet + (size_t)part * p.M * wide, s);
+        else finish(s);
     }
     if (p.parts == 1) return;
-    const int t0 = tile / p.per * p.per, t1 = min(t0 + p.per, p.blocks_m * p.blocks_n);
-    if (!meet_last(p.count + tile / p.per, (uint32_t)((t1 - t0) * p.parts), &flag)) return;
-    for (int t = t0; t < t1; ++t) {
-        const int tm0 = t % p.blocks_m * 16, tn0 = t / p.blocks_m * CB;
-        if (tm0 + m < p.M && m < 16)
-            finish(tm0 + m, tn0, q, meet_sum(p.part + (size_t)(tm0 + m) * wide + tn0 + 4 * q, p.parts, (size_t)p.M * wide));
-    }
+    if (!meet_last(p.count + tile, (uint32_t)p.parts, &flag)) return;
+    if (m < rows_here) finish(meet_sum(meet, p.parts, (size_t)p.M * wide));
 }
 
 // ---- quantizing --------------------------------------------------------------------
