@@ -112,8 +112,9 @@ int gsr_quantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group, const
                                        dim3(256), (hipStream_t)stream, p));
     const bool longer = group > 128;
     const dim3 grid((unsigned)cdiv(N, 256), (unsigned)std::min(matrices * (longer ? p.groups : cdiv(K, 128)), kGridY));
-    return status_of(launch_kernel(longer ? gsr::w4_quantize_kernel<true> : gsr::w4_quantize_kernel<false>, grid, dim3(256),
-                                   (hipStream_t)stream, p));
+    const auto f = zeros ? (longer ? gsr::w4_quantize_kernel<true, true> : gsr::w4_quantize_kernel<false, true>)
+                         : (longer ? gsr::w4_quantize_kernel<true, false> : gsr::w4_quantize_kernel<false, false>);
+    return status_of(launch_kernel(f, grid, dim3(256), (hipStream_t)stream, p));
 }
 
 int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group, const uint32_t* codes, const void* scales,

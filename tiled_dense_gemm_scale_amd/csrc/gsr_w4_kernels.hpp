@@ -107,10 +107,51 @@ struct W4Step {
         const float t = v * r;
         return fmaf(fmaf(-t, s, v), r, t);
     }
-    __device__ __forceinline__ uint32_t code(float v) const
+    // The codes of eight values as a word, each added in by one shift-and-add: the
+    // quotient between -z and 15 - z plus 3 2^22 is a float whose bits are
+    // 0x4b400000 and the quotient rounded to even; what eight of those bits and
+    // zero points make is added at the end.
+    template <class Value>
+    __device__ __forceinline__ uint32_t word(Value&& value) const
     {
-        const int q = (int)rintf(quotient(v)) + z;
-        return live ? (uint32_t)min(max(q, 0), 15) : (uint32_t)z;
+        const float least = (float)-z, most = (float)(15 - z);
+        uint32_t w = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = __builtin_amdgcn_fmed3f(quotient(value(i)), least, most) + 12582912.0f;
+            w += __builtin_bit_cast(uint32_t, q) << (4 * i);
+        }
+        return live ? w + ((uint32_t)z - 0x4b400000u) * 0x11111111u : 0x88888888u;
+    }
+};
+
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+
+// Four columns' least and largest values, two to a register, and the largest of
+// their bits without the sign: of an infinity or a NaN 0x7c00 or more.
+template <bool ZEROS>
+struct W4Range {
+    half2v lo[2] = {}, hi[2] = {};
+    ushort2v top[2] = {};
+    // Column j's least and largest value, a NaN as the least for such a one.
+    __device__ __forceinline__ void get(int j, float& least, float& most) const
+    {
+        const uint16_t t = top[j / 2][j & 1];
+        const float size = (float)__builtin_bit_cast(_Float16, t);
+        least = t >= 0x7c00u ? __builtin_nanf("") : ZEROS ? (float)lo[j / 2][j & 1] : -size;
+        most = ZEROS ? (float)hi[j / 2][j & 1] : size;
+    }
+    __device__ __forceinline__ void take(u32x2 v)
+    {
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            const uint32_t w = v[d];
+            top[d] = __builtin_elementwise_max(top[d], __builtin_bit_cast(ushort2v, w & 0x7fff7fffu));
+            if constexpr (ZEROS) {
+                lo[d] = __builtin_elementwise_min(lo[d], __builtin_bit_cast(half2v, w));
+                hi[d] = __builtin_elementwise_max(hi[d], __builtin_bit_cast(half2v, w));
+            }
+        }
     }
 };
 
@@ -118,7 +159,7 @@ struct W4Step {
 // the four waves of a workgroup have 128 rows, one to four groups, and tell each
 // other their largest values through LDS.  Larger groups are walked 128 rows at
 // a time, twice (LONG).
-template <bool LONG>
+template <bool LONG, bool ZEROS>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
 {
     __shared__ u32x4 least[4][64], most[4][64];  // four columns: lo, hi as floats
@@ -142,27 +183,20 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
                 if (k >= k_end) v[i] = u32x2{0u, 0u};
             }
         };
-        float lo[4] = {}, hi[4] = {};
-        bool odd[4] = {};
+        W4Range<ZEROS> range;
         for (int64_t k0 = k_span; k0 < k_end; k0 += 128) {
             load(k0);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint16_t h = (uint16_t)(v[i][j / 2] >> (16 * (j & 1)));
-                    const float x = (float)__builtin_bit_cast(_Float16, h);
-                    odd[j] |= (h & 0x7c00u) == 0x7c00u;
-                    lo[j] = fminf(lo[j], x);
-                    hi[j] = fmaxf(hi[j], x);
-                }
+            for (int i = 0; i < 32; ++i) range.take(v[i]);
         }
         __syncthreads();  // the last span's values are read
         u32x4 put_lo, put_hi;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // an infinity or a NaN travels as a NaN
-            put_lo[j] = odd[j] ? 0x7fc00000u : __builtin_bit_cast(uint32_t, lo[j]);
-            put_hi[j] = __builtin_bit_cast(uint32_t, hi[j]);
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            range.get(j, lo, hi);
+            put_lo[j] = __builtin_bit_cast(uint32_t, lo);
+            put_hi[j] = __builtin_bit_cast(uint32_t, hi);
         }
         least[wave][lane] = put_lo;
         most[wave][lane] = put_hi;
@@ -181,27 +215,25 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
                 ghi[j] = fmaxf(ghi[j], __builtin_bit_cast(float, (uint32_t)d[j]));
             }
         }
-        const W4Step st[4] = {{glo[0], ghi[0], godd[0], p.zeros != nullptr}, {glo[1], ghi[1], godd[1], p.zeros != nullptr},
-                              {glo[2], ghi[2], godd[2], p.zeros != nullptr}, {glo[3], ghi[3], godd[3], p.zeros != nullptr}};
+        const W4Step st[4] = {{glo[0], ghi[0], godd[0], ZEROS}, {glo[1], ghi[1], godd[1], ZEROS},
+                              {glo[2], ghi[2], godd[2], ZEROS}, {glo[3], ghi[3], godd[3], ZEROS}};
         const int64_t group = (LONG ? k_span : k_span + 32 * wave) >> p.glog2;
         if (live && wave == w0 && group < p.groups) {
             const size_t at = ((size_t)e * p.groups + group) * p.N + c;
             *(u32x2_at2*)(p.scales + at) = u32x2{join16(st[0].bits, st[1].bits), join16(st[2].bits, st[3].bits)};
-            if (p.zeros)
+            if (ZEROS)
                 *(u32_at1*)(p.zeros + at) = (uint32_t)st[0].z | (uint32_t)st[1].z << 8 | (uint32_t)st[2].z << 16 | (uint32_t)st[3].z << 24;
         }
         for (int64_t k0 = k_span; k0 < k_end; k0 += 128) {
             if (LONG) load(k0);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                u32x4 w = {0u, 0u, 0u, 0u};
+                u32x4 w;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint16_t h = (uint16_t)(v[8 * x + i][j / 2] >> (16 * (j & 1)));
-                        w[j] |= st[j].code((float)__builtin_bit_cast(_Float16, h)) << (4 * i);
-                    }
+                for (int j = 0; j < 4; ++j)
+                    w[j] = st[j].word([&](int i) {
+                        return (float)__builtin_bit_cast(_Float16, (uint16_t)(v[8 * x + i][j / 2] >> (16 * (j & 1))));
+                    });
                 const int64_t row = k0 / 8 + 4 * wave + x;
                 if (live && row < words) *(u32x4_at4*)(p.codes + ((size_t)e * words + row) * p.N + c) = w;
             }
@@ -266,9 +298,8 @@ __global__ void __launch_bounds__(256) w4_quantize_narrow_kernel(W4Convert p)
         p.scales[i] = st.bits;
         if (p.zeros) p.zeros[i] = (uint8_t)st.z;
         for (int64_t k = k0; k < k1; k += 8) {
-            uint32_t w = 0;
-            for (int x = 0; x < 8; ++x) w |= st.code(k + x < k1 ? half_at(b + (size_t)(k + x) * p.N) : 0.0f) << (4 * x);
-            p.codes[((size_t)e * words + k / 8) * p.N + n] = w;
+            p.codes[((size_t)e * words + k / 8) * p.N + n] =
+                st.word([&](int x) { return k + x < k1 ? half_at(b + (size_t)(k + x) * p.N) : 0.0f; });
         }
     }
 }
