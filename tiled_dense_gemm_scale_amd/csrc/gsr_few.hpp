@@ -87,12 +87,6 @@ struct FewPlan {
     int16_t slot[kStreamWaves][kFewRows];  // the slots of a wave's tile, ascending
 };
 
-__device__ __forceinline__ void wave_fence()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // Fills key and upto; returns the tiles.
 __device__ __forceinline__ int few_plan(FewPlan& s, const FewArgs& p)
 {
@@ -187,7 +181,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
     __shared__ FewPlan plan;
     __shared__ int expert_of[kStreamWaves], block_of[kStreamWaves], count_of[kStreamWaves];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int items = few_plan(plan, p) * p.blocks_up, units = (p.H + UNIT - 1) / UNIT;
     const int kl = few_split(items, p.waves_log2, units, 256 / UNIT, SETS - 1), kg = 1 << kl, cg = kStreamWaves >> kl;
     const int turn = wave & (kg - 1), half = kg / SETS;  // the waves of one matrix
@@ -203,9 +197,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
             at = few_item(plan, p.experts, item, p.blocks_up);
             count = few_rows(plan.slot[wave], plan.key, p.slots, at.e, at.tile);
             typename S::Rows rows(p.x, (uint64_t)p.T * (uint32_t)p.H * 2u);
-            rows.row((uint32_t)plan.slot[wave][min(l, count - 1)] / (uint32_t)p.k * (uint32_t)p.H);
+            rows.row((uint32_t)plan.slot[wave][min(stream_row(), count - 1)] / (uint32_t)p.k * (uint32_t)p.H);
             acc.clear();
-            S::run(S::matrix(w, at.e, p.H, p.F), p.H, p.F, at.turn * CB, rows, u0, u1, acc);
+            S::run(S::matrix(w, at.e, p.H, p.F), p.H, p.F, at.turn * CB, rows, u0, u1, lds + wave * 16 * CB, acc);
         }
         if ((threadIdx.x & 63) == 0) {
             expert_of[wave] = at.e;
@@ -265,13 +259,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
     __shared__ float weight_of[kStreamWaves][kFewRows];
     __shared__ int bias_of[kStreamWaves];  // the expert whose bias a wave's rows get, or -1
     __shared__ int flag;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 15;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nb = blockIdx.x / p.groups, group = blockIdx.x - nb * p.groups, n0 = nb * CB;
     for (int i = tid; i < p.T * QUADS; i += kStreamThreads) sums[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (tid < TOKENS) mask[0][tid] = mask[1][tid] = 0u;
     const int tiles = few_plan(plan, p), units = (p.F + UNIT - 1) / UNIT;
-    // every wave of the block has a job where that leaves each 256 rows of F
-    const int parts = max(1, min(p.groups * kStreamWaves / max(tiles, 1), units * UNIT / 256)), jobs = tiles * parts;
+    // every wave of the block has a job where that leaves each 128 rows of F
+    const int parts = max(1, min(p.groups * kStreamWaves / max(tiles, 1), units * UNIT / 128)), jobs = tiles * parts;
     const int j0 = jobs * group / p.groups, j1 = jobs * (group + 1) / p.groups;
 
     int turn = 0;
@@ -294,10 +288,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
             }
             typename S::Rows rows(p.hidden, (uint64_t)p.slots * (uint32_t)p.hidden_wide * 4u);
             rows.wide = p.hidden_wide;
-            rows.row((uint32_t)plan.slot[wave][min(l, count - 1)] * 2u * (uint32_t)p.hidden_wide);
+            rows.row((uint32_t)plan.slot[wave][min(stream_row(), count - 1)] * 2u * (uint32_t)p.hidden_wide);
             acc.clear();
             S::run(S::matrix(p.down, e, p.F, p.O), p.F, p.O, n0, rows, (int)((uint32_t)(units * part) / (uint32_t)parts),
-                   (int)((uint32_t)(units * (part + 1)) / (uint32_t)parts), acc);  // 2^17 units, 2^7 parts at most
+                   (int)((uint32_t)(units * (part + 1)) / (uint32_t)parts), lds + wave * 16 * CB, acc);  // 2^17 units, 2^7 parts at most
             stream_put<CPL>(lds + wave * 16 * CB, acc);
         }
         __syncthreads();

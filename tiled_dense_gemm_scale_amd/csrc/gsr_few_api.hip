@@ -42,9 +42,9 @@ Plan plan_of(bool w4, int64_t T, int64_t k, int64_t E, int64_t F, int64_t O)
     // as many workgroups as items, up to a power of two of them
     for (g.grid_up = 1, g.waves_log2 = 3; g.grid_up < kFewGrid && g.grid_up < g.blocks_up * most; g.grid_up *= 2) ++g.waves_log2;
     g.blocks = (int)cdiv(O, CB);
-    // a job is a tile and 256 rows of F at least, eight to a workgroup; at most
+    // a job is a tile and 128 rows of F at least, eight to a workgroup; at most
     // 128 blocks have more than one workgroup, and so a counter each
-    g.groups = (int)std::max<int64_t>(1, std::min({(int64_t)16, kFewGrid / std::max(g.blocks, 1), cdiv(most * cdiv(F, 256), gsr::kStreamWaves)}));
+    g.groups = (int)std::max<int64_t>(1, std::min({(int64_t)16, kFewGrid / std::max(g.blocks, 1), cdiv(most * cdiv(F, 128), gsr::kStreamWaves)}));
     g.hidden_wide = cdiv(F, 8) * 8;
     g.part_wide = g.blocks * CB;
     g.hidden_bytes = slots * g.hidden_wide * 4;  // two halves

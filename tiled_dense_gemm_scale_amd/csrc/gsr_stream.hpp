@@ -78,8 +78,35 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dword_rsrc(const void* at, uin
     return make_rsrc((const uint8_t*)at - behind, (uint32_t)min((bytes + behind + 3u) & ~(uint64_t)3, (uint64_t)0x7ffffffcu));
 }
 
-// The row of A that a lane reads, the l-th of 16, of a table of less than 2^31
-// bytes.  Rows past the last are that one again, whose sums nobody takes, and
+// A lane's place in the loads of A: lane t reads the eight values 8 c .. 8 c + 7
+// of the t / 4-th of 16 rows, c = t % 4 ^ t / 16, so that four lanes next to each
+// other read 64 bytes next to each other.  (As the matrix cores take A, row t % 16
+// and run t / 16, each lane's 16 bytes are an access of their own, three in four of
+// all: 64 tokens x 2 of 8 experts in 4 bits TURNED.)  stream_turn brings them
+// into that order through the wave's LDS; with that c no two lanes meet in a bank.
+__device__ __forceinline__ int stream_row() { return (int)(threadIdx.x & 63) >> 2; }
+__device__ __forceinline__ int stream_run() { return (int)(threadIdx.x & 3) ^ (int)((threadIdx.x >> 4) & 3); }
+
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int STEPS>
+__device__ __forceinline__ void stream_turn(u32x4 (&a)[STEPS], float* slice)
+{
+    const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+    u32x4* s = (u32x4*)slice;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) s[64 * i + lane] = a[i];
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) a[i] = s[64 * i + 4 * l + (g ^ (l >> 2))];
+    wave_fence();
+}
+
+// The row of A that a lane reads, of a table of less than 2^31 bytes.  Rows past the last are that one again, whose sums nobody takes, and
 // loads behind the table are zeros: no load is masked, and lanes with one address
 // are one access.  DW: every row starts on a dword.  A table can also hold
 // values as two halves, the value rounded and what that lost (stream_split); each
@@ -186,7 +213,8 @@ struct HalfStream {
     };
     struct Place {
         const uint16_t* b;
-        int K, N, c, g;
+        float* slice;
+        int K, N, c, g, run;
         uint32_t off[8];  // bytes from a step's first row
     };
 
@@ -205,8 +233,8 @@ struct HalfStream {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s.b[i] = load8_shifted(rs, p.off[i] + behind);
         }
-        s.a[0] = rows.load(k0 + 8 * p.g);
-        if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + k0 + 8 * p.g);
+        s.a[0] = rows.load(k0 + 8 * p.run);
+        if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + k0 + 8 * p.run);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -224,6 +252,7 @@ struct HalfStream {
 
     __device__ static __forceinline__ void multiply(Step& s, const Place& p, const Rows& rows, int u, Sums& acc, Sums& low)
     {
+        stream_turn(s.a, p.slice);
         if ((u + 1) * kStep > p.K) cut(s, p, rows, u * kStep);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {  // columns 2d and 2d + 1
@@ -243,13 +272,16 @@ struct HalfStream {
         }
     }
 
-    // acc += A[:, k] B[k, :] over the units u0 <= u < u1 of 32 k
+    // acc += A[:, k] B[k, :] over the units u0 <= u < u1 of 32 k; slice: this wave's
+    // LDS, 16 x CB floats
     __device__ static __forceinline__ void run(const HalfMatrix& m, int K, int N, int n0, const Rows& rows, int u0, int u1,
-                                               Sums& acc)
+                                               float* slice, Sums& acc)
     {
         const int lane = threadIdx.x & 63;
         Place p;
         p.b = m.b;
+        p.slice = slice;
+        p.run = stream_run();
         p.K = K;
         p.N = N;
         p.g = lane >> 4;
@@ -274,8 +306,8 @@ struct HalfStream {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) s.b[x] = x == i ? v : s.b[x];
             }
-            s.a[0] = rows.load(u * kStep + 8 * p.g);
-            if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + u * kStep + 8 * p.g);
+            s.a[0] = rows.load(u * kStep + 8 * p.run);
+            if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + u * kStep + 8 * p.run);
             multiply(s, p, rows, u, acc, low);
         }
         // The second halves' sums apart: where a weight is infinite the first

@@ -61,7 +61,7 @@ template <int FL, bool DW, bool SPLIT>
 struct W4Stream {
     static __device__ __forceinline__ int order(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
     static __device__ __forceinline__ u32x4 ordered(u32x4 a) { return SPLIT ? a : w4_order(a); }
-    static constexpr int CPL = 4, CB = 16 * CPL, STEPS = 4, UNIT = STEPS * kStep, ENDS = STEPS / FL, DEPTH = 2;
+    static constexpr int CPL = 4, CB = 16 * CPL, STEPS = 4, UNIT = STEPS * kStep, ENDS = STEPS / FL;
     typedef StreamSums<CPL> Sums;
     typedef StreamRows<DW> Rows;
 
@@ -74,7 +74,8 @@ struct W4Stream {
     struct Place {
         W4Matrix m;
         const uint8_t* zeros;  // m.zeros, or any readable bytes of that many
-        int K, N, c, g;
+        float* slice;
+        int K, N, c, g, run;
         uint32_t off[STEPS];   // bytes from a unit's first row of words
     };
 
@@ -93,8 +94,8 @@ struct W4Stream {
         }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            t.a[0][i] = rows.load(k0 + i * kStep + 8 * p.g);
-            if constexpr (SPLIT) t.a[1][i] = rows.load(rows.wide + k0 + i * kStep + 8 * p.g);
+            t.a[0][i] = rows.load(k0 + i * kStep + 8 * p.run);
+            if constexpr (SPLIT) t.a[1][i] = rows.load(rows.wide + k0 + i * kStep + 8 * p.run);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -121,6 +122,8 @@ struct W4Stream {
     __device__ static __forceinline__ void multiply(Batch& t, const Place& p, const Rows& rows, int u, Sums& acc)
     {
         const int left = p.K - u * UNIT;
+#pragma unroll
+        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) stream_turn(t.a[h], p.slice);
         if (left < UNIT) {  // behind a row of A lies the next one
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
@@ -171,9 +174,13 @@ struct W4Stream {
         }
         scale_of(v, u32x2{join16(s[0], s[1]), join16(s[2], s[3])}, zeros, p.m.zeros != nullptr);
         const int n = (SPLIT ? rows.wide : p.K) - k0 - 8 * p.g;
-        const u32x4 a = ordered(first8(rows.load(k0 + 8 * p.g), n));
+        u32x4 held[SPLIT ? 2 : 1];
+        held[0] = rows.load(k0 + 8 * p.run);
+        if constexpr (SPLIT) held[1] = rows.load(rows.wide + k0 + 8 * p.run);
+        stream_turn(held, p.slice);
+        const u32x4 a = ordered(first8(held[0], n));
         u32x4 a2 = {0u, 0u, 0u, 0u};
-        if constexpr (SPLIT) a2 = first8(rows.load(rows.wide + k0 + 8 * p.g), n);
+        if constexpr (SPLIT) a2 = first8(held[1], n);
 #pragma unroll
         for (int j = 0; j < CPL; ++j) {
             const u32x4 b = w4_values(w[j], v.lo[j], v.hi[j]);
@@ -184,12 +191,14 @@ struct W4Stream {
         }
     }
 
-    __device__ static __forceinline__ Place place(const W4Matrix& m, int K, int N, int n0)
+    __device__ static __forceinline__ Place place(const W4Matrix& m, int K, int N, int n0, float* slice)
     {
         const int lane = threadIdx.x & 63;
         Place p;
         p.m = m;
         p.zeros = m.zeros ? m.zeros : (const uint8_t*)m.scales;  // without zeros its loads are not looked at
+        p.slice = slice;
+        p.run = stream_run();
         p.K = K;
         p.N = N;
         p.g = lane >> 4;
@@ -199,11 +208,12 @@ struct W4Stream {
         return p;
     }
 
-    // acc += A[:, k] w[k, :] over the units u0 <= u < u1 of 128 k
+    // acc += A[:, k] w[k, :] over the units u0 <= u < u1 of 128 k; slice: this
+    // wave's LDS, 16 x CB floats
     __device__ static __forceinline__ void run(const W4Matrix& m, int K, int N, int n0, const Rows& rows,
-                                               int u0, int u1, Sums& acc)
+                                               int u0, int u1, float* slice, Sums& acc)
     {
-        const Place p = place(m, K, N, n0);
+        const Place p = place(m, K, N, n0, slice);
         if (u0 >= u1) return;
         if (N >= CPL) {
             stream_ring<Batch>(

@@ -36,18 +36,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
     const int all = p.blocks_m * p.blocks_n * p.parts, per_xcd = (all + 7) / 8;
     const int id = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
     if (id >= all) return;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = id % p.parts, tile = id / p.parts;
     const int m0 = tile % p.blocks_m * 16, n0 = tile / p.blocks_m * CB, rows_here = min(16, p.M - m0);
 
     typename S::Rows rows(p.a + (size_t)m0 * p.K, (uint64_t)rows_here * (uint32_t)p.K * 2u);
-    rows.row((uint32_t)min(l, rows_here - 1) * (uint32_t)p.K);
+    rows.row((uint32_t)min(stream_row(), rows_here - 1) * (uint32_t)p.K);
     const int units = (p.K + S::UNIT - 1) / S::UNIT;
     const int first = part * p.chunk, here = max(0, min(p.chunk, units - first));
     const int u0 = first + here * wave / kStreamWaves, u1 = first + here * (wave + 1) / kStreamWaves;
     typename S::Sums acc;
     acc.clear();
-    S::run(p.w, p.K, p.N, n0, rows, u0, u1, acc);
+    S::run(p.w, p.K, p.N, n0, rows, u0, u1, lds + wave * 16 * CB, acc);
 
     const int m = threadIdx.x / QUADS, q = threadIdx.x % QUADS;
     auto finish = [&](f32x4 s) {
