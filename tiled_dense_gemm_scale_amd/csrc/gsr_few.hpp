@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
         if (item < items) {
             at = few_item(plan, p.experts, item, p.blocks_up);
             count = few_rows(plan.slot[wave], plan.key, p.slots, at.e, at.tile);
-            typename S::Rows rows(p.x, (uint64_t)p.T * (uint32_t)p.H * 2u);
+            typename S::Rows rows(p.x, (uint64_t)p.T * (uint32_t)p.H * 2u, count);
             rows.row((uint32_t)plan.slot[wave][min(stream_row(), count - 1)] / (uint32_t)p.k * (uint32_t)p.H);
             acc.clear();
             S::run(S::matrix(w, at.e, p.H, p.F), p.H, p.F, at.turn * CB, rows, u0, u1, lds + wave * 16 * CB, acc);
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
                 token_of[wave][count] = -1;
                 bias_of[wave] = p.down.bias && part == 0 ? e : -1;
             }
-            typename S::Rows rows(p.hidden, (uint64_t)p.slots * (uint32_t)p.hidden_wide * 4u);
+            typename S::Rows rows(p.hidden, (uint64_t)p.slots * (uint32_t)p.hidden_wide * 4u, count);
             rows.wide = p.hidden_wide;
             rows.row((uint32_t)plan.slot[wave][min(stream_row(), count - 1)] * 2u * (uint32_t)p.hidden_wide);
             acc.clear();

@@ -117,8 +117,15 @@ struct StreamRows {
     __amdgpu_buffer_rsrc_t rs;
     uint32_t off;
     int wide = 0;
+    int run;   // the lane's place in a step's 32 values, in eights
+    bool turn;
 
-    __device__ __forceinline__ StreamRows(const uint16_t* table, uint64_t bytes) { rs = dword_rsrc(table, bytes, off); }
+    // `count` rows of a tile are looked at (the same in the whole wave)
+    __device__ __forceinline__ StreamRows(const uint16_t* table, uint64_t bytes, int count) : turn(count > 1)
+    {
+        rs = dword_rsrc(table, bytes, off);
+        run = turn ? stream_run() : (int)(threadIdx.x & 63) >> 4;
+    }
     __device__ __forceinline__ void row(uint32_t at) { off += 2u * at; }  // `at` values into the table
     __device__ __forceinline__ u32x4 load(int k) const
     {
@@ -214,7 +221,7 @@ struct HalfStream {
     struct Place {
         const uint16_t* b;
         float* slice;
-        int K, N, c, g, run;
+        int K, N, c, g;
         uint32_t off[8];  // bytes from a step's first row
     };
 
@@ -233,8 +240,8 @@ struct HalfStream {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s.b[i] = load8_shifted(rs, p.off[i] + behind);
         }
-        s.a[0] = rows.load(k0 + 8 * p.run);
-        if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + k0 + 8 * p.run);
+        s.a[0] = rows.load(k0 + 8 * rows.run);
+        if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + k0 + 8 * rows.run);
         __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -252,7 +259,7 @@ struct HalfStream {
 
     __device__ static __forceinline__ void multiply(Step& s, const Place& p, const Rows& rows, int u, Sums& acc, Sums& low)
     {
-        stream_turn(s.a, p.slice);
+        if (rows.turn) stream_turn(s.a, p.slice);
         if ((u + 1) * kStep > p.K) cut(s, p, rows, u * kStep);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {  // columns 2d and 2d + 1
@@ -281,7 +288,6 @@ struct HalfStream {
         Place p;
         p.b = m.b;
         p.slice = slice;
-        p.run = stream_run();
         p.K = K;
         p.N = N;
         p.g = lane >> 4;
@@ -306,8 +312,8 @@ struct HalfStream {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) s.b[x] = x == i ? v : s.b[x];
             }
-            s.a[0] = rows.load(u * kStep + 8 * p.run);
-            if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + u * kStep + 8 * p.run);
+            s.a[0] = rows.load(u * kStep + 8 * rows.run);
+            if constexpr (SPLIT) s.a[1] = rows.load(rows.wide + u * kStep + 8 * rows.run);
             multiply(s, p, rows, u, acc, low);
         }
         // The second halves' sums apart: where a weight is infinite the first

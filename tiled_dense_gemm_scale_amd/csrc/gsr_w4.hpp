@@ -75,7 +75,7 @@ struct W4Stream {
         W4Matrix m;
         const uint8_t* zeros;  // m.zeros, or any readable bytes of that many
         float* slice;
-        int K, N, c, g, run;
+        int K, N, c, g;
         uint32_t off[STEPS];   // bytes from a unit's first row of words
     };
 
@@ -94,8 +94,8 @@ struct W4Stream {
         }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            t.a[0][i] = rows.load(k0 + i * kStep + 8 * p.run);
-            if constexpr (SPLIT) t.a[1][i] = rows.load(rows.wide + k0 + i * kStep + 8 * p.run);
+            t.a[0][i] = rows.load(k0 + i * kStep + 8 * rows.run);
+            if constexpr (SPLIT) t.a[1][i] = rows.load(rows.wide + k0 + i * kStep + 8 * rows.run);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -122,8 +122,9 @@ struct W4Stream {
     __device__ static __forceinline__ void multiply(Batch& t, const Place& p, const Rows& rows, int u, Sums& acc)
     {
         const int left = p.K - u * UNIT;
+        if (rows.turn)
 #pragma unroll
-        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) stream_turn(t.a[h], p.slice);
+            for (int h = 0; h < (SPLIT ? 2 : 1); ++h) stream_turn(t.a[h], p.slice);
         if (left < UNIT) {  // behind a row of A lies the next one
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
@@ -175,9 +176,9 @@ struct W4Stream {
         scale_of(v, u32x2{join16(s[0], s[1]), join16(s[2], s[3])}, zeros, p.m.zeros != nullptr);
         const int n = (SPLIT ? rows.wide : p.K) - k0 - 8 * p.g;
         u32x4 held[SPLIT ? 2 : 1];
-        held[0] = rows.load(k0 + 8 * p.run);
-        if constexpr (SPLIT) held[1] = rows.load(rows.wide + k0 + 8 * p.run);
-        stream_turn(held, p.slice);
+        held[0] = rows.load(k0 + 8 * rows.run);
+        if constexpr (SPLIT) held[1] = rows.load(rows.wide + k0 + 8 * rows.run);
+        if (rows.turn) stream_turn(held, p.slice);
         const u32x4 a = ordered(first8(held[0], n));
         u32x4 a2 = {0u, 0u, 0u, 0u};
         if constexpr (SPLIT) a2 = first8(held[1], n);
@@ -198,7 +199,6 @@ struct W4Stream {
         p.m = m;
         p.zeros = m.zeros ? m.zeros : (const uint8_t*)m.scales;  // without zeros its loads are not looked at
         p.slice = slice;
-        p.run = stream_run();
         p.K = K;
         p.N = N;
         p.g = lane >> 4;

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
     const int part = id % p.parts, tile = id / p.parts;
     const int m0 = tile % p.blocks_m * 16, n0 = tile / p.blocks_m * CB, rows_here = min(16, p.M - m0);
 
-    typename S::Rows rows(p.a + (size_t)m0 * p.K, (uint64_t)rows_here * (uint32_t)p.K * 2u);
+    typename S::Rows rows(p.a + (size_t)m0 * p.K, (uint64_t)rows_here * (uint32_t)p.K * 2u, rows_here);
     rows.row((uint32_t)min(stream_row(), rows_here - 1) * (uint32_t)p.K);
     const int units = (p.K + S::UNIT - 1) / S::UNIT;
     const int first = part * p.chunk, here = max(0, min(p.chunk, units - first));
