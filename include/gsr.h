@@ -390,7 +390,7 @@ int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group,
  * alignment; matrices may be larger than 2^31 bytes, M is below 2^31.  The
  * products A[m,k] (q - zero) are summed in binary32, group by group, and the
  * scale multiplies a group's sum: the weights are not rounded.  Where many rows
- * make it faster (more than 16, commonly from 150 on) and the workspace holds K x N
+ * make it faster (more than 16, commonly from 200 on) and the workspace holds K x N
  * binary16 values, the weights are first written there as gsr_dequantize_w4 gives
  * them, each rounded once to binary16, and multiplied by the dense kernels.
  * A scale that is not finite makes its column's outputs not finite.

@@ -184,7 +184,7 @@ def test_product(gsr, case, act):
     assert (err <= bound).all()
 
 
-@pytest.mark.parametrize("case", [(1025, 2048, 1024, 128), (700, 1000, 4096, 64), (4000, 333, 1001, 32)], ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("case", [(1025, 2048, 1024, 128), (1500, 1000, 4096, 64), (16000, 333, 1001, 32)], ids=lambda c: "x".join(map(str, c)))
 def test_product_of_many_rows(gsr, case):
     """Many rows: the bits of the dense product with the weights' values, and the
     formula's within one more rounding; a workspace too small for the values keeps
@@ -324,7 +324,7 @@ def test_output_past_2_31_bytes(gsr):
 def test_captured_product_of_many_rows(gsr):
     """The weights' values and the dense product in a graph, replayed on new rows
     and new weights beside eager calls in the same workspace."""
-    M, N, K, group = 600, 2048, 1024, 128
+    M, N, K, group = 1100, 2048, 1024, 128
     rng = np.random.default_rng(5)
     q, s, z = weights(rng, K, N, group, True, False)
     w = handle(gsr, q, s, z, K, group)

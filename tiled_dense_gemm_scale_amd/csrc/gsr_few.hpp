@@ -9,10 +9,10 @@
 // choices hit, so there is no sort and no gather in front: every workgroup counts
 // the experts' slots from the ids itself, and every wave finds the slots of its
 // own expert and streams its columns of that expert's matrix past their rows
-// (gsr_stream.hpp), 16 of them: a tile.  An expert of more rows has more tiles,
-// on neighbouring waves, which read its weights from the caches.  How many tiles
-// there are is known on the device only, so the grid is fixed and the waves share
-// out what there is.
+// (gsr_stream.hpp), 16 of them: a tile.  An expert of more rows has more
+// tiles, on neighbouring waves, which read its weights from the caches.  How many
+// tiles there are is known on the device only, so the grid is fixed and the waves
+// share out what there is.
 //  * up: an item is a tile and a block of columns; 1, 2, 4 or 8 waves of a
 //    workgroup split its H, whichever leaves the fewest idle.
 //  * down: a workgroup has a block of columns; its waves take jobs, a tile and a
@@ -20,7 +20,17 @@
 //    experts.  The workgroups of a block meet in the workspace and the last one
 //    adds their sums in order, so equal inputs give equal bits.
 // Between the launches h is two fp16 values, rounded and what that lost, as the
-// matrix cores take it: one rounding to fp16 would be as large as that of out.
+// matrix cores take it: one rounding to fp16 would be as large as that of out, and
+// the error of out against 64 bits 0.00029 in place of 0.00021, its own rounding's
+// (64 tokens x 2 of 8 in 4 bits 129 us so and 154 with both halves, before A was
+// read as it is now; the others within 2 us).
+// Measured: 4096 -> 11008 -> 4096, 2 of 8 experts, one token: 361 MB in fp16 in 77
+// us (36 and 40 of them the launches' own), in 4 bits 93 MB in 36 us (16 and 19, of
+// which the ids, the tiles, the first loads and the meeting take about 5 each); 16
+// tokens x 8 of 64 gated experts 2048 -> 1024 -> 2048, 710 MB in 104 us and 194 MB
+// in 50.  With many tokens in 4 bits the waves spend half of their time on the
+// matrix cores' and the codes' instructions and else wait for loads: 64 tokens x 2
+// of 8 139 us (57 and 77) for 373 MB.
 #pragma once
 
 #include "gsr_stream.hpp"
@@ -154,7 +164,8 @@ __device__ __forceinline__ int few_rows(int16_t* list, const int16_t* key, int s
 
 // log2 of how many of a workgroup's waves split an item's K of `units` (2^least
 // at least): the count for which the rounds of `waves` (a power of two) waves,
-// each `fixed` units longer than its share of K, are shortest.
+// each `fixed` units longer than its share of K, are shortest.  (16 tokens x 8 of
+// 64 gated experts in fp16 with 1, 2, 4 and 8 waves: 143, 143, 113 and 117 us.)
 __device__ __forceinline__ int few_split(int items, int waves_log2, int units, int fixed, int least)
 {
     int best = least;
@@ -242,29 +253,30 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_up_kernel(FewArgs p)
     }
 }
 
-// out of a block of columns.  T is at most TOKENS.  A job's rows are weighed and
+// out of a block of columns.  A job's rows are weighed and
 // added to their tokens' sums in LDS: per token a mask of the waves that have
 // rows of it (two masks in turn, one cleared while the other is read), and its
 // first row in each; the rows of a token lie behind each other.
-template <int FORM, int TOKENS, bool DW>
+template <int FORM, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
 {
     using S = FewStream<FORM, DW, true>;
     constexpr int CPL = S::CPL, CB = S::CB, UNIT = S::UNIT, QUADS = CB / 4;
     __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
-    __shared__ f32x4 sums[TOKENS * QUADS];
+    __shared__ f32x4 sums[kFewTokens * QUADS];
     __shared__ FewPlan plan;
-    __shared__ uint32_t mask[2][TOKENS];
-    __shared__ int8_t row_of[kStreamWaves][TOKENS], token_of[kStreamWaves][kFewRows + 1];
+    __shared__ uint32_t mask[2][kFewTokens];
+    __shared__ int8_t row_of[kStreamWaves][kFewTokens], token_of[kStreamWaves][kFewRows + 1];
     __shared__ float weight_of[kStreamWaves][kFewRows];
     __shared__ int bias_of[kStreamWaves];  // the expert whose bias a wave's rows get, or -1
     __shared__ int flag;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nb = blockIdx.x / p.groups, group = blockIdx.x - nb * p.groups, n0 = nb * CB;
     for (int i = tid; i < p.T * QUADS; i += kStreamThreads) sums[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (tid < TOKENS) mask[0][tid] = mask[1][tid] = 0u;
+    if (tid < kFewTokens) mask[0][tid] = mask[1][tid] = 0u;
     const int tiles = few_plan(plan, p), units = (p.F + UNIT - 1) / UNIT;
-    // every wave of the block has a job where that leaves each 128 rows of F
+    // every wave of the block has a job where that leaves each 128 rows of F (7
+    // tokens x 3 of 10 experts 1001 -> 517 -> 1001 27.6 us, with 256 rows 29.3)
     const int parts = max(1, min(p.groups * kStreamWaves / max(tiles, 1), units * UNIT / 128)), jobs = tiles * parts;
     const int j0 = jobs * group / p.groups, j1 = jobs * (group + 1) / p.groups;
 
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) few_down_kernel(FewArgs p)
             sums[u] = s;
         }
         turn ^= 1;
-        if (tid < TOKENS) mask[turn][tid] = 0u;  // read before the barrier above
+        if (tid < kFewTokens) mask[turn][tid] = 0u;  // read before the barrier above
         __syncthreads();
     }
 

@@ -84,24 +84,22 @@ typedef void (*few_kernel)(gsr::FewArgs);
 struct Kernels {
     few_kernel up, gated, down;
 };
-// The second launch keeps its tokens' sums in LDS: 16 of them, or 64.
 template <int FORM, bool DW>
-Kernels kernels_of(int64_t T)
+Kernels kernels_of()
 {
     constexpr bool DD = DW || FORM != gsr::kFewHalf;  // its rows of A are h's, which lie on dwords
-    return Kernels{gsr::few_up_kernel<FORM, DW, false>, gsr::few_up_kernel<FORM, DW, true>,
-                   T <= 16 ? gsr::few_down_kernel<FORM, 16, DD> : gsr::few_down_kernel<FORM, gsr::kFewTokens, DD>};
+    return Kernels{gsr::few_up_kernel<FORM, DW, false>, gsr::few_up_kernel<FORM, DW, true>, gsr::few_down_kernel<FORM, DD>};
 }
 // For matrices of `w` (and `w2`, or null) of N columns, and rows of A of K values.
-Kernels kernels_at(int64_t T, const gsr_weights* w, const gsr_weights* w2, const void* a, int64_t K, int64_t N)
+Kernels kernels_at(const gsr_weights* w, const gsr_weights* w2, const void* a, int64_t K, int64_t N)
 {
     bool dwords = K % 2 == 0 && !misaligned(a, 4);
     if (w->group == 0) dwords = dwords && N % 2 == 0 && !misaligned(w->data, 4) && (w2 == nullptr || !misaligned(w2->data, 4));
     switch (w->group) {
-    case 0: return dwords ? kernels_of<gsr::kFewHalf, true>(T) : kernels_of<gsr::kFewHalf, false>(T);
-    case 32: return dwords ? kernels_of<gsr::kFewW4x1, true>(T) : kernels_of<gsr::kFewW4x1, false>(T);
-    case 64: return dwords ? kernels_of<gsr::kFewW4x2, true>(T) : kernels_of<gsr::kFewW4x2, false>(T);
-    default: return dwords ? kernels_of<gsr::kFewW4x4, true>(T) : kernels_of<gsr::kFewW4x4, false>(T);
+    case 0: return dwords ? kernels_of<gsr::kFewHalf, true>() : kernels_of<gsr::kFewHalf, false>();
+    case 32: return dwords ? kernels_of<gsr::kFewW4x1, true>() : kernels_of<gsr::kFewW4x1, false>();
+    case 64: return dwords ? kernels_of<gsr::kFewW4x2, true>() : kernels_of<gsr::kFewW4x2, false>();
+    default: return dwords ? kernels_of<gsr::kFewW4x4, true>() : kernels_of<gsr::kFewW4x4, false>();
     }
 }
 
@@ -173,11 +171,11 @@ int gsr_expert_mlp_few(int64_t tokens, int64_t k, int64_t experts, int64_t H, in
     p.groups = g.groups;
     hipStream_t s = (hipStream_t)stream;
     if (F > 0 && slots > 0) {
-        const Kernels f = kernels_at(tokens, up, gate, x, H, F);
+        const Kernels f = kernels_at(up, gate, x, H, F);
         const hipError_t err = launch_kernel(gate != nullptr ? f.gated : f.up, dim3((unsigned)g.grid_up), dim3(gsr::kStreamThreads), s, p);
         if (err != hipSuccess) return status_of(err);
     }
-    return status_of(launch_kernel(kernels_at(tokens, down, nullptr, p.hidden, p.hidden_wide, O).down, dim3((unsigned)(g.blocks * g.groups)), dim3(gsr::kStreamThreads), s, p));
+    return status_of(launch_kernel(kernels_at(down, nullptr, p.hidden, p.hidden_wide, O).down, dim3((unsigned)(g.blocks * g.groups)), dim3(gsr::kStreamThreads), s, p));
 }
 
 }  // extern "C"

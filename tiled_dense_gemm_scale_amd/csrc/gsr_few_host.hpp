@@ -1,5 +1,5 @@
 // gsr_few_host.hpp -- host helpers of the few-token entry points: operands as
-// ranges of bytes, 4-bit weights, and K (or F) cut into parts.
+// ranges of bytes, and 4-bit weights.
 #pragma once
 
 #include <algorithm>
@@ -50,19 +50,6 @@ inline uint64_t w4_scale_count(uint64_t matrices, int64_t K, int64_t N, int64_t 
 
 // Widths from here on are refused: a step's rows are addressed by 32-bit offsets.
 constexpr int64_t kStreamWidth = (int64_t)1 << 22;
-
-// `units` of K over parts so that `tiles` tiles make about `workgroups`, each
-// keeping `least` units.  With 256 workgroups tiles of more than one part are at
-// most 128, one to a counter.
-struct Parts {
-    int parts, chunk;
-};
-inline Parts stream_parts(int64_t tiles, int64_t units, int64_t least, int64_t workgroups)
-{
-    const int64_t want = std::min<int64_t>({16, workgroups / std::max<int64_t>(tiles, 1), units / least});
-    const int64_t chunk = cdiv(std::max<int64_t>(units, 1), std::max<int64_t>(want, 1));
-    return Parts{(int)std::max<int64_t>(1, cdiv(units, chunk)), (int)chunk};
-}
 
 }  // namespace host
 }  // namespace gsr

