@@ -127,6 +127,24 @@ def test_layer(gsr, case, form, act, gated):
     assert (err <= slack).all()
 
 
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("form", FORMS)
+def test_narrow_widths(gsr, form, gated):
+    """Every width of F and O up to 18, columns of fewer than a lane's among them:
+    the formula's values, and nothing written behind the last row."""
+    for n in range(1, 19):
+        for case in ((9, 2, 3, 40, n, 33, 0.2, 32), (9, 2, 3, 40, 24, n, 0.2, 32), (9, 2, 3, n, n, n, 0.2, 32)):
+            x, ids, w, hs, fs, biases = case_inputs(gsr, case, form, True, gated, True)
+            b64 = {m: None if b is None else b.astype(np.float64) for m, b in biases.items()}
+            out, _, _ = ref.layer(x.astype(np.float64), ids, w, fs["up"], fs["gate"], fs["down"], b64, "none")
+            buf = torch.full((9 * case[5] + 64,), 5.0, dtype=torch.float16, device=DEV)
+            say(f"few narrow {case} {form} gated={gated}")
+            got = call(gsr, x, ids, w, hs, biases, "none", workspace(gsr, case), out=buf[:9 * case[5]].view(9, case[5]))
+            with np.errstate(over="ignore"):
+                assert np.array_equal(got.cpu().numpy(), out.astype(np.float16)), case
+            assert bool((buf[9 * case[5]:] == 5.0).all()), case
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_named_twice(gsr, form):
     """A token that names an expert more than once has a term for each, and an

@@ -158,6 +158,23 @@ def test_product_of_whole_numbers(gsr, case, zeros):
     assert int(ws[:512].count_nonzero()) == 0
 
 
+def test_narrow_products(gsr):
+    """Every N and K up to 18 and around a block of columns, with and without zero
+    points; nothing written behind the last row."""
+    rng = np.random.default_rng(6)
+    for N in list(range(1, 19)) + [63, 64, 65, 66, 68, 127, 129]:
+        for M, K, zeros in ((5, 40, False), (21, 300, True), (3, N, True)):
+            q, s, z = weights(rng, K, N, 32, zeros, True)
+            a, bias = rng.integers(-2, 3, (M, K)).astype(np.float16), rng.integers(-50, 50, N).astype(np.float16)
+            want = (a.astype(np.float64) @ ref.values(q, s, z, 32) + bias).astype(np.float16)
+            buf = torch.full((M * N + 64,), 5.0, dtype=torch.float16, device=DEV)
+            say(f"w4 narrow {M}x{N}x{K} zeros={zeros}")
+            got = gsr.gemm_w4(torch.from_numpy(a).to(DEV), handle(gsr, q, s, z, K, 32), bias=torch.from_numpy(bias).to(DEV),
+                              activation="none", c=buf[:M * N].view(M, N))
+            assert np.array_equal(got.cpu().numpy(), want), (M, N, K)
+            assert bool((buf[M * N:] == 5.0).all()), (M, N, K)
+
+
 @pytest.mark.parametrize("act", ["relu", "gelu", "none"])
 @pytest.mark.parametrize("case", SHAPES, ids=lambda c: "x".join(map(str, c)))
 def test_product(gsr, case, act):

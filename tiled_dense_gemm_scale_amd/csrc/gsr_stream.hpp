@@ -362,12 +362,12 @@ __device__ __forceinline__ f32x4 stream_sum(const float* slices, int waves, int 
 }
 
 // The column of position 4q of the block from n0 (three more lie behind it; those
-// from N on are none), or -1 where the position's lane lies past N.
+// from N on are none), or -1 where the position or its lane lies past N.
 template <int CPL>
 __device__ __forceinline__ int stream_position(int n0, int q, int N)
 {
-    const int l = 4 * q / CPL;
-    return n0 + CPL * l < N ? stream_column<CPL>(n0, l, N) + 4 * q % CPL : -1;
+    const int l = 4 * q / CPL, col = stream_column<CPL>(n0, l, N) + 4 * q % CPL;
+    return n0 + CPL * l < N && col < N ? col : -1;
 }
 
 // Four fp16 values of a row of N from column `col` on (zeros past N), and back;
