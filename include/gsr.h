@@ -392,8 +392,11 @@ int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group,
  * scale multiplies a group's sum: the weights are not rounded.  Where many rows
  * make it faster (more than 16, commonly from 200 on) and the workspace holds K x N
  * binary16 values, the weights are first written there as gsr_dequantize_w4 gives
- * them, each rounded once to binary16, and multiplied by the dense kernels.
- * A scale that is not finite makes its column's outputs not finite.
+ * them, each rounded once to binary16, and multiplied by the dense kernels; a
+ * column with a group whose codes could stand for 65520 or more in size, the first
+ * value past binary16, keeps its weights unrounded there too.
+ * A scale that is not finite makes its column's outputs not finite, before the
+ * activation.
  *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its first
  *              512 bytes zero before the first call and again after each), of
  *              gsr_w4_workspace_bytes(M, N, K) bytes; with less or NULL K is

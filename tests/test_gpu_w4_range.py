@@ -1,0 +1,78 @@
+"""GPU tests of the product with 4-bit weights at the ends of its range."""
+import numpy as np
+import pytest
+import torch
+
+import w4_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def gsr(native):
+    import tiled_dense_gemm_scale_amd as g
+
+    assert torch.cuda.is_available(), "GPU tests need a visible MI355X"
+    return g
+
+
+def say(msg):
+    print("[gpu] " + msg, flush=True)
+
+
+def handle(gsr, q, s, z, K, group):
+    return gsr.W4(ref.pack(q).to(DEV), torch.from_numpy(s).to(DEV), None if z is None else torch.from_numpy(z).to(DEV), K, group)
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
+@pytest.mark.parametrize("case", [(1025, 2048, 1024, 128), (1500, 1000, 4096, 64), (16000, 333, 1001, 32), (400000, 3, 64, 32)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_weights_past_fp16(gsr, case, zeros):
+    """Many rows with the weights' values in the workspace: a column with a weight
+    that fp16 does not hold has the formula's values all the same, and no other
+    column's bits change; a scale that is not finite stays in its column."""
+    M, N, K, group = case
+    rng = np.random.default_rng(M + zeros)
+    G = -(-K // group)
+    q = rng.integers(0, 16, (K, N))
+    s = ((0.5 + rng.random((G, N))) * 0.2).astype(np.float16)
+    z = rng.integers(0, 16, (G, N)).astype(np.uint8) if zeros else None
+    at = np.arange(N)
+    s[0, at % 7 == 2], s[G - 1, at % 11 == 5] = 9360.0, -60000.0  # 7 x 9360 = 65520, the first past fp16
+    s[G // 2, at % 13 == 4] = 8188.0                             # 8 x 8188 = 65504 stays
+    if zeros:
+        z[G - 1, at % 17 == 8], s[G - 1, at % 17 == 8] = 255, 300.0
+    f = ref.values(q, s, z, group)
+    past = (np.abs(f) >= 65520).any(0)
+    assert past.any() and (N == 3 or not past.all())
+    if N > 3:
+        s[1, N - 2] = np.nan if zeros else np.inf
+    odd = ~np.isfinite(s).all(0)
+    w = handle(gsr, q, s, z, K, group)
+    a, bias = torch.randn(M, K, device=DEV).half(), torch.randn(N, device=DEV).half()
+    nbytes = gsr.w4_workspace_bytes(M, N, K)
+    assert nbytes == 512 + 2 * K * N  # the values are written out
+    alpha = 2.0 ** -9
+    say(f"w4 past fp16 {case} zeros={zeros}: {int(past.sum())} of {N} columns")
+    got = gsr.gemm_w4(a, w, gsr.new_workspace(nbytes), bias=bias, alpha=alpha, activation="none")
+    dense = gsr.gemm_scale_bias_act(a, gsr.dequantize_w4(w), bias, alpha, "none")
+    same = torch.from_numpy(~past & ~odd & (np.abs(f) <= 65504).all(0)).to(DEV)
+    # a column whose codes could stand for a weight past fp16 may keep its weights too
+    z64 = 8.0 if z is None else z.astype(np.float64)
+    near = (np.abs(s.astype(np.float64)) * np.maximum(z64, 15.0 - z64) >= 65520).any(0)
+    same &= torch.from_numpy(~near).to(DEV)
+    assert torch.equal(got[:, same], dense[:, same])
+    got = got.cpu().numpy().astype(np.float64)
+    assert not np.isfinite(got[:, odd]).any()
+    a64, b64 = a.cpu().numpy().astype(np.float64), bias.cpu().numpy().astype(np.float64)
+    v, top = alpha * (a64 @ f) + b64, alpha * (np.abs(a64) @ np.abs(f)) + np.abs(b64)
+    # half an fp16 step of each weight where the column's are rounded
+    rounded = np.where(past, 0.0, alpha * (np.abs(a64) @ ref.half_step(f)))
+    slack = ref.sum_slack(K + G + 2, top) + rounded
+    bound = slack + ref.half_step(np.abs(v) + slack)
+    cols = ~odd & (np.abs(v) + bound < 65504).all(0)
+    assert past[cols].any()
+    err = np.abs(got - v)[:, cols]
+    assert (err <= bound[:, cols]).all(), f"{np.count_nonzero(~(err <= bound[:, cols]))} of {err.size}"

@@ -102,10 +102,18 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, int64_t bytes, bool aligned)
 }
 
 typedef void (*gemm_kernel)(gsr::W4Gemm);
-template <bool DW>
-gemm_kernel gemm_form(int64_t group)
+struct GemmKernels {
+    gemm_kernel rows, past;
+};
+template <int FL>
+GemmKernels gemm_form(bool dwords)
 {
-    return group == 32 ? gsr::w4_rows_kernel<1, DW> : group == 64 ? gsr::w4_rows_kernel<2, DW> : gsr::w4_rows_kernel<4, DW>;
+    return dwords ? GemmKernels{gsr::w4_rows_kernel<FL, true>, gsr::w4_past_kernel<FL, true>}
+                  : GemmKernels{gsr::w4_rows_kernel<FL, false>, gsr::w4_past_kernel<FL, false>};
+}
+GemmKernels gemm_form(int64_t group, bool dwords)
+{
+    return group == 32 ? gemm_form<1>(dwords) : group == 64 ? gemm_form<2>(dwords) : gemm_form<4>(dwords);
 }
 
 }  // namespace
@@ -188,16 +196,6 @@ int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, int64
     st = check_device();
     if (st != GSR_SUCCESS) return st;
     const GemmPlan g = gemm_plan(M, N, K, (int64_t)w.bytes, !misaligned(A, 16) && !misaligned(bias, 8));
-    if (g.dense) {
-        void* values = (uint8_t*)workspace + gsr::kMeetBytes;
-        st = gsr_dequantize_w4(1, K, N, group, codes, scales, zeros, values, stream);
-        // the dense product's matrices are below 2^31 bytes
-        const int64_t rows = (kLimit - 1) / (2 * std::max(K, N)) / 256 * 256;
-        for (int64_t m = 0; m < M && st == GSR_SUCCESS; m += rows)
-            st = gemm_scale_bias_act(std::min(rows, M - m), N, K, (const uint8_t*)A + 2 * m * K, values, bias, (uint8_t*)C + 2 * m * N,
-                                     alpha, activation, stream);
-        return st;
-    }
     gsr::W4Gemm p{};
     p.a = (const uint16_t*)A;
     p.w = gsr::W4Matrix{codes, (const uint16_t*)scales, zeros, group_log2(group)};
@@ -210,14 +208,25 @@ int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, int64
     p.alpha = alpha;
     p.blocks_m = (int)g.blocks_m;
     p.blocks_n = (int)g.blocks_n;
+    const GemmKernels f = gemm_form(group, K % 2 == 0 && !misaligned(A, 4));
+    if (g.dense) {
+        void* values = (uint8_t*)workspace + gsr::kMeetBytes;
+        st = gsr_dequantize_w4(1, K, N, group, codes, scales, zeros, values, stream);
+        // the dense product's matrices are below 2^31 bytes
+        const int64_t rows = (kLimit - 1) / (2 * std::max(K, N)) / 256 * 256;
+        for (int64_t m = 0; m < M && st == GSR_SUCCESS; m += rows)
+            st = gemm_scale_bias_act(std::min(rows, M - m), N, K, (const uint8_t*)A + 2 * m * K, values, bias, (uint8_t*)C + 2 * m * N,
+                                     alpha, activation, stream);
+        if (st != GSR_SUCCESS) return st;
+        return status_of(launch_kernel(f.past, dim3((unsigned)g.blocks_n), dim3(gsr::kStreamThreads), (hipStream_t)stream, p));
+    }
     p.parts = g.parts;
     p.chunk = g.chunk;
     p.count = (uint32_t*)workspace;
     p.part = (float*)((uint8_t*)workspace + gsr::kMeetBytes);
     const int64_t grid = cdiv(g.blocks_m * g.blocks_n * g.parts, 8) * 8;
     if (!grid_fits(grid, gsr::kStreamThreads)) return GSR_ERROR_TOO_LARGE;
-    const gemm_kernel f = K % 2 == 0 && !misaligned(A, 4) ? gemm_form<true>(group) : gemm_form<false>(group);
-    return status_of(launch_kernel(f, dim3((unsigned)grid), dim3(gsr::kStreamThreads), (hipStream_t)stream, p));
+    return status_of(launch_kernel(f.rows, dim3((unsigned)grid), dim3(gsr::kStreamThreads), (hipStream_t)stream, p));
 }
 
 }  // extern "C"

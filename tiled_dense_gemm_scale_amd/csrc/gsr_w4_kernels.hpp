@@ -20,6 +20,32 @@ struct W4Gemm {
     uint32_t* count;
 };
 
+// The sums of a tile's rows m0 .. m0 + rows_here - 1 and columns from n0 over the
+// units first .. first + here - 1 of K, a run of them to each wave, into the waves'
+// slices of LDS.
+template <class S>
+__device__ __forceinline__ void w4_tile(const W4Gemm& p, int64_t m0, int rows_here, int n0, int first, int here, float* lds)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    typename S::Rows rows(p.a + (size_t)m0 * p.K, (uint64_t)rows_here * (uint32_t)p.K * 2u, rows_here);
+    rows.row((uint32_t)min(stream_row(), rows_here - 1) * (uint32_t)p.K);
+    const int u0 = first + here * wave / kStreamWaves, u1 = first + here * (wave + 1) / kStreamWaves;
+    typename S::Sums acc;
+    acc.clear();
+    S::run(p.w, p.K, p.N, n0, rows, u0, u1, lds + wave * 16 * S::CB, acc);
+    stream_put<S::CPL>(lds + wave * 16 * S::CB, acc);
+}
+
+// act(alpha s + bias) of four columns of a row of C from `col` on (those from N on
+// are none).
+__device__ __forceinline__ f32x4 w4_epilogue(const W4Gemm& p, int col, f32x4 s)
+{
+    const f32x4 b = p.bias ? half4_at(p.bias, col, p.N) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = activate(s[i] * p.alpha + b[i], p.act);
+    return s;
+}
+
 // A tile of 16 rows and 64 columns, whose workgroup's waves split its K, or a
 // part of it: then the tile's sums meet in the workspace and the workgroup that
 // comes last adds them.  One block of rows is bound by the codes' bytes and the
@@ -38,29 +64,17 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
     const int all = p.blocks_m * p.blocks_n * p.parts, per_xcd = (all + 7) / 8;
     const int id = (int)(blockIdx.x & 7) * per_xcd + (int)(blockIdx.x >> 3);
     if (id >= all) return;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = id % p.parts, tile = id / p.parts;
     const int m0 = tile % p.blocks_m * 16, n0 = tile / p.blocks_m * CB, rows_here = min(16, p.M - m0);
 
-    typename S::Rows rows(p.a + (size_t)m0 * p.K, (uint64_t)rows_here * (uint32_t)p.K * 2u, rows_here);
-    rows.row((uint32_t)min(stream_row(), rows_here - 1) * (uint32_t)p.K);
-    const int units = (p.K + S::UNIT - 1) / S::UNIT;
-    const int first = part * p.chunk, here = max(0, min(p.chunk, units - first));
-    const int u0 = first + here * wave / kStreamWaves, u1 = first + here * (wave + 1) / kStreamWaves;
-    typename S::Sums acc;
-    acc.clear();
-    S::run(p.w, p.K, p.N, n0, rows, u0, u1, lds + wave * 16 * CB, acc);
+    const int units = (p.K + S::UNIT - 1) / S::UNIT, first = part * p.chunk;
+    w4_tile<S>(p, m0, rows_here, n0, first, max(0, min(p.chunk, units - first)), lds);
 
     const int m = threadIdx.x / QUADS, q = threadIdx.x % QUADS;
     auto finish = [&](f32x4 s) {
         const int col = stream_position<CPL>(n0, q, p.N);
-        if (col < 0) return;
-        const f32x4 b = p.bias ? half4_at(p.bias, col, p.N) : f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = activate(s[i] * p.alpha + b[i], p.act);
-        put_half4(p.c + (size_t)(m0 + m) * p.N, col, p.N, s);
+        if (col >= 0) put_half4(p.c + (size_t)(m0 + m) * p.N, col, p.N, w4_epilogue(p, col, s));
     };
-    stream_put<CPL>(lds + wave * 16 * CB, acc);
     __syncthreads();
     const size_t wide = (size_t)p.blocks_n * CB;
     float* meet = p.part + (size_t)(m0 + m) * wide + n0 + 4 * q;
@@ -72,6 +86,53 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
     if (p.parts == 1) return;
     if (!meet_last(p.count + tile, (uint32_t)p.parts, &flag)) return;
     if (m < rows_here) finish(meet_sum(meet, p.parts, (size_t)p.M * wide));
+}
+
+// After a product with the weights' values rounded to fp16: the columns of which a
+// weight may not fit it (some |scale| times the farthest code from its zero point
+// is 65520 or more, the first value that rounds to an infinity), with the weights as
+// they are.  A workgroup has 64 columns and looks at their scales (0.7 MB of 11008
+// columns of 32 groups; 1025 x 11008 x 4096 120 us without this launch, 120 to 125 with
+// it); where one is so large it walks all rows, its waves each a part of K.  A scale that is not finite is left to the
+// product: its column's sums are not finite either way.
+template <int FL, bool DW>
+__global__ void __launch_bounds__(kStreamThreads, 2) w4_past_kernel(W4Gemm p)
+{
+    using S = W4Stream<FL, DW, false>;
+    constexpr int CPL = S::CPL, CB = S::CB, QUADS = CB / 4, ROWS = kStreamThreads / QUADS;
+    __shared__ __attribute__((aligned(16))) float lds[kStreamWaves * 16 * CB];
+    __shared__ uint32_t past[QUADS];  // bit i: column i of the quad
+    const int n0 = blockIdx.x * CB, m = threadIdx.x / QUADS, q = threadIdx.x % QUADS;
+    const int col = stream_position<CPL>(n0, q, p.N), groups = ((p.K - 1) >> p.w.glog2) + 1;
+    if (threadIdx.x < QUADS) past[threadIdx.x] = 0u;
+    __syncthreads();
+    uint32_t mine = 0u;
+    if (col >= 0)
+        for (int g = m; g < groups; g += ROWS)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (col + i >= p.N) break;
+                const size_t at = (size_t)g * p.N + col + i;
+                const float s = fabsf(half_at(p.w.scales + at)), z = p.w.zeros ? (float)p.w.zeros[at] : 8.0f;
+                if (s <= 65504.0f && s * fmaxf(z, 15.0f - z) >= 65520.0f) mine |= 1u << i;
+            }
+    if (mine) atomicOr(&past[q], mine);
+    __syncthreads();
+    bool any = false;
+    for (int i = 0; i < QUADS; ++i) any = any || past[i] != 0u;
+    if (!any) return;
+    for (int64_t m0 = 0; m0 < p.M; m0 += 16) {
+        const int rows_here = (int)min((int64_t)16, p.M - m0);
+        w4_tile<S>(p, m0, rows_here, n0, 0, (p.K + S::UNIT - 1) / S::UNIT, lds);
+        __syncthreads();
+        if (m < rows_here && col >= 0) {
+            const f32x4 s = w4_epilogue(p, col, stream_sum<CPL>(lds, kStreamWaves, m, q));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (past[q] >> i & 1u && col + i < p.N) p.c[(size_t)(m0 + m) * p.N + col + i] = to_half(s[i]);
+        }
+        __syncthreads();  // the next tile's sums
+    }
 }
 
 // ---- quantizing --------------------------------------------------------------------

@@ -102,7 +102,8 @@ def gemm_w4(a: torch.Tensor, w: W4, workspace: Optional[torch.Tensor] = None, bi
     matrix, bias (N,) fp16 or None, act "relu", "gelu" (tanh form) or "none".
     Products are summed in fp32 and scaled group by group; the weights are not
     rounded, but where many rows make it faster they are written to the workspace
-    as dequantize_w4 gives them and multiplied by the dense kernels.  workspace:
+    as dequantize_w4 gives them and multiplied by the dense kernels (but for the
+    columns whose weights could pass fp16's range, which stay as they are).  workspace:
     new_workspace(w4_workspace_bytes(M, N, K)), one per call that may run at the
     same time; with less, or None, neither that is done nor K split across
     workgroups.  Returns c (M, N)."""
