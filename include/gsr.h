@@ -400,7 +400,8 @@ int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group,
  *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its first
  *              512 bytes zero before the first call and again after each), of
  *              gsr_w4_workspace_bytes(M, N, K) bytes; with less or NULL K is
- *              not split across workgroups, and the weights are not written out
+ *              not split across workgroups, and the weights are not written out:
+ *              fewer than 512 + 2 K N bytes keep them unrounded for any M
  * Ownership, streams and errors as gemm_scale_bias_act_ws. */
 int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A,
                            int64_t group, const uint32_t* codes, const void* scales, const uint8_t* zeros,

@@ -1,4 +1,5 @@
-"""GPU tests of the product with 4-bit weights at the ends of its range."""
+"""GPU tests of the product with 4-bit weights at the ends of its range: weights
+past fp16, and weights that fp16 rounds."""
 import numpy as np
 import pytest
 import torch
@@ -76,3 +77,59 @@ def test_weights_past_fp16(gsr, case, zeros):
     assert past[cols].any()
     err = np.abs(got - v)[:, cols]
     assert (err <= bound[:, cols]).all(), f"{np.count_nonzero(~(err <= bound[:, cols]))} of {err.size}"
+
+
+def unrounded_inputs(gsr, M, N, K, group, zeros):
+    """Weights of 12 and 13 bits, (q - z) (1024 + c) / 1024 with odd q - z up to 7 and
+    q constant in a column; a row of A takes one weight and gives back another, so
+    the output is (q - z) (c1 - c2) / 1024 exactly."""
+    rng = np.random.default_rng(M + N + K)
+    G = -(-K // group)
+    c = rng.integers(0, 128, (G, N))
+    s = ((1024 + c) / 1024.0).astype(np.float16)
+    zero = 8 if not zeros else 6
+    q = np.broadcast_to(zero + rng.choice([-5, -3, 5, 7], N), (K, N))
+    z = np.full((G, N), zero, np.uint8) if zeros else None
+    a = np.zeros((M, K), np.float16)
+    for m in range(M):
+        k1, k2 = rng.choice(K, 2, replace=False)
+        a[m, k1], a[m, k2] = 1.0, -1.0
+    want = a.astype(np.float64) @ ref.values(q, s, z, group)
+    assert np.array_equal(want, want.astype(np.float16))
+    return torch.from_numpy(a).to(DEV), handle(gsr, q, s, z, K, group), want
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
+@pytest.mark.parametrize("case", [(2, 4096, 512, 128), (17, 1000, 1000, 32), (33, 514, 1024, 64), (64, 11008, 1024, 128),
+                                  (100, 4096, 4096, 256), (130, 4096, 1030, 128), (150, 2048, 4093, 32)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_weights_of_a_few_rows_are_not_rounded(gsr, case, zeros):
+    M, N, K, group = case
+    a, w, want = unrounded_inputs(gsr, M, N, K, group, zeros)
+    nbytes = gsr.w4_workspace_bytes(M, N, K)
+    assert nbytes != 512 + 2 * K * N  # nothing is written out
+    for ws in (gsr.new_workspace(nbytes), None):
+        say(f"w4 unrounded {case} zeros={zeros} workspace={ws is not None}")
+        got = gsr.gemm_w4(a, w, ws, activation="none").cpu().numpy()
+        assert np.array_equal(got, want), f"{np.count_nonzero(got != want)} of {want.size} differ"
+
+
+@pytest.mark.parametrize("case", [(1025, 2048, 1024, 128), (1500, 1000, 1000, 64), (4000, 333, 1001, 32)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_rounding_of_many_rows_is_the_callers_choice(gsr, case):
+    """The same workspace with and without the weights rounded."""
+    M, N, K, group = case
+    a, w, want = unrounded_inputs(gsr, M, N, K, group, True)
+    nbytes = 512 + 2 * K * N
+    ws = gsr.new_workspace(max(nbytes, gsr.w4_workspace_bytes(M, N, K)))
+    say(f"w4 choice of rounding {case}")
+    got = gsr.gemm_w4(a, w, ws, activation="none", round_weights=False).cpu().numpy()
+    assert np.array_equal(got, want), f"{np.count_nonzero(got != want)} of {want.size} differ"
+    if gsr.w4_workspace_bytes(M, N, K) == nbytes:
+        got = gsr.gemm_w4(a, w, ws, activation="none")
+        assert torch.equal(got, gsr.gemm_scale_bias_act(a, gsr.dequantize_w4(w), activation="none"))
+    # in a product whose rows are few nothing changes, its K split included
+    b, v, few = unrounded_inputs(gsr, 5, 512, 4096, 128, True)
+    ws = gsr.new_workspace(gsr.w4_workspace_bytes(5, 512, 4096))
+    assert torch.equal(gsr.gemm_w4(b, v, ws, activation="none"), gsr.gemm_w4(b, v, ws, activation="none", round_weights=False))
+    assert int(ws.count_nonzero()) > 0 and int(ws[:512].count_nonzero()) == 0  # parts met there

@@ -97,16 +97,18 @@ def dequantize_w4(w: W4, out: Optional[torch.Tensor] = None, stream=None) -> tor
 
 
 def gemm_w4(a: torch.Tensor, w: W4, workspace: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
-            alpha: float = 1.0, activation: str = "relu", c: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+            alpha: float = 1.0, activation: str = "relu", c: Optional[torch.Tensor] = None, stream=None,
+            round_weights: bool = True) -> torch.Tensor:
     """c = act(alpha * a @ w + bias) for a (M, K) fp16, w a W4 of one (K, N)
     matrix, bias (N,) fp16 or None, act "relu", "gelu" (tanh form) or "none".
     Products are summed in fp32 and scaled group by group; the weights are not
-    rounded, but where many rows make it faster they are written to the workspace
-    as dequantize_w4 gives them and multiplied by the dense kernels (but for the
-    columns whose weights could pass fp16's range, which stay as they are).  workspace:
-    new_workspace(w4_workspace_bytes(M, N, K)), one per call that may run at the
-    same time; with less, or None, neither that is done nor K split across
-    workgroups.  Returns c (M, N)."""
+    rounded, but where many rows make it faster (more than 16, commonly from 200
+    on) they are written to the workspace as dequantize_w4 gives them, each rounded
+    once to fp16, and multiplied by the dense kernels (but for the columns whose
+    weights could pass fp16's range, which stay as they are).  round_weights False:
+    never.  workspace: new_workspace(w4_workspace_bytes(M, N, K)), one per call that
+    may run at the same time; with less, or None, neither that is done nor K split
+    across workgroups.  Returns c (M, N)."""
     matrix("a", a, torch.float16, 2)
     (M, K), dev = a.shape, a.get_device()
     k, N, codes, scales, zeros = check_w4("w", w, dev, ())
@@ -116,6 +118,9 @@ def gemm_w4(a: torch.Tensor, w: W4, workspace: Optional[torch.Tensor] = None, bi
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
     wptr, wbytes = workspace_of(workspace, dev) if workspace is not None else (0, 0)
+    values = 512 + 2 * K * N  # what the weights' values take
+    if not round_weights and wbytes >= values and w4_workspace_bytes(M, N, K) == values:
+        wbytes = values - 1
 
     def go(s):
         o = output("c", c, torch.float16, (M, N), a)
