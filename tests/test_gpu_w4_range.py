@@ -1,5 +1,5 @@
 """GPU tests of the product with 4-bit weights at the ends of its range: weights
-past fp16, and weights that fp16 rounds."""
+past fp16, weights that fp16 rounds, and more rows than one launch has."""
 import numpy as np
 import pytest
 import torch
@@ -133,3 +133,24 @@ def test_rounding_of_many_rows_is_the_callers_choice(gsr, case):
     ws = gsr.new_workspace(gsr.w4_workspace_bytes(5, 512, 4096))
     assert torch.equal(gsr.gemm_w4(b, v, ws, activation="none"), gsr.gemm_w4(b, v, ws, activation="none", round_weights=False))
     assert int(ws.count_nonzero()) > 0 and int(ws[:512].count_nonzero()) == 0  # parts met there
+
+
+@pytest.mark.parametrize("N", [1, 70])
+def test_more_rows_than_a_launch_has(gsr, N):
+    """More tiles than the 2^23 workgroups of 512 threads that a launch can have,
+    without a workspace: every row, and nothing behind the last."""
+    K, group = 2, 32
+    M = (2 ** 23 // -(-N // 64)) * 16 + 33
+    q = np.arange(K * N).reshape(K, N) % 16
+    s = np.full((1, N), 0.5, np.float16)
+    w = handle(gsr, q, s, None, K, group)
+    a = torch.randint(-2, 3, (M, K), device=DEV, dtype=torch.int8).half()
+    f = torch.from_numpy(ref.values(q, s, None, group)).to(DEV).float()
+    buf = torch.full((M * N + 64,), 9.0, dtype=torch.float16, device=DEV)
+    say(f"w4 {M} rows of {N}")
+    gsr.gemm_w4(a, w, activation="none", c=buf[:M * N].view(M, N))
+    for m in range(0, M, 2 ** 24):
+        part = a[m:m + 2 ** 24].float()
+        want = (part[:, :1] * f[:1] + part[:, 1:] * f[1:]).half()
+        assert torch.equal(buf[m * N:m * N + want.numel()].view(-1, N), want), m
+    assert bool((buf[M * N:] == 9.0).all())

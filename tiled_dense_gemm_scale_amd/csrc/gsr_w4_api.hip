@@ -224,9 +224,19 @@ int gemm_w4_scale_bias_act(int64_t M, int64_t N, int64_t K, const void* A, int64
     p.chunk = g.chunk;
     p.count = (uint32_t*)workspace;
     p.part = (float*)((uint8_t*)workspace + gsr::kMeetBytes);
-    const int64_t grid = cdiv(g.blocks_m * g.blocks_n * g.parts, 8) * 8;
-    if (!grid_fits(grid, gsr::kStreamThreads)) return GSR_ERROR_TOO_LARGE;
-    return status_of(launch_kernel(f.rows, dim3((unsigned)grid), dim3(gsr::kStreamThreads), (hipStream_t)stream, p));
+    // A launch has fewer than 2^32 threads: more rows than that are several, each of
+    // whole tiles (with K split there are at most 128 tiles, and one).
+    const int64_t most = (((int64_t)1 << 32) / gsr::kStreamThreads - 8) / g.blocks_n / g.parts;
+    for (int64_t m = 0; m < M; m += 16 * most) {
+        p.M = (int)std::min(16 * most, M - m);
+        p.a = (const uint16_t*)A + m * K;
+        p.c = (uint16_t*)C + m * N;
+        p.blocks_m = (int)cdiv(p.M, 16);
+        const int64_t grid = cdiv((int64_t)p.blocks_m * g.blocks_n * g.parts, 8) * 8;
+        const hipError_t err = launch_kernel(f.rows, dim3((unsigned)grid), dim3(gsr::kStreamThreads), (hipStream_t)stream, p);
+        if (err != hipSuccess) return status_of(err);
+    }
+    return GSR_SUCCESS;
 }
 
 }  // extern "C"
