@@ -435,9 +435,11 @@ typedef struct gsr_weights {
  *   x        T x H;  up, gate  experts of H x F;  down  experts of F x O
  *   weights  T x k binary32, or NULL (ones)
  *   activation  any gsr_activation
- * Sums, biases, activation, gate and weights are binary32; h is kept to within
- * 2^-22 between the launches (an infinity beyond binary16's range) and out rounded
- * once.  A token's choices are added in an order that the ids alone decide: equal
+ * Sums, biases, activation, gate and weights are binary32; between the launches
+ * each h is kept to within 2^-22 of itself or 2^-36, whichever is more, and one that
+ * is not zero keeps its sign beside an infinite weight (an h beyond binary16's range
+ * is an infinity); out is rounded once.  A weight of a choice that is not finite makes its token's
+ * outputs not finite.  A token's choices are added in an order that the ids alone decide: equal
  * inputs give equal bits.  Either all matrices are binary16 or all are 4-bit, gate
  * and up of one group.  Values are row-major at any 2-byte alignment (codes 4).
  * T <= 64, T k <= 1024, experts <= 1024, widths below 2^22, T k F below 2^29 with F

@@ -19,8 +19,8 @@
 //    part of F, weigh their rows and add them per token in LDS, in order of the
 //    experts.  The workgroups of a block meet in the workspace and the last one
 //    adds their sums in order, so equal inputs give equal bits.
-// Between the launches h is two fp16 values, rounded and what that lost, as the
-// matrix cores take it: one rounding to fp16 would be as large as that of out, and
+// Between the launches h is two fp16 values, rounded and 2^11 times what that lost
+// (stream_split), as the matrix cores take it: one rounding to fp16 would be as large as that of out, and
 // the error of out against 64 bits 0.00029 in place of 0.00021, its own rounding's
 // (64 tokens x 2 of 8 in 4 bits 129 us so and 154 with both halves, before A was
 // read as it is now; the others within 2 us).

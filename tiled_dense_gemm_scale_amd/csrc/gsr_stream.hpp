@@ -112,7 +112,7 @@ __device__ __forceinline__ void stream_turn(u32x4 (&a)[STEPS], float* slice)
 // The row of A that a lane reads, of a table of less than 2^31 bytes.  Rows past the last are that one again, whose sums nobody takes, and
 // loads behind the table are zeros: no load is masked, and lanes with one address
 // are one access.  DW: every row starts on a dword.  A table can also hold
-// values as two halves, the value rounded and what that lost (stream_split); each
+// values as two halves, the value rounded and 2^11 times what that lost (stream_split); each
 // of a row's halves is `wide` values long, zeros at the end, the second behind the
 // first, and in the order of k that the stream multiplies in.
 template <bool DW>
@@ -138,14 +138,20 @@ struct StreamRows {
     }
 };
 
-// v as two fp16 values whose sum is within 2^-22 of it (an infinity alone).
+// v as two fp16 values, hi + lo / 2048: within 2^-22 of v, or 2^-36 where that is
+// more (|v| below 2^-14).  fp16's least step is 2^-24, so the rest is kept 2^11
+// larger, the most that the rest of the largest value, 16, leaves room for.  hi of a v that is not zero is
+// none either (then lo gives back the difference), so that v keeps its sign beside
+// an infinite weight; past fp16 hi is an infinity, alone.
+constexpr float kRest = 2048.0f;
 struct StreamHalves {
     uint16_t hi, lo;
 };
 __device__ __forceinline__ StreamHalves stream_split(float v)
 {
-    const _Float16 hi = (_Float16)v;
-    const float rest = v - (float)hi;
+    _Float16 hi = (_Float16)v;
+    if (hi == (_Float16)0.0f && v != 0.0f) hi = __builtin_bit_cast(_Float16, (uint16_t)(v < 0.0f ? 0x8001u : 1u));
+    const float rest = (v - (float)hi) * kRest;
     return StreamHalves{__builtin_bit_cast(uint16_t, hi),
                         __builtin_bit_cast(uint16_t, (_Float16)(fabsf((float)hi) <= 65504.0f ? rest : 0.0f))};
 }
@@ -329,7 +335,8 @@ struct HalfStream {
 #pragma unroll
             for (int j = 0; j < CPL; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc.v[j][r] += fabsf(acc.v[j][r]) < __builtin_inff() ? low.v[j][r] : 0.0f;
+                for (int r = 0; r < 4; ++r)
+                    acc.v[j][r] = fmaf(fabsf(acc.v[j][r]) < __builtin_inff() ? low.v[j][r] : 0.0f, 1.0f / kRest, acc.v[j][r]);
     }
 };
 

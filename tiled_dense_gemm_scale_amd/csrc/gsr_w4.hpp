@@ -138,22 +138,24 @@ struct W4Stream {
             if (e * FL * kStep >= left) break;  // no such group
             Scale v;
             scale_of(v, t.s[e], t.z[e], p.m.zeros != nullptr);
-            f32x4 sum[CPL];
+            f32x4 sum[CPL], low[CPL];  // low: of the second halves
 #pragma unroll
             for (int i = 0; i < FL; ++i) {
                 const u32x4 a = ordered(t.a[0][e * FL + i]);
 #pragma unroll
                 for (int j = 0; j < CPL; ++j) {
                     const u32x4 b = w4_values(t.w[e * FL + i][j], v.lo[j], v.hi[j]);
-                    sum[j] = mfma16(a, b, i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[j]);
-                    if constexpr (SPLIT) sum[j] = mfma16(t.a[1][e * FL + i], b, sum[j]);
+                    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+                    sum[j] = mfma16(a, b, i == 0 ? none : sum[j]);
+                    if constexpr (SPLIT) low[j] = mfma16(t.a[1][e * FL + i], b, i == 0 ? none : low[j]);
                 }
                 __builtin_amdgcn_sched_barrier(0);  // a step's values live no longer than it
             }
 #pragma unroll
             for (int j = 0; j < CPL; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc.v[j][r] = fmaf(v.s[j], sum[j][r], acc.v[j][r]);
+                for (int r = 0; r < 4; ++r)
+                    acc.v[j][r] = fmaf(v.s[j], SPLIT ? fmaf(low[j][r], 1.0f / kRest, sum[j][r]) : sum[j][r], acc.v[j][r]);
         }
     }
 
@@ -186,8 +188,13 @@ struct W4Stream {
 #pragma unroll
         for (int j = 0; j < CPL; ++j) {
             const u32x4 b = w4_values(w[j], v.lo[j], v.hi[j]);
-            f32x4 sum = mfma16(a, b, f32x4{0.f, 0.f, 0.f, 0.f});
-            if constexpr (SPLIT) sum = mfma16(a2, b, sum);
+            const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+            f32x4 sum = mfma16(a, b, none);
+            if constexpr (SPLIT) {
+                const f32x4 low = mfma16(a2, b, none);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sum[x] = fmaf(low[x], 1.0f / kRest, sum[x]);
+            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc.v[j][x] = fmaf(v.s[j], sum[x], acc.v[j][x]);
         }
