@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import w4_reference as ref
-from test_gpu_few import FORMS, call, case_inputs, dev, workspace
+from test_gpu_few import CASES, FORMS, call, case_inputs, dev, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -41,6 +41,44 @@ def layer(gsr, x, ids, weights, up, down, F, O, E, act="none"):
     T, k = ids.shape
     ws = gsr.new_workspace(gsr.expert_few_workspace_bytes(T, k, E, F, O))
     return gsr.expert_mlp_few(dev(x), dev(ids), dev(weights), up, down, ws, activation=act).cpu().numpy()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("tokens", [1, 3, 37])
+def test_rests_of_h_arrive(gsr, form, group, tokens):
+    """h = 4096 + c with c up to 8, of which fp16 keeps whole fours; the weights of
+    two neighbouring h cancel the 4096, so the outputs are sums of the rests of all
+    of F, its ragged end too, exactly."""
+    E, H, F, O = 2, 70, 846, 70
+    rng = np.random.default_rng(tokens + group)
+    up = np.zeros((E, H, F), np.int64)
+    up[:, 0] = 4
+    up[:, H - 1] = rng.integers(-8, 6, (E, F))
+    down = np.repeat(rng.integers(-5, 6, (E, F // 2, O)), 2, axis=1)
+    down[:, 1::2] *= -1
+    G = -(-F // group)
+    scale = 2.0 ** rng.integers(0, 3, (E, G, O))
+    x = np.zeros((tokens, H), np.float16)
+    x[:, 0], x[:, H - 1] = 1024.0, rng.choice([1.0, -1.0, 0.5], tokens)
+    ids = rng.integers(0, E, (tokens, 1)).astype(np.int32)
+    h = [x[t].astype(np.float64) @ up[ids[t, 0]] for t in range(tokens)]
+    assert all(np.count_nonzero(v != v.astype(np.float16).astype(np.float64)) > F // 3 for v in h)
+
+    def sums(h):
+        return np.stack([h[t] @ (down[ids[t, 0]] * scale[ids[t, 0]][np.arange(F) // group]) for t in range(tokens)])
+
+    want = sums(h)
+    # what the outputs would be without the rests, and with them in another place of their eights
+    rounded = [v.astype(np.float16).astype(np.float64) for v in h]
+    order = np.arange(F) // 8 * 8 + (np.arange(F) % 8 * 2 + np.arange(F) % 8 // 4) % 8
+    order = np.where(order < F, order, np.arange(F))
+    moved = [r + (v - r)[order] for r, v in zip(rounded, h)]
+    for other in (rounded, moved):
+        assert (np.abs(sums(other) - want) > ref.half_step(want) * 2).mean() > 0.5
+    say(f"few rests {form} group={group} tokens={tokens}")
+    got = layer(gsr, x, ids, None, whole_weights(gsr, form, group, up), whole_weights(gsr, form, group, down, scale), F, O, E)
+    assert np.array_equal(got, want.astype(np.float16)), f"{np.count_nonzero(got != want.astype(np.float16))} of {want.size}"
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
@@ -109,3 +147,38 @@ def test_infinite_weight_meets_a_small_h(gsr, O):
     sign = np.array([1.0, -1.0, 1.0, -1.0])
     assert np.array_equal(got[:, O - 1], sign * np.inf) and np.array_equal(got[:, 0], -sign * np.inf)
     assert np.isfinite(got[:, 1:O - 1]).all()
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("case", [c for c in CASES if c[3] > 24], ids=lambda c: "x".join(map(str, c)))
+def test_whole_numbers_all_over_h(gsr, case, form, gated):
+    """Inputs that are not zero at 24 places of all of H, its last among them."""
+    T, k, E, H, F, O, drop, group = case
+    x, ids, w, hs, fs, biases = case_inputs(gsr, case, form, True, gated, True, seed=3)
+    rng = np.random.default_rng(H)
+    keep = np.append(rng.choice(H - 1, 23, replace=False), H - 1)
+    x[:, np.setdiff1d(np.arange(H), keep)] = 0
+    x[:, H - 1] = rng.choice([-1.0, 1.0], T)
+    b64 = {n: None if b is None else b.astype(np.float64) for n, b in biases.items()}
+    out, _, hidden = ref.layer(x.astype(np.float64), ids, w, fs["up"], fs["gate"], fs["down"], b64, "none")
+    assert not hidden or max(np.abs(h).max() for h in hidden) <= 2048
+    say(f"few whole over H {case} {form} gated={gated}")
+    got = call(gsr, x, ids, w, hs, biases, "none", workspace(gsr, case)).cpu().numpy()
+    with np.errstate(over="ignore"):
+        want = out.astype(np.float16)
+    assert np.array_equal(got, want), f"{np.count_nonzero(got != want)} of {want.size} differ"
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_weights_of_choices_that_are_not_finite(gsr, form):
+    """They make their token's outputs not finite, and no other's."""
+    case = (6, 2, 4, 40, 1100, 50, 0.0, 64)
+    x, ids, w, hs, fs, biases = case_inputs(gsr, case, form, False, False, True, seed=2)
+    ws = workspace(gsr, case)
+    base = call(gsr, x, ids, w, hs, biases, "gelu", ws).cpu().numpy()
+    w[1, 0], w[4, 1] = np.inf, np.nan
+    say(f"few weights not finite {form}")
+    got = call(gsr, x, ids, w, hs, biases, "gelu", ws).cpu().numpy()
+    bad = np.isin(np.arange(6), (1, 4))
+    assert np.array_equal(got[~bad], base[~bad]) and not np.isfinite(got[bad]).any()
