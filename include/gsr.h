@@ -391,10 +391,11 @@ int gsr_dequantize_w4(int64_t matrices, int64_t K, int64_t N, int64_t group,
  * products A[m,k] (q - zero) are summed in binary32, group by group, and the
  * scale multiplies a group's sum: the weights are not rounded.  Where many rows
  * make it faster (more than 16, commonly from 200 on) and the workspace holds K x N
- * binary16 values, the weights are first written there as gsr_dequantize_w4 gives
- * them, each rounded once to binary16, and multiplied by the dense kernels; a
- * column with a group whose codes could stand for 65520 or more in size, the first
- * value past binary16, keeps its weights unrounded there too.
+ * binary16 values (512 + 2 K N bytes, which have to be below 2^31), the weights are
+ * first written there as gsr_dequantize_w4 gives them, each rounded once to
+ * binary16, and multiplied by the dense kernels; a column with a group whose codes
+ * could stand for 65520 or more in size, the first value past binary16, keeps its
+ * weights unrounded there too.
  * A scale that is not finite makes its column's outputs not finite, before the
  * activation.
  *   workspace  as gemm_scale_bias_act_ws's, whose counters it shares (its first
@@ -438,9 +439,9 @@ typedef struct gsr_weights {
  * Sums, biases, activation, gate and weights are binary32; between the launches
  * each h is kept to within 2^-22 of itself or 2^-36, whichever is more, and one that
  * is not zero keeps its sign beside an infinite weight (an h beyond binary16's range
- * is an infinity); out is rounded once.  A weight of a choice that is not finite makes its token's
- * outputs not finite.  A token's choices are added in an order that the ids alone decide: equal
- * inputs give equal bits.  Either all matrices are binary16 or all are 4-bit, gate
+ * is an infinity); out is rounded once.  weights[t,j] that are not finite make their
+ * token's outputs not finite.  A token's choices are added in an order that the ids
+ * alone decide: equal inputs give equal bits.  Either all matrices are binary16 or all are 4-bit, gate
  * and up of one group.  Values are row-major at any 2-byte alignment (codes 4).
  * T <= 64, T k <= 1024, experts <= 1024, widths below 2^22, T k F below 2^29 with F
  * in whole eights (GSR_ERROR_TOO_LARGE); for more tokens there are gsr_group_rows

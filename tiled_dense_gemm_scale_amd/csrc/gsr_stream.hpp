@@ -2,8 +2,9 @@
 // share of C (16 rows x CB columns) over a run of K, operands from memory
 // straight into registers.
 //
-// Such products are bound by the weights' bytes, so nothing stands between the
-// loads and the matrix cores: no LDS, no barrier.  A wave's 64 lanes hold an
+// Such products are bound by the weights' bytes, so nothing stands between their
+// loads and the matrix cores: no LDS, no barrier (rows of A pass through the wave's
+// own LDS where a tile has more than one, stream_turn).  A wave's 64 lanes hold an
 // MFMA 16x16x32 operand as 16 columns x 4 runs of 8 values of k.  With weights
 // in rows of N (k-major) lane (l, g) = (lane % 16, lane / 16) reads the CPL
 // columns c .. c + CPL - 1 of the rows 8g .. 8g + 7 of a step of 32 rows, which
@@ -14,7 +15,8 @@
 //
 // Waves of a workgroup take runs of K of their own and add their sums through
 // LDS in wave order.  One workgroup of eight waves has a CU to itself: its ring of
-// two units needs 150 to 240 registers a lane.
+// two units needs 150 to 244 registers a lane (and the few-token kernels keep 24 to 68
+// scalar values in lanes of them, which the scalar registers have no room for).
 //
 // Columns past N: a lane whose columns would pass N is moved back to end at N,
 // so its sums are those of columns that its neighbour has too, the same bits,
@@ -83,7 +85,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dword_rsrc(const void* at, uin
 // of the t / 4-th of 16 rows, c = t % 4 ^ t / 16, so that four lanes next to each
 // other read 64 bytes next to each other.  (As the matrix cores take A, row t % 16
 // and run t / 16, each lane's 16 bytes are an access of their own, four in five of
-// all: 64 tokens x 2 of 8 experts in 4 bits 154 us so and 138 this way.)
+// all: 64 tokens x 2 of 8 experts in 4 bits 154 us so, 138 with this step.)
 // stream_turn brings them into that order through the wave's LDS; with that c no
 // two lanes meet in a bank.  A tile of one row needs neither (one token x 2 of 8
 // experts in 4 bits 39.0 us turned, 37.7 not).
@@ -109,12 +111,13 @@ __device__ __forceinline__ void stream_turn(u32x4 (&a)[STEPS], float* slice)
     wave_fence();
 }
 
-// The row of A that a lane reads, of a table of less than 2^31 bytes.  Rows past the last are that one again, whose sums nobody takes, and
-// loads behind the table are zeros: no load is masked, and lanes with one address
-// are one access.  DW: every row starts on a dword.  A table can also hold
-// values as two halves, the value rounded and 2^11 times what that lost (stream_split); each
-// of a row's halves is `wide` values long, zeros at the end, the second behind the
-// first, and in the order of k that the stream multiplies in.
+// The row of A that a lane reads, of a table of less than 2^31 bytes.  Rows past the
+// last are that one again, whose sums nobody takes, and loads behind the table are
+// zeros: no load is masked, and lanes with one address are one access.  DW: every
+// row starts on a dword.  A table can also hold values as two halves, the value
+// rounded and 2^11 times what that lost (stream_split); each of a row's halves is
+// `wide` values long, zeros at the end, the second behind the first, and in the
+// order of k that the stream multiplies in.
 template <bool DW>
 struct StreamRows {
     __amdgpu_buffer_rsrc_t rs;
@@ -140,9 +143,9 @@ struct StreamRows {
 
 // v as two fp16 values, hi + lo / 2048: within 2^-22 of v, or 2^-36 where that is
 // more (|v| below 2^-14).  fp16's least step is 2^-24, so the rest is kept 2^11
-// larger, the most that the rest of the largest value, 16, leaves room for.  hi of a v that is not zero is
-// none either (then lo gives back the difference), so that v keeps its sign beside
-// an infinite weight; past fp16 hi is an infinity, alone.
+// larger, the most that the rest of the largest value, 16, leaves room for.  hi of a
+// v that is not zero is not zero either (lo then gives back the difference), so that
+// v keeps its sign beside an infinite weight; past fp16 hi is an infinity, alone.
 constexpr float kRest = 2048.0f;
 struct StreamHalves {
     uint16_t hi, lo;
@@ -194,9 +197,10 @@ struct StreamSums {
 // multiply(b, i) for n > 0 units in turn, the next one's loads in flight: load(b,
 // i) is called for the unit past the last too, and has to be one that reads
 // nothing new there, so that no wait depends on which way a branch went.  A third
-// unit gains nothing (fp16 one token x 2 of 8 experts 77 us either way; 16 x 11008 x
-// 4096 in 4 bits 11.3 us with two, 12.5 with three): with two, eight waves have the
-// 46 KB per CU in flight that the card's rate times its latency comes to.
+// unit gained nothing when it was tried (fp16 one token x 2 of 8 experts 77 us either
+// way; 16 x 11008 x 4096 in 4 bits 11.3 us with two, 12.5 with three): with two,
+// eight waves have the 46 KB per CU in flight that the card's rate times its latency
+// comes to.
 template <class Batch, class Load, class Multiply>
 __device__ __forceinline__ void stream_ring(int n, Load&& load, Multiply&& multiply)
 {

@@ -28,7 +28,9 @@ __device__ __forceinline__ half2v and_or(uint32_t w, uint32_t mask, uint32_t bas
 }
 
 // The eight values q - z of a word as an MFMA operand: dword i holds rows i and
-// i + 4.  A code behind the bits of 1024 in fp16 is 1024 + q, four bits higher
+// i + 4.  The conversion by a fixed exponent is a published one (Kim, Henry, Fahim and
+// Awadalla, "Who Says Elephants Can't Run", 2022); this form is for zero points of 8
+// bits.  A code behind the bits of 1024 in fp16 is 1024 + q, four bits higher
 // 1024 + 16 q, and the differences below are whole numbers of at most 9 bits,
 // so every value is exact.  lo: -(1024 + z), hi: -(64 + z), twice each.  Nine
 // instructions for eight weights; the loop is bound by them where the weights'

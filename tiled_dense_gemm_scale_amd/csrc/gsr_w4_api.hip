@@ -46,13 +46,17 @@ struct GemmPlan {
 
 // Many rows are bound by the matrix cores, whose tiles of 256 rows the stream does
 // not have: there the values are written out once, 2.5 bytes to and from memory
-// per weight, and the dense kernels multiply them.  That rounds each weight to fp16
-// (error of C against 64 bits 0.00021, its own rounding's, to 0.00027).  In us, the stream, and both
-// steps: 11008 x 4096 with 64 rows 21 and 37, 160 rows 45 and 56, 192 rows 59 and
-// 49, 1025 rows 273 and 107; 2048 x 2048 with 512 rows 19 and 23, 1025 rows 38 and
-// 27; 333 x 1001 with 4000 rows 27 and 44.  The stream takes 2 and for each round
+// per weight, the dense kernels multiply them, and a third launch looks after the
+// columns past fp16.  A matrix of 2^30 weights and more has no such way (the dense
+// kernels' are below 2^31 bytes): 1025 rows with 8192 x 131064 3.0 ms, with 8192 x
+// 131072 5.7.  That rounds each weight to fp16 (error of C against 64 bits
+// 0.00021, its own rounding's, to 0.00027).  In us, the stream, and the three steps:
+// 11008 x 4096 with 64 rows 21 and 37, 160 rows 45 and 56, 192 rows 56 and 50, 1025
+// rows 271 and 112; 2048 x 2048 with 512 rows 19 and 23, 1025 rows 36 and 30; 1000 x
+// 4096 with 1500 rows 45 and 40; 333 x 1001 with 4000 rows 26 and 44.  The stream takes 2 and for each round
 // of 256 workgroups 1.4 and 0.16 per unit of K (0.25 where rows of A start at odd
-// elements); the values 9 and 7 TB/s; the dense products their selector's time,
+// elements); the values 9 and 7 TB/s (the look at the scales is not counted: a call
+// among others sees 0 to 4 of its 4.8 us); the dense products their selector's time,
 // off the 128-bit path 34 ns per K or 340 TFLOP/s.
 bool dense_pays(int64_t M, int64_t N, int64_t K, bool vec)
 {

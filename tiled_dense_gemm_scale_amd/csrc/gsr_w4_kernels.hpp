@@ -50,9 +50,11 @@ __device__ __forceinline__ f32x4 w4_epilogue(const W4Gemm& p, int col, f32x4 s)
 // part of it: then the tile's sums meet in the workspace and the workgroup that
 // comes last adds them.  One block of rows is bound by the codes' bytes and the
 // chain of launch, loads and sums; more of them run beside each other and read the
-// codes again, from the caches.  4096 x 4096 with one row 7.4 us (8.7 MB), 11008 x
-// 4096 with 16 rows 9.7 (25 MB, 2.6 TB/s) and with 64 rows 21, 1001 x 4093 in
-// groups of 32 with 61 rows 10.5.
+// codes again, from the caches, and unpack them again: from some 100 rows on it is
+// slower than fp16 weights (11008 x 4096 with 128 rows 39 us and 31).  4096 x 4096 with
+// one row 7.0 us (8.7 MB), 11008 x 4096 with 16 rows 9.8 (25 MB, 2.6 TB/s; in groups of
+// 64 with zero points 10.4) and with 64 rows 21.5, 1001 x 4093 in groups of 32 with 61
+// rows 10.0.
 template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 {
@@ -92,9 +94,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 // weight may not fit it (some |scale| times the farthest code from its zero point
 // is 65520 or more, the first value that rounds to an infinity), with the weights as
 // they are.  A workgroup has 64 columns and looks at their scales (0.7 MB of 11008
-// columns of 32 groups; 1025 x 11008 x 4096 120 us without this launch, 120 to 125 with
-// it); where one is so large it walks all rows, its waves each a part of K.  A scale that is not finite is left to the
-// product: its column's sums are not finite either way.
+// columns of 32 groups, 4.8 us, most of it the launch's); where one is so large it
+// walks all rows, its waves each a part of K.  A scale that is not finite is left to
+// the product: its column's sums are not finite either way.
 template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_past_kernel(W4Gemm p)
 {
@@ -221,9 +223,10 @@ struct W4Range {
 // A wave has 256 columns, four per lane, and 32 rows of a group, in registers;
 // the four waves of a workgroup have 128 rows, one to four groups, and tell each
 // other their largest values through LDS.  Larger groups are walked 128 rows at
-// a time, twice (LONG).  4096 x 11008: 113 MB in 30 us, 3.8 TB/s: every wave loads
-// before it computes, 1376 workgroups on 1024 places; eight waves of 16 rows take
-// the same.
+// a time, twice (LONG).  4096 x 11008: 113 MB in 29 us, 3.9 TB/s, with zero points
+// 31: every wave loads before it computes, 1376 workgroups on 1024 places; eight
+// waves of 16 rows take the same.  (20 to 40 scalar values live in lanes of vector
+// registers.)
 template <bool LONG, bool ZEROS>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
 {
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(W4Convert p)
 }
 
 // 32 rows of four columns per lane, which are of one group.  4096 x 11008: 113 MB
-// in 19.5 us, 5.8 TB/s.
+// in 19 us, 6.0 TB/s.
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(W4Convert p)
 {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

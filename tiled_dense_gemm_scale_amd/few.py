@@ -1,6 +1,9 @@
 """A whole layer of routed experts for a few tokens in two launches, with the
 experts in fp16 or in 4 bits.  For serving: autograd records nothing, and there
-is no gradient here.  expert_mlp takes any number of tokens."""
+is no gradient here.  expert_mlp takes any number of tokens, of experts in fp16
+without a gate (and without SiLU); for more than 64 tokens 4-bit experts are
+dequantize_w4's values, and a gate is a second gemm_grouped and the caller's own
+product of the two."""
 from __future__ import annotations
 
 from typing import Optional, Union
