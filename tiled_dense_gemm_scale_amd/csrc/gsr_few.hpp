@@ -25,15 +25,15 @@
 // (64 tokens x 2 of 8 in 4 bits 129 us so and 154 with both halves, when A was read
 // row by row; the others within 2 us).
 // Measured: 4096 -> 11008 -> 4096, 2 of 8 experts, one token: 361 MB in fp16 in 77
-// us (36 and 40 of them the launches' own), in 4 bits 93 MB in 37 us (15 and 18, of
-// which the ids, the tiles, the first loads and the meeting take about 5 each); 16
-// tokens x 8 of 64 gated experts 2048 -> 1024 -> 2048, 710 MB in 104 to 110 us and 194
-// MB in 51.  With many tokens in 4 bits the waves wait 39 and 48 % of their time and
-// unpack codes for most of the rest: 64 tokens x 2 of 8 132 to 141 us (54 and 77) for
-// 373 MB.  With several rows to an expert the layer of four launches is as fast or
-// faster: 4096 -> 11008 in fp16, 2 of 8 experts, 16 tokens 266 us here and 272 there,
-// 32 272 and 266, 64 311 and 266 (8 of 64 experts 2048 -> 1024, 64 tokens 122 and
-// 127).
+// us (36 and 40 of them the launches' own), in 4 bits 93 MB in 34 to 38 us (15 and
+// 18, of which the ids, the tiles, the first loads and the meeting take about 5
+// each); 16 tokens x 8 of 64 gated experts 2048 -> 1024 -> 2048, 710 MB in 104 to
+// 113 us and 194 MB in 51.  With many tokens in 4 bits the waves wait 39 and 48 %
+// of their time and unpack codes for most of the rest: 64 tokens x 2 of 8 141 to
+// 144 us (54 and 77 under the profiler) for 373 MB.  With several rows to an expert
+// the layer of four launches is as fast or faster: 4096 -> 11008 in fp16, 2 of 8
+// experts, 16 tokens 266 us here and 272 there, 32 272 and 266, 64 311 and 266 (8
+// of 64 experts 2048 -> 1024, 64 tokens 122 and 127).
 #pragma once
 
 #include "gsr_stream.hpp"

@@ -56,7 +56,7 @@ struct GemmPlan {
 // 4096 with 1500 rows 45 and 40; 333 x 1001 with 4000 rows 26 and 44.  The stream takes 2 and for each round
 // of 256 workgroups 1.4 and 0.16 per unit of K (0.25 where rows of A start at odd
 // elements); the values 9 and 7 TB/s (the look at the scales is not counted: a call
-// among others sees 0 to 4 of its 4.8 us); the dense products their selector's time,
+// among others sees 0 to 4 of its 4.6 us); the dense products their selector's time,
 // off the 128-bit path 34 ns per K or 340 TFLOP/s.
 bool dense_pays(int64_t M, int64_t N, int64_t K, bool vec)
 {

@@ -53,7 +53,7 @@ __device__ __forceinline__ f32x4 w4_epilogue(const W4Gemm& p, int col, f32x4 s)
 // codes again, from the caches, and unpack them again: from some 100 rows on it is
 // slower than fp16 weights (11008 x 4096 with 128 rows 39 us and 31).  4096 x 4096 with
 // one row 7.0 us (8.7 MB), 11008 x 4096 with 16 rows 9.8 (25 MB, 2.6 TB/s; in groups of
-// 64 with zero points 10.4) and with 64 rows 21.5, 1001 x 4093 in groups of 32 with 61
+// 64 with zero points 10.5) and with 64 rows 21.5, 1001 x 4093 in groups of 32 with 61
 // rows 10.0.
 template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
@@ -94,9 +94,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2) w4_rows_kernel(W4Gemm p)
 // weight may not fit it (some |scale| times the farthest code from its zero point
 // is 65520 or more, the first value that rounds to an infinity), with the weights as
 // they are.  A workgroup has 64 columns and looks at their scales (0.7 MB of 11008
-// columns of 32 groups, 4.8 us, most of it the launch's); where one is so large it
-// walks all rows, its waves each a part of K.  A scale that is not finite is left to
-// the product: its column's sums are not finite either way.
+// columns of 32 groups, 4.6 us, most of it the launch's); where one is so large it
+// walks all rows, its waves each a part of K (1025 x 11008 x 4096 with such a column
+// 480 us, with nothing but such columns 500; trained weights have none).  A scale that
+// is not finite is left to the product: its column's sums are not finite either way.
 template <int FL, bool DW>
 __global__ void __launch_bounds__(kStreamThreads, 2) w4_past_kernel(W4Gemm p)
 {
