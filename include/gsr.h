@@ -437,7 +437,7 @@ typedef struct gsr_weights {
  *   weights  T x k binary32, or NULL (ones)
  *   activation  any gsr_activation
  * Sums, biases, activation, gate and weights are binary32; between the launches
- * each h is kept to within 2^-22 of itself or 2^-36, whichever is more, and one that
+ * each h is kept to within 2^-22 of itself or 2^-35, whichever is more, and one that
  * is not zero keeps its sign beside an infinite weight (an h beyond binary16's range
  * is an infinity); out is rounded once.  weights[t,j] that are not finite make their
  * token's outputs not finite.  A token's choices are added in an order that the ids

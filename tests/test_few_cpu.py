@@ -137,3 +137,19 @@ def test_python_refusals():
         gsr.gemm_w4(h, gsr.W4(i32, s, None, 64, 32))
     with pytest.raises(ValueError, match="device"):
         gsr.expert_mlp_few(h, i32, None, h, h, torch.zeros(1, dtype=torch.uint8))
+
+
+def test_bound_of_h():
+    """h as two halves, hi + lo / 2048, is within 2^-22 of itself or 2^-35, and hi is
+    zero for zeros alone: by the same steps in binary32 and binary16."""
+    rng = np.random.default_rng(0)
+    v = (2.0 ** rng.uniform(-149, 15.99, 400000) * rng.choice([-1.0, 1.0], 400000)).astype(np.float32)
+    edges = np.float32(2.0) ** np.arange(-149, 16, dtype=np.float32)
+    v = np.concatenate([v, edges, np.nextafter(edges, np.float32(0)), -np.nextafter(edges, np.float32(1e9)), [np.float32(65519.99)]])
+    hi = v.astype(np.float16)
+    lost = (hi == 0) & (v != 0)
+    hi[lost] = np.copysign(np.float16(2.0 ** -24), v[lost])
+    lo = ((v - hi.astype(np.float32)) * np.float32(2048)).astype(np.float16)
+    assert np.isfinite(hi).all() and np.isfinite(lo).all() and (np.sign(hi) == np.sign(v)).all()
+    v = v.astype(np.float64)
+    assert (np.abs(hi.astype(np.float64) + lo.astype(np.float64) / 2048 - v) <= np.maximum(np.abs(v) * 2.0 ** -22, 2.0 ** -35)).all()

@@ -141,11 +141,12 @@ struct StreamRows {
     }
 };
 
-// v as two fp16 values, hi + lo / 2048: within 2^-22 of v, or 2^-36 where that is
-// more (|v| below 2^-14).  fp16's least step is 2^-24, so the rest is kept 2^11
-// larger, the most that the rest of the largest value, 16, leaves room for.  hi of a
-// v that is not zero is not zero either (lo then gives back the difference), so that
-// v keeps its sign beside an infinite weight; past fp16 hi is an infinity, alone.
+// v as two fp16 values, hi + lo / 2048: within 2^-22 of v, or 2^-35 where that is
+// more (|v| below 2^-13).  fp16's least step is 2^-24, so the rest is kept 2^11
+// larger, the most that the rest of the largest value, 16, leaves room for; its own
+// rounding is then 2^-36.  hi of a v that is not zero is not zero either (lo gives
+// back the difference, rounded once more on the way), so that v keeps its sign beside
+// an infinite weight; past fp16 hi is an infinity, alone.
 constexpr float kRest = 2048.0f;
 struct StreamHalves {
     uint16_t hi, lo;

@@ -52,7 +52,7 @@ def expert_mlp_few(x: torch.Tensor, ids: torch.Tensor, weights: Optional[torch.T
     gate (E, H, F) and down (E, F, O) fp16, or all of them W4 of those sizes, up
     and gate of one group; biases (E, F), (E, F) and (E, O) fp16 or None; act
     "relu", "gelu" (tanh form), "silu" or "none".  Sums are fp32; h is kept to
-    within 2^-22 of itself or 2^-36, whichever is more, and becomes an infinity past
+    within 2^-22 of itself or 2^-35, whichever is more, and becomes an infinity past
     fp16's range.  workspace: new_workspace(expert_few_workspace_bytes(T, k, E, F, O)), one
     per call that may run at the same time.  Returns out (T, O)."""
     matrix("x", x, torch.float16, 2)
